@@ -58,13 +58,15 @@ typedef enum {
     CSA2_MODE_REUSE = 2     /* reuse the source layer's indices unchanged       */
 } csa2_mode;
 
-typedef enum { CSA2_BF16 = 0, CSA2_FP8_E4M3 = 1, CSA2_FP32 = 2 } csa2_dtype;
+typedef enum { CSA2_BF16 = 0, CSA2_FP8_E4M3 = 1, CSA2_FP32 = 2, CSA2_FP16 = 3 } csa2_dtype;
 
 /* Bits OR-ed into *err_flag by the kernels. */
 #define CSA2_FLAG_BAD_INDEX 0x1u  /* attention idx outside [-1, kv_len)              */
 #define CSA2_FLAG_BAD_POOL 0x2u   /* pool block id outside [-1, ceil(N/8))           */
 #define CSA2_FLAG_BAD_SLOT 0x4u   /* quantise dst_slot outside [0, n_slots)          */
 #define CSA2_FLAG_TIMEOUT 0x8u    /* a bounded on-chip wait gave up (results invalid)  */
+#define CSA2_FLAG_NO_BLOCKS 0x10u /* build_slots: the free list ran out, a request waits */
+#define CSA2_FLAG_NONFINITE 0x20u /* paged quantise: an infinity or NaN among the rows   */
 
 /* Fixed indexer shape: 4 heads of dimension 64, one 64-dim key per entry. */
 #define CSA2_INDEX_HEADS 4
@@ -366,6 +368,129 @@ csa2_status csa2_sparse_attn_fp4_noalloc(csa2_mode mode, int B, int T, int H, in
                                          float sm_scale, void *out, csa2_dtype out_dt, float *lse,
                                          uint32_t *err_flag, csa2_stream_t stream);
 size_t csa2_sparse_attn_noalloc_max_scratch_bytes(void);
+
+/*
+ * The paged 8-bit cache: attention layers of the same model that keep every
+ * token (no index, no compression) hold their keys and values as E4M3 codes
+ * in blocks of tokens, with one fp32 scale per block and KV head for the keys
+ * and one for the values.  The pages describe no such cache; its layout and
+ * rules are this library's own.
+ *
+ *   k_codes, v_codes  uint8 [n_blocks, Hkv, S, D], a block's rows of one head
+ *                     contiguous; S in {16, 32, 64, 128} tokens, D in {64, 128}
+ *   k_scale, v_scale  fp32 [n_blocks, Hkv]; a value is code * scale
+ *   block_table       int32 [B, M] (row stride table_stride): token position p
+ *                     of request b is row p % S of block block_table[b][p / S]
+ *   slot of a token   block * S + row, int64; -1: the token is not stored
+ *
+ * One step of a serving loop is csa2_build_slots (which blocks the new tokens
+ * go to), csa2_quantize_kv_fp8_paged (store them) per layer, then
+ * csa2_paged_attn_fp8 (attend) per layer.
+ */
+
+/*
+ * csa2_build_slots -- block tables and slot maps of a ragged batch, on the
+ * device, from the requests' lengths.
+ *
+ * Request b holds kv_len[b] tokens and brings n = new_len[b] more this step;
+ * n < 0 says that the request has ended: the ceil(kv_len[b] / S) blocks of its
+ * table row go back to the free list (its row is left as it is) and its
+ * length becomes 0.  The free list is a stack: free_list[0 .. free_count)
+ * holds free block ids, taken from its end.  Blocks of ended requests are put
+ * on top first (by request, then by position in the row), so that this step's
+ * requests may take them; then requests take blocks in order of b.  A request
+ * whose blocks are not there takes none and waits (CSA2_FLAG_NO_BLOCKS): its
+ * length stays, its tokens get slot -1; so do all later requests that need a
+ * new block.  One whose tokens do not fit its table row (kv_len + n > M * S)
+ * or the token budget T waits as well (CSA2_FLAG_BAD_SLOT).
+ *
+ * B          1..8192 requests; S >= 1 (any); M >= 1 with M * S and B * M < 2^31.
+ * T          rows of slots and positions, 0..2^30: the step's token budget.
+ * block_table  read where a request already has blocks, written where it takes
+ *            new ones; nothing else is touched.
+ * free_list  int32 [free_cap]; entries at and above the new count keep
+ *            whatever they hold.  Ids are moved, not interpreted, except that
+ *            a negative one gives its tokens slot -1 (CSA2_FLAG_BAD_INDEX).
+ * kv_len_out, free_count_out  int32 [B], [1]: the lengths and the count after
+ *            the step; may be kv_len and free_count themselves (a captured
+ *            step that is replayed).
+ * cu_len     int32 [B + 1]: the first row of each request among the step's
+ *            tokens (those of waiting requests counted), clamped to T.
+ * positions  int32 [T] or NULL, slots int64 [T]: position and slot of each
+ *            row; -1 for rows of waiting requests and behind the last one.
+ * A kv_len outside [0, M * S] or a free_count outside [0, free_cap] acts as the
+ * nearest bound, blocks that find no place in free_list are dropped
+ * (CSA2_FLAG_BAD_INDEX).
+ */
+csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int S, int64_t T, int64_t free_cap,
+                             const int32_t *kv_len, const int32_t *new_len, int32_t *block_table, int32_t *free_list,
+                             const int32_t *free_count, int32_t *kv_len_out, int32_t *free_count_out, int32_t *cu_len,
+                             int32_t *positions, int64_t *slots, uint32_t *err_flag, csa2_stream_t stream);
+
+/*
+ * csa2_quantize_kv_fp8_paged -- store new key and value rows in the paged
+ * cache.  Row r goes to slots[r].  For each block and head the rows that a
+ * call brings to it, together, set the scale:
+ *   need = the least power of two s >= 2^-126 with amax <= 448 s
+ *   s = need if the rows start the block (first row slot % S == 0), else
+ *       max(the block's scale, need)
+ *   code = E4M3(x / s), round to nearest even
+ * and where s grew, the rows stored before are re-encoded, E4M3(code * old / s):
+ * old / s is a power of two, so a stored value changes only by what falls
+ * below E4M3's subnormal step (2^-9 s).
+ *
+ * k, v    bf16 or fp16 [T, Hkv, D], 16-byte aligned, D contiguous; token and
+ *         head strides in elements, multiples of 8 (slices of a fused
+ *         projection's output fit).
+ * slots   int64 [T], as csa2_build_slots writes it.  -1 skips a row.  The rows
+ *         of one block stand next to each other, their slots counting up by
+ *         one; a row that breaks this inside a block is skipped with the rest of
+ *         its run, as is a slot outside [-1, n_blocks * S) (CSA2_FLAG_BAD_SLOT).
+ *         A block whose rows come in two separate runs is a data race.
+ * Infinities are stored as +-448 s and NaN as 0, neither counts toward amax
+ * (CSA2_FLAG_NONFINITE).  codes 16-byte, scales 4-byte aligned.
+ */
+csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, csa2_dtype dt, int64_t T, int Hkv, int D,
+                                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                       int64_t v_head_stride, const int64_t *slots, int64_t n_blocks, int S,
+                                       uint8_t *k_codes, uint8_t *v_codes, float *k_scale, float *v_scale,
+                                       uint32_t *err_flag, csa2_stream_t stream);
+
+/*
+ * csa2_paged_attn_fp8 -- causal attention of a ragged batch over the paged
+ * cache.  Request b's rows are cu_len[b] .. cu_len[b+1) of q, the last n =
+ * cu_len[b+1] - cu_len[b] of its kv_len[b] tokens: row i sits at position
+ * p = kv_len[b] - n + i and sees keys max(0, p - window + 1) .. p (window 0:
+ * all up to p).  Query head h reads KV head h / (Hq / Hkv).
+ *   z_j = sm_scale * q . (k_code_j * k_scale),  out = sum_j softmax(z)_j v_code_j * v_scale,
+ *   lse = log sum_j exp(z_j)
+ * A row that sees nothing gives out = 0, lse = -inf.  Rows of q behind the
+ * last request are not written.  Codes enter the tensor cores as exact f16, q
+ * as f16 scaled per row by a power of two (bf16 values within 2^-31 of the
+ * row's largest are exact); sums and softmax statistics are fp32, the weights
+ * of the values are rounded to f16.
+ *
+ * q, out  bf16 or fp16 [T, Hq, D], q with token and head strides in elements
+ *         (multiples of 8), out dense; 16-byte aligned.  Hq a multiple of Hkv.
+ * lse     fp32 [T, Hq] or NULL.
+ * kv_len int32 [B], cu_len int32 [B + 1] (clamped to [0, T]); tokens beyond
+ *         M * S are not there.  A table entry outside [0, n_blocks) where a
+ *         visible key should be hides its keys (CSA2_FLAG_BAD_INDEX).
+ * max_new upper bound (>= 1) of the rows of a request, known on the host: it only
+ *         chooses among kernels, every value >= 1 gives right results.
+ * Stored rows must hold no NaN code (csa2_quantize_kv_fp8_paged writes none);
+ * rows at or beyond kv_len may hold anything.
+ * workspace csa2_paged_attn_workspace_bytes() bytes, 16-byte aligned (at most
+ *         64 MiB): partial results of requests that several CTAs share.  Calls
+ *         that may overlap need one each.
+ */
+csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, const void *q,
+                                int64_t q_token_stride, int64_t q_head_stride, const uint8_t *k_codes,
+                                const uint8_t *v_codes, const float *k_scale, const float *v_scale, int64_t n_blocks,
+                                int S, const int32_t *block_table, int M, int64_t table_stride, const int32_t *kv_len,
+                                const int32_t *cu_len, int max_new, int window, float sm_scale, void *out, float *lse,
+                                uint32_t *err_flag, void *workspace, size_t ws_bytes, csa2_stream_t stream);
+size_t csa2_paged_attn_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new);
 
 /*
  * csa2_selftest_bounded_wait -- exercises the library's bounded wait on an

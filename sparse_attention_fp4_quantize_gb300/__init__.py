@@ -14,7 +14,10 @@ Names follow the C ABI: ``csa2_quantize_kv_fp4``, ``csa2_rope_quantize_kv_fp4``
 ``csa2_topk``, ``csa2_index_topk`` (fused decode indexer),
 ``csa2_index_topk_dense`` (fused indexer for many query tokens),
 ``csa2_sparse_attn_fp4`` (and ``csa2_sparse_attn_fp4_noalloc``),
-``csa2_swa_attn_fp8`` (sliding-window branch and merge),
+``csa2_swa_attn_fp8`` (sliding-window branch and merge), the paged 8-bit
+cache's ``csa2_build_slots`` (block tables and slot maps),
+``csa2_quantize_kv_fp8_paged`` (append) and ``csa2_paged_attn_fp8`` (attention;
+``paged.PagedCache`` keeps the buffers and calls the three in order),
 ``csa2_selftest_bounded_wait`` and the ``*_workspace_bytes`` helpers.
 """
 from __future__ import annotations
@@ -28,8 +31,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
-BF16, FP8_E4M3, FP32 = 0, 1, 2
+BF16, FP8_E4M3, FP32, FP16 = 0, 1, 2, 3
 FLAG_BAD_INDEX, FLAG_BAD_POOL, FLAG_BAD_SLOT, FLAG_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+FLAG_NO_BLOCKS, FLAG_NONFINITE = 0x10, 0x20
 INDEX_HEADS, INDEX_DIM, POOL_BLOCK, MAX_POOL, MAX_K = 4, 64, 8, 2048, 2048
 
 STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED", 3: "CSA2_ERR_WORKSPACE",
@@ -68,6 +72,12 @@ def _load() -> ctypes.CDLL:
         "csa2_sparse_attn_fp4_noalloc": ([i32, i32, i32, i32, i32, i32, P, P, P, i64, P, i32, P, f32, P, i32, P,
                                           P, P], i32),
         "csa2_sparse_attn_noalloc_max_scratch_bytes": ([], u64),
+        "csa2_build_slots": ([i32, i32, i64, i32, i64, i64, P, P, P, P, P, P, P, P, P, P, P, P], i32),
+        "csa2_quantize_kv_fp8_paged": ([P, P, i32, i64, i32, i32, i64, i64, i64, i64, P, i64, i32, P, P, P, P, P, P],
+                                       i32),
+        "csa2_paged_attn_fp8": ([i32, i64, i32, i32, i32, i32, P, i64, i64, P, P, P, P, i64, i32, P, i32, i64, P, P,
+                                 i32, i32, f32, P, P, P, P, u64, P], i32),
+        "csa2_paged_attn_workspace_bytes": ([i32, i64, i32, i32, i32, i32], u64),
         "csa2_selftest_bounded_wait": ([ctypes.c_uint32, P, P], i32),
         "csa2_status_string": ([i32], ctypes.c_char_p),
         "csa2_last_error": ([], ctypes.c_char_p),
@@ -89,6 +99,8 @@ def exported_symbols():
             "csa2_index_topk_dense_workspace_bytes", "csa2_sparse_attn_fp4", "csa2_sparse_attn_workspace_bytes",
             "csa2_sparse_attn_fp4_prefetch", "csa2_swa_attn_fp8",
             "csa2_sparse_attn_fp4_noalloc", "csa2_sparse_attn_noalloc_max_scratch_bytes",
+            "csa2_build_slots", "csa2_quantize_kv_fp8_paged", "csa2_paged_attn_fp8",
+            "csa2_paged_attn_workspace_bytes",
             "csa2_selftest_bounded_wait", "csa2_status_string", "csa2_last_error", "csa2_version"]
 
 
@@ -430,3 +442,158 @@ def csa2_sparse_attn_fp4_noalloc(mode, q, codes, scales, N, idx, out, sm_scale, 
 
 def noalloc_max_scratch_bytes() -> int:
     return int(_lib.csa2_sparse_attn_noalloc_max_scratch_bytes())
+
+
+# ------------------------------------------------------------------ paged 8-bit cache
+_I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
+_F8 = (torch.uint8, torch.float8_e4m3fn)
+_ROWS = {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16}
+
+
+def _want(t, name, dtypes, shape, dense=True):
+    """t has one of these dtypes and this shape (None: any extent) and, unless said otherwise, no gaps."""
+    if t.dtype not in dtypes:
+        raise TypeError("%s: %s elements do not fit this call" % (name, t.dtype))
+    if len(t.shape) != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if dense and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _want_flag(err_flag):
+    if err_flag is not None:
+        _flag(err_flag)
+
+
+def _table_stride(block_table):
+    """Row stride of a block table whose rows have no gaps between entries."""
+    M = block_table.shape[1]
+    if M > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table rows must be contiguous")
+    return block_table.stride(0) if block_table.shape[0] > 1 else M
+
+
+def _row_strides(x, name):
+    """(token, head) strides of rows [T, H, D] with contiguous channels."""
+    T, H, D = x.shape
+    st, sh, sd = x.stride()
+    if sd != 1 and D > 1:
+        raise ValueError("%s must have contiguous channels" % name)
+    st, sh = (st if T > 1 else H * D), (sh if H > 1 else D)     # strides of single rows say nothing
+    return st, sh
+
+
+def _launch(ts, stream, name, *args):
+    """Call the C function on the tensors' device (all of them on one)."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and (t.device != dev or not _on_device(t)):
+            raise ValueError("tensors must be CUDA tensors of one device")
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _check(getattr(_lib, name)(*args, _stream(stream)))
+    _check(getattr(_lib, name)(*args, _stream(stream)))
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def csa2_build_slots(kv_len, new_len, block_table, free_list, free_count, block_size, kv_len_out, free_count_out,
+                     cu_len, positions, slots, err_flag=None, stream=None):
+    """Block tables and slot maps of a step from the requests' lengths.
+    kv_len, new_len int32 [B] (new_len < 0: the request has ended), block_table
+    int32 [B, M] (updated in place), free_list int32 [capacity] with
+    free_count int32 [1] ids on it -> kv_len_out int32 [B], free_count_out
+    int32 [1] (may be the inputs), cu_len int32 [B + 1], positions int32 [T] or
+    None, slots int64 [T]."""
+    B, M = block_table.shape
+    T = slots.shape[0]
+    _want(kv_len, "kv_len", _I32, (B,))
+    _want(new_len, "new_len", _I32, (B,))
+    _want(block_table, "block_table", _I32, (B, M), dense=False)
+    _want(free_list, "free_list", _I32, (None,))
+    _want(free_count, "free_count", _I32, (1,))
+    _want(kv_len_out, "kv_len_out", _I32, (B,))
+    _want(free_count_out, "free_count_out", _I32, (1,))
+    _want(cu_len, "cu_len", _I32, (B + 1,))
+    _want(slots, "slots", _I64, (T,))
+    if positions is not None:
+        _want(positions, "positions", _I32, (T,))
+    _want_flag(err_flag)
+    _launch((kv_len, new_len, block_table, free_list, free_count, kv_len_out, free_count_out, cu_len, slots, positions,
+             err_flag), stream, "csa2_build_slots", B, M, _table_stride(block_table), int(block_size), T,
+            free_list.shape[0], _p(kv_len), _p(new_len), _p(block_table), _p(free_list), _p(free_count),
+            _p(kv_len_out), _p(free_count_out), _p(cu_len), _p(positions), _p(slots), _p(err_flag))
+
+
+def _planes(k_codes, v_codes, k_scale, v_scale):
+    n, H, S, D = k_codes.shape
+    _want(k_codes, "k_codes", _F8, (n, H, S, D))
+    _want(v_codes, "v_codes", _F8, (n, H, S, D))
+    _want(k_scale, "k_scale", _F32, (n, H))
+    _want(v_scale, "v_scale", _F32, (n, H))
+    return n, H, S, D
+
+
+def csa2_quantize_kv_fp8_paged(k, v, slots, k_codes, v_codes, k_scale, v_scale, err_flag=None, stream=None):
+    """k, v bf16 (or int16 bits) or fp16 [T, Hkv, D] (any token and head
+    strides that are multiples of 8), slots int64 [T] -> k_codes, v_codes
+    uint8 or float8_e4m3fn [n_blocks, Hkv, S, D], k_scale, v_scale fp32
+    [n_blocks, Hkv], updated in place."""
+    n, H, S, D = _planes(k_codes, v_codes, k_scale, v_scale)
+    T = slots.shape[0]
+    if k.dtype not in _ROWS or v.dtype != k.dtype:
+        raise TypeError("k and v must both be bf16 (or int16 bits) or fp16, got %s and %s" % (k.dtype, v.dtype))
+    _want(k, "k", (k.dtype,), (T, H, D), dense=False)
+    _want(v, "v", (k.dtype,), (T, H, D), dense=False)
+    _want(slots, "slots", _I64, (T,))
+    _want_flag(err_flag)
+    _launch((k, v, slots, k_codes, v_codes, k_scale, v_scale, err_flag), stream, "csa2_quantize_kv_fp8_paged",
+            _p(k), _p(v), _ROWS[k.dtype], T, H, D, *_row_strides(k, "k"), *_row_strides(v, "v"), _p(slots), n, S,
+            _p(k_codes), _p(v_codes), _p(k_scale), _p(v_scale), _p(err_flag))
+
+
+def csa2_paged_attn_workspace_bytes(B, T, Hq, Hkv, D, max_new) -> int:
+    return int(_lib.csa2_paged_attn_workspace_bytes(B, T, Hq, Hkv, D, max_new))
+
+
+def workspace_for_paged_attn(B, T, Hq, Hkv, D, max_new, device="cuda"):
+    """Allocate (through torch) the scratch csa2_paged_attn_fp8 needs, or None."""
+    n = csa2_paged_attn_workspace_bytes(B, T, Hq, Hkv, D, max_new)
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def csa2_paged_attn_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, kv_len, cu_len, out, sm_scale, max_new,
+                        window=0, lse=None, err_flag=None, workspace=None, stream=None):
+    """Causal attention of a ragged batch over the paged cache.  q bf16 (or
+    int16 bits) or fp16 [T, Hq, D] (any token and head strides that are
+    multiples of 8), planes as csa2_quantize_kv_fp8_paged, block_table int32
+    [B, M], kv_len int32 [B], cu_len int32 [B + 1] -> out [T, Hq, D] of q's
+    type, lse fp32 [T, Hq].  max_new: upper bound of a request's rows (a
+    hint).  workspace: a CUDA byte tensor of at least
+    csa2_paged_attn_workspace_bytes bytes (allocated here when None)."""
+    n, H, S, D = _planes(k_codes, v_codes, k_scale, v_scale)
+    T, Hq = q.shape[0], q.shape[1]
+    B, M = block_table.shape
+    if q.dtype not in _ROWS or out.dtype != q.dtype:
+        raise TypeError("q and out must both be bf16 (or int16 bits) or fp16, got %s and %s" % (q.dtype, out.dtype))
+    _want(q, "q", (q.dtype,), (T, Hq, D), dense=False)
+    _want(out, "out", (q.dtype,), (T, Hq, D))
+    _want(block_table, "block_table", _I32, (B, M), dense=False)
+    _want(kv_len, "kv_len", _I32, (B,))
+    _want(cu_len, "cu_len", _I32, (B + 1,))
+    if lse is not None:
+        _want(lse, "lse", _F32, (T, Hq))
+    _want_flag(err_flag)
+    if H < 1 or Hq % H:
+        raise ValueError("%d query heads do not divide over %d KV heads" % (Hq, H))
+    if workspace is None:
+        workspace = workspace_for_paged_attn(B, T, Hq, H, D, int(max_new), device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch((q, k_codes, v_codes, k_scale, v_scale, block_table, kv_len, cu_len, out, lse, err_flag, workspace), stream,
+            "csa2_paged_attn_fp8", B, T, Hq, H, D, _ROWS[q.dtype], _p(q), *_row_strides(q, "q"), _p(k_codes),
+            _p(v_codes), _p(k_scale), _p(v_scale), n, S, _p(block_table), M, _table_stride(block_table), _p(kv_len),
+            _p(cu_len), int(max_new), int(window), float(sm_scale), _p(out), _p(lse), _p(err_flag), _p(workspace), ws)

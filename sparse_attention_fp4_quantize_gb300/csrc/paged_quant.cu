@@ -1,0 +1,207 @@
+// csa2_quantize_kv_fp8_paged: bf16 / fp16 key and value rows -> E4M3 codes in
+// the blocks of the paged cache, one power-of-two scale per (block, head).
+//
+// A run is the rows that the call brings to one block.  The scale of the block
+// is the least power of two s with amax <= 448 s, not below the block's scale
+// if it holds earlier rows.  Powers of two, because E4M3 is a floating-point
+// format: x / s then only shifts the exponent, so a finer scale would move where
+// values are rounded but not how finely (3 mantissa bits either way), and when a
+// later row makes s grow by 2^k the stored codes are re-encoded exactly except
+// for bits that fall below the subnormal step 2^-9 s.  Errors do not pile up
+// over the S appends that a decoding request makes to a block.
+//
+// One warp takes one (run, head, K or V).  The warps of a CTA look at a window of
+// rows; the first row of a run finds its length with a ballot, other rows
+// are left to it.  First pass: the largest magnitude, as an integer maximum of
+// the sign-less bit patterns (order-preserving for both formats).  Second pass,
+// from L1: scale, round, store.  A row's D codes are contiguous, a run's rows
+// too, so loads and stores are 16 and 8 bytes per lane of full lines.
+#include "common.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kWarps = 8;
+
+struct PagedQuantArgs {
+    const uint16_t *x[2];            // k, v
+    int64_t token_stride[2], head_stride[2];
+    uint8_t *codes[2];
+    float *scale[2];
+    const int64_t *slots;
+    int64_t T, n_slots;
+    int H, S, window;
+    uint32_t *err_flag;
+};
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, bool half_type) {
+    if (half_type) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Two fp32 -> two E4M3 bytes (lo in the low byte), nearest even, saturating.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Least power of two s >= 2^-126 with amax <= 448 s: 448 = 1.75 * 2^8, so its
+// exponent is that of amax less 8, one more if amax's significand exceeds 1.75.
+__device__ __forceinline__ float scale_of(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // biased exponent of s
+    e = e < 1 ? 1 : e;
+    return __uint_as_float((uint32_t)e << 23);
+}
+
+template <int D, bool HALF>
+__global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQuantArgs a) {
+    constexpr int LPR = D / 8;            // lanes per row: 8 channels each
+    constexpr int RPW = 32 / LPR;         // rows per warp load
+    constexpr uint32_t INF = HALF ? 0x7C00u : 0x7F80u;
+    constexpr uint32_t ABS2 = 0x7FFF7FFFu, ALL = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = blockIdx.y * kWarps + warp;      // (head, K or V)
+    pdl_wait();
+    pdl_launch_dependents();
+    if (unit >= 2 * a.H) return;
+    const int kv = unit & 1, h = unit >> 1;
+    const uint16_t *x = a.x[kv] + h * a.head_stride[kv] + (lane % LPR) * 8;
+    const int64_t ts = a.token_stride[kv];
+    const int64_t w0 = (int64_t)blockIdx.x * a.window, w1 = w0 + a.window < a.T ? w0 + a.window : a.T;
+    for (int64_t i = w0; i < w1; ++i) {
+        const int64_t s0 = a.slots[i];
+        if (s0 < 0 || s0 >= a.n_slots) {
+            if (s0 != -1 && unit == 0 && lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
+            continue;
+        }
+        const int64_t block = s0 / a.S;
+        const int start = (int)(s0 - block * a.S);
+        if (i > 0) {
+            const int64_t before = a.slots[i - 1];
+            if (before >= 0 && before < a.n_slots && before / a.S == block) {   // part of that row's run, or breaks it
+                if (before != s0 - 1 && unit == 0 && lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
+                continue;
+            }
+        }
+        int n = 0;                        // rows of the run
+        for (const int most = a.S - start; n < most;) {
+            const int k = n + lane;
+            const bool in = k < most && i + k < a.T && a.slots[i + k] == s0 + k;
+            const uint32_t ok = __ballot_sync(ALL, in);
+            n += ok == ALL ? 32 : __ffs(~ok) - 1;
+            if (ok != ALL) break;
+        }
+
+        uint32_t m2 = 0;                  // largest sign-less patterns of the even and odd channels
+        for (int r = lane / LPR; r < n; r += RPW) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(x + (i + r) * ts);
+            m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(v.x & ABS2, v.y & ABS2)), __vmaxu2(v.z & ABS2, v.w & ABS2));
+        }
+        uint32_t top = __reduce_max_sync(ALL, max(m2 & 0xFFFFu, m2 >> 16));
+        const bool bad = top >= INF;
+        if (bad) {                        // infinities and NaN do not count
+            top = 0;
+            for (int r = lane / LPR; r < n; r += RPW)
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t u = x[(i + r) * ts + c] & 0x7FFFu;
+                    if (u < INF) top = max(top, u);
+                }
+            top = __reduce_max_sync(ALL, top);
+            if (lane == 0) flag_error(a.err_flag, CSA2_FLAG_NONFINITE);
+        }
+        const float need = scale_of(unpack2(top, HALF).x);
+        float *scale = a.scale[kv] + block * a.H + h;
+        uint8_t *dst = a.codes[kv] + ((block * a.H + h) * a.S + start) * (int64_t)D + (lane % LPR) * 8;
+        float s = need;
+        if (start > 0) {
+            const float old = *scale;
+            s = fmaxf(old, need);
+            if (s != old) {               // re-encode the rows stored before
+                const float ratio = old > 0.0f ? old / s : 0.0f;
+                for (int r = lane / LPR - start; r < 0; r += RPW) {
+                    uint2 *p = reinterpret_cast<uint2 *>(dst + (int64_t)r * D);
+                    uint2 c = *p;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t lo, hi;
+                        e4m3x4_to_f16x2x2(q ? c.y : c.x, lo, hi);
+                        const float2 f0 = unpack2(lo, true), f1 = unpack2(hi, true);
+                        (q ? c.y : c.x) = to_e4m3x2(f0.x * ratio, f0.y * ratio) |
+                                          (to_e4m3x2(f1.x * ratio, f1.y * ratio) << 16);
+                    }
+                    *p = c;
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) *scale = s;
+        const float inv = 1.0f / s;       // exact: a power of two
+        for (int r = lane / LPR; r < n; r += RPW) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(x + (i + r) * ts);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t c[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float2 f = unpack2(w[q], HALF);
+                if (bad) {
+                    if (f.x != f.x) f.x = 0.0f;
+                    if (f.y != f.y) f.y = 0.0f;
+                }
+                c[q] = to_e4m3x2(f.x * inv, f.y * inv);
+            }
+            *reinterpret_cast<uint2 *>(dst + (int64_t)r * D) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        }
+    }
+}
+
+}  // namespace
+}  // namespace csa2
+
+using namespace csa2;
+
+extern "C" csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, csa2_dtype dt, int64_t T, int Hkv,
+                                                  int D, int64_t k_token_stride, int64_t k_head_stride,
+                                                  int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                                                  int64_t n_blocks, int S, uint8_t *k_codes, uint8_t *v_codes,
+                                                  float *k_scale, float *v_scale, uint32_t *err_flag,
+                                                  csa2_stream_t stream) {
+    clear_error();
+    CSA2_REQUIRE(dt == CSA2_BF16 || dt == CSA2_FP16, "quantize_paged: rows must be bf16 or fp16");
+    CSA2_REQUIRE(T >= 0 && T <= (1ll << 30), "quantize_paged: T=%lld not in [0, 2^30]", (long long)T);
+    CSA2_REQUIRE(Hkv >= 1 && Hkv <= 65536, "quantize_paged: Hkv=%d not in [1, 65536]", Hkv);
+    CSA2_REQUIRE(n_blocks >= 0 && n_blocks < (1ll << 31), "quantize_paged: n_blocks=%lld", (long long)n_blocks);
+    CSA2_REQUIRE(S == 16 || S == 32 || S == 64 || S == 128, "quantize_paged: S=%d not in {16, 32, 64, 128}", S);
+    CSA2_REQUIRE(k_token_stride % 8 == 0 && k_head_stride % 8 == 0 && v_token_stride % 8 == 0 &&
+                     v_head_stride % 8 == 0 && k_token_stride >= 0 && k_head_stride >= 0 && v_token_stride >= 0 &&
+                     v_head_stride >= 0,
+                 "quantize_paged: strides must be multiples of 8, not negative");
+    if (D != 64 && D != 128) {
+        set_error("quantize_paged: D=%d not in {64, 128}", D);
+        return CSA2_ERR_UNSUPPORTED;
+    }
+    if (T == 0) return CSA2_OK;
+    CSA2_REQUIRE(k && v && slots, "quantize_paged: null pointer");
+    CSA2_REQUIRE((k_codes && v_codes && k_scale && v_scale) || n_blocks == 0, "quantize_paged: null pointer");
+    CSA2_REQUIRE(aligned(k, 16) && aligned(v, 16), "quantize_paged: k and v must be 16-byte aligned");
+    CSA2_REQUIRE(aligned(k_codes, 16) && aligned(v_codes, 16), "quantize_paged: codes must be 16-byte aligned");
+    CSA2_REQUIRE(aligned(k_scale, 4) && aligned(v_scale, 4) && aligned(slots, 8), "quantize_paged: misaligned scales / slots");
+    PagedQuantArgs a = {};
+    a.x[0] = (const uint16_t *)k, a.x[1] = (const uint16_t *)v;
+    a.token_stride[0] = k_token_stride, a.token_stride[1] = v_token_stride;
+    a.head_stride[0] = k_head_stride, a.head_stride[1] = v_head_stride;
+    a.codes[0] = k_codes, a.codes[1] = v_codes;
+    a.scale[0] = k_scale, a.scale[1] = v_scale;
+    a.slots = slots, a.T = T, a.n_slots = n_blocks * S, a.H = Hkv, a.S = S, a.err_flag = err_flag;
+    a.window = T <= 2048 ? 1 : 16;
+    while ((T + a.window - 1) / a.window > (1 << 24)) a.window *= 2;
+    const dim3 grid((unsigned)((T + a.window - 1) / a.window), (unsigned)((2 * Hkv + kWarps - 1) / kWarps));
+    void (*kern)(PagedQuantArgs);
+    if (dt == CSA2_FP16) kern = D == 64 ? quantize_fp8_paged_kernel<64, true> : quantize_fp8_paged_kernel<128, true>;
+    else kern = D == 64 ? quantize_fp8_paged_kernel<64, false> : quantize_fp8_paged_kernel<128, false>;
+    CSA2_CUDA_CALL(launch_pdl(kern, grid, dim3(kWarps * 32), 0, stream_of(stream), a),
+                   "quantize_fp8_paged_kernel launch");
+    CSA2_LAUNCH_CHECK("quantize_fp8_paged_kernel");
+    return CSA2_OK;
+}

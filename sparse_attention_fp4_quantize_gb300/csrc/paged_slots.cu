@@ -1,0 +1,251 @@
+// csa2_build_slots: block tables and slot maps of a ragged batch from the
+// requests' lengths.
+//
+// With S tokens per block, held_b = ceil(kv_b / S) and after_b =
+// ceil((kv_b + n_b) / S), everything a step needs is three prefix sums over the
+// requests:
+//   cu_b   = sum_{i<b} max(n_i, 0)             first row of request b
+//   a_b    = sum_{i<b} (after_i - held_i)      first block it takes (those that fit)
+//   f_b    = sum_{i<b, ended} held_i           where its blocks land on the free list
+// A block index is then looked up, not searched for in order: block a of the
+// step is entry size - 1 - a of the stack (free list, then freed blocks), and
+// entry n_free + k of that stack is block k - f_b of the ended request b that
+// holds k, found by bisection in f.
+//
+// One thread-block cluster does it in one launch: every CTA computes the
+// prefix sums of all requests itself (a few KB from L2, so no CTA waits for
+// another's sums), then the cluster's threads share the rows.  The results
+// kv_len_out, free_count_out are written after a cluster barrier, when every
+// CTA has read the inputs, so they may be the inputs themselves.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace csa2 {
+namespace {
+
+constexpr int kMaxRequests = 8192;
+
+struct SlotArgs {
+    int B, M, S;
+    int64_t table_stride, T, free_cap;
+    const int32_t *kv_len, *new_len;
+    int32_t *table, *free_list;
+    const int32_t *free_count;
+    int32_t *kv_out, *free_out, *cu, *positions;
+    int64_t *slots;
+    uint32_t *err_flag;
+};
+
+// Exclusive prefix sum over the block of one value per thread; total to all.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_sums, int64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int64_t s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();   // the previous scan's sums have been read
+    if (lane == 31) warp_sums[warp] = s;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+        const int64_t x = warp_sums[w];
+        if (w < warp) before += x;
+        all += x;
+    }
+    total = all;
+    return before + s - v;
+}
+
+// Last b with a[b] <= x, of the nondecreasing a[0..n), a[0] <= x.
+__device__ __forceinline__ int last_at_most(const int32_t *a, int n, int32_t x) {
+    int lo = 0, hi = n;   // a[lo] <= x, and a[hi] > x or hi == n
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void build_slots_kernel(SlotArgs a) {
+    extern __shared__ int32_t sm[];
+    __shared__ int64_t warp_sums[32];
+    __shared__ int32_t s_taken;
+    int32_t *s_cu = sm;                    // first row
+    int32_t *s_kv = s_cu + a.B;            // tokens held
+    int32_t *s_take = s_kv + a.B;          // first block taken, -1: waits
+    int32_t *s_freed = s_take + a.B;       // first place among the freed blocks
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, nt = blockDim.x;
+    const int per = (a.B + nt - 1) / nt, b0 = tid * per, b1 = min(a.B, b0 + per);
+    const int64_t cap = (int64_t)a.M * a.S;
+    uint32_t flags = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (tid == 0) s_taken = 0;
+
+    // rows and freed blocks; n is bounded by T + 1, which fits no budget
+    int64_t rows = 0, freed = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int64_t k = a.kv_len[b], n = a.new_len[b];
+        const int32_t kv = (int32_t)(k < 0 ? 0 : (k > cap ? cap : k));
+        if (kv != k) flags |= CSA2_FLAG_BAD_INDEX;
+        s_kv[b] = kv;
+        if (n > 0) rows += n < a.T + 1 ? n : a.T + 1;
+        if (n < 0) freed += (kv + (int64_t)a.S - 1) / a.S;
+    }
+    int64_t n_rows, n_freed;
+    int64_t cu = block_scan(rows, warp_sums, n_rows);
+    int64_t fr = block_scan(freed, warp_sums, n_freed);
+    const int64_t fc = *a.free_count;
+    const int64_t n_free = fc < 0 ? 0 : (fc > a.free_cap ? a.free_cap : fc);
+    if (fc != n_free) flags |= CSA2_FLAG_BAD_INDEX;
+    const int64_t size = n_free + n_freed;
+
+    int64_t need = 0;
+    const int64_t cu0 = cu;
+    for (int b = b0; b < b1; ++b) {
+        const int64_t n = a.new_len[b], kv = s_kv[b], held = (kv + a.S - 1) / a.S;
+        s_cu[b] = (int32_t)(cu < a.T ? cu : a.T);
+        s_freed[b] = (int32_t)fr;
+        if (n > 0) {
+            cu += n < a.T + 1 ? n : a.T + 1;
+            if (cu <= a.T && kv + n <= cap) need += (kv + n + a.S - 1) / a.S - held;
+        } else if (n < 0) {
+            fr += held;
+        }
+    }
+    int64_t n_need;
+    int64_t take = block_scan(need, warp_sums, n_need);
+    int taken = 0;
+    cu = cu0;
+    for (int b = b0; b < b1; ++b) {
+        const int64_t n = a.new_len[b], kv = s_kv[b], held = (kv + a.S - 1) / a.S;
+        int32_t first = -1;
+        if (n == 0) first = 0;
+        if (n > 0) {
+            cu += n < a.T + 1 ? n : a.T + 1;
+            if (cu <= a.T && kv + n <= cap) {
+                const int64_t more = (kv + n + a.S - 1) / a.S - held;
+                if (more == 0 || take + more <= size) {
+                    first = more ? (int32_t)take : 0;
+                    if (more) taken = (int)(take + more);
+                } else {
+                    flags |= CSA2_FLAG_NO_BLOCKS;
+                }
+                take += more;
+            } else {
+                flags |= CSA2_FLAG_BAD_SLOT;
+            }
+        }
+        s_take[b] = first;
+    }
+    if (taken) atomicMax(&s_taken, taken);   // a maximum: the same in any order
+    __syncthreads();
+    int64_t count = size - s_taken;
+    if (count > a.free_cap) {
+        count = a.free_cap;
+        flags |= CSA2_FLAG_BAD_INDEX;
+    }
+
+    auto freed_block = [&](int64_t k) -> int32_t {
+        const int b = last_at_most(s_freed, a.B, (int32_t)k);
+        return a.table[b * a.table_stride + (k - s_freed[b])];
+    };
+    const int64_t step = (int64_t)ranks * nt;
+    const int64_t end = n_rows < a.T ? n_rows : a.T;
+    for (int64_t t = (int64_t)rank * nt + tid; t < a.T; t += step) {
+        int64_t slot = -1;
+        int32_t pos = -1;
+        if (t < end) {
+            const int b = last_at_most(s_cu, a.B, (int32_t)t);
+            const int32_t first = s_take[b];
+            if (first >= 0) {
+                const uint32_t kv = s_kv[b], p = kv + (uint32_t)(t - s_cu[b]), S = a.S;
+                const uint32_t page = p / S, row = p - page * S, held = (kv + S - 1) / S;
+                int32_t block;
+                int32_t *entry = a.table + b * a.table_stride + page;
+                if (page < held) {
+                    block = *entry;
+                } else {
+                    const int64_t at = size - 1 - (first + (int64_t)(page - held));
+                    block = at < n_free ? a.free_list[at] : freed_block(at - n_free);
+                    if (row == 0) *entry = block;   // the block's first token is among the new ones
+                }
+                pos = (int32_t)p;
+                if (block >= 0) slot = (int64_t)block * S + row;
+                else flags |= CSA2_FLAG_BAD_INDEX;
+            }
+        }
+        a.slots[t] = slot;
+        if (a.positions) a.positions[t] = pos;
+    }
+    for (int64_t k = (int64_t)rank * nt + tid; k < count - n_free; k += step) a.free_list[n_free + k] = freed_block(k);
+    if (flags) flag_error(a.err_flag, flags);
+
+    cluster.sync();   // every CTA has read kv_len, new_len and free_count
+    if (rank == 0) {
+        for (int b = tid; b < a.B; b += nt) {
+            const int64_t n = a.new_len[b];
+            const int32_t kv = s_kv[b];
+            a.kv_out[b] = n < 0 ? 0 : (s_take[b] >= 0 ? (int32_t)(kv + n) : kv);
+            a.cu[b] = s_cu[b];
+        }
+        if (tid == 0) {
+            a.cu[a.B] = (int32_t)end;
+            *a.free_out = (int32_t)count;
+        }
+    }
+}
+
+}  // namespace
+}  // namespace csa2
+
+using namespace csa2;
+
+extern "C" csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int S, int64_t T, int64_t free_cap,
+                                        const int32_t *kv_len, const int32_t *new_len, int32_t *block_table,
+                                        int32_t *free_list, const int32_t *free_count, int32_t *kv_len_out,
+                                        int32_t *free_count_out, int32_t *cu_len, int32_t *positions, int64_t *slots,
+                                        uint32_t *err_flag, csa2_stream_t stream) {
+    clear_error();
+    CSA2_REQUIRE(B >= 1 && B <= kMaxRequests, "build_slots: B=%d not in [1, %d]", B, kMaxRequests);
+    CSA2_REQUIRE(S >= 1 && M >= 1 && (int64_t)M * S < (1ll << 31), "build_slots: S=%d, M=%d: need M * S < 2^31", S, M);
+    CSA2_REQUIRE((int64_t)B * M < (1ll << 31), "build_slots: B * M = %lld entries", (long long)B * M);
+    CSA2_REQUIRE(table_stride >= M, "build_slots: table_stride=%lld < M=%d", (long long)table_stride, M);
+    CSA2_REQUIRE(T >= 0 && T <= (1ll << 30), "build_slots: T=%lld not in [0, 2^30]", (long long)T);
+    CSA2_REQUIRE(free_cap >= 0 && free_cap < (1ll << 31), "build_slots: free_cap=%lld", (long long)free_cap);
+    CSA2_REQUIRE(kv_len && new_len && block_table && free_count && kv_len_out && free_count_out && cu_len,
+                 "build_slots: null pointer");
+    CSA2_REQUIRE((free_list || free_cap == 0) && (slots || T == 0), "build_slots: null pointer");
+    CSA2_REQUIRE(aligned(slots, 8), "build_slots: slots must be 8-byte aligned");
+    const SlotArgs args = {B, M, S, table_stride, T, free_cap, kv_len, new_len, block_table, free_list, free_count,
+                           kv_len_out, free_count_out, cu_len, positions, slots, err_flag};
+    const size_t smem = (size_t)B * 4 * sizeof(int32_t);
+    static bool done[64];
+    if (smem > 40 * 1024)
+        CSA2_CUDA_CALL(ensure_smem_limit((const void *)build_slots_kernel, kMaxRequests * 16, done),
+                       "build_slots: shared memory limit");
+    const int64_t work = T > B ? T : B;
+    cudaLaunchConfig_t cfg = {};
+    const int ctas = work > 4096 ? 8 : 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(work <= 256 ? 256 : 1024);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream_of(stream);
+    cudaLaunchAttribute at[2] = {pdl_attribute(), {}};
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    CSA2_CUDA_CALL(cudaLaunchKernelEx(&cfg, build_slots_kernel, args), "build_slots_kernel launch");
+    CSA2_LAUNCH_CHECK("build_slots_kernel");
+    return CSA2_OK;
+}
