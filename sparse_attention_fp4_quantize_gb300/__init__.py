@@ -445,58 +445,92 @@ def noalloc_max_scratch_bytes() -> int:
 
 
 # ------------------------------------------------------------------ paged 8-bit cache
-_I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
-_F8 = (torch.uint8, torch.float8_e4m3fn)
+# A serving loop makes these calls a few times per layer and step, on kernels of
+# a few microseconds: one comparison per property and tensor, the reason for a
+# refusal is worked out afterwards.
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _ROWS = {torch.bfloat16: BF16, torch.int16: BF16, torch.float16: FP16}
 
 
-def _want(t, name, dtypes, shape, dense=True):
-    """t has one of these dtypes and this shape (None: any extent) and, unless said otherwise, no gaps."""
-    if t.dtype not in dtypes:
-        raise TypeError("%s: %s elements do not fit this call" % (name, t.dtype))
-    if len(t.shape) != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+def _refuse(t, name, dtype, shape, dev, dense):
+    if t.dtype is not dtype:
+        raise TypeError("%s: %s elements do not fit this call (%s)" % (name, t.dtype, dtype))
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if dense and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if t.get_device() != dev:
+        raise ValueError("tensors must be CUDA tensors of one device (%s is on %s)" % (name, t.device))
+    raise ValueError("%s must be contiguous" % name if dense else "%s: strides do not fit this call" % name)
 
 
-def _want_flag(err_flag):
-    if err_flag is not None:
-        _flag(err_flag)
+def _arg(t, name, dtype, shape, dev):
+    """Pointer of a tensor of this dtype and shape without gaps, on device dev."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev, True)
 
 
-def _table_stride(block_table):
-    """Row stride of a block table whose rows have no gaps between entries."""
-    M = block_table.shape[1]
-    if M > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table rows must be contiguous")
-    return block_table.stride(0) if block_table.shape[0] > 1 else M
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
-def _row_strides(x, name):
-    """(token, head) strides of rows [T, H, D] with contiguous channels."""
-    T, H, D = x.shape
+def _flag_arg(err_flag, dev):
+    if err_flag is None:
+        return None
+    _flag(err_flag)
+    if err_flag.get_device() != dev:
+        raise ValueError("tensors must be CUDA tensors of one device (err_flag is on %s)" % err_flag.device)
+    return err_flag.data_ptr()
+
+
+def _rows_arg(x, name, dtype, shape, dev):
+    """(pointer, token stride, head stride) of rows [T, H, D] with contiguous channels."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != dev:
+        _refuse(x, name, dtype, shape, dev, False)
     st, sh, sd = x.stride()
-    if sd != 1 and D > 1:
+    if sd != 1:
         raise ValueError("%s must have contiguous channels" % name)
-    st, sh = (st if T > 1 else H * D), (sh if H > 1 else D)     # strides of single rows say nothing
-    return st, sh
+    # the stride of an extent of one says nothing
+    return x.data_ptr(), st if shape[0] > 1 else shape[1] * shape[2], sh if shape[1] > 1 else shape[2]
 
 
-def _launch(ts, stream, name, *args):
-    """Call the C function on the tensors' device (all of them on one)."""
-    dev = ts[0].device
-    for t in ts:
-        if t is not None and (t.device != dev or not _on_device(t)):
-            raise ValueError("tensors must be CUDA tensors of one device")
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+def _table_arg(t, shape, dev):
+    """(pointer, row stride) of a block table whose rows have no gaps between entries."""
+    st, s1 = t.stride()
+    if t.dtype is not _I32 or t.get_device() != dev or (s1 != 1 and shape[1] > 1):
+        _refuse(t, "block_table", _I32, shape, dev, False)
+    return t.data_ptr(), st if shape[0] > 1 else shape[1]
+
+
+def _planes_args(k_codes, v_codes, k_scale, v_scale, dev):
+    shape = k_codes.shape
+    if len(shape) != 4:
+        raise ValueError("k_codes must be [n_blocks, Hkv, S, D], got %s" % (tuple(shape),))
+    kd, vd = k_codes.dtype, v_codes.dtype
+    if not (kd is torch.uint8 or kd is torch.float8_e4m3fn) or not (vd is torch.uint8 or vd is torch.float8_e4m3fn):
+        raise TypeError("k_codes and v_codes must be E4M3 (uint8 or float8_e4m3fn), got %s and %s" % (kd, vd))
+    return (_arg(k_codes, "k_codes", kd, shape, dev), _arg(v_codes, "v_codes", vd, shape, dev),
+            _arg(k_scale, "k_scale", _F32, shape[:2], dev), _arg(v_scale, "v_scale", _F32, shape[:2], dev))
+
+
+def _device_of(t):
+    dev = t.get_device()
+    if dev < 0 and not _on_device(t):
+        raise ValueError("tensors must be CUDA tensors")
+    return dev
+
+
+def _launch(fn, dev, stream, *args):
+    """Call the C function on device dev, on the given stream or that device's current one."""
+    if dev < 0:                                   # no such device: a stand-in for the library
+        return _check(fn(*args, _stream(stream)))
+    s = _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, s)
+    else:
         with torch.cuda.device(dev):
-            return _check(getattr(_lib, name)(*args, _stream(stream)))
-    _check(getattr(_lib, name)(*args, _stream(stream)))
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
+            rc = fn(*args, s)
+    if rc != 0:
+        _check(rc)
 
 
 def csa2_build_slots(kv_len, new_len, block_table, free_list, free_count, block_size, kv_len_out, free_count_out,
@@ -507,33 +541,17 @@ def csa2_build_slots(kv_len, new_len, block_table, free_list, free_count, block_
     free_count int32 [1] ids on it -> kv_len_out int32 [B], free_count_out
     int32 [1] (may be the inputs), cu_len int32 [B + 1], positions int32 [T] or
     None, slots int64 [T]."""
+    dev = _device_of(kv_len)
     B, M = block_table.shape
-    T = slots.shape[0]
-    _want(kv_len, "kv_len", _I32, (B,))
-    _want(new_len, "new_len", _I32, (B,))
-    _want(block_table, "block_table", _I32, (B, M), dense=False)
-    _want(free_list, "free_list", _I32, (None,))
-    _want(free_count, "free_count", _I32, (1,))
-    _want(kv_len_out, "kv_len_out", _I32, (B,))
-    _want(free_count_out, "free_count_out", _I32, (1,))
-    _want(cu_len, "cu_len", _I32, (B + 1,))
-    _want(slots, "slots", _I64, (T,))
-    if positions is not None:
-        _want(positions, "positions", _I32, (T,))
-    _want_flag(err_flag)
-    _launch((kv_len, new_len, block_table, free_list, free_count, kv_len_out, free_count_out, cu_len, slots, positions,
-             err_flag), stream, "csa2_build_slots", B, M, _table_stride(block_table), int(block_size), T,
-            free_list.shape[0], _p(kv_len), _p(new_len), _p(block_table), _p(free_list), _p(free_count),
-            _p(kv_len_out), _p(free_count_out), _p(cu_len), _p(positions), _p(slots), _p(err_flag))
-
-
-def _planes(k_codes, v_codes, k_scale, v_scale):
-    n, H, S, D = k_codes.shape
-    _want(k_codes, "k_codes", _F8, (n, H, S, D))
-    _want(v_codes, "v_codes", _F8, (n, H, S, D))
-    _want(k_scale, "k_scale", _F32, (n, H))
-    _want(v_scale, "v_scale", _F32, (n, H))
-    return n, H, S, D
+    (T,), (cap,) = slots.shape, free_list.shape
+    one = (B,)
+    table, stride = _table_arg(block_table, (B, M), dev)
+    _launch(_lib.csa2_build_slots, dev, stream, B, M, stride, block_size, T, cap,
+            _arg(kv_len, "kv_len", _I32, one, dev), _arg(new_len, "new_len", _I32, one, dev), table,
+            _arg(free_list, "free_list", _I32, (cap,), dev), _arg(free_count, "free_count", _I32, (1,), dev),
+            _arg(kv_len_out, "kv_len_out", _I32, one, dev), _arg(free_count_out, "free_count_out", _I32, (1,), dev),
+            _arg(cu_len, "cu_len", _I32, (B + 1,), dev), _opt(positions, "positions", _I32, (T,), dev),
+            _arg(slots, "slots", _I64, (T,), dev), _flag_arg(err_flag, dev))
 
 
 def csa2_quantize_kv_fp8_paged(k, v, slots, k_codes, v_codes, k_scale, v_scale, err_flag=None, stream=None):
@@ -541,17 +559,17 @@ def csa2_quantize_kv_fp8_paged(k, v, slots, k_codes, v_codes, k_scale, v_scale, 
     strides that are multiples of 8), slots int64 [T] -> k_codes, v_codes
     uint8 or float8_e4m3fn [n_blocks, Hkv, S, D], k_scale, v_scale fp32
     [n_blocks, Hkv], updated in place."""
-    n, H, S, D = _planes(k_codes, v_codes, k_scale, v_scale)
-    T = slots.shape[0]
-    if k.dtype not in _ROWS or v.dtype != k.dtype:
-        raise TypeError("k and v must both be bf16 (or int16 bits) or fp16, got %s and %s" % (k.dtype, v.dtype))
-    _want(k, "k", (k.dtype,), (T, H, D), dense=False)
-    _want(v, "v", (k.dtype,), (T, H, D), dense=False)
-    _want(slots, "slots", _I64, (T,))
-    _want_flag(err_flag)
-    _launch((k, v, slots, k_codes, v_codes, k_scale, v_scale, err_flag), stream, "csa2_quantize_kv_fp8_paged",
-            _p(k), _p(v), _ROWS[k.dtype], T, H, D, *_row_strides(k, "k"), *_row_strides(v, "v"), _p(slots), n, S,
-            _p(k_codes), _p(v_codes), _p(k_scale), _p(v_scale), _p(err_flag))
+    dev = _device_of(k)
+    kc, vc, ks, vs = _planes_args(k_codes, v_codes, k_scale, v_scale, dev)
+    n, H, S, D = k_codes.shape
+    (T,) = slots.shape
+    dt = _ROWS.get(k.dtype)
+    if dt is None:
+        raise TypeError("k and v must be bf16 (or int16 bits) or fp16, got %s" % k.dtype)
+    kp, kt, kh = _rows_arg(k, "k", k.dtype, (T, H, D), dev)
+    vp, vt, vh = _rows_arg(v, "v", k.dtype, (T, H, D), dev)
+    _launch(_lib.csa2_quantize_kv_fp8_paged, dev, stream, kp, vp, dt, T, H, D, kt, kh, vt, vh,
+            _arg(slots, "slots", _I64, (T,), dev), n, S, kc, vc, ks, vs, _flag_arg(err_flag, dev))
 
 
 def csa2_paged_attn_workspace_bytes(B, T, Hq, Hkv, D, max_new) -> int:
@@ -573,27 +591,24 @@ def csa2_paged_attn_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, kv_l
     type, lse fp32 [T, Hq].  max_new: upper bound of a request's rows (a
     hint).  workspace: a CUDA byte tensor of at least
     csa2_paged_attn_workspace_bytes bytes (allocated here when None)."""
-    n, H, S, D = _planes(k_codes, v_codes, k_scale, v_scale)
-    T, Hq = q.shape[0], q.shape[1]
+    dev = _device_of(q)
+    kc, vc, ks, vs = _planes_args(k_codes, v_codes, k_scale, v_scale, dev)
+    n, H, S, D = k_codes.shape
+    T, Hq = q.shape[:2]
     B, M = block_table.shape
-    if q.dtype not in _ROWS or out.dtype != q.dtype:
-        raise TypeError("q and out must both be bf16 (or int16 bits) or fp16, got %s and %s" % (q.dtype, out.dtype))
-    _want(q, "q", (q.dtype,), (T, Hq, D), dense=False)
-    _want(out, "out", (q.dtype,), (T, Hq, D))
-    _want(block_table, "block_table", _I32, (B, M), dense=False)
-    _want(kv_len, "kv_len", _I32, (B,))
-    _want(cu_len, "cu_len", _I32, (B + 1,))
-    if lse is not None:
-        _want(lse, "lse", _F32, (T, Hq))
-    _want_flag(err_flag)
+    dt = _ROWS.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be bf16 (or int16 bits) or fp16, got %s" % q.dtype)
     if H < 1 or Hq % H:
         raise ValueError("%d query heads do not divide over %d KV heads" % (Hq, H))
+    shape = (T, Hq, D)
+    qp, qt, qh = _rows_arg(q, "q", q.dtype, shape, dev)
+    table, stride = _table_arg(block_table, (B, M), dev)
     if workspace is None:
-        workspace = workspace_for_paged_attn(B, T, Hq, H, D, int(max_new), device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+        workspace = workspace_for_paged_attn(B, T, Hq, H, D, max_new, device=q.device)
     ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch((q, k_codes, v_codes, k_scale, v_scale, block_table, kv_len, cu_len, out, lse, err_flag, workspace), stream,
-            "csa2_paged_attn_fp8", B, T, Hq, H, D, _ROWS[q.dtype], _p(q), *_row_strides(q, "q"), _p(k_codes),
-            _p(v_codes), _p(k_scale), _p(v_scale), n, S, _p(block_table), M, _table_stride(block_table), _p(kv_len),
-            _p(cu_len), int(max_new), int(window), float(sm_scale), _p(out), _p(lse), _p(err_flag), _p(workspace), ws)
+    _launch(_lib.csa2_paged_attn_fp8, dev, stream, B, T, Hq, H, D, dt, qp, qt, qh, kc, vc, ks, vs, n, S, table, M,
+            stride, _arg(kv_len, "kv_len", _I32, (B,), dev), _arg(cu_len, "cu_len", _I32, (B + 1,), dev), max_new,
+            window, sm_scale, _arg(out, "out", q.dtype, shape, dev), _opt(lse, "lse", _F32, (T, Hq), dev),
+            _flag_arg(err_flag, dev),
+            None if workspace is None else _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev), ws)

@@ -20,6 +20,8 @@ namespace csa2 {
 namespace {
 
 constexpr int kAttnWarps = 4;
+constexpr int kTileKeys = 32;       // keys per warp tile
+constexpr int kStages = 2;          // tiles in flight per warp
 
 struct PagedAttnArgs {
     int B, Hq, Hkv, G, S, M, window;
@@ -32,6 +34,7 @@ struct PagedAttnArgs {
     uint16_t *out;
     float *lse;
     uint32_t *err_flag;
+    float *partial;                 // [2 * CTAs][16 MT rows][D + 4]: o, m, mv, l
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -71,148 +74,378 @@ __device__ __forceinline__ Request request_of(const PagedAttnArgs &a, int b) {
     return r;
 }
 
-// A warp's share of the softmax over keys for 16 rows: lane (g, t) = (lane / 4,
-// lane % 4) holds rows g and g + 8.  Fragment layouts are chosen so that every
-// load of codes is contiguous: in q . k, lane t's part of the contraction is
-// channels [t D/4, (t+1) D/4); in P v, lane g's output columns of the B operand
-// are channels [g D/8, (g+1) D/8), so the accumulators of lane t are channels
-// [t D/4, (t+1) D/4) of its two rows.
+// Work of the split kernel.  A unit is (request, KV head, tile of R = 16 MT
+// rows); it has tiles_of(request) tiles of 32 keys, the same for all row tiles
+// of a request, at least one so that every row gets its output.  The units'
+// tiles, in the order of requests, heads and row tiles, are one long line that
+// the CTAs cut into equal shares: a ragged batch loads every SM alike, and a
+// long context is split over as many CTAs as it is worth.
+struct Plan {
+    int64_t share;                  // tiles per CTA, a multiple of the warps
+    int b;                          // request that holds the CTA's first tile
+    int64_t base;                   // its first tile in the line
+    int64_t total;
+};
+__device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r) {
+    const int64_t p = (int64_t)r.kv - r.n - a.window + 1;      // lowest key of the first row's window
+    return a.window > 0 && p > 0 ? (int)p & ~(kTileKeys - 1) : 0;
+}
+__device__ __forceinline__ int tiles_of(const PagedAttnArgs &a, const Request &r) {
+    const int keys = r.kv - first_key(a, r);
+    return keys > 0 ? (keys + kTileKeys - 1) / kTileKeys : 1;
+}
+template <int R>
+__device__ __forceinline__ int units_of(const PagedAttnArgs &a, const Request &r) {
+    return (r.n * a.G + R - 1) / R * a.Hkv;
+}
+
+// Every thread of the block takes a run of requests; a prefix sum over the
+// threads finds the total and the thread that holds the CTA's first tile.
+template <int R>
+__device__ __forceinline__ Plan plan_of(const PagedAttnArgs &a, int cta, int ctas, int64_t *s_sum, int64_t *s_found) {
+    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + nt - 1) / nt, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request_of(a, b);
+        mine += (int64_t)units_of<R>(a, r) * tiles_of(a, r);
+    }
+    int64_t s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += y;
+    }
+    if (lane == 31) s_sum[warp] = s;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    Plan p;
+    p.total = total;
+    const int64_t even = (total + ctas - 1) / ctas;
+    p.share = (even + kAttnWarps - 1) / kAttnWarps * kAttnWarps;
+    const int64_t t0 = cta * p.share;
+    int64_t at = before + s - mine;
+    if (t0 >= at && t0 < at + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const Request r = request_of(a, b);
+            const int64_t w = (int64_t)units_of<R>(a, r) * tiles_of(a, r);
+            if (t0 < at + w) {
+                s_found[0] = b;
+                s_found[1] = at;
+                break;
+            }
+            at += w;
+        }
+    }
+    __syncthreads();
+    p.b = (int)s_found[0];          // meaningless if t0 >= total
+    p.base = s_found[1];
+    return p;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of D-byte rows, swizzled so
+// that the fragment loads below meet every bank once.
 template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+struct StageMeta {
+    float ks[2], vs[2];             // scales of the two 16-key halves
+    int stored[2];                  // keys of each half that are there
+};
+
+// A warp's share of the softmax over keys for 16 MT rows: lane (g, t) =
+// (lane / 4, lane % 4) holds rows g and g + 8 of each 16.  Fragment layouts are
+// chosen so that every load of codes is contiguous: in q . k, lane t's part of
+// the contraction is channels [t D/4, (t+1) D/4); in P v, lane g's output
+// columns of the B operand are channels [g D/8, (g+1) D/8), so the accumulators
+// of lane t are channels [t D/4, (t+1) D/4) of its rows.
+template <int D, int MT>
 struct Tile {
     static constexpr int KS = D / 16;                // k-steps of q . k
     static constexpr int NT = D / 8;                 // n-tiles of P v
-    uint32_t q[KS][4];
-    float o[NT][4];
-    float m[2], mv[2], l[2];                         // running maxima (log2), sum of P of this lane's keys
+    uint32_t q[MT][KS][4];
+    float o[MT][NT][4];
+    float m[2 * MT], mv[2 * MT], l[2 * MT];          // running maxima (log2), sum of P of this lane's keys
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        m[0] = m[1] = mv[0] = mv[1] = __int_as_float(0xff800000);
-        l[0] = l[1] = 0.0f;
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r) {
+            m[r] = mv[r] = __int_as_float(0xff800000);
+            l[r] = 0.0f;
+        }
     }
 
-    // 16 keys of one block: kc, vc point at their first code rows.  zf: logit
-    // factor per row (with the block's k_scale); vis0..1: keys [lo, hi) of the
-    // 16 that rows g, g + 8 see; stored: how many of the 16 are stored rows.
-    __device__ __forceinline__ void keys16(const uint8_t *kc, const uint8_t *vc, const float (&zf)[2], float vs,
-                                           const int (&lo)[2], const int (&hi)[2], int stored) {
+    // 32 keys from shared memory (codes at kb, vb).  zf: logit factor per row; a
+    // row sees keys [lo, hi) of the 32, as far as they are stored.
+    __device__ __forceinline__ void keys32(uint32_t kb, uint32_t vb, const StageMeta &meta, const float (&zf)[2 * MT],
+                                           const int (&lo)[2 * MT], const int (&hi)[2 * MT]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        constexpr int KW = D / 16;                   // words of a key row per lane
-        uint32_t kw[2][KW];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < KW / 4; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(kc + (8 * i + g) * D + t * (D / 4) + 16 * c);
-                kw[i][4 * c] = v.x, kw[i][4 * c + 1] = v.y, kw[i][4 * c + 2] = v.z, kw[i][4 * c + 3] = v.w;
-            }
-        constexpr int VW = D / 32;                   // words of a value row per lane
-        uint32_t vw[4][VW];
+        constexpr uint32_t ALL = 0xFFFFFFFFu;
+        const float NEG_INF = __int_as_float(0xff800000);
+        float s[MT][4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int key = 2 * t + (i & 1) + 8 * (i >> 1);
-            const uint8_t *p = vc + key * D + g * (D / 8);
-            if constexpr (VW == 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(p);
-                vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
-            } else {
-                const uint2 v = *reinterpret_cast<const uint2 *>(p);
-                vw[i][0] = v.x, vw[i][1] = v.y;
-            }
-            if (key >= stored) {                     // not a stored row: whatever is there must not meet a zero weight
+            uint32_t kw[D / 16];
 #pragma unroll
-                for (int w = 0; w < VW; ++w) vw[i][w] = 0u;
+            for (int c = 0; c < D / 64; ++c) {
+                const uint4 v = lds128(kb + chunk_at<D>(8 * i + g, t * (D / 64) + c));
+                kw[4 * c] = v.x, kw[4 * c + 1] = v.y, kw[4 * c + 2] = v.z, kw[4 * c + 3] = v.w;
             }
-        }
-        float s[2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+            for (int x = 0; x < MT; ++x) s[x][i][0] = s[x][i][1] = s[x][i][2] = s[x][i][3] = 0.0f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 uint32_t b0, b1;
-                e4m3x4_to_f16x2x2(kw[i][k], b0, b1);
-                mma_f16_16816(s[i], q[k][0], q[k][1], q[k][2], q[k][3], b0, b1);
+                e4m3x4_to_f16x2x2(kw[k], b0, b1);
+#pragma unroll
+                for (int x = 0; x < MT; ++x)
+                    mma_f16_16816(s[x][i], q[x][k][0], q[x][k][1], q[x][k][2], q[x][k][3], b0, b1);
             }
         }
-        const float NEG_INF = __int_as_float(0xff800000);
-        const float ve = (float)((int)((__float_as_uint(vs) >> 23) & 0xFFu) - 127);
-        uint32_t p[2][2];
+        const float ve[2] = {(float)((int)((__float_as_uint(meta.vs[0]) >> 23) & 0xFFu) - 127),
+                             (float)((int)((__float_as_uint(meta.vs[1]) >> 23) & 0xFFu) - 127)};
+        uint32_t p[MT][4][2];
+        float grow[2 * MT];
+        bool grew = false;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float z[4], top = NEG_INF;
+        for (int r = 0; r < 2 * MT; ++r) {
+            float z[8], top[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int u = 0; u < 2; ++u) {
+                const float f = zf[r] * meta.ks[u];
+                const int end = min(hi[r], 16 * u + meta.stored[u]);
+                top[u] = NEG_INF;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int key = 8 * i + 2 * t + c;
-                    const float v = s[i][2 * r + c] * zf[r];
-                    z[2 * i + c] = key >= lo[r] && key < hi[r] ? v : NEG_INF;
-                    top = fmaxf(top, z[2 * i + c]);
-                }
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const float m1 = fmaxf(m[r], top), mv1 = fmaxf(mv[r], top + ve);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int key = 16 * u + 8 * i + 2 * t + c;
+                        const float v = s[r / 2][2 * u + i][2 * (r & 1) + c] * f;
+                        z[4 * u + 2 * i + c] = key >= lo[r] && key < end ? v : NEG_INF;
+                        top[u] = fmaxf(top[u], z[4 * u + 2 * i + c]);
+                    }
+                top[u] = fmaxf(top[u], __shfl_xor_sync(ALL, top[u], 1));
+                top[u] = fmaxf(top[u], __shfl_xor_sync(ALL, top[u], 2));
+            }
+            const float m1 = fmaxf(m[r], fmaxf(top[0], top[1]));
+            const float mv1 = fmaxf(mv[r], fmaxf(top[0] + ve[0], top[1] + ve[1]));
             const float ref = m1 == NEG_INF ? 0.0f : m1, refv = mv1 == NEG_INF ? 0.0f : mv1;
             l[r] *= ex2(m[r] - ref);
-            const float grow = ex2(mv[r] - refv);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                o[j][2 * r] *= grow;
-                o[j][2 * r + 1] *= grow;
-            }
+            grow[r] = ex2(mv[r] - refv);
+            grew |= mv1 != mv[r];
             m[r] = m1, mv[r] = mv1;
-            const float f = fminf(vs * ex2(ref - refv), 1e38f);
-            float w[4];
+            const float g2 = ex2(ref - refv);
+            float w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = ex2(z[i] - ref);
-                l[r] += e;
-                w[i] = z[i] == NEG_INF ? 0.0f : e * f;
+            for (int u = 0; u < 2; ++u) {
+                const float f = fminf(meta.vs[u] * g2, 1e38f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = ex2(z[4 * u + i] - ref);
+                    l[r] += e;
+                    w[4 * u + i] = z[4 * u + i] == NEG_INF ? 0.0f : e * f;
+                }
             }
-            p[0][r] = pack_f16(w[0], w[1]);
-            p[1][r] = pack_f16(w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[r / 2][i][r & 1] = pack_f16(w[2 * i], w[2 * i + 1]);
+        }
+        if (__any_sync(ALL, grew)) {
+#pragma unroll
+            for (int x = 0; x < MT; ++x)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[x][j][0] *= grow[2 * x], o[x][j][1] *= grow[2 * x];
+                    o[x][j][2] *= grow[2 * x + 1], o[x][j][3] *= grow[2 * x + 1];
+                }
         }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-            // bytes of keys (2t, 2t+1) and (2t+8, 2t+9) interleaved: pairs along the keys
-            const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-            const uint32_t c0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), c1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-            uint32_t b0[4], b1[4];
-            e4m3x4_to_f16x2x2(a0, b0[0], b0[1]);
-            e4m3x4_to_f16x2x2(a1, b0[2], b0[3]);
-            e4m3x4_to_f16x2x2(c0, b1[0], b1[1]);
-            e4m3x4_to_f16x2x2(c1, b1[2], b1[3]);
+        for (int u = 0; u < 2; ++u) {
+            constexpr int VW = D / 32;               // words of a value row per lane
+            uint32_t vw[4][VW];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) mma_f16_16816(o[4 * w + x], p[0][0], p[0][1], p[1][0], p[1][1], b0[x], b1[x]);
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (D == 128) {
+                    const uint4 v = lds128(vb + chunk_at<D>(16 * u + 2 * t + (i & 1) + 8 * (i >> 1), g));
+                    vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
+                } else {
+                    // odd t reads its second key first: even and odd rows share a 128-byte line
+                    const int key = 16 * u + 2 * t + ((i ^ t) & 1) + 8 * (i >> 1);
+                    const uint2 v = lds64(vb + chunk_at<D>(key, g >> 1) + 8 * (g & 1));
+                    vw[i][0] = v.x, vw[i][1] = v.y;
+                }
+            }
+            if constexpr (D == 64) {
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        const uint32_t x = vw[i][w], y = vw[i + 1][w];
+                        vw[i][w] = t & 1 ? y : x;
+                        vw[i + 1][w] = t & 1 ? x : y;
+                    }
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                // bytes of keys (2t, 2t+1) and (2t+8, 2t+9) interleaved: pairs along the keys
+                const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+                const uint32_t c0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), c1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+                uint32_t b0[4], b1[4];
+                e4m3x4_to_f16x2x2(a0, b0[0], b0[1]);
+                e4m3x4_to_f16x2x2(a1, b0[2], b0[3]);
+                e4m3x4_to_f16x2x2(c0, b1[0], b1[1]);
+                e4m3x4_to_f16x2x2(c1, b1[2], b1[3]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int x = 0; x < MT; ++x)
+                        mma_f16_16816(o[x][4 * w + c], p[x][2 * u][0], p[x][2 * u][1], p[x][2 * u + 1][0],
+                                      p[x][2 * u + 1][1], b0[c], b1[c]);
+            }
         }
     }
 };
 
+template <int D, int MT>
+constexpr int attn_smem() {
+    constexpr int ring = kAttnWarps * kStages * 2 * kTileKeys * D, merge = kAttnWarps * 16 * (D + 4) * 4;
+    return ring > merge ? ring : merge;
+}
+
+// 8 threads per row, D / 8 channels each: o = x * inv in the output's type, lse.
 template <int D, bool HALF>
-__global__ void __launch_bounds__(kAttnWarps * 32) paged_attn_kernel(PagedAttnArgs a) {
-    __shared__ float s_o[kAttnWarps][16][D + 4];
+__device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row, int part, const float *x, float M, float l) {
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    uint32_t w[D / 16];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) w[c] = pack_out<HALF>(x[2 * c] * inv, x[2 * c + 1] * inv);
+    uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + part * (D / 8));
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    if (a.lse && part == 0) a.lse[o_row] = l > 0.0f || l != l ? (M + log2f(l)) * 0.69314718055994531f : __int_as_float(0xff800000);
+}
+
+template <int D, int MT, bool HALF>
+__global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_split_kernel(PagedAttnArgs a) {
+    constexpr int R = 16 * MT;
+    constexpr uint32_t ALL = 0xFFFFFFFFu;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_st[kAttnWarps][16][3];
+    __shared__ StageMeta s_meta[kAttnWarps][kStages];
+    __shared__ int64_t s_sum[kAttnWarps], s_found[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int h = blockIdx.y;
     const float NEG_INF = __int_as_float(0xff800000);
     pdl_wait();
     pdl_launch_dependents();
-    for (int b = blockIdx.z; b < a.B; b += gridDim.z) {
+    const Plan plan = plan_of<R>(a, blockIdx.x, gridDim.x, s_sum, s_found);
+    int64_t at = blockIdx.x * plan.share;
+    const int64_t stop = min(plan.total, at + plan.share);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * 2 * kTileKeys * D);
+    int64_t base = plan.base;
+    for (int b = plan.b; at < stop && b < a.B; ++b) {
         const Request rq = request_of(a, b);
-        const int rows = rq.n * a.G;
-        for (int r0 = blockIdx.x * 16; r0 < rows; r0 += gridDim.x * 16) {
-            Tile<D> tile;
+        const int tiles = tiles_of(a, rq), row_tiles = (rq.n * a.G + R - 1) / R, key0 = first_key(a, rq);
+        const int64_t end = base + (int64_t)row_tiles * a.Hkv * tiles;
+        while (at < stop && at < end) {
+            // segment: tiles [ta, tb) of one unit
+            const int unit = (int)((at - base) / tiles), ta = (int)((at - base) - (int64_t)unit * tiles);
+            const int tb = (int)min((int64_t)tiles, ta + (stop - at));
+            const int h = unit / row_tiles, r0 = (unit - h * row_tiles) * R, rows = rq.n * a.G;
+            at += tb - ta;
+
+            Tile<D, MT> tile;
             tile.clear();
-            int pos[2], first[2];
-            float zf[2];
+            int pos[2 * MT], first[2 * MT];
+            float zf[2 * MT];
+            // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / 2, half lane % 2) of 16 of them
+            const int count = tb - ta > warp ? (tb - ta - warp + kAttnWarps - 1) / kAttnWarps : 0;
+            const int32_t *table = a.table + b * a.table_stride;
+            auto entry = [&](int i) -> int32_t {     // block of this lane's half of the 16 tiles from i on
+                const int key = key0 + (ta + warp + (i + (lane >> 1)) * kAttnWarps) * kTileKeys + 16 * (lane & 1);
+                return i + (lane >> 1) < count && key < rq.kv ? table[key / a.S] : -1;
+            };
+            int32_t block = entry(0), block_next = entry(16);
+            float ks = 0.0f, vs = 0.0f;
+            auto scales = [&]() {
+                const bool ok = block >= 0 && block < a.n_blocks;
+                ks = ok ? a.k_scale[(int64_t)block * a.Hkv + h] : 0.0f;
+                vs = ok ? a.v_scale[(int64_t)block * a.Hkv + h] : 0.0f;
+            };
+            scales();
+            auto issue = [&](int i) {                // start the copy of this warp's tile i
+                if (i < count) {
+                    if (i && (i & 15) == 0) {
+                        block = block_next;
+                        block_next = entry(i + 16);
+                        scales();
+                    }
+                    const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
+                    const uint32_t dst = ring + (i % kStages) * (2 * kTileKeys * D);
+                    constexpr int CPR = D / 16, RPI = 32 / CPR;      // chunks per row, rows per instruction
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = r0 + g + 8 * r;
+                    for (int u = 0; u < 2; ++u) {
+                        const int who = 2 * (i & 15) + u;
+                        const int32_t bl = __shfl_sync(ALL, block, who);
+                        int stored = min(16, rq.kv - key - 16 * u);
+                        if (bl < 0 || bl >= a.n_blocks) {
+                            if (stored > 0 && lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+                            stored = 0;
+                        }
+                        stored = max(stored, 0);
+                        if (lane == who) {
+                            StageMeta &m = s_meta[warp][i % kStages];
+                            m.ks[u] = ks, m.vs[u] = vs, m.stored[u] = stored;
+                        }
+                        const int64_t off = stored ? (((int64_t)bl * a.Hkv + h) * a.S + (key + 16 * u) % a.S) * D : 0;
+                        const int c = lane % CPR;
+#pragma unroll
+                        for (int x = 0; x < 16 / RPI; ++x) {
+                            const int r = x * RPI + lane / CPR;
+                            const uint32_t n = r < stored ? 16 : 0;          // rows that are not there read as zero
+                            const int64_t src = off + (n ? r * D + c * 16 : 0);
+                            const uint32_t to = dst + chunk_at<D>(16 * u + r, c);
+                            cp_async16(to, a.k_codes + src, n);
+                            cp_async16(to + kTileKeys * D, a.v_codes + src, n);
+                        }
+                    }
+                }
+                cp_async_commit();
+            };
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+#pragma unroll
+            for (int r = 0; r < 2 * MT; ++r) {
+                const int row = r0 + 16 * (r / 2) + g + 8 * (r & 1);
                 const bool real = row < rows;
                 const int tok = real ? row / a.G : 0, hq = h * a.G + (real ? row - tok * a.G : 0);
-                pos[r] = real ? rq.kv - rq.n + tok : -1;
+                pos[r] = real ? max(-1, rq.kv - rq.n + tok) : -1;
                 first[r] = a.window > 0 ? max(0, pos[r] - a.window + 1) : 0;
                 const uint16_t *src = a.q + (rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride + t * (D / 4);
                 uint32_t w[D / 8];
@@ -228,88 +461,199 @@ __global__ void __launch_bounds__(kAttnWarps * 32) paged_attn_kernel(PagedAttnAr
                     const float2 f = unpack_in<HALF>(w[c]);
                     top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                // largest magnitude to [2^14, 2^15); a row below 2^-100 keeps its factor's limit
+                top = fmaxf(top, __shfl_xor_sync(ALL, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(ALL, top, 2));
+                // largest magnitude to [2^14, 2^15); a row below 2^-100 keeps that factor
                 const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
                 const float mul = HALF ? 1.0f : __uint_as_float((uint32_t)(127 + 14 - e) << 23);
                 zf[r] = a.logit_scale / mul;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const float2 f0 = unpack_in<HALF>(w[2 * k]), f1 = unpack_in<HALF>(w[2 * k + 1]);
-                    tile.q[k][r] = pack_f16(f0.x * mul, f0.y * mul);
-                    tile.q[k][2 + r] = pack_f16(f1.x * mul, f1.y * mul);
+                    tile.q[r / 2][k][r & 1] = pack_f16(f0.x * mul, f0.y * mul);
+                    tile.q[r / 2][k][2 + (r & 1)] = pack_f16(f1.x * mul, f1.y * mul);
                 }
             }
-            // keys that some row of the tile sees
-            const int last_tok = (min(r0 + 16, rows) - 1) / a.G, first_tok = r0 / a.G;
-            const int end = min(rq.kv, rq.kv - rq.n + last_tok + 1);
-            int begin = 0;
-            if (a.window > 0) begin = max(0, rq.kv - rq.n + first_tok - a.window + 1) & ~15;
-            for (int j = begin + 16 * warp; j < end; j += 16 * kAttnWarps) {
-                const int32_t block = a.table[b * a.table_stride + j / a.S];
-                if (block < 0 || block >= a.n_blocks) {
-                    if (lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
-                    continue;
-                }
-                const int64_t bh = (int64_t)block * a.Hkv + h;
-                const float ks = a.k_scale[bh], vs = a.v_scale[bh];
-                const int64_t at = (bh * a.S + j % a.S) * D;
-                const float z[2] = {zf[0] * ks, zf[1] * ks};
-                const int lo[2] = {first[0] - j, first[1] - j}, hi[2] = {pos[0] + 1 - j, pos[1] + 1 - j};
-                tile.keys16(a.k_codes + at, a.v_codes + at, z, vs, lo, hi, rq.kv - j);
+            for (int i = 0; i < count; ++i) {
+                issue(i + kStages - 1);
+                cp_async_wait<kStages - 1>();
+                __syncwarp();
+                const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
+                int lo[2 * MT], hi[2 * MT];
+#pragma unroll
+                for (int r = 0; r < 2 * MT; ++r) lo[r] = first[r] - key, hi[r] = pos[r] + 1 - key;
+                const uint32_t kb = ring + (i % kStages) * (2 * kTileKeys * D);
+                tile.keys32(kb, kb + kTileKeys * D, s_meta[warp][i % kStages], zf, lo, hi);
+                __syncwarp();
             }
-            // the warps' shares meet in shared memory
-            __syncthreads();
+            cp_async_wait<0>();
+
+            // the warps' shares meet in shared memory, 16 rows at a time
+            const bool whole = ta == 0 && tb == tiles;
+            float *s_o = reinterpret_cast<float *>(smem);
+            constexpr int LD = D + 4;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float l = tile.l[r];
-                l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-                l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-                if (t == 0) {
-                    s_st[warp][g + 8 * r][0] = tile.m[r];
-                    s_st[warp][g + 8 * r][1] = tile.mv[r];
-                    s_st[warp][g + 8 * r][2] = l;
-                }
+            for (int x = 0; x < MT; ++x) {
+                __syncthreads();
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    s_o[warp][g + 8 * r][t * (D / 4) + j] = tile.o[j][2 * r];
-                    s_o[warp][g + 8 * r][t * (D / 4) + D / 8 + j] = tile.o[j][2 * r + 1];
-                }
-            }
-            __syncthreads();
-            const int row = r0 + tid / 8, part = tid % 8;   // 8 threads per row, D / 8 channels each
-            if (row < rows) {
-                float M = NEG_INF, l = 0.0f, f[kAttnWarps];
-                for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, s_st[w][tid / 8][0]);
-                const float ref = M == NEG_INF ? 0.0f : M;
-                for (int w = 0; w < kAttnWarps; ++w) {
-                    l += s_st[w][tid / 8][2] * ex2(s_st[w][tid / 8][0] - ref);
-                    f[w] = s_st[w][tid / 8][1] == NEG_INF ? 0.0f : exp2f(s_st[w][tid / 8][1] - ref);
-                }
-                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-                const int tok = row / a.G, hq = h * a.G + row - tok * a.G;
-                const int64_t o_row = (rq.row0 + tok) * a.Hq + hq;
-                uint32_t w32[D / 16];
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    float x[2] = {0.0f, 0.0f};
-                    for (int w = 0; w < kAttnWarps; ++w) {
-                        x[0] += f[w] * s_o[w][tid / 8][part * (D / 8) + 2 * c];
-                        x[1] += f[w] * s_o[w][tid / 8][part * (D / 8) + 2 * c + 1];
+                for (int y = 0; y < 2; ++y) {
+                    const int r = 2 * x + y;
+                    float l = tile.l[r];
+                    l += __shfl_xor_sync(ALL, l, 1);
+                    l += __shfl_xor_sync(ALL, l, 2);
+                    if (t == 0) {
+                        s_st[warp][g + 8 * y][0] = tile.m[r];
+                        s_st[warp][g + 8 * y][1] = tile.mv[r];
+                        s_st[warp][g + 8 * y][2] = l;
                     }
-                    w32[c] = pack_out<HALF>(x[0] * inv, x[1] * inv);
-                }
-                uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + o_row * D + part * (D / 8));
+                    float *dst = s_o + (warp * 16 + g + 8 * y) * LD + t * (D / 4);
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    reinterpret_cast<uint4 *>(dst)[c] = make_uint4(w32[4 * c], w32[4 * c + 1], w32[4 * c + 2], w32[4 * c + 3]);
-                if (a.lse && part == 0)
-                    a.lse[o_row] = l > 0.0f || l != l ? (M + log2f(l)) * 0.69314718055994531f : NEG_INF;
+                    for (int j = 0; j < D / 8; j += 4) {
+                        *reinterpret_cast<float4 *>(dst + j) = make_float4(tile.o[x][j][2 * y], tile.o[x][j + 1][2 * y],
+                                                                           tile.o[x][j + 2][2 * y], tile.o[x][j + 3][2 * y]);
+                        *reinterpret_cast<float4 *>(dst + D / 8 + j) =
+                            make_float4(tile.o[x][j][2 * y + 1], tile.o[x][j + 1][2 * y + 1], tile.o[x][j + 2][2 * y + 1],
+                                        tile.o[x][j + 3][2 * y + 1]);
+                    }
+                }
+                __syncthreads();
+                const int y = tid / 8, part = tid % 8, row = r0 + 16 * x + y;
+                if (row < rows) {
+                    float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[D / 8];
+#pragma unroll
+                    for (int w = 0; w < kAttnWarps; ++w) {
+                        M = fmaxf(M, s_st[w][y][0]);
+                        MV = fmaxf(MV, s_st[w][y][1]);
+                    }
+                    const float ref = M == NEG_INF ? 0.0f : M, refv = MV == NEG_INF ? 0.0f : MV;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) o[c] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kAttnWarps; ++w) {
+                        l += s_st[w][y][2] * ex2(s_st[w][y][0] - ref);
+                        const float f = ex2(s_st[w][y][1] - refv);
+                        const float *src = s_o + (w * 16 + y) * LD + part * (D / 8);
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) o[c] += f * src[c];
+                    }
+                    if (whole) {
+                        const float f = exp2f(refv - ref);
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) o[c] *= f;
+                        const int tok = row / a.G;
+                        store_row<D, HALF>(a, (rq.row0 + tok) * a.Hq + h * a.G + row - tok * a.G, part, o, M, l);
+                    } else {
+                        float *dst = a.partial + ((2 * (int64_t)blockIdx.x + (ta == 0)) * R + 16 * x + y) * LD;
+#pragma unroll
+                        for (int c = 0; c < D / 8; c += 4)
+                            *reinterpret_cast<float4 *>(dst + part * (D / 8) + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                        if (part == 0) *reinterpret_cast<float4 *>(dst + D) = make_float4(M, MV, l, 0.0f);
+                    }
+                }
             }
+            __syncthreads();
         }
+        base = end;
     }
 }
+
+// Joins the partial results of units that several CTAs share.  Block (c, y)
+// takes rows 4 y .. 4 y + 3 (of each 16) of the unit that CTA c began and did not
+// finish; CTA c's part is slot 2 c + 1, those of the CTAs after it slots 2 c'.
+template <int D, int MT, bool HALF>
+__global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a) {
+    constexpr int R = 16 * MT, LD = D + 4;
+    __shared__ int64_t s_sum[4], s_found[2];
+    __shared__ float s_o[4][4 * MT][LD];
+    const int ctas = gridDim.x, c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const float NEG_INF = __int_as_float(0xff800000);
+    pdl_wait();
+    pdl_launch_dependents();
+    const Plan plan = plan_of<R>(a, c, ctas, s_sum, s_found);
+    const int64_t t0 = c * plan.share, last = min(plan.total, t0 + plan.share) - 1;
+    if (t0 >= plan.total) return;
+    int64_t base = plan.base;
+    for (int b = plan.b; b < a.B; ++b) {                     // the request of the CTA's last tile
+        const Request rq = request_of(a, b);
+        const int tiles = tiles_of(a, rq), row_tiles = (rq.n * a.G + R - 1) / R;
+        const int64_t end = base + (int64_t)row_tiles * a.Hkv * tiles;
+        if (last >= end) {
+            base = end;
+            continue;
+        }
+        const int unit = (int)((last - base) / tiles);
+        const int64_t u0 = base + (int64_t)unit * tiles, u1 = u0 + tiles;
+        if (u0 < t0 || u1 <= last + 1) return;       // begun by an earlier CTA, or finished by this one
+        const int64_t c1 = (u1 - 1) / plan.share;    // the CTA with the unit's last tile
+        const int h = unit / row_tiles, r0 = (unit - h * row_tiles) * R, rows = rq.n * a.G;
+        // each warp joins every fourth part of its rows, then the warps' results meet
+        constexpr int TPR = 32 / (4 * MT), CH = D / TPR;     // threads per row in a warp, channels per thread
+        const int rr = lane / TPR, x0 = (lane % TPR) * CH;
+        const int row = r0 + 16 * (rr / 4) + 4 * blockIdx.y + rr % 4, in_unit = row - r0;
+        float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) o[i] = 0.0f;
+        if (row < rows) {
+            for (int64_t x = c + warp; x <= c1; x += 4) {
+                const float *src = a.partial + ((x == c ? 2 * x + 1 : 2 * x) * R + in_unit) * LD;
+                const float4 st = *reinterpret_cast<const float4 *>(src + D);
+                const float M1 = fmaxf(M, st.x), MV1 = fmaxf(MV, st.y);
+                const float ref = M1 == NEG_INF ? 0.0f : M1, refv = MV1 == NEG_INF ? 0.0f : MV1;
+                l = l * ex2(M - ref) + st.z * ex2(st.x - ref);
+                const float f0 = ex2(MV - refv), f1 = ex2(st.y - refv);
+#pragma unroll
+                for (int i = 0; i < CH; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + x0 + i);
+                    o[i] = o[i] * f0 + v.x * f1, o[i + 1] = o[i + 1] * f0 + v.y * f1;
+                    o[i + 2] = o[i + 2] * f0 + v.z * f1, o[i + 3] = o[i + 3] * f0 + v.w * f1;
+                }
+                M = M1, MV = MV1;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) s_o[warp][rr][x0 + i] = o[i];
+        if (x0 == 0) s_o[warp][rr][D] = M, s_o[warp][rr][D + 1] = MV, s_o[warp][rr][D + 2] = l;
+        __syncthreads();
+        if (tid < 4 * MT * 8) {
+            const int y = tid / 8, part = tid % 8, orow = r0 + 16 * (y / 4) + 4 * blockIdx.y + y % 4;
+            if (orow < rows) {
+                float Ma = NEG_INF, MVa = NEG_INF, la = 0.0f, acc[D / 8];
+                for (int w = 0; w < 4; ++w) Ma = fmaxf(Ma, s_o[w][y][D]), MVa = fmaxf(MVa, s_o[w][y][D + 1]);
+                const float ref = Ma == NEG_INF ? 0.0f : Ma, refv = MVa == NEG_INF ? 0.0f : MVa;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) acc[i] = 0.0f;
+                for (int w = 0; w < 4; ++w) {
+                    la += s_o[w][y][D + 2] * ex2(s_o[w][y][D] - ref);
+                    const float f = ex2(s_o[w][y][D + 1] - refv);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) acc[i] += f * s_o[w][y][part * (D / 8) + i];
+                }
+                const float f = exp2f(refv - ref);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) acc[i] *= f;
+                const int tok = orow / a.G;
+                store_row<D, HALF>(a, (rq.row0 + tok) * a.Hq + h * a.G + orow - tok * a.G, part, acc, Ma, la);
+            }
+        }
+        return;
+    }
+}
+
+template <int D, int MT, bool HALF>
+cudaError_t launch_split(const PagedAttnArgs &a, int ctas, cudaStream_t stream) {
+    static bool done[64];
+    constexpr int smem = attn_smem<D, MT>();
+    cudaError_t e = ensure_smem_limit((const void *)paged_attn_split_kernel<D, MT, HALF>, smem, done);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(paged_attn_split_kernel<D, MT, HALF>, dim3(ctas), dim3(kAttnWarps * 32), smem, stream, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_attn_join_kernel<D, MT, HALF>, dim3(ctas, 4), dim3(128), 0, stream, a);
+}
+
+// CTAs that run at once: three per SM (one row tile of 16), two (of 32).
+inline int split_ctas(int MT) { return num_sms() * (MT == 1 ? 3 : 2); }
+// Row tiles of 16 or, when more than 16 rows share a KV head, of 32.
+inline int row_tile(int G, int max_new) { return (int64_t)G * max_new > 16 ? 2 : 1; }
 
 }  // namespace
 }  // namespace csa2
@@ -317,8 +661,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32) paged_attn_kernel(PagedAttnAr
 using namespace csa2;
 
 extern "C" size_t csa2_paged_attn_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new) {
-    (void)B, (void)T, (void)Hq, (void)Hkv, (void)D, (void)max_new;
-    return 0;
+    if (B <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0 || max_new <= 0) return 0;
+    const int MT = row_tile(Hq / Hkv, max_new);
+    return (size_t)2 * split_ctas(MT) * 16 * MT * (D + 4) * sizeof(float);
 }
 
 extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, const void *q,
@@ -357,15 +702,19 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
         set_error("paged_attn: workspace of %zu bytes (16-byte aligned) needed, %zu given", need, ws_bytes);
         return CSA2_ERR_WORKSPACE;
     }
-    const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window, T, n_blocks, table_stride, q_token_stride,
+    const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride, q_token_stride,
                              q_head_stride, (const uint16_t *)q, k_codes, v_codes, k_scale, v_scale, block_table,
-                             kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag};
-    const int64_t tiles = ((int64_t)max_new * a.G + 15) / 16;
-    const dim3 grid((unsigned)(tiles < (1 << 20) ? tiles : (1 << 20)), (unsigned)Hkv, (unsigned)(B < 65535 ? B : 65535));
-    void (*kern)(PagedAttnArgs);
-    if (dt == CSA2_FP16) kern = D == 64 ? paged_attn_kernel<64, true> : paged_attn_kernel<128, true>;
-    else kern = D == 64 ? paged_attn_kernel<64, false> : paged_attn_kernel<128, false>;
-    CSA2_CUDA_CALL(launch_pdl(kern, grid, dim3(kAttnWarps * 32), 0, stream_of(stream), a), "paged_attn_kernel launch");
-    CSA2_LAUNCH_CHECK("paged_attn_kernel");
+                             kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag,
+                             (float *)workspace};
+    const int MT = row_tile(a.G, max_new), ctas = split_ctas(MT);
+    cudaError_t (*go)(const PagedAttnArgs &, int, cudaStream_t);
+    if (dt == CSA2_FP16)
+        go = D == 64 ? (MT == 1 ? launch_split<64, 1, true> : launch_split<64, 2, true>)
+                     : (MT == 1 ? launch_split<128, 1, true> : launch_split<128, 2, true>);
+    else
+        go = D == 64 ? (MT == 1 ? launch_split<64, 1, false> : launch_split<64, 2, false>)
+                     : (MT == 1 ? launch_split<128, 1, false> : launch_split<128, 2, false>);
+    CSA2_CUDA_CALL(go(a, ctas, stream_of(stream)), "paged_attn_split_kernel launch");
+    CSA2_LAUNCH_CHECK("paged_attn_split_kernel");
     return CSA2_OK;
 }
