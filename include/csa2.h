@@ -378,7 +378,7 @@ size_t csa2_sparse_attn_noalloc_max_scratch_bytes(void);
  *
  *   k_codes, v_codes  uint8 [n_blocks, Hkv, S, D], a block's rows of one head
  *                     contiguous; S in {16, 32, 64, 128} tokens, D in {64, 128}
- *   k_scale, v_scale  fp32 [n_blocks, Hkv]; a value is code * scale
+ *   k_scale, v_scale  fp32 [n_blocks, Hkv], not negative; a value is code * scale
  *   block_table       int32 [B, M] (row stride table_stride): token position p
  *                     of request b is row p % S of block block_table[b][p / S]
  *   slot of a token   block * S + row, int64; -1: the token is not stored

@@ -14,138 +14,14 @@
 // z and the running maximum Mv of z + log2(v_scale) (its exponent), and feeds
 // P_j v_scale 2^(M - Mv) <= 2 to the product: no weight that matters is lost to
 // f16's range, whatever the ratio of the scales.
-#include "common.cuh"
+#include "paged_attn.cuh"
 
 namespace csa2 {
 namespace {
 
 constexpr int kAttnWarps = 4;
-constexpr int kTileKeys = 32;       // keys per warp tile
+constexpr int kTileKeys = kSplitKeys;   // keys per warp tile
 constexpr int kStages = 2;          // tiles in flight per warp
-
-struct PagedAttnArgs {
-    int B, Hq, Hkv, G, S, M, window;
-    int64_t T, n_blocks, table_stride, q_token_stride, q_head_stride;
-    const uint16_t *q;
-    const uint8_t *k_codes, *v_codes;
-    const float *k_scale, *v_scale;
-    const int32_t *table, *kv_len, *cu_len;
-    float logit_scale;              // sm_scale * log2(e)
-    uint16_t *out;
-    float *lse;
-    uint32_t *err_flag;
-    float *partial;                 // [2 * CTAs][16 MT rows][D + 4]: o, m, mv, l
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <bool HALF>
-__device__ __forceinline__ float2 unpack_in(uint32_t w) {
-    if (HALF) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-template <bool HALF>
-__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
-    if (HALF) return pack_f16(lo, hi);
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Request b's rows and keys, clamped to what the tensors hold.
-struct Request {
-    int64_t row0;
-    int n, kv;
-};
-__device__ __forceinline__ Request request_of(const PagedAttnArgs &a, int b) {
-    const int64_t c0 = a.cu_len[b], c1 = a.cu_len[b + 1], cap = (int64_t)a.M * a.S, k = a.kv_len[b];
-    Request r;
-    r.row0 = c0 < 0 ? 0 : (c0 > a.T ? a.T : c0);
-    const int64_t e = c1 < r.row0 ? r.row0 : (c1 > a.T ? a.T : c1);
-    r.n = (int)(e - r.row0);
-    r.kv = (int)(k < 0 ? 0 : (k > cap ? cap : k));
-    return r;
-}
-
-// Work of the split kernel.  A unit is (request, KV head, tile of R = 16 MT
-// rows); it has tiles_of(request) tiles of 32 keys, the same for all row tiles
-// of a request, at least one so that every row gets its output.  The units'
-// tiles, in the order of requests, heads and row tiles, are one long line that
-// the CTAs cut into equal shares: a ragged batch loads every SM alike, and a
-// long context is split over as many CTAs as it is worth.
-struct Plan {
-    int64_t share;                  // tiles per CTA, a multiple of the warps
-    int b;                          // request that holds the CTA's first tile
-    int64_t base;                   // its first tile in the line
-    int64_t total;
-};
-__device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r) {
-    const int64_t p = (int64_t)r.kv - r.n - a.window + 1;      // lowest key of the first row's window
-    return a.window > 0 && p > 0 ? (int)p & ~(kTileKeys - 1) : 0;
-}
-__device__ __forceinline__ int tiles_of(const PagedAttnArgs &a, const Request &r) {
-    const int keys = r.kv - first_key(a, r);
-    return keys > 0 ? (keys + kTileKeys - 1) / kTileKeys : 1;
-}
-template <int R>
-__device__ __forceinline__ int units_of(const PagedAttnArgs &a, const Request &r) {
-    return (r.n * a.G + R - 1) / R * a.Hkv;
-}
-
-// Every thread of the block takes a run of requests; a prefix sum over the
-// threads finds the total and the thread that holds the CTA's first tile.
-template <int R>
-__device__ __forceinline__ Plan plan_of(const PagedAttnArgs &a, int cta, int ctas, int64_t *s_sum, int64_t *s_found) {
-    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.B + nt - 1) / nt, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Request r = request_of(a, b);
-        mine += (int64_t)units_of<R>(a, r) * tiles_of(a, r);
-    }
-    int64_t s = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += y;
-    }
-    if (lane == 31) s_sum[warp] = s;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int w = 0; w < nt / 32; ++w) {
-        if (w < warp) before += s_sum[w];
-        total += s_sum[w];
-    }
-    Plan p;
-    p.total = total;
-    const int64_t even = (total + ctas - 1) / ctas;
-    p.share = (even + kAttnWarps - 1) / kAttnWarps * kAttnWarps;
-    const int64_t t0 = cta * p.share;
-    int64_t at = before + s - mine;
-    if (t0 >= at && t0 < at + mine) {
-        for (int b = b0; b < b1; ++b) {
-            const Request r = request_of(a, b);
-            const int64_t w = (int64_t)units_of<R>(a, r) * tiles_of(a, r);
-            if (t0 < at + w) {
-                s_found[0] = b;
-                s_found[1] = at;
-                break;
-            }
-            at += w;
-        }
-    }
-    __syncthreads();
-    p.b = (int)s_found[0];          // meaningless if t0 >= total
-    p.base = s_found[1];
-    return p;
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
@@ -338,19 +214,6 @@ constexpr int attn_smem() {
     return ring > merge ? ring : merge;
 }
 
-// 8 threads per row, D / 8 channels each: o = x * inv in the output's type, lse.
-template <int D, bool HALF>
-__device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row, int part, const float *x, float M, float l) {
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    uint32_t w[D / 16];
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) w[c] = pack_out<HALF>(x[2 * c] * inv, x[2 * c + 1] * inv);
-    uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + part * (D / 8));
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-    if (a.lse && part == 0) a.lse[o_row] = l > 0.0f || l != l ? (M + log2f(l)) * 0.69314718055994531f : __int_as_float(0xff800000);
-}
-
 template <int D, int MT, bool HALF>
 __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_split_kernel(PagedAttnArgs a) {
     constexpr int R = 16 * MT;
@@ -363,20 +226,20 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
     const float NEG_INF = __int_as_float(0xff800000);
     pdl_wait();
     pdl_launch_dependents();
-    const Plan plan = plan_of<R>(a, blockIdx.x, gridDim.x, s_sum, s_found);
+    using Work = SplitWork<R>;
+    const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kAttnWarps, s_sum, s_found);
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * 2 * kTileKeys * D);
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
         const Request rq = request_of(a, b);
-        const int tiles = tiles_of(a, rq), row_tiles = (rq.n * a.G + R - 1) / R, key0 = first_key(a, rq);
-        const int64_t end = base + (int64_t)row_tiles * a.Hkv * tiles;
+        const int64_t end = base + Work::tiles(a, rq);
+        const int key0 = Work::first_key(a, rq), rows = rq.n * a.G;
         while (at < stop && at < end) {
             // segment: tiles [ta, tb) of one unit
-            const int unit = (int)((at - base) / tiles), ta = (int)((at - base) - (int64_t)unit * tiles);
-            const int tb = (int)min((int64_t)tiles, ta + (stop - at));
-            const int h = unit / row_tiles, r0 = (unit - h * row_tiles) * R, rows = rq.n * a.G;
+            const Place pl = Work::place(a, rq, at - base);
+            const int h = pl.h, r0 = pl.r0, ta = pl.tile, tb = (int)min((int64_t)pl.tiles, ta + (stop - at));
             at += tb - ta;
 
             Tile<D, MT> tile;
@@ -489,7 +352,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
             cp_async_wait<0>();
 
             // the warps' shares meet in shared memory, 16 rows at a time
-            const bool whole = ta == 0 && tb == tiles;
+            const bool whole = ta == 0 && tb == pl.tiles;
             float *s_o = reinterpret_cast<float *>(smem);
             constexpr int LD = D + 4;
 #pragma unroll
@@ -557,45 +420,40 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
     }
 }
 
-// Joins the partial results of units that several CTAs share.  Block (c, y)
-// takes rows 4 y .. 4 y + 3 (of each 16) of the unit that CTA c began and did not
-// finish; CTA c's part is slot 2 c + 1, those of the CTAs after it slots 2 c'.
-template <int D, int MT, bool HALF>
-__global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a) {
-    constexpr int R = 16 * MT, LD = D + 4;
-    __shared__ int64_t s_sum[4], s_found[2];
-    __shared__ float s_o[4][4 * MT][LD];
-    const int ctas = gridDim.x, c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// Joins the partial results of a unit that several CTAs share: the unit that
+// CTA c began and did not finish.  CTA c's part is slot 2 c + 1, those of the
+// CTAs after it slots 2 c'.  A block takes JR rows of the unit; each of its four
+// warps joins every fourth part of them, then the warps' results meet.
+template <int D, bool HALF, typename Work, int JR>
+__device__ __forceinline__ void join_unit(const PagedAttnArgs &a, const float *partial, int c, int ctas, int round, int y0,
+                                          float (*s_o)[16][D + 4], int64_t *s_sum, int64_t *s_found) {
+    constexpr int R = Work::ROWS, LD = D + 4;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float NEG_INF = __int_as_float(0xff800000);
-    pdl_wait();
-    pdl_launch_dependents();
-    const Plan plan = plan_of<R>(a, c, ctas, s_sum, s_found);
+    const Plan plan = plan_of<Work>(a, c, ctas, round, s_sum, s_found);
     const int64_t t0 = c * plan.share, last = min(plan.total, t0 + plan.share) - 1;
-    if (t0 >= plan.total) return;
+    if (t0 >= plan.total || last + 1 == plan.total) return;
     int64_t base = plan.base;
-    for (int b = plan.b; b < a.B; ++b) {                     // the request of the CTA's last tile
+    for (int b = plan.b; b < a.B; ++b) {             // the request of the CTA's last tile
         const Request rq = request_of(a, b);
-        const int tiles = tiles_of(a, rq), row_tiles = (rq.n * a.G + R - 1) / R;
-        const int64_t end = base + (int64_t)row_tiles * a.Hkv * tiles;
+        const int64_t end = base + Work::tiles(a, rq);
         if (last >= end) {
             base = end;
             continue;
         }
-        const int unit = (int)((last - base) / tiles);
-        const int64_t u0 = base + (int64_t)unit * tiles, u1 = u0 + tiles;
+        const Place pl = Work::place(a, rq, last - base);
+        const int64_t u0 = last - pl.tile, u1 = u0 + pl.tiles;
         if (u0 < t0 || u1 <= last + 1) return;       // begun by an earlier CTA, or finished by this one
         const int64_t c1 = (u1 - 1) / plan.share;    // the CTA with the unit's last tile
-        const int h = unit / row_tiles, r0 = (unit - h * row_tiles) * R, rows = rq.n * a.G;
-        // each warp joins every fourth part of its rows, then the warps' results meet
-        constexpr int TPR = 32 / (4 * MT), CH = D / TPR;     // threads per row in a warp, channels per thread
-        const int rr = lane / TPR, x0 = (lane % TPR) * CH;
-        const int row = r0 + 16 * (rr / 4) + 4 * blockIdx.y + rr % 4, in_unit = row - r0;
+        const int rows = rq.n * a.G;
+        constexpr int TPR = 32 / JR, CH = D / TPR;   // threads per row in a warp, channels per thread
+        const int rr = lane / TPR, x0 = (lane % TPR) * CH, in_unit = y0 + rr;
         float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) o[i] = 0.0f;
-        if (row < rows) {
+        if (pl.r0 + in_unit < rows) {
             for (int64_t x = c + warp; x <= c1; x += 4) {
-                const float *src = a.partial + ((x == c ? 2 * x + 1 : 2 * x) * R + in_unit) * LD;
+                const float *src = partial + ((x == c ? 2 * x + 1 : 2 * x) * R + in_unit) * LD;
                 const float4 st = *reinterpret_cast<const float4 *>(src + D);
                 const float M1 = fmaxf(M, st.x), MV1 = fmaxf(MV, st.y);
                 const float ref = M1 == NEG_INF ? 0.0f : M1, refv = MV1 == NEG_INF ? 0.0f : MV1;
@@ -614,9 +472,9 @@ __global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a) {
         for (int i = 0; i < CH; ++i) s_o[warp][rr][x0 + i] = o[i];
         if (x0 == 0) s_o[warp][rr][D] = M, s_o[warp][rr][D + 1] = MV, s_o[warp][rr][D + 2] = l;
         __syncthreads();
-        if (tid < 4 * MT * 8) {
-            const int y = tid / 8, part = tid % 8, orow = r0 + 16 * (y / 4) + 4 * blockIdx.y + y % 4;
-            if (orow < rows) {
+        if (tid < JR * 8) {
+            const int y = tid / 8, part = tid % 8, row = pl.r0 + y0 + y;
+            if (row < rows) {
                 float Ma = NEG_INF, MVa = NEG_INF, la = 0.0f, acc[D / 8];
                 for (int w = 0; w < 4; ++w) Ma = fmaxf(Ma, s_o[w][y][D]), MVa = fmaxf(MVa, s_o[w][y][D + 1]);
                 const float ref = Ma == NEG_INF ? 0.0f : Ma, refv = MVa == NEG_INF ? 0.0f : MVa;
@@ -631,29 +489,72 @@ __global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a) {
                 const float f = exp2f(refv - ref);
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) acc[i] *= f;
-                const int tok = orow / a.G;
-                store_row<D, HALF>(a, (rq.row0 + tok) * a.Hq + h * a.G + orow - tok * a.G, part, acc, Ma, la);
+                const int tok = row / a.G;
+                store_row<D, HALF>(a, (rq.row0 + tok) * a.Hq + pl.h * a.G + row - tok * a.G, part, acc, Ma, la);
             }
         }
         return;
     }
 }
 
+// Blocks [0, 4 split_ctas) join the split kernel's units of 16 MT rows, 4 MT rows
+// each; the others the tile kernel's of 256 rows, 16 rows each.
 template <int D, int MT, bool HALF>
-cudaError_t launch_split(const PagedAttnArgs &a, int ctas, cudaStream_t stream) {
-    static bool done[64];
-    constexpr int smem = attn_smem<D, MT>();
-    cudaError_t e = ensure_smem_limit((const void *)paged_attn_split_kernel<D, MT, HALF>, smem, done);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(paged_attn_split_kernel<D, MT, HALF>, dim3(ctas), dim3(kAttnWarps * 32), smem, stream, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attn_join_kernel<D, MT, HALF>, dim3(ctas, 4), dim3(128), 0, stream, a);
+__global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a, int split_ctas, int tc_ctas) {
+    __shared__ int64_t s_sum[4], s_found[2];
+    __shared__ float s_o[4][16][D + 4];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int x = blockIdx.x, n = 4 * split_ctas;
+    if (x < n)
+        join_unit<D, HALF, SplitWork<16 * MT>, 4 * MT>(a, a.partial, x / 4, split_ctas, kAttnWarps, x % 4 * 4 * MT, s_o, s_sum,
+                                                       s_found);
+    else
+        join_unit<D, HALF, TcWork, 16>(a, a.partial_tc, (x - n) / 16, tc_ctas, kTcRound, (x - n) % 16 * 16, s_o, s_sum,
+                                       s_found);
 }
 
-// CTAs that run at once: three per SM (one row tile of 16), two (of 32).
-inline int split_ctas(int MT) { return num_sms() * (MT == 1 ? 3 : 2); }
-// Row tiles of 16 or, when more than 16 rows share a KV head, of 32.
-inline int row_tile(int G, int max_new) { return (int64_t)G * max_new > 16 ? 2 : 1; }
+template <int D, int MT, bool HALF>
+cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cudaStream_t stream) {
+    static bool done[64];
+    constexpr int smem = attn_smem<D, MT>();
+    cudaError_t e = cudaSuccess;
+    if (split_ctas) {
+        e = ensure_smem_limit((const void *)paged_attn_split_kernel<D, MT, HALF>, smem, done);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(paged_attn_split_kernel<D, MT, HALF>, dim3(split_ctas), dim3(kAttnWarps * 32), smem, stream, a);
+        if (e != cudaSuccess) return e;
+    }
+    if (tc_ctas) {
+        e = launch_paged_attn_tc(a, D, HALF, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(paged_attn_join_kernel<D, MT, HALF>, dim3(4 * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
+                      split_ctas, tc_ctas);
+}
+
+// Which kernels a call launches.  Rows of one request that share a KV head are
+// G * max_new at most.  Up to 32 of them the split kernel takes every request (a
+// row tile of 16, or of 32 that reads the keys once for all).  Beyond, requests
+// of more than 16 rows go to the tile kernel; the split kernel then runs for
+// the others, unless there is but one request.
+struct Choice {
+    int MT, split_ctas, tc_ctas, split_rows;
+};
+inline Choice choose(int B, int G, int max_new) {
+    const int64_t rows = (int64_t)G * max_new;
+    Choice c = {1, num_sms() * 3, 0, 0x7FFFFFFF};    // CTAs that run at once: three per SM, two with 32 rows
+    if (rows > 32) {
+        c.tc_ctas = paged_attn_tc_ctas();
+        c.split_rows = B > 1 ? 16 : 0;
+        if (B == 1) c.split_ctas = 0;
+    } else if (rows > 16) {
+        c.MT = 2;
+        c.split_ctas = num_sms() * 2;
+    }
+    return c;
+}
+inline size_t split_partial_floats(const Choice &c, int D) { return (size_t)2 * c.split_ctas * 16 * c.MT * (D + 4); }
 
 }  // namespace
 }  // namespace csa2
@@ -662,8 +563,8 @@ using namespace csa2;
 
 extern "C" size_t csa2_paged_attn_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new) {
     if (B <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0 || max_new <= 0) return 0;
-    const int MT = row_tile(Hq / Hkv, max_new);
-    return (size_t)2 * split_ctas(MT) * 16 * MT * (D + 4) * sizeof(float);
+    const Choice c = choose(B, Hq / Hkv, max_new);
+    return (split_partial_floats(c, D) + (size_t)2 * c.tc_ctas * kTcRows * (D + 4)) * sizeof(float);
 }
 
 extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, const void *q,
@@ -679,7 +580,7 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
     CSA2_REQUIRE(B >= 0 && B <= 65536, "paged_attn: B=%d not in [0, 65536]", B);
     CSA2_REQUIRE(T >= 0 && T <= (1ll << 30), "paged_attn: T=%lld not in [0, 2^30]", (long long)T);
     CSA2_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536, "paged_attn: Hq=%d, Hkv=%d", Hq, Hkv);
-    CSA2_REQUIRE(T * (Hq / Hkv) < (1ll << 31), "paged_attn: T * Hq / Hkv = %lld rows", (long long)(T * (Hq / Hkv)));
+    CSA2_REQUIRE(T * (Hq / Hkv) <= (1ll << 30), "paged_attn: T * Hq / Hkv = %lld rows", (long long)(T * (Hq / Hkv)));
     CSA2_REQUIRE(S == 16 || S == 32 || S == 64 || S == 128, "paged_attn: S=%d not in {16, 32, 64, 128}", S);
     CSA2_REQUIRE(M >= 1 && (int64_t)M * S < (1ll << 31), "paged_attn: M=%d: need 1 <= M, M * S < 2^31", M);
     CSA2_REQUIRE(table_stride >= M, "paged_attn: table_stride=%lld < M=%d", (long long)table_stride, M);
@@ -702,19 +603,20 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
         set_error("paged_attn: workspace of %zu bytes (16-byte aligned) needed, %zu given", need, ws_bytes);
         return CSA2_ERR_WORKSPACE;
     }
-    const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride, q_token_stride,
-                             q_head_stride, (const uint16_t *)q, k_codes, v_codes, k_scale, v_scale, block_table,
-                             kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag,
-                             (float *)workspace};
-    const int MT = row_tile(a.G, max_new), ctas = split_ctas(MT);
-    cudaError_t (*go)(const PagedAttnArgs &, int, cudaStream_t);
+    const Choice c = choose(B, Hq / Hkv, max_new);
+    float *partial = (float *)workspace;
+    const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride,
+                             q_token_stride, q_head_stride, (const uint16_t *)q, k_codes, v_codes, k_scale, v_scale,
+                             block_table, kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag,
+                             c.split_rows, partial, partial + split_partial_floats(c, D)};
+    cudaError_t (*go)(const PagedAttnArgs &, int, int, cudaStream_t);
     if (dt == CSA2_FP16)
-        go = D == 64 ? (MT == 1 ? launch_split<64, 1, true> : launch_split<64, 2, true>)
-                     : (MT == 1 ? launch_split<128, 1, true> : launch_split<128, 2, true>);
+        go = D == 64 ? (c.MT == 1 ? launch_attn<64, 1, true> : launch_attn<64, 2, true>)
+                     : (c.MT == 1 ? launch_attn<128, 1, true> : launch_attn<128, 2, true>);
     else
-        go = D == 64 ? (MT == 1 ? launch_split<64, 1, false> : launch_split<64, 2, false>)
-                     : (MT == 1 ? launch_split<128, 1, false> : launch_split<128, 2, false>);
-    CSA2_CUDA_CALL(go(a, ctas, stream_of(stream)), "paged_attn_split_kernel launch");
-    CSA2_LAUNCH_CHECK("paged_attn_split_kernel");
+        go = D == 64 ? (c.MT == 1 ? launch_attn<64, 1, false> : launch_attn<64, 2, false>)
+                     : (c.MT == 1 ? launch_attn<128, 1, false> : launch_attn<128, 2, false>);
+    CSA2_CUDA_CALL(go(a, c.split_ctas, c.tc_ctas, stream_of(stream)), "paged_attn launch");
+    CSA2_LAUNCH_CHECK("paged_attn kernels");
     return CSA2_OK;
 }

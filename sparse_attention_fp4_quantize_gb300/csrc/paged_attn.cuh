@@ -1,0 +1,213 @@
+// Shared parts of the paged attention (csa2_paged_attn_fp8): arguments, the
+// requests' rows and keys, the line of work that CTAs share out, and the output
+// of a row.
+#pragma once
+
+#include "common.cuh"
+
+namespace csa2 {
+
+struct PagedAttnArgs {
+    int B, Hq, Hkv, G, S, M, window;
+    int64_t T, n_blocks, table_stride, q_token_stride, q_head_stride;
+    const uint16_t *q;
+    const uint8_t *k_codes, *v_codes;
+    const float *k_scale, *v_scale;
+    const int32_t *table, *kv_len, *cu_len;
+    float logit_scale;              // sm_scale * log2(e)
+    uint16_t *out;
+    float *lse;
+    uint32_t *err_flag;
+    int split_rows;                 // requests of more rows than this are the tile kernel's
+    float *partial;                 // split kernel's [2 * CTAs][16 MT rows][D + 4]: o, m, mv, l
+    float *partial_tc;              // tile kernel's [2 * CTAs][256 rows][D + 4]
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <bool HALF>
+__device__ __forceinline__ float2 unpack_in(uint32_t w) {
+    if (HALF) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+    if (HALF) return pack_f16(lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Request b's rows and keys, clamped to what the tensors hold.
+struct Request {
+    int64_t row0;
+    int n, kv;
+};
+__device__ __forceinline__ Request request_of(const PagedAttnArgs &a, int b) {
+    const int64_t c0 = a.cu_len[b], c1 = a.cu_len[b + 1], cap = (int64_t)a.M * a.S, k = a.kv_len[b];
+    Request r;
+    r.row0 = c0 < 0 ? 0 : (c0 > a.T ? a.T : c0);
+    const int64_t e = c1 < r.row0 ? r.row0 : (c1 > a.T ? a.T : c1);
+    r.n = (int)(e - r.row0);
+    r.kv = (int)(k < 0 ? 0 : (k > cap ? cap : k));
+    return r;
+}
+
+// A request's work is a number of units (KV head, tile of query rows), each a
+// number of key tiles.  The units' key tiles, in the order of requests, heads
+// and row tiles, are one long line that the CTAs cut into equal shares: a ragged
+// batch loads every SM alike, and a long context is split over as many CTAs as
+// it is worth.  A CTA's piece of a unit is a segment; only its first and its
+// last segment can be parts of a unit.
+struct Plan {
+    int64_t share;                  // key tiles per CTA, a multiple of `round`
+    int b;                          // request that holds the CTA's first tile (if there is one)
+    int64_t base;                   // that request's first tile in the line
+    int64_t total;
+};
+
+// Every thread of the block takes a run of requests; a prefix sum over the
+// threads finds the total and the thread that holds the CTA's first tile.
+template <typename Work>
+__device__ __forceinline__ Plan plan_of(const PagedAttnArgs &a, int cta, int ctas, int round, int64_t *s_sum,
+                                        int64_t *s_found) {
+    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + nt - 1) / nt, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += Work::tiles(a, request_of(a, b));
+    int64_t s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += y;
+    }
+    if (lane == 31) s_sum[warp] = s;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    Plan p;
+    p.total = total;
+    const int64_t even = (total + ctas - 1) / ctas;
+    p.share = (even + round - 1) / round * round;
+    const int64_t t0 = cta * p.share;
+    int64_t at = before + s - mine;
+    if (t0 >= at && t0 < at + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const int64_t w = Work::tiles(a, request_of(a, b));
+            if (t0 < at + w) {
+                s_found[0] = b;
+                s_found[1] = at;
+                break;
+            }
+            at += w;
+        }
+    }
+    __syncthreads();
+    p.b = (int)s_found[0];
+    p.base = s_found[1];
+    return p;
+}
+
+// Where in a unit a place of the line is.
+struct Place {
+    int h, r0, tile, tiles;         // KV head, first row, key tile of the unit, the unit's key tiles
+};
+
+// The split kernel's work: units of R = 16 MT rows, key tiles of 32; every row
+// tile of a request has the same tiles, at least one so that each row gets its
+// output.
+constexpr int kSplitKeys = 32;
+template <int R>
+struct SplitWork {
+    static constexpr int ROWS = R;
+    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r) {
+        const int64_t p = (int64_t)r.kv - r.n - a.window + 1;      // lowest key of the first row's window
+        return a.window > 0 && p > 0 ? (int)p & ~(kSplitKeys - 1) : 0;
+    }
+    static __device__ __forceinline__ int unit_tiles(const PagedAttnArgs &a, const Request &r) {
+        const int keys = r.kv - first_key(a, r);
+        return keys > 0 ? (keys + kSplitKeys - 1) / kSplitKeys : 1;
+    }
+    static __device__ __forceinline__ int64_t tiles(const PagedAttnArgs &a, const Request &r) {
+        const int rows = r.n * a.G;
+        return rows > a.split_rows ? 0 : (int64_t)((rows + R - 1) / R) * a.Hkv * unit_tiles(a, r);
+    }
+    static __device__ __forceinline__ Place place(const PagedAttnArgs &a, const Request &r, int64_t off) {
+        const int row_tiles = (r.n * a.G + R - 1) / R, per = unit_tiles(a, r);
+        const int unit = (int)(off / per);
+        Place p;
+        p.h = unit / row_tiles;
+        p.r0 = (unit - p.h * row_tiles) * R;
+        p.tile = (int)(off - (int64_t)unit * per);
+        p.tiles = per;
+        return p;
+    }
+};
+
+// The tile kernel's work: units of 256 rows, key tiles of 128, for each row tile
+// those that its first to last row see.
+constexpr int kTcRows = 256, kTcKeys = 128, kTcRound = 2;
+struct TcWork {
+    static constexpr int ROWS = kTcRows;
+    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r, int r0) {
+        const int64_t p = (int64_t)r.kv - r.n + r0 / a.G - a.window + 1;
+        return a.window > 0 && p > 0 ? (int)p & ~(kTcKeys - 1) : 0;
+    }
+    static __device__ __forceinline__ int unit_tiles(const PagedAttnArgs &a, const Request &r, int r0) {
+        const int last = (min(r0 + kTcRows, r.n * a.G) - 1) / a.G;
+        const int keys = min(r.kv, r.kv - r.n + last + 1) - first_key(a, r, r0);
+        return keys > 0 ? (keys + kTcKeys - 1) / kTcKeys : 1;
+    }
+    static __device__ __forceinline__ int64_t head_tiles(const PagedAttnArgs &a, const Request &r) {
+        int64_t n = 0;
+        for (int r0 = 0; r0 < r.n * a.G; r0 += kTcRows) n += unit_tiles(a, r, r0);
+        return n;
+    }
+    static __device__ __forceinline__ int64_t tiles(const PagedAttnArgs &a, const Request &r) {
+        return r.n * a.G <= a.split_rows ? 0 : head_tiles(a, r) * a.Hkv;
+    }
+    static __device__ __forceinline__ Place place(const PagedAttnArgs &a, const Request &r, int64_t off) {
+        const int64_t per = head_tiles(a, r);
+        Place p;
+        p.h = (int)(off / per);
+        int64_t left = off - p.h * per;
+        p.r0 = 0;
+        for (;; p.r0 += kTcRows) {
+            p.tiles = unit_tiles(a, r, p.r0);
+            if (left < p.tiles) break;
+            left -= p.tiles;
+        }
+        p.tile = (int)left;
+        return p;
+    }
+};
+
+// 8 threads per row, D / 8 channels each: o = x * inv in the output's type, lse.
+template <int D, bool HALF>
+__device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row, int part, const float *x, float M, float l) {
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    uint32_t w[D / 16];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) w[c] = pack_out<HALF>(x[2 * c] * inv, x[2 * c + 1] * inv);
+    uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + part * (D / 8));
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    if (a.lse && part == 0) a.lse[o_row] = l > 0.0f || l != l ? (M + log2f(l)) * 0.69314718055994531f : __int_as_float(0xff800000);
+}
+
+
+// The tile kernel (paged_attn_tc.cu): one CTA per SM.
+int paged_attn_tc_ctas();
+cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, int D, bool half, cudaStream_t stream);
+
+}  // namespace csa2
