@@ -23,6 +23,21 @@ struct PagedAttnArgs {
     float *partial_tc;              // tile kernel's [2 * CTAs][256 rows][D + 4]
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -159,36 +174,56 @@ struct SplitWork {
 constexpr int kTcRows = 256, kTcKeys = 128, kTcRound = 2;
 struct TcWork {
     static constexpr int ROWS = kTcRows;
-    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r, int r0) {
-        const int64_t p = (int64_t)r.kv - r.n + r0 / a.G - a.window + 1;
+    // A walk over the row tiles of a request, without a division per step.
+    struct Rows {
+        int G, q256, m256, q255, m255;
+        int r0, tok, rem;                 // first row = tok * G + rem
+        __device__ __forceinline__ Rows(int g) : G(g), q256(kTcRows / g), m256(kTcRows % g), q255((kTcRows - 1) / g),
+                                                 m255((kTcRows - 1) % g), r0(0), tok(0), rem(0) {}
+        __device__ __forceinline__ void next() {
+            r0 += kTcRows;
+            tok += q256;
+            rem += m256;
+            if (rem >= G) ++tok, rem -= G;
+        }
+        __device__ __forceinline__ int last_tok() const { return tok + q255 + (rem + m255 >= G); }
+    };
+    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r, const Rows &w) {
+        const int64_t p = (int64_t)r.kv - r.n + w.tok - a.window + 1;
         return a.window > 0 && p > 0 ? (int)p & ~(kTcKeys - 1) : 0;
     }
-    static __device__ __forceinline__ int unit_tiles(const PagedAttnArgs &a, const Request &r, int r0) {
-        const int last = (min(r0 + kTcRows, r.n * a.G) - 1) / a.G;
-        const int keys = min(r.kv, r.kv - r.n + last + 1) - first_key(a, r, r0);
+    static __device__ __forceinline__ int unit_tiles(const PagedAttnArgs &a, const Request &r, const Rows &w) {
+        const int last = min(w.last_tok(), r.n - 1);
+        const int keys = min(r.kv, r.kv - r.n + last + 1) - first_key(a, r, w);
         return keys > 0 ? (keys + kTcKeys - 1) / kTcKeys : 1;
     }
+    static __device__ __forceinline__ bool mine(const PagedAttnArgs &a, const Request &r) { return r.n * a.G > a.split_rows; }
     static __device__ __forceinline__ int64_t head_tiles(const PagedAttnArgs &a, const Request &r) {
         int64_t n = 0;
-        for (int r0 = 0; r0 < r.n * a.G; r0 += kTcRows) n += unit_tiles(a, r, r0);
+        for (Rows w(a.G); w.r0 < r.n * a.G; w.next()) n += unit_tiles(a, r, w);
         return n;
     }
     static __device__ __forceinline__ int64_t tiles(const PagedAttnArgs &a, const Request &r) {
-        return r.n * a.G <= a.split_rows ? 0 : head_tiles(a, r) * a.Hkv;
+        return mine(a, r) ? head_tiles(a, r) * a.Hkv : 0;
     }
-    static __device__ __forceinline__ Place place(const PagedAttnArgs &a, const Request &r, int64_t off) {
+    // The unit of place `off` of the request's tiles; `w` is left at its row tile.
+    static __device__ __forceinline__ Place place(const PagedAttnArgs &a, const Request &r, int64_t off, Rows &w) {
         const int64_t per = head_tiles(a, r);
         Place p;
         p.h = (int)(off / per);
         int64_t left = off - p.h * per;
-        p.r0 = 0;
-        for (;; p.r0 += kTcRows) {
-            p.tiles = unit_tiles(a, r, p.r0);
+        for (;; w.next()) {
+            p.tiles = unit_tiles(a, r, w);
             if (left < p.tiles) break;
             left -= p.tiles;
         }
+        p.r0 = w.r0;
         p.tile = (int)left;
         return p;
+    }
+    static __device__ __forceinline__ Place place(const PagedAttnArgs &a, const Request &r, int64_t off) {
+        Rows w(a.G);
+        return place(a, r, off, w);
     }
 };
 

@@ -25,8 +25,12 @@ namespace csa2 {
 namespace {
 
 constexpr int kSoftWarps = 8, kConvWarps = 4, kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kTcThreads = (kMmaWarp + 1) * 32;
-constexpr uint32_t kPolls = 1u << 22;
+constexpr int kTcThreads = 512;              // four warpgroups, as the register shares go by warpgroup
+// Registers per thread: 512 x 128 at launch; the softmax warpgroups, which hold
+// a row's 128 scores, take what the others give up.
+constexpr int kSoftRegs = 184, kConvRegs = 80, kMmaRegs = 64;
+static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * 128, "register shares exceed the launch's");
+constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after that many naps (ns, ended by the arrival)
 constexpr float kSlack = 8.0f;               // log2: how far a tile may exceed a reference
 constexpr int kMetas = 4;                    // key tiles whose scales are kept
 
@@ -35,13 +39,23 @@ struct TileMeta {
     uint32_t missing[4];                     // per converting warp: its groups that are not stored (a bit each)
 };
 
+// A piece of a unit.  One warp works out the CTA's segments and hands them to the
+// others through a ring in shared memory.
+constexpr int kSegs = 4;
+struct alignas(16) Segment {
+    Request rq;
+    Place pl;
+    int b, tb;                               // request, end of its key tiles [pl.tile, tb)
+    int rows, key0;                          // rows of the request and KV head (0: no more segments); key of the unit's first tile
+};
+
 template <int D>
 struct Lay {
     static constexpr uint32_t GROUP = D * 16;            // core matrices of 8 rows: D / 8 x 128 bytes
     static constexpr uint32_t Q = 128 * D * 2, KV = kTcKeys * D * 2;
-    static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q, OFF_V = OFF_K + 2 * KV, OFF_META = OFF_V + 2 * KV,
-                              OFF_BAR = OFF_META + kMetas * sizeof(TileMeta);
-    static constexpr int BARS = 21;
+    static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q, OFF_V = OFF_K + 2 * KV, OFF_STAGE = OFF_V + 2 * KV, OFF_META = OFF_STAGE + KV,
+                              OFF_SEG = OFF_META + kMetas * sizeof(TileMeta), OFF_BAR = OFF_SEG + kSegs * sizeof(Segment);
+    static constexpr int BARS = 29;
     static constexpr uint32_t USED = OFF_BAR + BARS * 8 + 8;
     static constexpr uint32_t SMEM = USED + 128 > 120 * 1024 ? USED + 128 : 120 * 1024;   // one CTA per SM (TMEM)
     static constexpr uint32_t COL_S = 0, COL_O = 256;    // TMEM columns: S0, S1 (P over them), O0, O1
@@ -83,54 +97,77 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Bounded wait of a whole warp (every lane gets the same answer) that also gives
-// up once another warp has raised the abort word.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_word) {
-    uint32_t ok = 0;
-    for (uint32_t i = 0; i < kPolls && !ok; ++i) {
+// Bounded wait of one thread that also gives up once another has raised the
+// abort word; and of a whole warp, every lane of which gets the same answer.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int *abort_word) {
+    for (uint32_t i = 0; i < kPolls; ++i) {
+        uint32_t ok;
         asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(bar), "r"(parity)
+            : "r"(bar), "r"(parity), "r"(kNap)
             : "memory");
-        if (!ok && (i & 63) == 63 && *abort_word) break;
+        if (ok) return true;
+        if (*abort_word) break;
     }
-    if (__all_sync(0xFFFFFFFFu, ok)) return true;
     *abort_word = 1;
     return false;
 }
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_word) {
+    return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, abort_word));
+}
 
-// The CTA's segments in order; every role walks them by itself.
-struct Segment {
-    Request rq;
-    Place pl;
-    int b, tb;                    // request, end of its key tiles [pl.tile, tb)
-    int rows, key0;               // rows of the request and KV head; key of the unit's first tile
-};
+// Logit factor of a key: not 0, so that a hidden score of -inf stays -inf.
+__device__ __forceinline__ float factor(float zf, float ks) { return fmaxf(zf * ks, 1e-38f); }
+
+// The CTA's segments in order.
 struct Walk {
     int64_t at, stop, base;
-    int b;
+    Request rq;
+    TcWork::Rows rows;
+    int b, h;                     // h < 0: before the first segment
+    __device__ __forceinline__ Walk(const PagedAttnArgs &a, const Plan &p, int cta)
+        : at(cta * p.share), stop(min(p.total, at + p.share)), base(p.base), rows(a.G), b(p.b), h(-1) {}
     __device__ __forceinline__ bool next(const PagedAttnArgs &a, Segment &s) {
-        for (; at < stop && b < a.B; ++b) {
-            s.rq = request_of(a, b);
-            const int64_t end = base + TcWork::tiles(a, s.rq);
-            if (at < end) {
-                s.pl = TcWork::place(a, s.rq, at - base);
-                s.b = b;
-                s.tb = (int)min((int64_t)s.pl.tiles, s.pl.tile + (stop - at));
-                s.rows = s.rq.n * a.G;
-                s.key0 = TcWork::first_key(a, s.rq, s.pl.r0);
-                at += s.tb - s.pl.tile;
-                return true;
+        if (at >= stop) return false;
+        if (h < 0) {
+            rq = request_of(a, b);
+            s.pl = TcWork::place(a, rq, at - base, rows);
+            h = s.pl.h;
+        } else {                                          // the row tile, head or request after the last one
+            rows.next();
+            if (rows.r0 >= rq.n * a.G) {
+                rows = TcWork::Rows(a.G);
+                if (++h == a.Hkv) {
+                    h = 0;
+                    do {
+                        if (++b >= a.B) return false;
+                        rq = request_of(a, b);
+                    } while (!TcWork::mine(a, rq));
+                }
             }
-            base = end;
+            s.pl.h = h;
+            s.pl.r0 = rows.r0;
+            s.pl.tile = 0;
+            s.pl.tiles = TcWork::unit_tiles(a, rq, rows);
         }
-        return false;
+        s.rq = rq;
+        s.b = b;
+        s.tb = (int)min((int64_t)s.pl.tiles, s.pl.tile + (stop - at));
+        s.rows = rq.n * a.G;
+        s.key0 = TcWork::first_key(a, rq, rows);
+        at += s.tb - s.pl.tile;
+        return true;
     }
 };
 
@@ -157,21 +194,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     auto ofull = [&](int i) { return bar0 + 8u * (14 + i); };
     auto mfull = [&](int i) { return bar0 + 8u * (16 + i); };
     const uint32_t drain = bar0 + 8u * 20;
+    auto segfull = [&](int i) { return bar0 + 8u * (21 + i); };
+    auto segempty = [&](int i) { return bar0 + 8u * (25 + i); };
+    Segment *segs = reinterpret_cast<Segment *>(smem + L::OFF_SEG);
     const float NEG_INF = __int_as_float(0xff800000);
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(kfull(i), kConvWarps);
-            tc::mbar_init(kempty(i), 1);
+            tc::mbar_init(kempty(i), 2);
             tc::mbar_init(vfull(i), kConvWarps);
-            tc::mbar_init(vempty(i), 1);
+            tc::mbar_init(vempty(i), 2);
             tc::mbar_init(qfull(i), 4);
             tc::mbar_init(sfull(i), 1);
             tc::mbar_init(pfull(i), 4);
             tc::mbar_init(ofull(i), 1);
         }
         for (int i = 0; i < kMetas; ++i) tc::mbar_init(mfull(i), kConvWarps);
-        tc::mbar_init(drain, 1);
+        tc::mbar_init(drain, 2);
+        for (int i = 0; i < kSegs; ++i) {
+            tc::mbar_init(segfull(i), 1);
+            tc::mbar_init(segempty(i), kSoftWarps + kConvWarps + 2);   // each warp that reads it
+        }
         *abort_word = 0;
         tc::mbar_init_fence();
     }
@@ -183,197 +227,238 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     pdl_wait();
     pdl_launch_dependents();
     const Plan plan = plan_of<TcWork>(a, blockIdx.x, gridDim.x, kTcRound, s_sum, s_found);
-    Walk walk;
-    walk.at = blockIdx.x * plan.share;
-    walk.stop = min(plan.total, walk.at + plan.share);
-    walk.base = plan.base;
-    walk.b = plan.b;
     bool run = true;
+    uint32_t n_seg = 0;
+    // The next segment: of a whole warp, or of its one working thread.  False: none, or given up.
+    auto next_seg = [&](Segment &s) -> bool {
+        const uint32_t i = n_seg % kSegs, par = (n_seg / kSegs) & 1;
+        ++n_seg;
+        if (!wait_bar(segfull(i), par, abort_word)) return false;
+        s = segs[i];
+        __syncwarp();
+        if (lane == 0) arrive(segempty(i));
+        return s.rows > 0;
+    };
+    auto next_seg_one = [&](Segment &s) -> bool {
+        const uint32_t i = n_seg % kSegs, par = (n_seg / kSegs) & 1;
+        ++n_seg;
+        if (!wait_one(segfull(i), par, abort_word)) return false;
+        s = segs[i];
+        arrive(segempty(i));
+        return s.rows > 0;
+    };
 
-    if (warp == kMmaWarp) {
-        // ---- every MMA: S of the next key tile goes out behind P V of this one
-        constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, kTcKeys, false, false);
-        constexpr uint32_t idesc_o = tc::idesc_f16_f32(128, D, false, true);
-        const uint64_t dq = tc::desc_noswizzle(sb + L::OFF_Q, 128, L::GROUP);
-        const uint64_t dk = tc::desc_noswizzle(sb + L::OFF_K, 128, L::GROUP);
-        const uint64_t dv = tc::desc_noswizzle(sb + L::OFF_V, L::GROUP, 128);
-        uint32_t nk = 0, segs[2] = {0, 0}, np[2] = {0, 0};   // key tiles, segments and P tiles so far
-        auto issue_s = [&](int sub, uint32_t tile, bool first) -> bool {
-            if (first && !wait_bar(qfull(sub), segs[sub]++ & 1, abort_word)) return false;
-            if (!wait_bar(kfull(tile & 1), (tile >> 1) & 1, abort_word)) return false;
-            tc::fence_after();
-            if (lane == 0) {
-                const uint64_t q = tc::desc_at(dq, sub * L::Q), k = tc::desc_at(dk, (tile & 1) * L::KV);
+    if (warp >= kMmaWarp) {
+        // ---- the MMAs, one warp (one thread of it) per sub-tile: the waits and
+        // commits of one overlap the other's products.  S of the next key tile
+        // goes out behind P V of this one, which it may only overwrite then: the
+        // products of one thread run in order.  A sub-tile without rows in the
+        // segment only hands the buffers on.
+        fewer_regs<kMmaRegs>();
+        const int sub = warp - kMmaWarp;
+        if (warp == kMmaWarp + 2 && lane == 0) {
+            // ---- the segments, and one of no rows behind the last
+            Walk walk(a, plan, blockIdx.x);
+            for (bool more = true; more; ++n_seg) {
+                Segment s = {};
+                more = walk.next(a, s);
+                const uint32_t i = n_seg % kSegs;
+                if (!wait_one(segempty(i), ((n_seg / kSegs) & 1) ^ 1, abort_word)) break;
+                segs[i] = s;
+                arrive(segfull(i));
+            }
+        }
+        if (lane == 0 && sub < 2) {
+            constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, kTcKeys, false, false);
+            constexpr uint32_t idesc_o = tc::idesc_f16_f32(128, D, false, true);
+            const uint64_t dq = tc::desc_noswizzle(sb + L::OFF_Q + sub * L::Q, 128, L::GROUP);
+            const uint64_t dk = tc::desc_noswizzle(sb + L::OFF_K, 128, L::GROUP);
+            const uint64_t dv = tc::desc_noswizzle(sb + L::OFF_V, L::GROUP, 128);
+            const uint32_t ts = tmem + L::COL_S + sub * 128, to = tmem + L::COL_O + sub * D;
+            uint32_t nk = 0, nq = 0, np = 0;             // key tiles, segments with this sub-tile, its P tiles so far
+            auto issue_s = [&](uint32_t tile) -> bool {
+                if (!wait_one(kfull(tile & 1), (tile >> 1) & 1, abort_word)) return false;
+                tc::fence_after();
+                const uint64_t k = tc::desc_at(dk, (tile & 1) * L::KV);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    tc::mma_f16(tmem + L::COL_S + sub * 128, tc::desc_at(q, ks * 256), tc::desc_at(k, ks * 256), idesc_s,
-                                ks > 0);
+                    tc::mma_f16(ts, tc::desc_at(dq, ks * 256), tc::desc_at(k, ks * 256), idesc_s, ks > 0);
                 tc::commit(sfull(sub));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto issue_o = [&](int sub, uint32_t tile, bool first) -> bool {
-            if (!wait_bar(pfull(sub), np[sub]++ & 1, abort_word)) return false;
-            if (!wait_bar(vfull(tile & 1), (tile >> 1) & 1, abort_word)) return false;
-            tc::fence_after();
-            if (lane == 0) {
+                tc::commit(kempty(tile & 1));
+                return true;
+            };
+            auto issue_o = [&](uint32_t tile, bool first) -> bool {
+                if (!wait_one(vfull(tile & 1), (tile >> 1) & 1, abort_word)) return false;
+                if (!wait_one(pfull(sub), np++ & 1, abort_word)) return false;
+                tc::fence_after();
                 const uint64_t v = tc::desc_at(dv, (tile & 1) * L::KV);
 #pragma unroll
                 for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                    tc::mma_f16_ta(tmem + L::COL_O + sub * D, tmem + L::COL_S + sub * 128 + ks * 8,
-                                   tc::desc_at(v, ks * 2 * L::GROUP), idesc_o, !first || ks > 0);
+                    tc::mma_f16_ta(to, ts + ks * 8, tc::desc_at(v, ks * 2 * L::GROUP), idesc_o, !first || ks > 0);
                 tc::commit(ofull(sub));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto release = [&](uint32_t bar) {
-            if (lane == 0) tc::commit(bar);
-            __syncwarp();
-        };
-        Segment seg;
-        bool more = walk.next(a, seg);
-        int active = 0;
-        if (more) {
-            active = seg.rows - seg.pl.r0 > 128 ? 2 : 1;
-            for (int sub = 0; run && sub < active; ++sub) run = issue_s(sub, nk, true);
-            release(kempty(0));
-        }
-        while (run && more) {
-            const int n = seg.tb - seg.pl.tile, subs = active;
-            for (int j = 0; run && j < n; ++j, ++nk) {
-                const bool last = j == n - 1;
-                if (!last) {
-                    for (int sub = 0; run && sub < subs; ++sub)
-                        run = issue_o(sub, nk, j == 0) && issue_s(sub, nk + 1, false);
-                    release(vempty(nk & 1));
-                    release(kempty((nk + 1) & 1));
-                } else {
-                    for (int sub = 0; run && sub < subs; ++sub) run = issue_o(sub, nk, j == 0);
-                    release(vempty(nk & 1));
-                    more = walk.next(a, seg);
-                    if (run && more) {
-                        active = seg.rows - seg.pl.r0 > 128 ? 2 : 1;
-                        for (int sub = 0; run && sub < active; ++sub) run = issue_s(sub, nk + 1, true);
-                        release(kempty((nk + 1) & 1));
+                tc::commit(vempty(tile & 1));
+                return true;
+            };
+            // a segment without this sub-tile: its buffers count as read once they are filled
+            auto pass = [&](uint32_t tile, uint32_t full, uint32_t empty) -> bool {
+                if (!wait_one(full, (tile >> 1) & 1, abort_word)) return false;
+                arrive(empty);
+                return true;
+            };
+            Segment seg;
+            bool more = next_seg_one(seg), started = false;
+            while (run && more) {
+                const int n = seg.tb - seg.pl.tile;
+                const bool takes = sub == 0 || seg.rows - seg.pl.r0 > 128;
+                if (takes && !started) run = wait_one(qfull(sub), nq++ & 1, abort_word) && issue_s(nk);
+                if (!takes && !started) run = pass(nk, kfull(nk & 1), kempty(nk & 1));
+                bool next_takes = takes;
+                for (int j = 0; run && j < n; ++j, ++nk) {
+                    const bool last = j == n - 1;
+                    run = takes ? issue_o(nk, j == 0) : pass(nk, vfull(nk & 1), vempty(nk & 1));
+                    if (!run) break;
+                    if (last) {
+                        more = next_seg_one(seg);
+                        if (!more) continue;
+                        next_takes = sub == 0 || seg.rows - seg.pl.r0 > 128;
+                        if (next_takes && !wait_one(qfull(sub), nq++ & 1, abort_word)) {
+                            run = false;
+                            break;
+                        }
                     }
+                    run = next_takes ? issue_s(nk + 1) : pass(nk + 1, kfull((nk + 1) & 1), kempty((nk + 1) & 1));
                 }
+                started = true;
             }
+            tc::commit(drain);                           // products still in flight end before the tensor memory is given back
         }
+        __syncwarp();
     } else if (warp >= kSoftWarps) {
         // ---- codes -> f16 tiles.  A warp takes 32 keys of a tile; lane = (row of
         // 8, 16-byte chunk), so a quarter-warp's stores fill a core matrix.
         // Scales go to a ring of kMetas: tile j + 4's are written once V of tile j + 3
         // is, for which P V of tile j + 1 had to be done, so both softmaxes are past
         // tile j and its slot is free.
-        constexpr int CH = D / 64, N = 4 * CH;           // 64-byte column groups, loads per thread and operand
+        fewer_regs<kConvRegs>();
+        constexpr int CH = D / 64, N = 4 * CH;           // 64-byte column groups, 16-byte pieces per thread and operand
         const int cw = warp - kSoftWarps, row = lane & 7, chunk = lane >> 3;
         uint32_t nt = 0;
         Segment ahead;
-        uint4 kc[N], vc[N];
         float sc[2][2] = {};
         uint32_t miss = 0;
         int tile_ahead = 0;
-        bool have = walk.next(a, ahead);
-        int32_t blk[2];
-        auto blocks = [&]() {                            // block ids of this warp's two 16-key groups of the tile ahead
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int key = ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * u;
-                blk[u] = key < ahead.rq.kv ? a.table[ahead.b * a.table_stride + key / a.S] : -1;
-            }
-        };
-        int64_t off[2];
+        bool have = next_seg(ahead);
+        // lane = (tile lane / 2, 16-key group lane % 2) of 16 tiles: block id and scales
+        int32_t blk = -1;
+        float bks = 0.0f, bvs = 0.0f;
+        int batch = -1;                                  // first tile of the 16, -1: none
+        int64_t off[2] = {-1, -1};
         auto offsets = [&]() {
+            if (batch < 0 || tile_ahead >= batch + 16) {
+                batch = tile_ahead;
+                const int key = ahead.key0 + (batch + (lane >> 1)) * kTcKeys + 32 * cw + 16 * (lane & 1);
+                const bool there = batch + (lane >> 1) < ahead.tb && key < ahead.rq.kv;
+                blk = there ? a.table[ahead.b * a.table_stride + key / a.S] : -1;
+                if (blk < 0 || blk >= a.n_blocks) {
+                    if (there) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+                    blk = -1;
+                }
+                const int64_t bh = blk < 0 ? 0 : (int64_t)blk * a.Hkv + ahead.pl.h;
+                bks = blk < 0 ? 0.0f : a.k_scale[bh];
+                bvs = blk < 0 ? 0.0f : a.v_scale[bh];
+            }
             miss = 0;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int key = ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * u;
-                const bool there = key < ahead.rq.kv, ok = there && blk[u] >= 0 && blk[u] < a.n_blocks;
-                if (there && !ok && lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
-                if (!ok) miss |= 1u << (2 * cw + u);
-                const int64_t bh = ok ? (int64_t)blk[u] * a.Hkv + ahead.pl.h : 0;
-                sc[u][0] = ok ? a.k_scale[bh] : 0.0f;
-                sc[u][1] = ok ? a.v_scale[bh] : 0.0f;
-                off[u] = ok ? (bh * a.S + key % a.S) * D : -1;
+                const int from = 2 * (tile_ahead - batch) + u, key = ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * u;
+                const int32_t bl = __shfl_sync(ALL, blk, from);
+                sc[u][0] = __shfl_sync(ALL, bks, from);
+                sc[u][1] = __shfl_sync(ALL, bvs, from);
+                if (bl < 0) miss |= 1u << (2 * cw + u);
+                off[u] = bl < 0 ? -1 : (((int64_t)bl * a.Hkv + ahead.pl.h) * a.S + (key & (a.S - 1))) * D;
             }
         };
-        auto fetch = [&](const uint8_t *codes, uint4 (&c)[N]) {
+        // A thread's pieces of the next tile travel into its own places of shared
+        // memory (registers would do, but the softmax has them), so it waits for
+        // its own copies only.
+        const uint32_t stage_k = sb + L::OFF_STAGE + (32 * cw + lane) * 16, stage_v = stage_k + L::KV / 2;
+        auto fetch = [&](uint32_t stage, const uint8_t *codes) {
+            if (have) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int g = i / CH, r = 8 * (g & 1) + row;                 // 8-key group of the warp's 32, row of its 16
-                const int key = ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * (g >> 1) + r;
-                c[i] = make_uint4(0, 0, 0, 0);                               // rows that are not there read as zero
-                if (off[g >> 1] >= 0 && key < ahead.rq.kv)
-                    c[i] = *reinterpret_cast<const uint4 *>(codes + off[g >> 1] + r * D + 64 * (i % CH) + 16 * chunk);
+                for (int i = 0; i < N; ++i) {
+                    const int g = i / CH, r = 8 * (g & 1) + row;             // 8-key group of the warp's 32, row of its 16
+                    const int key = ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * (g >> 1) + r;
+                    const bool there = off[g >> 1] >= 0 && key < ahead.rq.kv;
+                    const int64_t at = there ? off[g >> 1] + r * D + 64 * (i % CH) + 16 * chunk : 0;
+                    cp_async16(stage + i * 2048, codes + at, there ? 16 : 0);    // rows that are not there read as zero
+                }
             }
+            cp_async_commit();
         };
-        auto store = [&](uint32_t dst, const uint4 (&c)[N]) {
+        auto store = [&](uint32_t dst, uint32_t stage) {
+            cp_async_wait<1>();                          // all but the newest of the copies
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int g = i / CH;
                 const uint32_t to = dst + (4 * cw + g) * L::GROUP + (8 * (i % CH) + 2 * chunk) * 128 + row * 16;
+                const uint4 c = lds128(stage + i * 2048);
                 uint32_t h[8];
-                e4m3x4_to_f16x2x2(c[i].x, h[0], h[1]);
-                e4m3x4_to_f16x2x2(c[i].y, h[2], h[3]);
-                e4m3x4_to_f16x2x2(c[i].z, h[4], h[5]);
-                e4m3x4_to_f16x2x2(c[i].w, h[6], h[7]);
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + 128), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
+                e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
+                e4m3x4_to_f16x2x2(c.z, h[4], h[5]);
+                e4m3x4_to_f16x2x2(c.w, h[6], h[7]);
+                sts128(to, h[0], h[1], h[2], h[3]);
+                sts128(to + 128, h[4], h[5], h[6], h[7]);
             }
         };
-        auto step = [&]() {                              // the tile after the one ahead
-            if (++tile_ahead >= ahead.tb) {
-                have = walk.next(a, ahead);
-                tile_ahead = ahead.pl.tile;
-            }
-        };
-        if (have) {
-            tile_ahead = ahead.pl.tile;
-            blocks();
-            offsets();
-            fetch(a.k_codes, kc);
-            fetch(a.v_codes, vc);
-        }
-        while (run && have) {
+        tile_ahead = ahead.pl.tile;
+        bool loaded = false;                             // tile nt is on its way
+        while (loaded || have) {
             const int buf = nt & 1;
             const uint32_t par = ((nt >> 1) & 1) ^ 1;
-            if (!wait_bar(kempty(buf), par, abort_word)) break;
-            TileMeta &m = metas[nt % kMetas];
-            if (lane == 0) {
+            if (loaded) {
+                if (!wait_bar(kempty(buf), par, abort_word)) break;
+                TileMeta &m = metas[nt % kMetas];
+                if (lane == 0) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) m.ks[2 * cw + u] = sc[u][0], m.vs[2 * cw + u] = sc[u][1];
-                m.missing[cw] = miss;
-                arrive(mfull(nt % kMetas));
+                    for (int u = 0; u < 2; ++u) m.ks[2 * cw + u] = sc[u][0], m.vs[2 * cw + u] = sc[u][1];
+                    m.missing[cw] = miss;
+                    arrive(mfull(nt % kMetas));
+                }
+                store(sb + L::OFF_K + buf * L::KV, stage_k);
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(kfull(buf));
             }
-            store(sb + L::OFF_K + buf * L::KV, kc);
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(kfull(buf));
-            step();
+            if (have) offsets();
+            fetch(stage_k, a.k_codes);
+            if (loaded) {
+                if (!wait_bar(vempty(buf), par, abort_word)) break;
+                store(sb + L::OFF_V + buf * L::KV, stage_v);
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(vfull(buf));
+                ++nt;
+            }
+            loaded = have;
+            fetch(stage_v, a.v_codes);
             if (have) {
-                blocks();
-                offsets();
-                fetch(a.k_codes, kc);
+                if (++tile_ahead >= ahead.tb) {          // the tile after the one that travels
+                    have = next_seg(ahead);
+                    tile_ahead = ahead.pl.tile;
+                    batch = -1;
+                }
             }
-            if (!wait_bar(vempty(buf), par, abort_word)) break;
-            store(sb + L::OFF_V + buf * L::KV, vc);
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(vfull(buf));
-            if (have) fetch(a.v_codes, vc);
-            ++nt;
         }
     } else {
+        more_regs<kSoftRegs>();
         // ---- softmax: thread = row
         const int sub = warp >> 2, rr = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + L::COL_S + sub * 128, to = tmem + lanes + L::COL_O + sub * D;
         uint32_t nt = 0, ns = 0;                         // key tiles of the CTA so far; of this sub-tile
-        Segment seg, nxt;
-        bool more = walk.next(a, seg);
-        float zf = 0.0f, zf_next = 0.0f;
+        Segment seg;
+        float zf = 0.0f;
         auto load_q = [&](const Segment &s) {            // this thread's row of Q into shared memory, its logit factor
             const int row = s.pl.r0 + 128 * sub + rr;
             const bool real = row < s.rows;
@@ -394,7 +479,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             }
             const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
             const float mul = HALF ? 1.0f : __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            zf_next = fabsf(a.logit_scale) / mul;
+            zf = fabsf(a.logit_scale) / mul;
             const uint32_t flip = a.logit_scale < 0.0f ? 0x80008000u : 0u;   // the sign goes to q: factors are not negative
             const uint32_t dst = sb + L::OFF_Q + sub * L::Q + (rr >> 3) * L::GROUP + (rr & 7) * 16;
 #pragma unroll 4
@@ -409,171 +494,177 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     }
                     w[c] ^= flip;
                 }
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + i * 128), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                sts128(dst + i * 128, w[0], w[1], w[2], w[3]);
             }
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) arrive(qfull(sub));
         };
-        auto takes = [&](const Segment &s) { return sub == 0 || s.rows - s.pl.r0 > 128; };
-        if (more && takes(seg)) load_q(seg);
-        while (run && more) {
-            const int n = seg.tb - seg.pl.tile;
-            bool nxt_more = false;
-            if (!takes(seg)) {
-                nt += n;
-                nxt_more = walk.next(a, nxt);
-                if (nxt_more && takes(nxt)) load_q(nxt);
-            } else {
-                zf = zf_next;
-                const int row = seg.pl.r0 + 128 * sub + rr;
-                const bool real = row < seg.rows;
-                const int tok = real ? row / a.G : 0, hq = seg.pl.h * a.G + (real ? row - tok * a.G : 0);
-                // rows that are not there see everything: they hold no warp back, and are not stored
-                const int pos = real ? max(-1, seg.rq.kv - seg.rq.n + tok) : 0x7FFFFFF0;
-                const int first = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
-                float M = NEG_INF, MV = NEG_INF, l = 0.0f;
-                for (int j = 0; j < n; ++j, ++nt, ++ns) {
-                    if (!wait_bar(mfull(nt % kMetas), (nt / kMetas) & 1, abort_word) ||
-                        !wait_bar(sfull(sub), ns & 1, abort_word)) {
-                        run = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    const TileMeta &m = metas[nt % kMetas];
-                    const int key0 = seg.key0 + (seg.pl.tile + j) * kTcKeys;
-                    const uint32_t missing = m.missing[0] | m.missing[1] | m.missing[2] | m.missing[3];
-                    const int lo = max(first - key0, 0), hi = min(pos + 1 - key0, kTcKeys);
-                    const bool masked = __any_sync(ALL, lo > 0 || hi < kTcKeys || missing != 0);
-                    // does the row see key k of the tile
-                    auto sees = [&](int k) { return k >= lo && k < hi && !((missing >> (k >> 4)) & 1); };
-                    float tz = NEG_INF, tv = NEG_INF;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        tc::tmem_ld32(ts + 32 * c, r);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float vs = m.vs[2 * c + g], f = zf * m.ks[2 * c + g];
-                            float t = NEG_INF;
-                            if (masked) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (sees(32 * c + 16 * g + i)) t = fmaxf(t, __uint_as_float(r[16 * g + i]));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 2)
-                                    t = max3(t, __uint_as_float(r[16 * g + i]), __uint_as_float(r[16 * g + i + 1]));
-                            }
-                            t = t == NEG_INF ? t : t * f;
-                            tz = fmaxf(tz, t);
-                            tv = fmaxf(tv, t + (float)((int)((__float_as_uint(vs) >> 23) & 0xFFu) - 127));
-                        }
-                    }
-                    if (tz > M + kSlack || (M == NEG_INF && tz > M)) {
-                        l *= ex2(M - tz);
-                        M = tz;
-                    }
-                    const bool move = tv > MV + kSlack || (MV == NEG_INF && tv > MV);
-                    const float grow = move ? ex2(MV - tv) : 1.0f;
-                    if (move) MV = tv;
-                    if (j > 0 && __any_sync(ALL, move)) {            // O so far to the new reference, once P V is done
-                        if (!wait_bar(ofull(sub), (ns - 1) & 1, abort_word)) {
-                            run = false;
-                            break;
-                        }
-                        tc::fence_after();
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t r[32];
-                            tc::tmem_ld32(to + 32 * c, r);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * grow);
-                            tc::tmem_st32(to + 32 * c, r);
-                        }
-                    }
-                    const float ref = M == NEG_INF ? 0.0f : M, refv = MV == NEG_INF ? 0.0f : MV;
-                    const float g2 = ex2(ref - refv);
-                    const uint64_t nref = f2(-ref, -ref);
-                    uint64_t sum = f2(0.0f, 0.0f);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32], p[16];
-                        tc::tmem_ld32(ts + 32 * c, r);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float f = zf * m.ks[2 * c + g], w = fminf(m.vs[2 * c + g] * g2, 1e38f);
-                            const uint64_t ff = f2(f, f), ww = f2(w, w);
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 z = un2(fma2(f2u(r[16 * g + i], r[16 * g + i + 1]), ff, nref));
-                                float e0 = ex2(z.x), e1 = ex2(z.y);
-                                if (masked) {
-                                    if (!sees(32 * c + 16 * g + i)) e0 = 0.0f;
-                                    if (!sees(32 * c + 16 * g + i + 1)) e1 = 0.0f;
-                                }
-                                const uint64_t e = f2(e0, e1);
-                                sum = add2(sum, e);
-                                const float2 x = un2(mul2(e, ww));
-                                p[8 * g + i / 2] = pack_f16(x.x, x.y);
-                            }
-                        }
-                        tc::tmem_st16(ts + 16 * c, p);
-                    }
-                    const float2 s2 = un2(sum);
-                    l += s2.x + s2.y;
-                    tc::tmem_st_wait();
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(pfull(sub));
-                }
-                if (!run) break;
-                nxt_more = walk.next(a, nxt);
-                if (nxt_more && takes(nxt)) load_q(nxt);             // Q is free: S of the last tile is done
+        int row = 0, n = 0;                              // this thread's row, the segment's key tiles
+        bool busy = false, real = false, whole = false, first_part = false;
+        int64_t o_row = 0;
+        float M = NEG_INF, MV = NEG_INF, l = 0.0f;
+        for (;;) {
+            Segment nxt;
+            const bool more = next_seg(nxt);
+            const bool takes = more && (sub == 0 || nxt.rows - nxt.pl.r0 > 128);
+            if (takes) load_q(nxt);                      // Q is free: S of the last tile is done
+            if (busy) {                                  // O of the segment before
                 if (!wait_bar(ofull(sub), (ns - 1) & 1, abort_word)) break;
                 tc::fence_after();
-                const bool whole = seg.pl.tile == 0 && seg.tb == seg.pl.tiles;
                 const float ref = M == NEG_INF ? 0.0f : M, refv = MV == NEG_INF ? 0.0f : MV;
                 const float scale = exp2f(refv - ref), inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-                const int64_t o_row = (seg.rq.row0 + tok) * a.Hq + hq;
-                float *part = a.partial_tc + ((2 * (int64_t)blockIdx.x + (seg.pl.tile == 0)) * kTcRows + 128 * sub + rr) * (D + 4);
-#pragma unroll
+                float *part = a.partial_tc + ((2 * (int64_t)blockIdx.x + first_part) * kTcRows + 128 * sub + rr) * (D + 4);
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[32];
+                    __syncwarp();
                     tc::tmem_ld32(to + 32 * c, r);
                     tc::tmem_ld_wait();
-                    if (!real) continue;
-                    if (whole) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = pack_out<HALF>(__uint_as_float(r[2 * i]) * scale * inv, __uint_as_float(r[2 * i + 1]) * scale * inv);
+                    if (real && whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + 32 * c);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                    } else {
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4 *>(part + 32 * c + 4 * i) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                            for (int x = 0; x < 4; ++x)
+                                w[x] = pack_out<HALF>(__uint_as_float(r[i + 2 * x]) * scale * inv,
+                                                      __uint_as_float(r[i + 2 * x + 1]) * scale * inv);
+                            dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (real) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<uint4 *>(part + 32 * c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
                     }
                 }
+                __syncwarp();
                 tc::fence_before();
                 if (real && whole && a.lse)
                     a.lse[o_row] = l > 0.0f || l != l ? (M + log2f(l)) * 0.69314718055994531f : NEG_INF;
                 if (real && !whole) *reinterpret_cast<float4 *>(part + D) = make_float4(M, MV, l, 0.0f);
             }
+            if (!more) break;
             seg = nxt;
-            more = nxt_more;
+            n = seg.tb - seg.pl.tile;
+            busy = takes;
+            if (!busy) {
+                nt += n;
+                continue;
+            }
+            row = seg.pl.r0 + 128 * sub + rr;
+            real = row < seg.rows;
+            const int tok = real ? row / a.G : 0;
+            o_row = (seg.rq.row0 + tok) * a.Hq + seg.pl.h * a.G + (row - tok * a.G);
+            whole = seg.pl.tile == 0 && seg.tb == seg.pl.tiles;
+            first_part = seg.pl.tile == 0;
+            // rows that are not there see everything: they hold no warp back, and are not stored
+            const int pos = real ? max(-1, seg.rq.kv - seg.rq.n + tok) : 0x7FFFFFF0;
+            const int first = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            M = MV = NEG_INF;
+            l = 0.0f;
+            for (int j = 0; j < n; ++j, ++nt, ++ns) {
+                if (!wait_bar(mfull(nt % kMetas), (nt / kMetas) & 1, abort_word) || !wait_bar(sfull(sub), ns & 1, abort_word)) {
+                    run = false;
+                    break;
+                }
+                tc::fence_after();
+                const TileMeta &m = metas[nt % kMetas];
+                const int key0 = seg.key0 + (seg.pl.tile + j) * kTcKeys;
+                const uint32_t missing = m.missing[0] | m.missing[1] | m.missing[2] | m.missing[3];
+                const int lo = max(first - key0, 0), hi = min(pos + 1 - key0, kTcKeys);
+                const bool masked = __any_sync(ALL, lo > 0 || hi < kTcKeys || missing != 0);
+                uint32_t r[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + 32 * c, r[c]);
+                tc::tmem_ld_wait();
+                if (masked) {                                        // scores of keys that the row does not see: -inf
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int l0 = max(lo - 32 * c, 0), h0 = min(hi - 32 * c, 32);
+                        uint32_t seen = h0 <= 0 || l0 >= 32 ? 0u : (0xFFFFFFFFu >> (32 - h0)) & (0xFFFFFFFFu << l0);
+                        if ((missing >> (2 * c)) & 1) seen &= 0xFFFF0000u;
+                        if ((missing >> (2 * c)) & 2) seen &= 0x0000FFFFu;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((seen >> i) & 1)) r[c][i] = 0xff800000u;
+                    }
+                }
+                float tz = NEG_INF, tv = NEG_INF;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t *x = &r[c / 2][16 * (c & 1)];
+                    float t0 = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+                    float t1 = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+#pragma unroll
+                    for (int i = 6; i < 14; i += 4) {
+                        t0 = max3(t0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                        t1 = max3(t1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                    }
+                    const float t = fmaxf(max3(t0, __uint_as_float(x[14]), __uint_as_float(x[15])), t1) * factor(zf, m.ks[c]);
+                    tz = fmaxf(tz, t);
+                    tv = fmaxf(tv, t + (float)((int)((__float_as_uint(m.vs[c]) >> 23) & 0xFFu) - 127));
+                }
+                // a reference moves when the scores exceed it by more than the slack, or at the row's first key
+                const bool up = tz > M + kSlack || (M == NEG_INF && tz > M);
+                const bool upv = tv > MV + kSlack || (MV == NEG_INF && tv > MV);
+                if (__any_sync(ALL, up || upv)) {
+                    if (up) {
+                        l *= ex2(M - tz);
+                        M = tz;
+                    }
+                    const float grow = upv ? ex2(MV - tv) : 1.0f;
+                    if (upv) MV = tv;
+                    if (j > 0 && __any_sync(ALL, upv)) {             // O so far to the new reference, once P V is done
+                        if (!wait_bar(ofull(sub), (ns - 1) & 1, abort_word)) {
+                            run = false;
+                            break;
+                        }
+                        tc::fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < D / 16; ++x) {
+                            uint32_t o[16];
+                            tc::tmem_ld16(to + 16 * x, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * grow);
+                            tc::tmem_st16(to + 16 * x, o);
+                        }
+                    }
+                }
+                const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(ref - (MV == NEG_INF ? 0.0f : MV));
+                const uint64_t nref = f2(-ref, -ref);
+                uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const float f = factor(zf, m.ks[2 * c + g]), w = fminf(m.vs[2 * c + g] * g2, 1e38f);
+                        const uint64_t ff = f2(f, f), ww = f2(w, w);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float2 z = un2(fma2(f2u(r[c][16 * g + i], r[c][16 * g + i + 1]), ff, nref));
+                            const uint64_t e = f2(ex2(z.x), ex2(z.y));
+                            if (i & 2) sum1 = add2(sum1, e);
+                            else sum0 = add2(sum0, e);
+                            const float2 x = un2(mul2(e, ww));
+                            p[8 * g + i / 2] = pack_f16(x.x, x.y);
+                        }
+                    }
+                    tc::tmem_st16(ts + 16 * c, p);
+                }
+                const float2 s2 = un2(add2(sum0, sum1));
+                l += s2.x + s2.y;
+                tc::tmem_st_wait();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(pfull(sub));
+            }
+            if (!run) break;
         }
     }
-    if (*abort_word && warp == kMmaWarp) {
-        // MMAs still in flight end before the tensor memory is given back (bounded)
-        if (lane == 0) tc::commit(drain);
-        tc::mbar_wait(drain, 0, kPolls);
-    }
+    if (warp >= kMmaWarp && warp < kMmaWarp + 2) tc::mbar_wait(drain, 0, 1u << 20);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
