@@ -31,6 +31,7 @@ constexpr int kTcThreads = 512;              // four warpgroups, as the register
 constexpr int kSoftRegs = 184, kConvRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * 128, "register shares exceed the launch's");
 constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after that many naps (ns, ended by the arrival)
+constexpr uint32_t kLockPolls = 1u << 24;
 constexpr float kSlack = 8.0f;               // log2: how far a tile may exceed a reference
 constexpr int kMetas = 4;                    // key tiles whose scales are kept
 
@@ -56,7 +57,7 @@ struct Lay {
     static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * Q, OFF_V = OFF_K + 2 * KV, OFF_STAGE = OFF_V + 2 * KV, OFF_META = OFF_STAGE + KV,
                               OFF_SEG = OFF_META + kMetas * sizeof(TileMeta), OFF_BAR = OFF_SEG + kSegs * sizeof(Segment);
     static constexpr int BARS = 29;
-    static constexpr uint32_t USED = OFF_BAR + BARS * 8 + 8;
+    static constexpr uint32_t USED = OFF_BAR + BARS * 8 + 12;
     static constexpr uint32_t SMEM = USED + 128 > 120 * 1024 ? USED + 128 : 120 * 1024;   // one CTA per SM (TMEM)
     static constexpr uint32_t COL_S = 0, COL_O = 256;    // TMEM columns: S0, S1 (P over them), O0, O1
 };
@@ -109,8 +110,14 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 // Bounded wait of one thread that also gives up once another has raised the
 // abort word; and of a whole warp, every lane of which gets the same answer.
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int *abort_word) {
+    uint32_t ok;                             // most waits are over before they begin: asked without going to sleep
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
     for (uint32_t i = 0; i < kPolls; ++i) {
-        uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
@@ -183,6 +190,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     TileMeta *metas = reinterpret_cast<TileMeta *>(smem + L::OFF_META);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_BAR + L::BARS * 8);
     volatile int *abort_word = reinterpret_cast<volatile int *>(smem + L::OFF_BAR + L::BARS * 8 + 4);
+    unsigned int *tensor_lock = reinterpret_cast<unsigned int *>(smem + L::OFF_BAR + L::BARS * 8 + 8);
     const uint32_t bar0 = sb + L::OFF_BAR;
     auto kfull = [&](int i) { return bar0 + 8u * i; };
     auto kempty = [&](int i) { return bar0 + 8u * (2 + i); };
@@ -217,6 +225,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             tc::mbar_init(segempty(i), kSoftWarps + kConvWarps + 2);   // each warp that reads it
         }
         *abort_word = 0;
+        *tensor_lock = 0;
         tc::mbar_init_fence();
     }
     if (warp == 0) tc::tmem_alloc(tmem_slot, 512);
@@ -249,11 +258,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     };
 
     if (warp >= kMmaWarp) {
-        // ---- the MMAs, one warp (one thread of it) per sub-tile: the waits and
-        // commits of one overlap the other's products.  S of the next key tile
-        // goes out behind P V of this one, which it may only overwrite then: the
-        // products of one thread run in order.  A sub-tile without rows in the
-        // segment only hands the buffers on.
+        // ---- the MMAs, one warp (one thread of it) per sub-tile: the waits of one,
+        // each worth 1.5 products of idle tensor cores, overlap the other's
+        // products.  S of the next key tile goes out behind P V of this one, which it
+        // may only overwrite then: the products of one thread run in order.  The two
+        // take turns by a lock, P V and S at a time: interleaved, both sub-tiles would
+        // get their scores late and at once, and the softmaxes would run side by side
+        // and then the tensor cores alone.  The lock is given up with half of S to
+        // go, so that the other's first product is there when they end.  A sub-tile
+        // without rows in the segment only hands the buffers on.
         fewer_regs<kMmaRegs>();
         const int sub = warp - kMmaWarp;
         if (warp == kMmaWarp + 2 && lane == 0) {
@@ -276,59 +289,85 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             const uint64_t dv = tc::desc_noswizzle(sb + L::OFF_V, L::GROUP, 128);
             const uint32_t ts = tmem + L::COL_S + sub * 128, to = tmem + L::COL_O + sub * D;
             uint32_t nk = 0, nq = 0, np = 0;             // key tiles, segments with this sub-tile, its P tiles so far
-            auto issue_s = [&](uint32_t tile) -> bool {
-                if (!wait_one(kfull(tile & 1), (tile >> 1) & 1, abort_word)) return false;
-                tc::fence_after();
+            auto lock = [&]() -> bool {
+                for (uint32_t i = 0; i < kLockPolls; ++i) {
+                    if (atomicCAS(tensor_lock, 0u, 1u) == 0u) return true;
+                    if (*abort_word) break;
+                }
+                *abort_word = 1;
+                return false;
+            };
+            auto unlock = [&]() { *reinterpret_cast<volatile unsigned int *>(tensor_lock) = 0u; };
+            auto issue_s = [&](uint32_t tile) {
                 const uint64_t k = tc::desc_at(dk, (tile & 1) * L::KV);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    if (ks == D / 32) unlock();
                     tc::mma_f16(ts, tc::desc_at(dq, ks * 256), tc::desc_at(k, ks * 256), idesc_s, ks > 0);
+                }
                 tc::commit(sfull(sub));
                 tc::commit(kempty(tile & 1));
-                return true;
             };
-            auto issue_o = [&](uint32_t tile, bool first) -> bool {
-                if (!wait_one(vfull(tile & 1), (tile >> 1) & 1, abort_word)) return false;
-                if (!wait_one(pfull(sub), np++ & 1, abort_word)) return false;
-                tc::fence_after();
+            auto issue_o = [&](uint32_t tile, bool first) {
                 const uint64_t v = tc::desc_at(dv, (tile & 1) * L::KV);
 #pragma unroll
                 for (int ks = 0; ks < kTcKeys / 16; ++ks)
                     tc::mma_f16_ta(to, ts + ks * 8, tc::desc_at(v, ks * 2 * L::GROUP), idesc_o, !first || ks > 0);
                 tc::commit(ofull(sub));
                 tc::commit(vempty(tile & 1));
+            };
+            auto wait_k = [&](uint32_t tile) { return wait_one(kfull(tile & 1), (tile >> 1) & 1, abort_word); };
+            auto wait_v = [&](uint32_t tile) { return wait_one(vfull(tile & 1), (tile >> 1) & 1, abort_word); };
+            auto wait_q = [&]() { return wait_one(qfull(sub), nq++ & 1, abort_word); };
+            auto wait_p = [&]() { return wait_one(pfull(sub), np++ & 1, abort_word); };
+            // a segment without this sub-tile: its buffers count as read once they are filled
+            auto pass_k = [&](uint32_t tile) -> bool {
+                if (!wait_k(tile)) return false;
+                arrive(kempty(tile & 1));
                 return true;
             };
-            // a segment without this sub-tile: its buffers count as read once they are filled
-            auto pass = [&](uint32_t tile, uint32_t full, uint32_t empty) -> bool {
-                if (!wait_one(full, (tile >> 1) & 1, abort_word)) return false;
-                arrive(empty);
+            auto pass_v = [&](uint32_t tile) -> bool {
+                if (!wait_v(tile)) return false;
+                arrive(vempty(tile & 1));
                 return true;
             };
             Segment seg;
-            bool more = next_seg_one(seg), started = false;
+            bool more = next_seg_one(seg);
             while (run && more) {
                 const int n = seg.tb - seg.pl.tile;
                 const bool takes = sub == 0 || seg.rows - seg.pl.r0 > 128;
-                if (takes && !started) run = wait_one(qfull(sub), nq++ & 1, abort_word) && issue_s(nk);
-                if (!takes && !started) run = pass(nk, kfull(nk & 1), kempty(nk & 1));
-                bool next_takes = takes;
-                for (int j = 0; run && j < n; ++j, ++nk) {
-                    const bool last = j == n - 1;
-                    run = takes ? issue_o(nk, j == 0) : pass(nk, vfull(nk & 1), vempty(nk & 1));
+                // S of the first key tile (P V of the segment before is on its way)
+                if (takes) {
+                    run = wait_q() && wait_k(nk) && lock();
                     if (!run) break;
-                    if (last) {
-                        more = next_seg_one(seg);
-                        if (!more) continue;
-                        next_takes = sub == 0 || seg.rows - seg.pl.r0 > 128;
-                        if (next_takes && !wait_one(qfull(sub), nq++ & 1, abort_word)) {
-                            run = false;
-                            break;
-                        }
-                    }
-                    run = next_takes ? issue_s(nk + 1) : pass(nk + 1, kfull((nk + 1) & 1), kempty((nk + 1) & 1));
+                    tc::fence_after();
+                    issue_s(nk);
+                } else if (!(run = pass_k(nk))) {
+                    break;
                 }
-                started = true;
+                for (int j = 0; run && j < n - 1; ++j, ++nk) {
+                    if (takes) {
+                        run = wait_v(nk) && wait_k(nk + 1) && wait_p() && lock();
+                        if (!run) break;
+                        tc::fence_after();
+                        issue_o(nk, j == 0);
+                        issue_s(nk + 1);
+                    } else {
+                        run = pass_v(nk) && pass_k(nk + 1);
+                    }
+                }
+                if (!run) break;
+                if (takes) {
+                    run = wait_v(nk) && wait_p() && lock();
+                    if (!run) break;
+                    tc::fence_after();
+                    issue_o(nk, n == 1);
+                    unlock();
+                } else if (!(run = pass_v(nk))) {
+                    break;
+                }
+                ++nk;
+                more = next_seg_one(seg);
             }
             tc::commit(drain);                           // products still in flight end before the tensor memory is given back
         }
