@@ -29,13 +29,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
-// Byte offset of 16-byte chunk c of row r in a tile of D-byte rows, swizzled so
-// that the fragment loads below meet every bank once.
-template <int D>
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-    return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
-
 struct StageMeta {
     float ks[2], vs[2];             // scales of the two 16-key halves
     int stored[2];                  // keys of each half that are there

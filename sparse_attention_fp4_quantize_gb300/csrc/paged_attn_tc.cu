@@ -16,8 +16,8 @@
 //   warps 8-11       load codes (a key tile ahead, in registers), convert, store
 //   warp 12          issues every MMA
 // While one sub-tile's softmax runs, the tensor cores have the other's products.
-// The running references M, Mv (paged_attn.cu) move only when a tile exceeds them
-// by more than 2^8, so O in TMEM is rescaled rarely; the weights stay below 2^9.
+// The running references M, Mv (paged_attn.cu) move only when a tile's scores
+// exceed them far enough to matter to f16, so O in TMEM is rescaled rarely.
 #include "paged_attn.cuh"
 #include "tc.cuh"
 
@@ -32,11 +32,13 @@ constexpr int kSoftRegs = 184, kConvRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * 128, "register shares exceed the launch's");
 constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after that many naps (ns, ended by the arrival)
 constexpr uint32_t kLockPolls = 1u << 24;
-constexpr float kSlack = 8.0f;               // log2: how far a tile may exceed a reference
+constexpr float kSlack = 8.0f;               // log2: how far a tile may exceed a reference before it moves
+constexpr float kSpread = 64.0f;             // log2: how far scales may lie apart in the common case
+constexpr float kMostP = 16384.0f, kMostL = 1e30f;   // its bounds on a tile's sum of P (f16 ends at 65504) and gain of l
 constexpr int kMetas = 4;                    // key tiles whose scales are kept
 
 struct TileMeta {
-    float ks[8], vs[8];                      // scales of the 16-key groups
+    float ks[8], vs[8], lg[8], rv[8];        // scales of the 16-key groups; log2 and reciprocal of v's
     uint32_t missing[4];                     // per converting warp: its groups that are not stored (a bit each)
 };
 
@@ -383,69 +385,72 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         const int cw = warp - kSoftWarps, row = lane & 7, chunk = lane >> 3;
         uint32_t nt = 0;
         Segment ahead;
-        float sc[2][2] = {};
-        uint32_t miss = 0;
         int tile_ahead = 0;
         bool have = next_seg(ahead);
-        // lane = (tile lane / 2, 16-key group lane % 2) of 16 tiles: block id and scales
-        int32_t blk = -1;
-        float bks = 0.0f, bvs = 0.0f;
-        int batch = -1;                                  // first tile of the 16, -1: none
-        int64_t off[2] = {-1, -1};
+        // lane = (tile lane / 2, 16-key group lane % 2) of 16 tiles: code offset (-1: not stored) and scales
+        int64_t boff = -1;
+        float bks = 0.0f, bvs = 0.0f, blg = 0.0f, brv = 0.0f;
+        uint32_t bmiss = 0;
+        int batch = -1, cur = 0;                         // first tile of the 16 (-1: none), the one to be stored next
+        int64_t off[2] = {0, 0};
+        int rows[2] = {0, 0};                            // stored rows of the two groups
         auto offsets = [&]() {
             if (batch < 0 || tile_ahead >= batch + 16) {
                 batch = tile_ahead;
                 const int key = ahead.key0 + (batch + (lane >> 1)) * kTcKeys + 32 * cw + 16 * (lane & 1);
                 const bool there = batch + (lane >> 1) < ahead.tb && key < ahead.rq.kv;
-                blk = there ? a.table[ahead.b * a.table_stride + key / a.S] : -1;
-                if (blk < 0 || blk >= a.n_blocks) {
-                    if (there) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
-                    blk = -1;
-                }
-                const int64_t bh = blk < 0 ? 0 : (int64_t)blk * a.Hkv + ahead.pl.h;
-                bks = blk < 0 ? 0.0f : a.k_scale[bh];
-                bvs = blk < 0 ? 0.0f : a.v_scale[bh];
+                const int32_t blk = there ? a.table[ahead.b * a.table_stride + key / a.S] : -1;
+                const bool ok = blk >= 0 && blk < a.n_blocks;
+                if (there && !ok) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+                const int64_t bh = ok ? (int64_t)blk * a.Hkv + ahead.pl.h : 0;
+                boff = ok ? (bh * a.S + (key & (a.S - 1))) * D : -1;
+                bks = ok ? a.k_scale[bh] : 0.0f;
+                bvs = ok ? a.v_scale[bh] : 0.0f;
+                blg = log2f(bvs);
+                brv = 1.0f / bvs;
+                bmiss = __ballot_sync(ALL, !ok);
             }
-            miss = 0;
+            cur = tile_ahead - batch;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int from = 2 * (tile_ahead - batch) + u, key = ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * u;
-                const int32_t bl = __shfl_sync(ALL, blk, from);
-                sc[u][0] = __shfl_sync(ALL, bks, from);
-                sc[u][1] = __shfl_sync(ALL, bvs, from);
-                if (bl < 0) miss |= 1u << (2 * cw + u);
-                off[u] = bl < 0 ? -1 : (((int64_t)bl * a.Hkv + ahead.pl.h) * a.S + (key & (a.S - 1))) * D;
+                const int64_t at = __shfl_sync(ALL, boff, 2 * cur + u);
+                const int left = ahead.rq.kv - (ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * u);
+                rows[u] = at < 0 ? 0 : min(left, 16);
+                off[u] = at < 0 ? 0 : at;
             }
         };
-        // A thread's pieces of the next tile travel into its own places of shared
-        // memory (registers would do, but the softmax has them), so it waits for
-        // its own copies only.
-        const uint32_t stage_k = sb + L::OFF_STAGE + (32 * cw + lane) * 16, stage_v = stage_k + L::KV / 2;
+        // The next tile's rows travel into the warp's own part of shared memory
+        // (registers would do, but the softmax has them): whole rows per copy, chunks
+        // swizzled, so that copies touch full lines and the reads below every bank.
+        const uint32_t stage_k = sb + L::OFF_STAGE + cw * 32 * D, stage_v = stage_k + L::KV / 2;
         auto fetch = [&](uint32_t stage, const uint8_t *codes) {
             if (have) {
+                constexpr int CPR = D / 16, RPI = 32 / CPR;                  // chunks per row, rows per copy
+                const int c = lane % CPR, r0 = lane / CPR;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int g = i / CH, r = 8 * (g & 1) + row;             // 8-key group of the warp's 32, row of its 16
-                    const int key = ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * (g >> 1) + r;
-                    const bool there = off[g >> 1] >= 0 && key < ahead.rq.kv;
-                    const int64_t at = there ? off[g >> 1] + r * D + 64 * (i % CH) + 16 * chunk : 0;
-                    cp_async16(stage + i * 2048, codes + at, there ? 16 : 0);    // rows that are not there read as zero
+                    const int u = i / (N / 2), r = (i % (N / 2)) * RPI + r0; // 16-key group, row of it
+                    const bool there = r < rows[u];                          // rows that are not there read as zero
+                    cp_async16(stage + chunk_at<D>(16 * u + r, c), codes + (there ? off[u] + r * D + 16 * c : 0), there ? 16 : 0);
                 }
             }
             cp_async_commit();
         };
         auto store = [&](uint32_t dst, uint32_t stage) {
             cp_async_wait<1>();                          // all but the newest of the copies
+            __syncwarp();
+            uint4 c[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) c[i] = lds128(stage + chunk_at<D>(8 * (i / CH) + row, 4 * (i % CH) + chunk));
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int g = i / CH;
                 const uint32_t to = dst + (4 * cw + g) * L::GROUP + (8 * (i % CH) + 2 * chunk) * 128 + row * 16;
-                const uint4 c = lds128(stage + i * 2048);
                 uint32_t h[8];
-                e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
-                e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
-                e4m3x4_to_f16x2x2(c.z, h[4], h[5]);
-                e4m3x4_to_f16x2x2(c.w, h[6], h[7]);
+                e4m3x4_to_f16x2x2(c[i].x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(c[i].y, h[2], h[3]);
+                e4m3x4_to_f16x2x2(c[i].z, h[4], h[5]);
+                e4m3x4_to_f16x2x2(c[i].w, h[6], h[7]);
                 sts128(to, h[0], h[1], h[2], h[3]);
                 sts128(to + 128, h[4], h[5], h[6], h[7]);
             }
@@ -456,20 +461,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             const int buf = nt & 1;
             const uint32_t par = ((nt >> 1) & 1) ^ 1;
             if (loaded) {
-                if (!wait_bar(kempty(buf), par, abort_word)) break;
                 TileMeta &m = metas[nt % kMetas];
-                if (lane == 0) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) m.ks[2 * cw + u] = sc[u][0], m.vs[2 * cw + u] = sc[u][1];
-                    m.missing[cw] = miss;
-                    arrive(mfull(nt % kMetas));
+                if ((lane >> 1) == cur) {                // the lanes with the tile's scales
+                    const int u = 2 * cw + (lane & 1);
+                    m.ks[u] = bks, m.vs[u] = bvs, m.lg[u] = blg, m.rv[u] = brv;
+                    if (!(lane & 1)) m.missing[cw] = ((bmiss >> lane) & 3) << (2 * cw);
                 }
+                __syncwarp();
+                if (lane == 0) arrive(mfull(nt % kMetas));
+            }
+            if (have) offsets();
+            if (loaded) {
+                if (!wait_bar(kempty(buf), par, abort_word)) break;
                 store(sb + L::OFF_K + buf * L::KV, stage_k);
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive(kfull(buf));
             }
-            if (have) offsets();
             fetch(stage_k, a.k_codes);
             if (loaded) {
                 if (!wait_bar(vempty(buf), par, abort_word)) break;
@@ -613,41 +621,87 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 const uint32_t missing = m.missing[0] | m.missing[1] | m.missing[2] | m.missing[3];
                 const int lo = max(first - key0, 0), hi = min(pos + 1 - key0, kTcKeys);
                 const bool masked = __any_sync(ALL, lo > 0 || hi < kTcKeys || missing != 0);
-                uint32_t r[4][32];
+                // scores of the keys 32 c .. 32 c + 31 that the row does not see: -inf
+                auto hide = [&](int c, uint32_t (&r)[32]) {
+                    const int l0 = max(lo - 32 * c, 0), h0 = min(hi - 32 * c, 32);
+                    uint32_t seen = h0 <= 0 || l0 >= 32 ? 0u : (0xFFFFFFFFu >> (32 - h0)) & (0xFFFFFFFFu << l0);
+                    if ((missing >> (2 * c)) & 1) seen &= 0xFFFF0000u;
+                    if ((missing >> (2 * c)) & 2) seen &= 0x0000FFFFu;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + 32 * c, r[c]);
-                tc::tmem_ld_wait();
-                if (masked) {                                        // scores of keys that the row does not see: -inf
+                    for (int i = 0; i < 32; ++i)
+                        if (!((seen >> i) & 1)) r[i] = 0xff800000u;
+                };
+                // The common case, one exponential and no maximum: with the references as
+                // they are, P = 2^(s f + log2 vs - Mv), and l gains sum P / vs 2^(Mv - M).
+                // It stands unless the sum of a row's P shows that one may leave f16, or
+                // a scale is so far from the others that P would not carry its keys' part
+                // of l; P goes to TMEM when that is known.
+                bool fast = false;
+                {
+                    const float4 lg0 = *reinterpret_cast<const float4 *>(m.lg), lg1 = *reinterpret_cast<const float4 *>(m.lg + 4);
+                    const float least = fminf(fminf(fminf(lg0.x, lg0.y), fminf(lg0.z, lg0.w)), fminf(fminf(lg1.x, lg1.y), fminf(lg1.z, lg1.w)));
+                    const float most = fmaxf(fmaxf(fmaxf(lg0.x, lg0.y), fmaxf(lg0.z, lg0.w)), fmaxf(fmaxf(lg1.x, lg1.y), fmaxf(lg1.z, lg1.w)));
+                    fast = __all_sync(ALL, !masked && M - MV + least > -kSpread && M - MV + most < kSpread);
+                }
+                if (fast) {
+                    const float back = ex2(MV - M);
+                    uint32_t p[4][16];
+                    float gain = 0.0f, total = 0.0f;
+                    uint32_t r[2][32];
+                    tc::tmem_ld32(ts, r[0]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int l0 = max(lo - 32 * c, 0), h0 = min(hi - 32 * c, 32);
-                        uint32_t seen = h0 <= 0 || l0 >= 32 ? 0u : (0xFFFFFFFFu >> (32 - h0)) & (0xFFFFFFFFu << l0);
-                        if ((missing >> (2 * c)) & 1) seen &= 0xFFFF0000u;
-                        if ((missing >> (2 * c)) & 2) seen &= 0x0000FFFFu;
+                        tc::tmem_ld_wait();
+                        if (c < 3) tc::tmem_ld32(ts + 32 * (c + 1), r[(c + 1) & 1]);
+                        const float2 ks = *reinterpret_cast<const float2 *>(&m.ks[2 * c]), lg = *reinterpret_cast<const float2 *>(&m.lg[2 * c]),
+                                     rv = *reinterpret_cast<const float2 *>(&m.rv[2 * c]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((seen >> i) & 1)) r[c][i] = 0xff800000u;
+                        for (int g = 0; g < 2; ++g) {
+                            const float f = factor(zf, g ? ks.y : ks.x), at = (g ? lg.y : lg.x) - MV;
+                            const uint64_t ff = f2(f, f), aa = f2(at, at);
+                            uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 z = un2(fma2(f2u(r[c & 1][16 * g + i], r[c & 1][16 * g + i + 1]), ff, aa));
+                                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                                if (i & 2) sum1 = add2(sum1, f2(e0, e1));
+                                else sum0 = add2(sum0, f2(e0, e1));
+                                p[c][8 * g + i / 2] = pack_f16(e0, e1);
+                            }
+                            const float2 x = un2(add2(sum0, sum1));
+                            const float y = x.x + x.y;
+                            total += y;
+                            gain += y * (g ? rv.y : rv.x);
+                        }
+                    }
+                    fast = __all_sync(ALL, total < kMostP && gain * back < kMostL);
+                    if (fast) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tc::tmem_st16(ts + 16 * c, p[c]);
+                        l += gain * back;
                     }
                 }
-                float tz = NEG_INF, tv = NEG_INF;
+                if (!fast) {
+                    float tz = NEG_INF, tv = NEG_INF;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tc::tmem_ld32(ts + 32 * c, r);
+                        tc::tmem_ld_wait();
+                        if (masked) hide(c, r);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t *x = &r[c / 2][16 * (c & 1)];
-                    float t0 = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-                    float t1 = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+                        for (int g = 0; g < 2; ++g) {
+                            float t = __uint_as_float(r[16 * g]);
 #pragma unroll
-                    for (int i = 6; i < 14; i += 4) {
-                        t0 = max3(t0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                        t1 = max3(t1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                            for (int i = 1; i < 15; i += 2) t = max3(t, __uint_as_float(r[16 * g + i]), __uint_as_float(r[16 * g + i + 1]));
+                            t = fmaxf(t, __uint_as_float(r[16 * g + 15])) * factor(zf, m.ks[2 * c + g]);
+                            tz = fmaxf(tz, t);
+                            tv = fmaxf(tv, t + (float)((int)((__float_as_uint(m.vs[2 * c + g]) >> 23) & 0xFFu) - 127));
+                        }
                     }
-                    const float t = fmaxf(max3(t0, __uint_as_float(x[14]), __uint_as_float(x[15])), t1) * factor(zf, m.ks[c]);
-                    tz = fmaxf(tz, t);
-                    tv = fmaxf(tv, t + (float)((int)((__float_as_uint(m.vs[c]) >> 23) & 0xFFu) - 127));
-                }
-                // a reference moves when the scores exceed it by more than the slack, or at the row's first key
-                const bool up = tz > M + kSlack || (M == NEG_INF && tz > M);
-                const bool upv = tv > MV + kSlack || (MV == NEG_INF && tv > MV);
-                if (__any_sync(ALL, up || upv)) {
+                    // a reference moves when the scores exceed it by more than the slack, or at the row's first key
+                    const bool up = tz > M + kSlack || (M == NEG_INF && tz > M);
+                    const bool upv = tv > MV + kSlack || (MV == NEG_INF && tv > MV);
                     if (up) {
                         l *= ex2(M - tz);
                         M = tz;
@@ -670,31 +724,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                             tc::tmem_st16(to + 16 * x, o);
                         }
                     }
-                }
-                const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(ref - (MV == NEG_INF ? 0.0f : MV));
-                const uint64_t nref = f2(-ref, -ref);
-                uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
+                    const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(ref - (MV == NEG_INF ? 0.0f : MV));
+                    const uint64_t nref = f2(-ref, -ref);
+                    uint64_t sum = f2(0.0f, 0.0f);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32], p[16];
+                        tc::tmem_ld32(ts + 32 * c, r);
+                        tc::tmem_ld_wait();
+                        if (masked) hide(c, r);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
+                        for (int g = 0; g < 2; ++g) {
+                            const float f = factor(zf, m.ks[2 * c + g]), w = fminf(m.vs[2 * c + g] * g2, 1e38f);
+                            const uint64_t ff = f2(f, f), ww = f2(w, w);
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float f = factor(zf, m.ks[2 * c + g]), w = fminf(m.vs[2 * c + g] * g2, 1e38f);
-                        const uint64_t ff = f2(f, f), ww = f2(w, w);
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float2 z = un2(fma2(f2u(r[c][16 * g + i], r[c][16 * g + i + 1]), ff, nref));
-                            const uint64_t e = f2(ex2(z.x), ex2(z.y));
-                            if (i & 2) sum1 = add2(sum1, e);
-                            else sum0 = add2(sum0, e);
-                            const float2 x = un2(mul2(e, ww));
-                            p[8 * g + i / 2] = pack_f16(x.x, x.y);
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 z = un2(fma2(f2u(r[16 * g + i], r[16 * g + i + 1]), ff, nref));
+                                const uint64_t e = f2(ex2(z.x), ex2(z.y));
+                                sum = add2(sum, e);
+                                const float2 x = un2(mul2(e, ww));
+                                p[8 * g + i / 2] = pack_f16(x.x, x.y);
+                            }
                         }
+                        tc::tmem_st16(ts + 16 * c, p);
                     }
-                    tc::tmem_st16(ts + 16 * c, p);
+                    const float2 s2 = un2(sum);
+                    l += s2.x + s2.y;
                 }
-                const float2 s2 = un2(add2(sum0, sum1));
-                l += s2.x + s2.y;
                 tc::tmem_st_wait();
                 tc::fence_before();
                 __syncwarp();
