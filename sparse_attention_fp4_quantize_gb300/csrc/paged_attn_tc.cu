@@ -28,7 +28,7 @@ constexpr int kSoftWarps = 8, kConvWarps = 4, kMmaWarp = kSoftWarps + kConvWarps
 constexpr int kTcThreads = 512;              // four warpgroups, as the register shares go by warpgroup
 // Registers per thread: 512 x 128 at launch; the softmax warpgroups, which hold
 // a row's 128 scores, take what the others give up.
-constexpr int kSoftRegs = 184, kConvRegs = 80, kMmaRegs = 64;
+constexpr int kSoftRegs = 176, kConvRegs = 80, kMmaRegs = 80;
 static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * 128, "register shares exceed the launch's");
 constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after that many naps (ns, ended by the arrival)
 constexpr uint32_t kLockPolls = 1u << 24;
@@ -506,42 +506,58 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         uint32_t nt = 0, ns = 0;                         // key tiles of the CTA so far; of this sub-tile
         Segment seg;
         float zf = 0.0f;
-        auto load_q = [&](const Segment &s) {            // this thread's row of Q into shared memory, its logit factor
-            const int row = s.pl.r0 + 128 * sub + rr;
-            const bool real = row < s.rows;
-            const int tok = real ? row / a.G : 0, hq = s.pl.h * a.G + (real ? row - tok * a.G : 0);
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (s.rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride);
-            float top = 0.0f;
-            if (!HALF) {                                 // read twice, the second time from L1: registers are scarce
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = real ? src[i] : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        // The warp's 32 rows of Q into shared memory; zf: the logit factor of this
+        // thread's row.  A load takes 64 bytes of 8 rows (lane % 8 the row), so that a
+        // quarter-warp's stores fill a core matrix.
+        auto load_q = [&](const Segment &s) {
+            constexpr int CH = D / 32;                   // 16-byte chunks of a row per lane
+            const int r8 = lane & 7, c4 = lane >> 3, w0 = s.pl.r0 + 128 * sub + 32 * (warp & 3);
+            uint4 v[4][CH];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 f = unpack_in<HALF>(w[c]);
-                        top = max3(top, fabsf(f.x), fabsf(f.y));
-                    }
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int row = w0 + 8 * i + r8;
+                const bool real = row < s.rows;
+                const int tok = real ? row / a.G : 0, hq = s.pl.h * a.G + (real ? row - tok * a.G : 0);
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (s.rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride) + c4;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) v[i][c] = real ? src[4 * c] : make_uint4(0, 0, 0, 0);
             }
-            const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-            const float mul = HALF ? 1.0f : __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            zf = fabsf(a.logit_scale) / mul;
             const uint32_t flip = a.logit_scale < 0.0f ? 0x80008000u : 0u;   // the sign goes to q: factors are not negative
-            const uint32_t dst = sb + L::OFF_Q + sub * L::Q + (rr >> 3) * L::GROUP + (rr & 7) * 16;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 v = real ? src[i] : make_uint4(0, 0, 0, 0);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t dst = sb + L::OFF_Q + sub * L::Q + 4 * (warp & 3) * L::GROUP + c4 * 128 + r8 * 16;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (!HALF) {
-                        const float2 f = unpack_in<HALF>(w[c]);
-                        w[c] = pack_f16(f.x * mul, f.y * mul);
+            for (int i = 0; i < 4; ++i) {
+                float mul = 1.0f;
+                if (!HALF) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float2 f = unpack_in<HALF>(w[x]);
+                            top = max3(top, fabsf(f.x), fabsf(f.y));
+                        }
                     }
-                    w[c] ^= flip;
+                    top = fmaxf(top, __shfl_xor_sync(ALL, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(ALL, top, 16));
+                    // largest magnitude to [2^14, 2^15); a row below 2^-100 keeps that factor
+                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+                    mul = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
                 }
-                sts128(dst + i * 128, w[0], w[1], w[2], w[3]);
+                if (i == c4) zf = fabsf(a.logit_scale) / mul;    // row 8 i + r8 is this thread's
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if (!HALF) {
+                            const float2 f = unpack_in<HALF>(w[x]);
+                            w[x] = pack_f16(f.x * mul, f.y * mul);
+                        }
+                        w[x] ^= flip;
+                    }
+                    sts128(dst + i * L::GROUP + c * 512, w[0], w[1], w[2], w[3]);
+                }
             }
             tc::fence_async_smem();
             __syncwarp();
@@ -568,16 +584,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     __syncwarp();
                     tc::tmem_ld32(to + 32 * c, r);
                     tc::tmem_ld_wait();
-                    if (real && whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + 32 * c);
+                    if (whole) {
+                        // four lanes exchange their four 16-byte pieces, so that a store takes 64 bytes of 8 rows
+                        uint32_t w[4][4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t w[4];
+                        for (int i = 0; i < 16; ++i)
+                            w[i / 4][i % 4] = pack_out<HALF>(__uint_as_float(r[2 * i]) * scale * inv, __uint_as_float(r[2 * i + 1]) * scale * inv);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                w[x] = pack_out<HALF>(__uint_as_float(r[i + 2 * x]) * scale * inv,
-                                                      __uint_as_float(r[i + 2 * x + 1]) * scale * inv);
-                            dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int d = 1; d < 4; d *= 2)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                if (x & d) continue;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    const bool up = lane & d;
+                                    const uint32_t got = __shfl_xor_sync(ALL, up ? w[x][y] : w[x + d][y], d);
+                                    (up ? w[x][y] : w[x + d][y]) = got;
+                                }
+                            }
+                        // piece x is now row (lane & ~3) + x's, its 16 bytes at lane % 4
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int64_t o = __shfl_sync(ALL, o_row, (lane & ~3) + x);
+                            if (__shfl_sync(ALL, (int)real, (lane & ~3) + x))
+                                *reinterpret_cast<uint4 *>(a.out + o * D + 32 * c + 8 * (lane & 3)) = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
                         }
                     } else if (real) {
 #pragma unroll
