@@ -22,6 +22,8 @@ namespace {
 constexpr int kAttnWarps = 4;
 constexpr int kTileKeys = kSplitKeys;   // keys per warp tile
 constexpr int kStages = 2;          // tiles in flight per warp
+// CTAs that an SM holds at once (registers; 3 x 64 KB of shared memory for 128 channels).
+constexpr int split_per_sm(int NT) { return NT == 4 ? 2 : 3; }
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
@@ -34,113 +36,136 @@ struct StageMeta {
     int stored[2];                  // keys of each half that are there
 };
 
-// A warp's share of the softmax over keys for 16 MT rows: lane (g, t) =
-// (lane / 4, lane % 4) holds rows g and g + 8 of each 16.  Fragment layouts are
-// chosen so that every load of codes is contiguous: in q . k, lane t's part of
-// the contraction is channels [t D/4, (t+1) D/4); in P v, lane g's output
-// columns of the B operand are channels [g D/8, (g+1) D/8), so the accumulators
-// of lane t are channels [t D/4, (t+1) D/4) of its rows.
-template <int D, int MT>
+// 8 x 8 halves, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// A warp's share of the softmax over keys for 8 NT rows.  Both products are
+// computed transposed, S^T = K . Q^T and O^T = V^T . P^T, with the keys and the
+// channels on the 16 rows of an MMA and the query rows on its 8 columns: a decode
+// step's rows (the heads of a group) are few, and 8 fill what 16 would leave half
+// empty.  Lane (g, t) = (lane / 4, lane % 4).  The fragments are chosen so that
+// every load of codes is contiguous:
+//   S^T  A: keys g, g + 8; lane t's part of the contraction is channels
+//        [t D/4, (t+1) D/4).  B: the same channels of query row g.
+//        C: keys g, g + 8 of query rows 2 t, 2 t + 1.
+//   P^T  C transposed 8 x 8 at a time (keys 2 t, 2 t + 1 of query row g).
+//   O^T  A: channels of lane g are [g D/8, (g+1) D/8), interleaved by keys; C: those
+//        channels of query rows 2 t, 2 t + 1.
+template <int D, int NT>
 struct Tile {
     static constexpr int KS = D / 16;                // k-steps of q . k
-    static constexpr int NT = D / 8;                 // n-tiles of P v
-    uint32_t q[MT][KS][4];
-    float o[MT][NT][4];
-    float m[2 * MT], mv[2 * MT], l[2 * MT];          // running maxima (log2), sum of P of this lane's keys
+    static constexpr int MO = D / 16;                // 16-channel tiles of O^T
+    uint32_t q[NT][KS][2];
+    float o[NT][MO][4];
+    float m[NT][2], mv[NT][2], l[NT][2];             // rows 2 t, 2 t + 1: running maxima (log2), sum of P of this lane's keys
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int x = 0; x < NT; ++x) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 2 * MT; ++r) {
-            m[r] = mv[r] = __int_as_float(0xff800000);
-            l[r] = 0.0f;
+            for (int j = 0; j < MO; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.0f;
+            m[x][0] = m[x][1] = mv[x][0] = mv[x][1] = __int_as_float(0xff800000);
+            l[x][0] = l[x][1] = 0.0f;
         }
     }
 
-    // 32 keys from shared memory (codes at kb, vb).  zf: logit factor per row; a
-    // row sees keys [lo, hi) of the 32, as far as they are stored.
-    __device__ __forceinline__ void keys32(uint32_t kb, uint32_t vb, const StageMeta &meta, const float (&zf)[2 * MT],
-                                           const int (&lo)[2 * MT], const int (&hi)[2 * MT]) {
+    // 32 keys from shared memory (codes at kb, vb).  zf: logit factor per row.  With
+    // MASK a row sees keys [lo, hi) of the 32, as far as they are stored; without,
+    // all of them.
+    template <bool MASK>
+    __device__ __forceinline__ void keys32(uint32_t kb, uint32_t vb, const StageMeta &meta, const float (&zf)[NT][2],
+                                           const int (&lo)[NT][2], const int (&hi)[NT][2]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         constexpr uint32_t ALL = 0xFFFFFFFFu;
         const float NEG_INF = __int_as_float(0xff800000);
-        float s[MT][4][4];
+        float s[NT][2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t kw[D / 16];
+        for (int u = 0; u < 2; ++u) {
+            uint32_t kw[2][D / 16];
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const uint4 v = lds128(kb + chunk_at<D>(8 * i + g, t * (D / 64) + c));
-                kw[4 * c] = v.x, kw[4 * c + 1] = v.y, kw[4 * c + 2] = v.z, kw[4 * c + 3] = v.w;
-            }
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int x = 0; x < MT; ++x) s[x][i][0] = s[x][i][1] = s[x][i][2] = s[x][i][3] = 0.0f;
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 v = lds128(kb + chunk_at<D>(16 * u + 8 * h + g, t * (D / 64) + c));
+                    kw[h][4 * c] = v.x, kw[h][4 * c + 1] = v.y, kw[h][4 * c + 2] = v.z, kw[h][4 * c + 3] = v.w;
+                }
+#pragma unroll
+            for (int x = 0; x < NT; ++x) s[x][u][0] = s[x][u][1] = s[x][u][2] = s[x][u][3] = 0.0f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16x2x2(kw[k], b0, b1);
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x2x2(kw[0][k], a0, a2);
+                e4m3x4_to_f16x2x2(kw[1][k], a1, a3);
 #pragma unroll
-                for (int x = 0; x < MT; ++x)
-                    mma_f16_16816(s[x][i], q[x][k][0], q[x][k][1], q[x][k][2], q[x][k][3], b0, b1);
+                for (int x = 0; x < NT; ++x) mma_f16_16816(s[x][u], a0, a1, a2, a3, q[x][k][0], q[x][k][1]);
             }
         }
         const float ve[2] = {(float)((int)((__float_as_uint(meta.vs[0]) >> 23) & 0xFFu) - 127),
                              (float)((int)((__float_as_uint(meta.vs[1]) >> 23) & 0xFFu) - 127)};
-        uint32_t p[MT][4][2];
-        float grow[2 * MT];
+        uint32_t p[NT][2][2];
+        float grow[NT][2];
         bool grew = false;
 #pragma unroll
-        for (int r = 0; r < 2 * MT; ++r) {
-            float z[8], top[2];
+        for (int x = 0; x < NT; ++x) {
+            float w[2][4];                           // [row][16 u + 8 h + g at 2 u + h]
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float f = zf[r] * meta.ks[u];
-                const int end = min(hi[r], 16 * u + meta.stored[u]);
-                top[u] = NEG_INF;
+            for (int r = 0; r < 2; ++r) {
+                float z[4], top[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int u = 0; u < 2; ++u) {
+                    const float f = zf[x][r] * meta.ks[u];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int key = 16 * u + 8 * i + 2 * t + c;
-                        const float v = s[r / 2][2 * u + i][2 * (r & 1) + c] * f;
-                        z[4 * u + 2 * i + c] = key >= lo[r] && key < end ? v : NEG_INF;
-                        top[u] = fmaxf(top[u], z[4 * u + 2 * i + c]);
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = 16 * u + 8 * h + g;
+                        float v = s[x][u][2 * h + r] * f;
+                        if (MASK && !(key >= lo[x][r] && key < hi[x][r] && 8 * h + g < meta.stored[u])) v = NEG_INF;
+                        z[2 * u + h] = v;
                     }
-                top[u] = fmaxf(top[u], __shfl_xor_sync(ALL, top[u], 1));
-                top[u] = fmaxf(top[u], __shfl_xor_sync(ALL, top[u], 2));
-            }
-            const float m1 = fmaxf(m[r], fmaxf(top[0], top[1]));
-            const float mv1 = fmaxf(mv[r], fmaxf(top[0] + ve[0], top[1] + ve[1]));
-            const float ref = m1 == NEG_INF ? 0.0f : m1, refv = mv1 == NEG_INF ? 0.0f : mv1;
-            l[r] *= ex2(m[r] - ref);
-            grow[r] = ex2(mv[r] - refv);
-            grew |= mv1 != mv[r];
-            m[r] = m1, mv[r] = mv1;
-            const float g2 = ex2(ref - refv);
-            float w[8];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float f = fminf(meta.vs[u] * g2, 1e38f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = ex2(z[4 * u + i] - ref);
-                    l[r] += e;
-                    w[4 * u + i] = z[4 * u + i] == NEG_INF ? 0.0f : e * f;
+                    top[u] = fmaxf(z[2 * u], z[2 * u + 1]);
                 }
+                // the row's keys are spread over the 8 lanes of equal t
+                float tz = fmaxf(top[0], top[1]), tv = fmaxf(top[0] + ve[0], top[1] + ve[1]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    tz = fmaxf(tz, __shfl_xor_sync(ALL, tz, d));
+                    if (ve[0] != ve[1]) tv = fmaxf(tv, __shfl_xor_sync(ALL, tv, d));
+                }
+                if (ve[0] == ve[1]) tv = tz + ve[0];
+                const float m1 = fmaxf(m[x][r], tz), mv1 = fmaxf(mv[x][r], tv);
+                const float ref = m1 == NEG_INF ? 0.0f : m1, refv = mv1 == NEG_INF ? 0.0f : mv1;
+                float sum = l[x][r] * ex2(m[x][r] - ref);
+                grow[x][r] = ex2(mv[x][r] - refv);
+                grew |= mv1 != mv[x][r];
+                m[x][r] = m1, mv[x][r] = mv1;
+                const float g2 = ex2(ref - refv);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float f = fminf(meta.vs[u] * g2, 1e38f);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float e = ex2(z[2 * u + h] - ref);
+                        sum += e;
+                        w[r][2 * u + h] = MASK && z[2 * u + h] == NEG_INF ? 0.0f : e * f;
+                    }
+                }
+                l[x][r] = sum;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[r / 2][i][r & 1] = pack_f16(w[2 * i], w[2 * i + 1]);
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) p[x][u][h] = transpose8x8(pack_f16(w[0][2 * u + h], w[1][2 * u + h]));
         }
         if (__any_sync(ALL, grew)) {
 #pragma unroll
-            for (int x = 0; x < MT; ++x)
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[x][j][0] *= grow[2 * x], o[x][j][1] *= grow[2 * x];
-                    o[x][j][2] *= grow[2 * x + 1], o[x][j][3] *= grow[2 * x + 1];
+                for (int j = 0; j < MO; ++j) {
+                    o[x][j][0] *= grow[x][0], o[x][j][1] *= grow[x][1];
+                    o[x][j][2] *= grow[x][0], o[x][j][3] *= grow[x][1];
                 }
         }
 #pragma unroll
@@ -164,9 +189,9 @@ struct Tile {
                 for (int i = 0; i < 4; i += 2)
 #pragma unroll
                     for (int w = 0; w < VW; ++w) {
-                        const uint32_t x = vw[i][w], y = vw[i + 1][w];
-                        vw[i][w] = t & 1 ? y : x;
-                        vw[i + 1][w] = t & 1 ? x : y;
+                        const uint32_t a = vw[i][w], b = vw[i + 1][w];
+                        vw[i][w] = t & 1 ? b : a;
+                        vw[i + 1][w] = t & 1 ? a : b;
                     }
             }
 #pragma unroll
@@ -174,34 +199,33 @@ struct Tile {
                 // bytes of keys (2t, 2t+1) and (2t+8, 2t+9) interleaved: pairs along the keys
                 const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
                 const uint32_t c0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), c1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-                uint32_t b0[4], b1[4];
-                e4m3x4_to_f16x2x2(a0, b0[0], b0[1]);
-                e4m3x4_to_f16x2x2(a1, b0[2], b0[3]);
-                e4m3x4_to_f16x2x2(c0, b1[0], b1[1]);
-                e4m3x4_to_f16x2x2(c1, b1[2], b1[3]);
+                uint32_t lo4[4], hi4[4];             // channels 4 w .. 4 w + 3: the low keys, the high keys
+                e4m3x4_to_f16x2x2(a0, lo4[0], lo4[1]);
+                e4m3x4_to_f16x2x2(a1, lo4[2], lo4[3]);
+                e4m3x4_to_f16x2x2(c0, hi4[0], hi4[1]);
+                e4m3x4_to_f16x2x2(c1, hi4[2], hi4[3]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int x = 0; x < MT; ++x)
-                        mma_f16_16816(o[x][4 * w + c], p[x][2 * u][0], p[x][2 * u][1], p[x][2 * u + 1][0],
-                                      p[x][2 * u + 1][1], b0[c], b1[c]);
+                    for (int x = 0; x < NT; ++x)
+                        mma_f16_16816(o[x][2 * w + c], lo4[2 * c], lo4[2 * c + 1], hi4[2 * c], hi4[2 * c + 1], p[x][u][0], p[x][u][1]);
             }
         }
     }
 };
 
-template <int D, int MT>
+template <int D, int NT>
 constexpr int attn_smem() {
-    constexpr int ring = kAttnWarps * kStages * 2 * kTileKeys * D, merge = kAttnWarps * 16 * (D + 4) * 4;
+    constexpr int ring = kAttnWarps * kStages * 2 * kTileKeys * D, merge = kAttnWarps * 8 * (D + 4) * 4;
     return ring > merge ? ring : merge;
 }
 
-template <int D, int MT, bool HALF>
-__global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_split_kernel(PagedAttnArgs a) {
-    constexpr int R = 16 * MT;
+template <int D, int NT, bool HALF>
+__global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_split_kernel(PagedAttnArgs a) {
+    constexpr int R = 8 * NT;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_st[kAttnWarps][16][3];
+    __shared__ float s_st[kAttnWarps][8][3];
     __shared__ StageMeta s_meta[kAttnWarps][kStages];
     __shared__ int64_t s_sum[kAttnWarps], s_found[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -212,6 +236,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
     const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kAttnWarps, s_sum, s_found);
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
+    if (tid == 0) a.join[blockIdx.x].last = -1;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * 2 * kTileKeys * D);
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
@@ -222,12 +247,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
             // segment: tiles [ta, tb) of one unit
             const Place pl = Work::place(a, rq, at - base);
             const int h = pl.h, r0 = pl.r0, ta = pl.tile, tb = (int)min((int64_t)pl.tiles, ta + (stop - at));
+            if (tid == 0 && ta == 0 && tb < pl.tiles)
+                a.join[blockIdx.x] = {rq.row0, h, r0, rows, (int)((at + pl.tiles - 1) / plan.share), {0, 0}};
             at += tb - ta;
 
-            Tile<D, MT> tile;
-            tile.clear();
-            int pos[2 * MT], first[2 * MT];
-            float zf[2 * MT];
             // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / 2, half lane % 2) of 16 of them
             const int count = tb - ta > warp ? (tb - ta - warp + kAttnWarps - 1) / kAttnWarps : 0;
             const int32_t *table = a.table + b * a.table_stride;
@@ -237,46 +260,55 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
             };
             int32_t block = entry(0), block_next = entry(16);
             float ks = 0.0f, vs = 0.0f;
-            auto scales = [&]() {
-                const bool ok = block >= 0 && block < a.n_blocks;
-                ks = ok ? a.k_scale[(int64_t)block * a.Hkv + h] : 0.0f;
-                vs = ok ? a.v_scale[(int64_t)block * a.Hkv + h] : 0.0f;
+            int64_t off = -1;                        // code offset of the half's first row, -1: not there
+            auto scales = [&](int i) {
+                const int key = key0 + (ta + warp + (i + (lane >> 1)) * kAttnWarps) * kTileKeys + 16 * (lane & 1);
+                const bool there = i + (lane >> 1) < count && key < rq.kv, ok = there && block >= 0 && block < a.n_blocks;
+                if (there && !ok) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+                const int64_t bh = ok ? (int64_t)block * a.Hkv + h : 0;
+                ks = ok ? a.k_scale[bh] : 0.0f;
+                vs = ok ? a.v_scale[bh] : 0.0f;
+                off = ok ? (bh * a.S + (key & (a.S - 1))) * D : -1;
             };
-            scales();
+            scales(0);
             auto issue = [&](int i) {                // start the copy of this warp's tile i
                 if (i < count) {
                     if (i && (i & 15) == 0) {
                         block = block_next;
                         block_next = entry(i + 16);
-                        scales();
+                        scales(i);
                     }
                     const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
                     const uint32_t dst = ring + (i % kStages) * (2 * kTileKeys * D);
                     constexpr int CPR = D / 16, RPI = 32 / CPR;      // chunks per row, rows per instruction
+                    const int c = lane % CPR, r1 = lane / CPR;
+                    const uint32_t who = 2 * (i & 15);
+                    if ((lane >> 1) == (i & 15)) {
+                        StageMeta &m = s_meta[warp][i % kStages];
+                        m.ks[lane & 1] = ks, m.vs[lane & 1] = vs;
+                        m.stored[lane & 1] = off < 0 ? 0 : min(16, rq.kv - key - 16 * (lane & 1));
+                    }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const int who = 2 * (i & 15) + u;
-                        const int32_t bl = __shfl_sync(ALL, block, who);
-                        int stored = min(16, rq.kv - key - 16 * u);
-                        if (bl < 0 || bl >= a.n_blocks) {
-                            if (stored > 0 && lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
-                            stored = 0;
-                        }
-                        stored = max(stored, 0);
-                        if (lane == who) {
-                            StageMeta &m = s_meta[warp][i % kStages];
-                            m.ks[u] = ks, m.vs[u] = vs, m.stored[u] = stored;
-                        }
-                        const int64_t off = stored ? (((int64_t)bl * a.Hkv + h) * a.S + (key + 16 * u) % a.S) * D : 0;
-                        const int c = lane % CPR;
+                        const int64_t from = __shfl_sync(ALL, off, who + u);
+                        const int stored = from < 0 ? 0 : rq.kv - key - 16 * u;
+                        const int64_t lane_at = (from < 0 ? 0 : from) + r1 * D + 16 * c;
+                        const uint8_t *ksrc = a.k_codes + lane_at, *vsrc = a.v_codes + lane_at;
+                        if (stored >= 16) {
 #pragma unroll
-                        for (int x = 0; x < 16 / RPI; ++x) {
-                            const int r = x * RPI + lane / CPR;
-                            const uint32_t n = r < stored ? 16 : 0;          // rows that are not there read as zero
-                            const int64_t src = off + (n ? r * D + c * 16 : 0);
-                            const uint32_t to = dst + chunk_at<D>(16 * u + r, c);
-                            cp_async16(to, a.k_codes + src, n);
-                            cp_async16(to + kTileKeys * D, a.v_codes + src, n);
+                            for (int x = 0; x < 16 / RPI; ++x) {
+                                const uint32_t to = dst + chunk_at<D>(16 * u + x * RPI + r1, c);
+                                cp_async16(to, ksrc + x * RPI * D, 16);
+                                cp_async16(to + kTileKeys * D, vsrc + x * RPI * D, 16);
+                            }
+                        } else {                     // rows that are not there read as zero
+#pragma unroll
+                            for (int x = 0; x < 16 / RPI; ++x) {
+                                const bool there = x * RPI + r1 < stored;
+                                const uint32_t to = dst + chunk_at<D>(16 * u + x * RPI + r1, c);
+                                cp_async16(to, there ? ksrc + x * RPI * D : a.k_codes, there ? 16 : 0);
+                                cp_async16(to + kTileKeys * D, there ? vsrc + x * RPI * D : a.v_codes, there ? 16 : 0);
+                            }
                         }
                     }
                 }
@@ -285,38 +317,53 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
 #pragma unroll
             for (int i = 0; i < kStages - 1; ++i) issue(i);
 
+            Tile<D, NT> tile;
+            tile.clear();
+            int pos[NT][2], first[NT][2];
+            float zf[NT][2];
+            int all_lo = 0, all_hi = 0x7FFFFFFF;     // keys that every real row of this lane sees
 #pragma unroll
-            for (int r = 0; r < 2 * MT; ++r) {
-                const int row = r0 + 16 * (r / 2) + g + 8 * (r & 1);
-                const bool real = row < rows;
-                const int tok = real ? row / a.G : 0, hq = h * a.G + (real ? row - tok * a.G : 0);
-                pos[r] = real ? max(-1, rq.kv - rq.n + tok) : -1;
-                first[r] = a.window > 0 ? max(0, pos[r] - a.window + 1) : 0;
-                const uint16_t *src = a.q + (rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride + t * (D / 4);
-                uint32_t w[D / 8];
-                float top = 0.0f;
+            for (int x = 0; x < NT; ++x) {
+                {                                    // B operand: row g, channels [t D/4, (t+1) D/4)
+                    const int row = r0 + 8 * x + g;
+                    const bool real = row < rows;
+                    const int tok = real ? row / a.G : 0, hq = h * a.G + (real ? row - tok * a.G : 0);
+                    const uint16_t *src = a.q + (rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride + t * (D / 4);
+                    uint32_t w[D / 8];
+                    float top = 0.0f;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (real) v = *reinterpret_cast<const uint4 *>(src + 8 * c);
-                    w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (real) v = *reinterpret_cast<const uint4 *>(src + 8 * c);
+                        w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+                    }
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const float2 f = unpack_in<HALF>(w[c]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(ALL, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(ALL, top, 2));
+                    // largest magnitude to [2^14, 2^15); a row below 2^-100 keeps that factor
+                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+                    const float mul = HALF ? 1.0f : __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                    const float f = a.logit_scale / mul;
+                    zf[x][0] = __shfl_sync(ALL, f, 8 * t);
+                    zf[x][1] = __shfl_sync(ALL, f, 8 * t + 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const float2 f0 = unpack_in<HALF>(w[2 * k]), f1 = unpack_in<HALF>(w[2 * k + 1]);
+                        tile.q[x][k][0] = pack_f16(f0.x * mul, f0.y * mul);
+                        tile.q[x][k][1] = pack_f16(f1.x * mul, f1.y * mul);
+                    }
                 }
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const float2 f = unpack_in<HALF>(w[c]);
-                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-                top = fmaxf(top, __shfl_xor_sync(ALL, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(ALL, top, 2));
-                // largest magnitude to [2^14, 2^15); a row below 2^-100 keeps that factor
-                const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-                const float mul = HALF ? 1.0f : __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                zf[r] = a.logit_scale / mul;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const float2 f0 = unpack_in<HALF>(w[2 * k]), f1 = unpack_in<HALF>(w[2 * k + 1]);
-                    tile.q[r / 2][k][r & 1] = pack_f16(f0.x * mul, f0.y * mul);
-                    tile.q[r / 2][k][2 + (r & 1)] = pack_f16(f1.x * mul, f1.y * mul);
+                for (int r = 0; r < 2; ++r) {        // the lane's rows of S^T and O^T
+                    const int row = r0 + 8 * x + 2 * t + r;
+                    const bool real = row < rows;
+                    pos[x][r] = real ? max(-1, rq.kv - rq.n + row / a.G) : -1;
+                    first[x][r] = a.window > 0 ? max(0, pos[x][r] - a.window + 1) : 0;
+                    if (real) all_lo = max(all_lo, first[x][r]), all_hi = min(all_hi, pos[x][r] + 1);
                 }
             }
             for (int i = 0; i < count; ++i) {
@@ -324,47 +371,48 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
                 cp_async_wait<kStages - 1>();
                 __syncwarp();
                 const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
-                int lo[2 * MT], hi[2 * MT];
+                int lo[NT][2], hi[NT][2];
 #pragma unroll
-                for (int r = 0; r < 2 * MT; ++r) lo[r] = first[r] - key, hi[r] = pos[r] + 1 - key;
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) lo[x][r] = first[x][r] - key, hi[x][r] = pos[x][r] + 1 - key;
                 const uint32_t kb = ring + (i % kStages) * (2 * kTileKeys * D);
-                tile.keys32(kb, kb + kTileKeys * D, s_meta[warp][i % kStages], zf, lo, hi);
+                const StageMeta &meta = s_meta[warp][i % kStages];
+                // rows that are not there may see everything: they are not stored
+                const bool whole = key >= all_lo && key + kTileKeys <= all_hi && meta.stored[0] == 16 && meta.stored[1] == 16;
+                if (__all_sync(ALL, whole)) tile.template keys32<false>(kb, kb + kTileKeys * D, meta, zf, lo, hi);
+                else tile.template keys32<true>(kb, kb + kTileKeys * D, meta, zf, lo, hi);
                 __syncwarp();
             }
             cp_async_wait<0>();
 
-            // the warps' shares meet in shared memory, 16 rows at a time
+            // the warps' shares meet in shared memory, 8 rows at a time
             const bool whole = ta == 0 && tb == pl.tiles;
             float *s_o = reinterpret_cast<float *>(smem);
             constexpr int LD = D + 4;
 #pragma unroll
-            for (int x = 0; x < MT; ++x) {
+            for (int x = 0; x < NT; ++x) {
                 __syncthreads();
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int r = 2 * x + y;
-                    float l = tile.l[r];
-                    l += __shfl_xor_sync(ALL, l, 1);
-                    l += __shfl_xor_sync(ALL, l, 2);
-                    if (t == 0) {
-                        s_st[warp][g + 8 * y][0] = tile.m[r];
-                        s_st[warp][g + 8 * y][1] = tile.mv[r];
-                        s_st[warp][g + 8 * y][2] = l;
-                    }
-                    float *dst = s_o + (warp * 16 + g + 8 * y) * LD + t * (D / 4);
+                for (int r = 0; r < 2; ++r) {
+                    float l = tile.l[x][r];
 #pragma unroll
-                    for (int j = 0; j < D / 8; j += 4) {
-                        *reinterpret_cast<float4 *>(dst + j) = make_float4(tile.o[x][j][2 * y], tile.o[x][j + 1][2 * y],
-                                                                           tile.o[x][j + 2][2 * y], tile.o[x][j + 3][2 * y]);
-                        *reinterpret_cast<float4 *>(dst + D / 8 + j) =
-                            make_float4(tile.o[x][j][2 * y + 1], tile.o[x][j + 1][2 * y + 1], tile.o[x][j + 2][2 * y + 1],
-                                        tile.o[x][j + 3][2 * y + 1]);
+                    for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(ALL, l, d);
+                    if (g == 0) {
+                        s_st[warp][2 * t + r][0] = tile.m[x][r];
+                        s_st[warp][2 * t + r][1] = tile.mv[x][r];
+                        s_st[warp][2 * t + r][2] = l;
                     }
+                    float *dst = s_o + (warp * 8 + 2 * t + r) * LD + g * (D / 8);
+#pragma unroll
+                    for (int j = 0; j < D / 16; j += 2)
+                        *reinterpret_cast<float4 *>(dst + 2 * j) = make_float4(tile.o[x][j][r], tile.o[x][j][2 + r],
+                                                                               tile.o[x][j + 1][r], tile.o[x][j + 1][2 + r]);
                 }
                 __syncthreads();
-                const int y = tid / 8, part = tid % 8, row = r0 + 16 * x + y;
+                const int y = tid / 16, part = tid % 16, row = r0 + 8 * x + y;   // 16 threads per row, D / 16 channels each
                 if (row < rows) {
-                    float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[D / 8];
+                    float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[D / 16];
 #pragma unroll
                     for (int w = 0; w < kAttnWarps; ++w) {
                         M = fmaxf(M, s_st[w][y][0]);
@@ -372,26 +420,29 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
                     }
                     const float ref = M == NEG_INF ? 0.0f : M, refv = MV == NEG_INF ? 0.0f : MV;
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) o[c] = 0.0f;
+                    for (int c = 0; c < D / 16; ++c) o[c] = 0.0f;
 #pragma unroll
                     for (int w = 0; w < kAttnWarps; ++w) {
                         l += s_st[w][y][2] * ex2(s_st[w][y][0] - ref);
                         const float f = ex2(s_st[w][y][1] - refv);
-                        const float *src = s_o + (w * 16 + y) * LD + part * (D / 8);
+                        const float *src = s_o + (w * 8 + y) * LD + part * (D / 16);
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c) o[c] += f * src[c];
+                        for (int c = 0; c < D / 16; c += 4) {
+                            const float4 v = *reinterpret_cast<const float4 *>(src + c);
+                            o[c] += f * v.x, o[c + 1] += f * v.y, o[c + 2] += f * v.z, o[c + 3] += f * v.w;
+                        }
                     }
                     if (whole) {
                         const float f = exp2f(refv - ref);
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c) o[c] *= f;
+                        for (int c = 0; c < D / 16; ++c) o[c] *= f;
                         const int tok = row / a.G;
-                        store_row<D, HALF>(a, (rq.row0 + tok) * a.Hq + h * a.G + row - tok * a.G, part, o, M, l);
+                        store_row<D, HALF, 16>(a, (rq.row0 + tok) * a.Hq + h * a.G + row - tok * a.G, part, o, M, l);
                     } else {
-                        float *dst = a.partial + ((2 * (int64_t)blockIdx.x + (ta == 0)) * R + 16 * x + y) * LD;
+                        float *dst = a.partial + ((2 * (int64_t)blockIdx.x + (ta == 0)) * R + 8 * x + y) * LD;
 #pragma unroll
-                        for (int c = 0; c < D / 8; c += 4)
-                            *reinterpret_cast<float4 *>(dst + part * (D / 8) + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                        for (int c = 0; c < D / 16; c += 4)
+                            *reinterpret_cast<float4 *>(dst + part * (D / 16) + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                         if (part == 0) *reinterpret_cast<float4 *>(dst + D) = make_float4(M, MV, l, 0.0f);
                     }
                 }
@@ -402,141 +453,127 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MT == 1 ? 3 : 2) paged_attn_s
     }
 }
 
-// Joins the partial results of a unit that several CTAs share: the unit that
-// CTA c began and did not finish.  CTA c's part is slot 2 c + 1, those of the
-// CTAs after it slots 2 c'.  A block takes JR rows of the unit; each of its four
-// warps joins every fourth part of them, then the warps' results meet.
-template <int D, bool HALF, typename Work, int JR>
-__device__ __forceinline__ void join_unit(const PagedAttnArgs &a, const float *partial, int c, int ctas, int round, int y0,
-                                          float (*s_o)[16][D + 4], int64_t *s_sum, int64_t *s_found) {
-    constexpr int R = Work::ROWS, LD = D + 4;
+// Joins the parts of the unit that CTA c began and did not finish.  A block takes
+// JR rows of the unit from y0 on; each of its four warps joins every fourth part of
+// them, then the warps' results meet.
+template <int D, bool HALF, int R, int JR>
+__device__ __forceinline__ void join_unit(const PagedAttnArgs &a, const JoinUnit &unit, const float *partial, int c, int y0,
+                                          float (*s_o)[16][D + 4]) {
+    constexpr int LD = D + 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float NEG_INF = __int_as_float(0xff800000);
-    const Plan plan = plan_of<Work>(a, c, ctas, round, s_sum, s_found);
-    const int64_t t0 = c * plan.share, last = min(plan.total, t0 + plan.share) - 1;
-    if (t0 >= plan.total || last + 1 == plan.total) return;
-    int64_t base = plan.base;
-    for (int b = plan.b; b < a.B; ++b) {             // the request of the CTA's last tile
-        const Request rq = request_of(a, b);
-        const int64_t end = base + Work::tiles(a, rq);
-        if (last >= end) {
-            base = end;
-            continue;
-        }
-        const Place pl = Work::place(a, rq, last - base);
-        const int64_t u0 = last - pl.tile, u1 = u0 + pl.tiles;
-        if (u0 < t0 || u1 <= last + 1) return;       // begun by an earlier CTA, or finished by this one
-        const int64_t c1 = (u1 - 1) / plan.share;    // the CTA with the unit's last tile
-        const int rows = rq.n * a.G;
-        constexpr int TPR = 32 / JR, CH = D / TPR;   // threads per row in a warp, channels per thread
-        const int rr = lane / TPR, x0 = (lane % TPR) * CH, in_unit = y0 + rr;
-        float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[CH];
+    const int c1 = unit.last, rows = unit.rows, r0 = unit.r0;
+    if (c1 < 0 || r0 + y0 >= rows) return;
+    constexpr int TPR = 32 / JR, CH = D / TPR;   // threads per row in a warp, channels per thread
+    const int rr = lane / TPR, x0 = (lane % TPR) * CH, in_unit = y0 + rr;
+    float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) o[i] = 0.0f;
-        if (pl.r0 + in_unit < rows) {
-            for (int64_t x = c + warp; x <= c1; x += 4) {
-                const float *src = partial + ((x == c ? 2 * x + 1 : 2 * x) * R + in_unit) * LD;
-                const float4 st = *reinterpret_cast<const float4 *>(src + D);
-                const float M1 = fmaxf(M, st.x), MV1 = fmaxf(MV, st.y);
-                const float ref = M1 == NEG_INF ? 0.0f : M1, refv = MV1 == NEG_INF ? 0.0f : MV1;
-                l = l * ex2(M - ref) + st.z * ex2(st.x - ref);
-                const float f0 = ex2(MV - refv), f1 = ex2(st.y - refv);
+    for (int i = 0; i < CH; ++i) o[i] = 0.0f;
+    if (r0 + in_unit < rows) {
+        for (int x = c + warp; x <= c1; x += 4) {
+            const float *src = partial + ((int64_t)(x == c ? 2 * x + 1 : 2 * x) * R + in_unit) * LD;
+            const float4 st = *reinterpret_cast<const float4 *>(src + D);
+            const float M1 = fmaxf(M, st.x), MV1 = fmaxf(MV, st.y);
+            const float ref = M1 == NEG_INF ? 0.0f : M1, refv = MV1 == NEG_INF ? 0.0f : MV1;
+            l = l * ex2(M - ref) + st.z * ex2(st.x - ref);
+            const float f0 = ex2(MV - refv), f1 = ex2(st.y - refv);
 #pragma unroll
-                for (int i = 0; i < CH; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src + x0 + i);
-                    o[i] = o[i] * f0 + v.x * f1, o[i + 1] = o[i + 1] * f0 + v.y * f1;
-                    o[i + 2] = o[i + 2] * f0 + v.z * f1, o[i + 3] = o[i + 3] * f0 + v.w * f1;
-                }
-                M = M1, MV = MV1;
+            for (int i = 0; i < CH; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + x0 + i);
+                o[i] = o[i] * f0 + v.x * f1, o[i + 1] = o[i + 1] * f0 + v.y * f1;
+                o[i + 2] = o[i + 2] * f0 + v.z * f1, o[i + 3] = o[i + 3] * f0 + v.w * f1;
             }
+            M = M1, MV = MV1;
         }
+    }
 #pragma unroll
-        for (int i = 0; i < CH; ++i) s_o[warp][rr][x0 + i] = o[i];
-        if (x0 == 0) s_o[warp][rr][D] = M, s_o[warp][rr][D + 1] = MV, s_o[warp][rr][D + 2] = l;
-        __syncthreads();
-        if (tid < JR * 8) {
-            const int y = tid / 8, part = tid % 8, row = pl.r0 + y0 + y;
-            if (row < rows) {
-                float Ma = NEG_INF, MVa = NEG_INF, la = 0.0f, acc[D / 8];
-                for (int w = 0; w < 4; ++w) Ma = fmaxf(Ma, s_o[w][y][D]), MVa = fmaxf(MVa, s_o[w][y][D + 1]);
-                const float ref = Ma == NEG_INF ? 0.0f : Ma, refv = MVa == NEG_INF ? 0.0f : MVa;
+    for (int i = 0; i < CH; ++i) s_o[warp][rr][x0 + i] = o[i];
+    if (x0 == 0) s_o[warp][rr][D] = M, s_o[warp][rr][D + 1] = MV, s_o[warp][rr][D + 2] = l;
+    __syncthreads();
+    if (tid < JR * 8) {
+        const int y = tid / 8, part = tid % 8, row = r0 + y0 + y;
+        if (row < rows) {
+            float Ma = NEG_INF, MVa = NEG_INF, la = 0.0f, acc[D / 8];
+            for (int w = 0; w < 4; ++w) Ma = fmaxf(Ma, s_o[w][y][D]), MVa = fmaxf(MVa, s_o[w][y][D + 1]);
+            const float ref = Ma == NEG_INF ? 0.0f : Ma, refv = MVa == NEG_INF ? 0.0f : MVa;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) acc[i] = 0.0f;
-                for (int w = 0; w < 4; ++w) {
-                    la += s_o[w][y][D + 2] * ex2(s_o[w][y][D] - ref);
-                    const float f = ex2(s_o[w][y][D + 1] - refv);
+            for (int i = 0; i < D / 8; ++i) acc[i] = 0.0f;
+            for (int w = 0; w < 4; ++w) {
+                la += s_o[w][y][D + 2] * ex2(s_o[w][y][D] - ref);
+                const float f = ex2(s_o[w][y][D + 1] - refv);
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) acc[i] += f * s_o[w][y][part * (D / 8) + i];
-                }
-                const float f = exp2f(refv - ref);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) acc[i] *= f;
-                const int tok = row / a.G;
-                store_row<D, HALF>(a, (rq.row0 + tok) * a.Hq + pl.h * a.G + row - tok * a.G, part, acc, Ma, la);
+                for (int i = 0; i < D / 8; ++i) acc[i] += f * s_o[w][y][part * (D / 8) + i];
             }
+            const float f = exp2f(refv - ref);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) acc[i] *= f;
+            const int tok = row / a.G;
+            store_row<D, HALF, 8>(a, (unit.row0 + tok) * a.Hq + unit.h * a.G + row - tok * a.G, part, acc, Ma, la);
         }
-        return;
     }
 }
 
-// Blocks [0, 4 split_ctas) join the split kernel's units of 16 MT rows, 4 MT rows
-// each; the others the tile kernel's of 256 rows, 16 rows each.
-template <int D, int MT, bool HALF>
+// The first blocks join the split kernel's units of 8 NT rows, at most 8 rows each;
+// the others the tile kernel's of 256 rows, 16 rows each.
+template <int D, int NT, bool HALF>
 __global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a, int split_ctas, int tc_ctas) {
-    __shared__ int64_t s_sum[4], s_found[2];
     __shared__ float s_o[4][16][D + 4];
+    constexpr int JR = NT == 1 ? 4 : 8, JB = 8 * NT / JR;      // rows per block, blocks per unit
     pdl_wait();
     pdl_launch_dependents();
-    const int x = blockIdx.x, n = 4 * split_ctas;
-    if (x < n)
-        join_unit<D, HALF, SplitWork<16 * MT>, 4 * MT>(a, a.partial, x / 4, split_ctas, kAttnWarps, x % 4 * 4 * MT, s_o, s_sum,
-                                                       s_found);
-    else
-        join_unit<D, HALF, TcWork, 16>(a, a.partial_tc, (x - n) / 16, tc_ctas, kTcRound, (x - n) % 16 * 16, s_o, s_sum,
-                                       s_found);
+    const int x = blockIdx.x, n = JB * split_ctas;
+    if (x < n) join_unit<D, HALF, 8 * NT, JR>(a, a.join[x / JB], a.partial, x / JB, x % JB * JR, s_o);
+    else join_unit<D, HALF, kTcRows, 16>(a, a.join_tc[(x - n) / 16], a.partial_tc, (x - n) / 16, (x - n) % 16 * 16, s_o);
 }
 
-template <int D, int MT, bool HALF>
+template <int D, int NT, bool HALF>
 cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cudaStream_t stream) {
     static bool done[64];
-    constexpr int smem = attn_smem<D, MT>();
+    constexpr int smem = attn_smem<D, NT>();
     cudaError_t e = cudaSuccess;
     if (split_ctas) {
-        e = ensure_smem_limit((const void *)paged_attn_split_kernel<D, MT, HALF>, smem, done);
+        e = ensure_smem_limit((const void *)paged_attn_split_kernel<D, NT, HALF>, smem, done);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(paged_attn_split_kernel<D, MT, HALF>, dim3(split_ctas), dim3(kAttnWarps * 32), smem, stream, a);
+        e = launch_pdl(paged_attn_split_kernel<D, NT, HALF>, dim3(split_ctas), dim3(kAttnWarps * 32), smem, stream, a);
         if (e != cudaSuccess) return e;
     }
     if (tc_ctas) {
         e = launch_paged_attn_tc(a, D, HALF, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(paged_attn_join_kernel<D, MT, HALF>, dim3(4 * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
+    constexpr int JB = NT == 1 ? 2 : NT;
+    return launch_pdl(paged_attn_join_kernel<D, NT, HALF>, dim3(JB * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
                       split_ctas, tc_ctas);
 }
 
+template <int D, bool HALF>
+cudaError_t launch_attn_nt(int NT, const PagedAttnArgs &a, int split_ctas, int tc_ctas, cudaStream_t stream) {
+    if (NT == 1) return launch_attn<D, 1, HALF>(a, split_ctas, tc_ctas, stream);
+    if (NT == 2) return launch_attn<D, 2, HALF>(a, split_ctas, tc_ctas, stream);
+    return launch_attn<D, 4, HALF>(a, split_ctas, tc_ctas, stream);
+}
+
 // Which kernels a call launches.  Rows of one request that share a KV head are
-// G * max_new at most.  Up to 32 of them the split kernel takes every request (a
-// row tile of 16, or of 32 that reads the keys once for all).  Beyond, requests
-// of more than 16 rows go to the tile kernel; the split kernel then runs for
-// the others, unless there is but one request.
+// G * max_new at most.  Up to 32 of them the split kernel takes every request, in
+// row tiles of 8, 16 or 32 that read the keys once for all.  Beyond, requests with
+// more rows than a single token's tile holds go to the tile kernel; the split
+// kernel then runs for the others, unless there is but one request.
 struct Choice {
-    int MT, split_ctas, tc_ctas, split_rows;
+    int NT, split_ctas, tc_ctas, split_rows;
 };
 inline Choice choose(int B, int G, int max_new) {
     const int64_t rows = (int64_t)G * max_new;
-    Choice c = {1, num_sms() * 3, 0, 0x7FFFFFFF};    // CTAs that run at once: three per SM, two with 32 rows
+    const int64_t tile = rows <= 32 ? rows : G;
+    Choice c = {tile <= 8 ? 1 : (tile <= 16 ? 2 : 4), 0, 0, 0x7FFFFFFF};
+    c.split_ctas = num_sms() * split_per_sm(c.NT);
     if (rows > 32) {
         c.tc_ctas = paged_attn_tc_ctas();
-        c.split_rows = B > 1 ? 16 : 0;
+        c.split_rows = B > 1 ? 8 * c.NT : 0;
         if (B == 1) c.split_ctas = 0;
-    } else if (rows > 16) {
-        c.MT = 2;
-        c.split_ctas = num_sms() * 2;
     }
     return c;
 }
-inline size_t split_partial_floats(const Choice &c, int D) { return (size_t)2 * c.split_ctas * 16 * c.MT * (D + 4); }
+inline size_t split_partial_floats(const Choice &c, int D) { return (size_t)2 * c.split_ctas * 8 * c.NT * (D + 4); }
 
 }  // namespace
 }  // namespace csa2
@@ -546,7 +583,8 @@ using namespace csa2;
 extern "C" size_t csa2_paged_attn_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new) {
     if (B <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0 || max_new <= 0) return 0;
     const Choice c = choose(B, Hq / Hkv, max_new);
-    return (split_partial_floats(c, D) + (size_t)2 * c.tc_ctas * kTcRows * (D + 4)) * sizeof(float);
+    return (c.split_ctas + c.tc_ctas) * sizeof(JoinUnit) +
+           (split_partial_floats(c, D) + (size_t)2 * c.tc_ctas * kTcRows * (D + 4)) * sizeof(float);
 }
 
 extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, const void *q,
@@ -586,19 +624,15 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
         return CSA2_ERR_WORKSPACE;
     }
     const Choice c = choose(B, Hq / Hkv, max_new);
-    float *partial = (float *)workspace;
+    JoinUnit *join = (JoinUnit *)workspace;
+    float *partial = (float *)(join + c.split_ctas + c.tc_ctas);
     const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride,
                              q_token_stride, q_head_stride, (const uint16_t *)q, k_codes, v_codes, k_scale, v_scale,
                              block_table, kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag,
-                             c.split_rows, partial, partial + split_partial_floats(c, D)};
-    cudaError_t (*go)(const PagedAttnArgs &, int, int, cudaStream_t);
-    if (dt == CSA2_FP16)
-        go = D == 64 ? (c.MT == 1 ? launch_attn<64, 1, true> : launch_attn<64, 2, true>)
-                     : (c.MT == 1 ? launch_attn<128, 1, true> : launch_attn<128, 2, true>);
-    else
-        go = D == 64 ? (c.MT == 1 ? launch_attn<64, 1, false> : launch_attn<64, 2, false>)
-                     : (c.MT == 1 ? launch_attn<128, 1, false> : launch_attn<128, 2, false>);
-    CSA2_CUDA_CALL(go(a, c.split_ctas, c.tc_ctas, stream_of(stream)), "paged_attn launch");
+                             c.split_rows, join, join + c.split_ctas, partial, partial + split_partial_floats(c, D)};
+    auto go = dt == CSA2_FP16 ? (D == 64 ? launch_attn_nt<64, true> : launch_attn_nt<128, true>)
+                              : (D == 64 ? launch_attn_nt<64, false> : launch_attn_nt<128, false>);
+    CSA2_CUDA_CALL(go(c.NT, a, c.split_ctas, c.tc_ctas, stream_of(stream)), "paged_attn launch");
     CSA2_LAUNCH_CHECK("paged_attn kernels");
     return CSA2_OK;
 }

@@ -7,6 +7,14 @@
 
 namespace csa2 {
 
+// A unit that a CTA began and did not finish, for the kernel that joins the parts:
+// CTA c's part is slot 2 c + 1, those of the CTAs after it, to the last, slots 2 c'.
+struct JoinUnit {
+    int64_t row0;                   // first row of the request
+    int h, r0, rows, last;          // KV head, first row of the unit, rows of the request, last CTA (-1: no such unit)
+    int pad[2];
+};
+
 struct PagedAttnArgs {
     int B, Hq, Hkv, G, S, M, window;
     int64_t T, n_blocks, table_stride, q_token_stride, q_head_stride;
@@ -19,7 +27,8 @@ struct PagedAttnArgs {
     float *lse;
     uint32_t *err_flag;
     int split_rows;                 // requests of more rows than this are the tile kernel's
-    float *partial;                 // split kernel's [2 * CTAs][16 MT rows][D + 4]: o, m, mv, l
+    JoinUnit *join, *join_tc;       // one per CTA of the split and of the tile kernel
+    float *partial;                 // split kernel's [2 * CTAs][8 NT rows][D + 4]: o, m, mv, l
     float *partial_tc;              // tile kernel's [2 * CTAs][256 rows][D + 4]
 };
 
@@ -145,7 +154,7 @@ struct Place {
     int h, r0, tile, tiles;         // KV head, first row, key tile of the unit, the unit's key tiles
 };
 
-// The split kernel's work: units of R = 16 MT rows, key tiles of 32; every row
+// The split kernel's work: units of R = 8 NT rows, key tiles of 32; every row
 // tile of a request has the same tiles, at least one so that each row gets its
 // output.
 constexpr int kSplitKeys = 32;
@@ -234,19 +243,23 @@ struct TcWork {
     }
 };
 
-// 8 threads per row, D / 8 channels each: o = x * inv in the output's type, lse.
-template <int D, bool HALF>
+// P threads per row, D / P channels each: o = x / l in the output's type, lse.
+template <int D, bool HALF, int P>
 __device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row, int part, const float *x, float M, float l) {
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    uint32_t w[D / 16];
+    constexpr int W = D / P / 2;
+    uint32_t w[W];
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) w[c] = pack_out<HALF>(x[2 * c] * inv, x[2 * c + 1] * inv);
-    uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + part * (D / 8));
+    for (int c = 0; c < W; ++c) w[c] = pack_out<HALF>(x[2 * c] * inv, x[2 * c + 1] * inv);
+    uint16_t *dst = a.out + o_row * D + part * (D / P);
+    if constexpr (W == 2) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    } else {
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        for (int c = 0; c < W; c += 4) *reinterpret_cast<uint4 *>(dst + 2 * c) = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+    }
     if (a.lse && part == 0) a.lse[o_row] = l > 0.0f || l != l ? (M + log2f(l)) * 0.69314718055994531f : __int_as_float(0xff800000);
 }
-
 
 // The tile kernel (paged_attn_tc.cu): one CTA per SM.
 int paged_attn_tc_ctas();

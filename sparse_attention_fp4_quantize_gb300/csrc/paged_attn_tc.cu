@@ -274,9 +274,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         if (warp == kMmaWarp + 2 && lane == 0) {
             // ---- the segments, and one of no rows behind the last
             Walk walk(a, plan, blockIdx.x);
+            JoinUnit *join = a.join_tc + blockIdx.x;
+            join->last = -1;
             for (bool more = true; more; ++n_seg) {
                 Segment s = {};
+                const int64_t at = walk.at;
                 more = walk.next(a, s);
+                if (more && s.pl.tile == 0 && s.tb < s.pl.tiles)
+                    *join = {s.rq.row0, s.pl.h, s.pl.r0, s.rows, (int)((at + s.pl.tiles - 1) / plan.share), {0, 0}};
                 const uint32_t i = n_seg % kSegs;
                 if (!wait_one(segempty(i), ((n_seg / kSegs) & 1) ^ 1, abort_word)) break;
                 segs[i] = s;

@@ -10,12 +10,13 @@
 // for bits that fall below the subnormal step 2^-9 s.  Errors do not pile up
 // over the S appends that a decoding request makes to a block.
 //
-// One warp takes one (run, head, K or V).  The warps of a CTA look at a window of
-// rows; the first row of a run finds its length with a ballot, other rows
-// are left to it.  First pass: the largest magnitude, as an integer maximum of
-// the sign-less bit patterns (order-preserving for both formats).  Second pass,
-// from L1: scale, round, store.  A row's D codes are contiguous, a run's rows
-// too, so loads and stores are 16 and 8 bytes per lane of full lines.
+// One warp takes one (run, head, K or V).  A warp looks at a window of up to 32
+// rows with one load per lane: a run begins where the block changes, and its length
+// comes from ballots over the slots behind it.  First pass: the largest magnitude,
+// as an integer maximum of the sign-less bit patterns (order-preserving for both
+// formats).  Second pass, from L1: scale, round, store.  A row's D codes are
+// contiguous, a run's rows too, so loads and stores are 16 and 8 bytes per lane of
+// full lines, eight loads in flight per lane.
 #include "common.cuh"
 
 namespace csa2 {
@@ -30,7 +31,7 @@ struct PagedQuantArgs {
     float *scale[2];
     const int64_t *slots;
     int64_t T, n_slots;
-    int H, S, window;
+    int H, S, shift, window;       // S = 1 << shift; rows per window (at most 32)
     uint32_t *err_flag;
 };
 
@@ -66,38 +67,45 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQu
     pdl_wait();
     pdl_launch_dependents();
     if (unit >= 2 * a.H) return;
-    const int kv = unit & 1, h = unit >> 1;
-    const uint16_t *x = a.x[kv] + h * a.head_stride[kv] + (lane % LPR) * 8;
-    const int64_t ts = a.token_stride[kv];
-    const int64_t w0 = (int64_t)blockIdx.x * a.window, w1 = w0 + a.window < a.T ? w0 + a.window : a.T;
-    for (int64_t i = w0; i < w1; ++i) {
-        const int64_t s0 = a.slots[i];
-        if (s0 < 0 || s0 >= a.n_slots) {
-            if (s0 != -1 && unit == 0 && lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
-            continue;
-        }
-        const int64_t block = s0 / a.S;
-        const int start = (int)(s0 - block * a.S);
-        if (i > 0) {
-            const int64_t before = a.slots[i - 1];
-            if (before >= 0 && before < a.n_slots && before / a.S == block) {   // part of that row's run, or breaks it
-                if (before != s0 - 1 && unit == 0 && lane == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
-                continue;
-            }
-        }
+    const int h = unit >> 1;
+    const bool is_v = unit & 1;
+    const uint16_t *x = (is_v ? a.x[1] : a.x[0]) + h * (is_v ? a.head_stride[1] : a.head_stride[0]) + (lane % LPR) * 8;
+    const int64_t ts = is_v ? a.token_stride[1] : a.token_stride[0];
+    uint8_t *codes = is_v ? a.codes[1] : a.codes[0];
+    float *scales = is_v ? a.scale[1] : a.scale[0];
+    const int64_t w0 = (int64_t)blockIdx.x * a.window;
+
+    // lane = row of the window: its slot, the one before it
+    const int64_t mine = w0 + lane;
+    const bool in = lane < a.window && mine < a.T;
+    const int64_t slot = in ? a.slots[mine] : -1, prev = in && mine > 0 ? a.slots[mine - 1] : -1;
+    const bool valid = slot >= 0 && slot < a.n_slots;
+    const bool goes_on = valid && prev >= 0 && prev < a.n_slots && prev >> a.shift == slot >> a.shift;
+    if (unit == 0 && ((slot != -1 && !valid) || (goes_on && prev != slot - 1))) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
+    for (uint32_t leads = __ballot_sync(ALL, valid && !goes_on); leads; leads &= leads - 1) {
+        const int lead = __ffs(leads) - 1;
+        const int64_t i = w0 + lead, s0 = __shfl_sync(ALL, slot, lead), block = s0 >> a.shift;
+        const int start = (int)(s0 & (a.S - 1));
+        float *scale = scales + block * a.H + h;
+        const float old = start > 0 ? *scale : 0.0f;
         int n = 0;                        // rows of the run
         for (const int most = a.S - start; n < most;) {
             const int k = n + lane;
-            const bool in = k < most && i + k < a.T && a.slots[i + k] == s0 + k;
-            const uint32_t ok = __ballot_sync(ALL, in);
+            const bool same = k < most && i + k < a.T && a.slots[i + k] == s0 + k;
+            const uint32_t ok = __ballot_sync(ALL, same);
             n += ok == ALL ? 32 : __ffs(~ok) - 1;
             if (ok != ALL) break;
         }
 
         uint32_t m2 = 0;                  // largest sign-less patterns of the even and odd channels
-        for (int r = lane / LPR; r < n; r += RPW) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(x + (i + r) * ts);
-            m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(v.x & ABS2, v.y & ABS2)), __vmaxu2(v.z & ABS2, v.w & ABS2));
+        const uint16_t *row = x + (i + lane / LPR) * ts;
+        for (int r = lane / LPR; r < n; r += 8 * RPW, row += 8 * RPW * ts) {
+            uint4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = r + q * RPW < n ? *reinterpret_cast<const uint4 *>(row + q * RPW * ts) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(v[q].x & ABS2, v[q].y & ABS2)), __vmaxu2(v[q].z & ABS2, v[q].w & ABS2));
         }
         uint32_t top = __reduce_max_sync(ALL, max(m2 & 0xFFFFu, m2 >> 16));
         const bool bad = top >= INF;
@@ -112,11 +120,9 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQu
             if (lane == 0) flag_error(a.err_flag, CSA2_FLAG_NONFINITE);
         }
         const float need = scale_of(unpack2(top, HALF).x);
-        float *scale = a.scale[kv] + block * a.H + h;
-        uint8_t *dst = a.codes[kv] + ((block * a.H + h) * a.S + start) * (int64_t)D + (lane % LPR) * 8;
+        uint8_t *dst = codes + ((block * a.H + h) * a.S + start) * (int64_t)D + (lane % LPR) * 8;
         float s = need;
         if (start > 0) {
-            const float old = *scale;
             s = fmaxf(old, need);
             if (s != old) {               // re-encode the rows stored before
                 const float ratio = old > 0.0f ? old / s : 0.0f;
@@ -138,21 +144,29 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQu
         __syncwarp();
         if (lane == 0) *scale = s;
         const float inv = 1.0f / s;       // exact: a power of two
-        for (int r = lane / LPR; r < n; r += RPW) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(x + (i + r) * ts);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t c[4];
+        row = x + (i + lane / LPR) * ts;
+        for (int r = lane / LPR; r < n; r += 8 * RPW, row += 8 * RPW * ts) {
+            uint4 v[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float2 f = unpack2(w[q], HALF);
-                if (bad) {
-                    if (f.x != f.x) f.x = 0.0f;
-                    if (f.y != f.y) f.y = 0.0f;
+            for (int q = 0; q < 8; ++q) v[q] = r + q * RPW < n ? *reinterpret_cast<const uint4 *>(row + q * RPW * ts) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+                uint32_t c[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float2 f = unpack2(w[k], HALF);
+                    if (bad) {
+                        if (f.x != f.x) f.x = 0.0f;
+                        if (f.y != f.y) f.y = 0.0f;
+                    }
+                    c[k] = to_e4m3x2(f.x * inv, f.y * inv);
                 }
-                c[q] = to_e4m3x2(f.x * inv, f.y * inv);
+                if (r + q * RPW < n)
+                    *reinterpret_cast<uint2 *>(dst + (int64_t)(r + q * RPW) * D) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
             }
-            *reinterpret_cast<uint2 *>(dst + (int64_t)r * D) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         }
+        __syncwarp();
     }
 }
 
@@ -194,8 +208,11 @@ extern "C" csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, 
     a.codes[0] = k_codes, a.codes[1] = v_codes;
     a.scale[0] = k_scale, a.scale[1] = v_scale;
     a.slots = slots, a.T = T, a.n_slots = n_blocks * S, a.H = Hkv, a.S = S, a.err_flag = err_flag;
-    a.window = T <= 2048 ? 1 : 16;
-    while ((T + a.window - 1) / a.window > (1 << 24)) a.window *= 2;
+    a.shift = S == 16 ? 4 : (S == 32 ? 5 : (S == 64 ? 6 : 7));
+    // as many warps as run at once (48 per SM), each with at least one row to look at
+    const int64_t at_once = (int64_t)num_sms() * 48;
+    const int64_t window = (T * 2 * Hkv + at_once - 1) / at_once;
+    a.window = (int)(window < 1 ? 1 : (window > 32 ? 32 : window));
     const dim3 grid((unsigned)((T + a.window - 1) / a.window), (unsigned)((2 * Hkv + kWarps - 1) / kWarps));
     void (*kern)(PagedQuantArgs);
     if (dt == CSA2_FP16) kern = D == 64 ? quantize_fp8_paged_kernel<64, true> : quantize_fp8_paged_kernel<128, true>;

@@ -37,28 +37,44 @@ struct SlotArgs {
     int32_t *kv_out, *free_out, *cu, *positions;
     int64_t *slots;
     uint32_t *err_flag;
+    bool wide;                       // slots and positions are 16-byte aligned
 };
 
-// Exclusive prefix sum over the block of one value per thread; total to all.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_sums, int64_t &total) {
+// Exclusive prefix sums over the block of N values per thread; totals to all.
+template <int N>
+__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t (*warp_sums)[32], int64_t (&total)[N]) {
+    constexpr uint32_t ALL = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int64_t s = v;
+    int64_t s[N], w[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += y;
-    }
-    __syncthreads();   // the previous scan's sums have been read
-    if (lane == 31) warp_sums[warp] = s;
+    for (int n = 0; n < N; ++n) s[n] = v[n];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int64_t y = __shfl_up_sync(ALL, s[n], o);
+            if (lane >= o) s[n] += y;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int n = 0; n < N; ++n) warp_sums[n][warp] = s[n];
     __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        const int64_t x = warp_sums[w];
-        if (w < warp) before += x;
-        all += x;
+    // every warp scans the warps' sums by itself
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = lane < warps ? warp_sums[n][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int64_t y = __shfl_up_sync(ALL, w[n], o);
+            if (lane >= o) w[n] += y;
+        }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        total[n] = __shfl_sync(ALL, w[n], 31);
+        const int64_t before = __shfl_sync(ALL, w[n], warp - 1);     // of lane 31 for warp 0, not used
+        v[n] = (warp ? before : 0) + s[n] - v[n];
     }
-    total = all;
-    return before + s - v;
 }
 
 // Last b with a[b] <= x, of the nondecreasing a[0..n), a[0] <= x.
@@ -74,7 +90,7 @@ __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int32_t x) 
 
 __global__ void build_slots_kernel(SlotArgs a) {
     extern __shared__ int32_t sm[];
-    __shared__ int64_t warp_sums[32];
+    __shared__ int64_t warp_sums[3][32];
     __shared__ int32_t s_taken;
     int32_t *s_cu = sm;                    // first row
     int32_t *s_kv = s_cu + a.B;            // tokens held
@@ -100,10 +116,11 @@ __global__ void build_slots_kernel(SlotArgs a) {
         if (n > 0) rows += n < a.T + 1 ? n : a.T + 1;
         if (n < 0) freed += (kv + (int64_t)a.S - 1) / a.S;
     }
-    int64_t n_rows, n_freed;
-    int64_t cu = block_scan(rows, warp_sums, n_rows);
-    int64_t fr = block_scan(freed, warp_sums, n_freed);
     const int64_t fc = *a.free_count;
+    int64_t sums[2] = {rows, freed}, totals[2];
+    block_scan<2>(sums, warp_sums, totals);
+    int64_t cu = sums[0], fr = sums[1];
+    const int64_t n_rows = totals[0], n_freed = totals[1];
     const int64_t n_free = fc < 0 ? 0 : (fc > a.free_cap ? a.free_cap : fc);
     if (fc != n_free) flags |= CSA2_FLAG_BAD_INDEX;
     const int64_t size = n_free + n_freed;
@@ -121,8 +138,9 @@ __global__ void build_slots_kernel(SlotArgs a) {
             fr += held;
         }
     }
-    int64_t n_need;
-    int64_t take = block_scan(need, warp_sums, n_need);
+    int64_t wanted[1] = {need}, n_need[1];
+    block_scan<1>(wanted, warp_sums + 2, n_need);
+    int64_t take = wanted[0];
     int taken = 0;
     cu = cu0;
     for (int b = b0; b < b1; ++b) {
@@ -158,33 +176,53 @@ __global__ void build_slots_kernel(SlotArgs a) {
         const int b = last_at_most(s_freed, a.B, (int32_t)k);
         return a.table[b * a.table_stride + (k - s_freed[b])];
     };
+    // four rows per thread and step: one search, and mostly one block, for all of them
     const int64_t step = (int64_t)ranks * nt;
     const int64_t end = n_rows < a.T ? n_rows : a.T;
-    for (int64_t t = (int64_t)rank * nt + tid; t < a.T; t += step) {
-        int64_t slot = -1;
-        int32_t pos = -1;
-        if (t < end) {
-            const int b = last_at_most(s_cu, a.B, (int32_t)t);
+    const uint32_t S = a.S;
+    for (int64_t t0 = ((int64_t)rank * nt + tid) * 4; t0 < a.T; t0 += step * 4) {
+        int64_t slot[4];
+        int32_t pos[4], b = 0, block = -1;
+        uint32_t page = 0xFFFFFFFFu;                 // whose block is at hand
+        if (t0 < end) b = last_at_most(s_cu, a.B, (int32_t)t0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t t = t0 + i;
+            slot[i] = -1;
+            pos[i] = -1;
+            if (t >= end) continue;
+            while (b + 1 < a.B && s_cu[b + 1] <= t) ++b, page = 0xFFFFFFFFu;
             const int32_t first = s_take[b];
-            if (first >= 0) {
-                const uint32_t kv = s_kv[b], p = kv + (uint32_t)(t - s_cu[b]), S = a.S;
-                const uint32_t page = p / S, row = p - page * S, held = (kv + S - 1) / S;
-                int32_t block;
+            if (first < 0) continue;
+            const uint32_t kv = s_kv[b], p = kv + (uint32_t)(t - s_cu[b]), now = p / S, row = p - now * S;
+            if (now != page) {
+                page = now;
+                const uint32_t held = (kv + S - 1) / S;
                 int32_t *entry = a.table + b * a.table_stride + page;
                 if (page < held) {
                     block = *entry;
                 } else {
                     const int64_t at = size - 1 - (first + (int64_t)(page - held));
                     block = at < n_free ? a.free_list[at] : freed_block(at - n_free);
-                    if (row == 0) *entry = block;   // the block's first token is among the new ones
+                    if (row == 0) *entry = block;    // the block's first token is among the new ones
                 }
-                pos = (int32_t)p;
-                if (block >= 0) slot = (int64_t)block * S + row;
-                else flags |= CSA2_FLAG_BAD_INDEX;
             }
+            pos[i] = (int32_t)p;
+            if (block >= 0) slot[i] = (int64_t)block * S + row;
+            else flags |= CSA2_FLAG_BAD_INDEX;
         }
-        a.slots[t] = slot;
-        if (a.positions) a.positions[t] = pos;
+        if (a.wide && t0 + 4 <= a.T) {
+            reinterpret_cast<longlong2 *>(a.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
+            reinterpret_cast<longlong2 *>(a.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
+            if (a.positions) *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t0 + i < a.T) {
+                    a.slots[t0 + i] = slot[i];
+                    if (a.positions) a.positions[t0 + i] = pos[i];
+                }
+        }
     }
     for (int64_t k = (int64_t)rank * nt + tid; k < count - n_free; k += step) a.free_list[n_free + k] = freed_block(k);
     if (flags) flag_error(a.err_flag, flags);
@@ -226,17 +264,18 @@ extern "C" csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int 
     CSA2_REQUIRE((free_list || free_cap == 0) && (slots || T == 0), "build_slots: null pointer");
     CSA2_REQUIRE(aligned(slots, 8), "build_slots: slots must be 8-byte aligned");
     const SlotArgs args = {B, M, S, table_stride, T, free_cap, kv_len, new_len, block_table, free_list, free_count,
-                           kv_len_out, free_count_out, cu_len, positions, slots, err_flag};
+                           kv_len_out, free_count_out, cu_len, positions, slots, err_flag,
+                           aligned(slots, 16) && aligned(positions, 16)};
     const size_t smem = (size_t)B * 4 * sizeof(int32_t);
     static bool done[64];
     if (smem > 40 * 1024)
         CSA2_CUDA_CALL(ensure_smem_limit((const void *)build_slots_kernel, kMaxRequests * 16, done),
                        "build_slots: shared memory limit");
-    const int64_t work = T > B ? T : B;
+    const int64_t work = (T + 3) / 4 > B ? (T + 3) / 4 : B;     // threads that have something to do
     cudaLaunchConfig_t cfg = {};
-    const int ctas = work > 4096 ? 8 : 1;
+    const int ctas = (T + 3) / 4 > 1024 ? 8 : 1;
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(work <= 256 ? 256 : 1024);
+    cfg.blockDim = dim3(work <= 128 ? 128 : (work <= 512 ? 512 : 1024));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream_of(stream);
     cudaLaunchAttribute at[2] = {pdl_attribute(), {}};
