@@ -21,7 +21,8 @@ namespace {
 
 constexpr int kAttnWarps = 4;
 constexpr int kTileKeys = kSplitKeys;   // keys per warp tile
-constexpr int kStages = 2;          // tiles in flight per warp
+template <int D>
+constexpr int kStages = D == 64 ? 4 : 2;   // tiles in flight per warp: 16 KB
 // CTAs that an SM holds at once (registers; 3 x 64 KB of shared memory for 128 channels).
 constexpr int split_per_sm(int NT) { return NT == 4 ? 2 : 3; }
 
@@ -216,7 +217,7 @@ struct Tile {
 
 template <int D, int NT>
 constexpr int attn_smem() {
-    constexpr int ring = kAttnWarps * kStages * 2 * kTileKeys * D, merge = kAttnWarps * 8 * (D + 4) * 4;
+    constexpr int ring = kAttnWarps * kStages<D> * 2 * kTileKeys * D, merge = kAttnWarps * 8 * (D + 4) * 4;
     return ring > merge ? ring : merge;
 }
 
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_st[kAttnWarps][8][3];
-    __shared__ StageMeta s_meta[kAttnWarps][kStages];
+    __shared__ StageMeta s_meta[kAttnWarps][kStages<D>];
     __shared__ int64_t s_sum[kAttnWarps], s_found[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
     if (tid == 0) a.join[blockIdx.x].last = -1;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * 2 * kTileKeys * D);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages<D> * 2 * kTileKeys * D);
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
         const Request rq = request_of(a, b);
@@ -279,12 +280,12 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                         scales(i);
                     }
                     const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
-                    const uint32_t dst = ring + (i % kStages) * (2 * kTileKeys * D);
+                    const uint32_t dst = ring + (i % kStages<D>) * (2 * kTileKeys * D);
                     constexpr int CPR = D / 16, RPI = 32 / CPR;      // chunks per row, rows per instruction
                     const int c = lane % CPR, r1 = lane / CPR;
                     const uint32_t who = 2 * (i & 15);
                     if ((lane >> 1) == (i & 15)) {
-                        StageMeta &m = s_meta[warp][i % kStages];
+                        StageMeta &m = s_meta[warp][i % kStages<D>];
                         m.ks[lane & 1] = ks, m.vs[lane & 1] = vs;
                         m.stored[lane & 1] = off < 0 ? 0 : min(16, rq.kv - key - 16 * (lane & 1));
                     }
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                 cp_async_commit();
             };
 #pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) issue(i);
+            for (int i = 0; i < kStages<D> - 1; ++i) issue(i);
 
             Tile<D, NT> tile;
             tile.clear();
@@ -367,8 +368,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                 }
             }
             for (int i = 0; i < count; ++i) {
-                issue(i + kStages - 1);
-                cp_async_wait<kStages - 1>();
+                issue(i + kStages<D> - 1);
+                cp_async_wait<kStages<D> - 1>();
                 __syncwarp();
                 const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
                 int lo[NT][2], hi[NT][2];
@@ -376,8 +377,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                 for (int x = 0; x < NT; ++x)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) lo[x][r] = first[x][r] - key, hi[x][r] = pos[x][r] + 1 - key;
-                const uint32_t kb = ring + (i % kStages) * (2 * kTileKeys * D);
-                const StageMeta &meta = s_meta[warp][i % kStages];
+                const uint32_t kb = ring + (i % kStages<D>) * (2 * kTileKeys * D);
+                const StageMeta &meta = s_meta[warp][i % kStages<D>];
                 // rows that are not there may see everything: they are not stored
                 const bool whole = key >= all_lo && key + kTileKeys <= all_hi && meta.stored[0] == 16 && meta.stored[1] == 16;
                 if (__all_sync(ALL, whole)) tile.template keys32<false>(kb, kb + kTileKeys * D, meta, zf, lo, hi);
@@ -454,76 +455,101 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
 }
 
 // Joins the parts of the unit that CTA c began and did not finish.  A block takes
-// JR rows of the unit from y0 on; each of its four warps joins every fourth part of
-// them, then the warps' results meet.
-template <int D, bool HALF, int R, int JR>
+// 4 JR rows of the unit from y0 on if ROWS (few parts: each warp JR rows and all
+// parts), else JR rows (many parts: each warp every fourth part, then the warps'
+// results meet).  Four parts are loaded at a time.
+template <int D, bool HALF, int R, int JR, bool ROWS>
 __device__ __forceinline__ void join_unit(const PagedAttnArgs &a, const JoinUnit &unit, const float *partial, int c, int y0,
-                                          float (*s_o)[16][D + 4]) {
-    constexpr int LD = D + 4;
+                                          float (*s_o)[JR][D + 4]) {
+    constexpr int LD = D + 4, STEP = ROWS ? 1 : 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float NEG_INF = __int_as_float(0xff800000);
     const int c1 = unit.last, rows = unit.rows, r0 = unit.r0;
     if (c1 < 0 || r0 + y0 >= rows) return;
-    constexpr int TPR = 32 / JR, CH = D / TPR;   // threads per row in a warp, channels per thread
-    const int rr = lane / TPR, x0 = (lane % TPR) * CH, in_unit = y0 + rr;
+    constexpr int TPR = 32 / JR, CH = D / TPR;       // threads per row in a warp, channels per thread: 4 of every 4 TPR
+    const int rr = lane / TPR, x0 = (lane % TPR) * 4, in_unit = y0 + (ROWS ? warp * JR : 0) + rr;
     float M = NEG_INF, MV = NEG_INF, l = 0.0f, o[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) o[i] = 0.0f;
     if (r0 + in_unit < rows) {
-        for (int x = c + warp; x <= c1; x += 4) {
-            const float *src = partial + ((int64_t)(x == c ? 2 * x + 1 : 2 * x) * R + in_unit) * LD;
-            const float4 st = *reinterpret_cast<const float4 *>(src + D);
-            const float M1 = fmaxf(M, st.x), MV1 = fmaxf(MV, st.y);
-            const float ref = M1 == NEG_INF ? 0.0f : M1, refv = MV1 == NEG_INF ? 0.0f : MV1;
-            l = l * ex2(M - ref) + st.z * ex2(st.x - ref);
-            const float f0 = ex2(MV - refv), f1 = ex2(st.y - refv);
+        for (int x = c + (ROWS ? 0 : warp); x <= c1; x += 4 * STEP) {
+            float4 st[4], v[4][CH / 4];
 #pragma unroll
-            for (int i = 0; i < CH; i += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(src + x0 + i);
-                o[i] = o[i] * f0 + v.x * f1, o[i + 1] = o[i + 1] * f0 + v.y * f1;
-                o[i + 2] = o[i + 2] * f0 + v.z * f1, o[i + 3] = o[i + 3] * f0 + v.w * f1;
+            for (int k = 0; k < 4; ++k) {
+                const int y = x + k * STEP;
+                const float *src = partial + ((int64_t)(y == c ? 2 * y + 1 : 2 * y) * R + in_unit) * LD;
+                st[k] = y <= c1 ? *reinterpret_cast<const float4 *>(src + D) : make_float4(NEG_INF, NEG_INF, 0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < CH / 4; ++i)
+                    v[k][i] = y <= c1 ? *reinterpret_cast<const float4 *>(src + x0 + 4 * TPR * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            const float M1 = fmaxf(fmaxf(fmaxf(M, st[0].x), fmaxf(st[1].x, st[2].x)), st[3].x);
+            const float MV1 = fmaxf(fmaxf(fmaxf(MV, st[0].y), fmaxf(st[1].y, st[2].y)), st[3].y);
+            const float ref = M1 == NEG_INF ? 0.0f : M1, refv = MV1 == NEG_INF ? 0.0f : MV1, f0 = ex2(MV - refv);
+            l *= ex2(M - ref);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) o[i] *= f0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                l += st[k].z * ex2(st[k].x - ref);
+                const float f = ex2(st[k].y - refv);
+#pragma unroll
+                for (int i = 0; i < CH / 4; ++i) {
+                    o[4 * i] += v[k][i].x * f, o[4 * i + 1] += v[k][i].y * f;
+                    o[4 * i + 2] += v[k][i].z * f, o[4 * i + 3] += v[k][i].w * f;
+                }
             }
             M = M1, MV = MV1;
         }
     }
+    // the rows, whole, through shared memory: of all warps, or of this one
 #pragma unroll
-    for (int i = 0; i < CH; ++i) s_o[warp][rr][x0 + i] = o[i];
+    for (int i = 0; i < CH / 4; ++i)
+        *reinterpret_cast<float4 *>(&s_o[warp][rr][x0 + 4 * TPR * i]) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     if (x0 == 0) s_o[warp][rr][D] = M, s_o[warp][rr][D + 1] = MV, s_o[warp][rr][D + 2] = l;
     __syncthreads();
-    if (tid < JR * 8) {
-        const int y = tid / 8, part = tid % 8, row = r0 + y0 + y;
-        if (row < rows) {
-            float Ma = NEG_INF, MVa = NEG_INF, la = 0.0f, acc[D / 8];
-            for (int w = 0; w < 4; ++w) Ma = fmaxf(Ma, s_o[w][y][D]), MVa = fmaxf(MVa, s_o[w][y][D + 1]);
-            const float ref = Ma == NEG_INF ? 0.0f : Ma, refv = MVa == NEG_INF ? 0.0f : MVa;
+    constexpr int N = ROWS ? 4 * JR : JR;            // rows of the block, 8 threads each
+    for (int u = tid; u < N * 8; u += 128) {
+        const int y = u / 8, part = u % 8, row = r0 + y0 + y;
+        if (row >= rows) continue;
+        float Ma = NEG_INF, MVa = NEG_INF, la = 0.0f, acc[D / 8];
+        constexpr int W = ROWS ? 1 : 4;
+        const int w0 = ROWS ? y / JR : 0, yy = ROWS ? y % JR : y;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) acc[i] = 0.0f;
-            for (int w = 0; w < 4; ++w) {
-                la += s_o[w][y][D + 2] * ex2(s_o[w][y][D] - ref);
-                const float f = ex2(s_o[w][y][D + 1] - refv);
+        for (int w = 0; w < W; ++w) Ma = fmaxf(Ma, s_o[w0 + w][yy][D]), MVa = fmaxf(MVa, s_o[w0 + w][yy][D + 1]);
+        const float ref = Ma == NEG_INF ? 0.0f : Ma, refv = MVa == NEG_INF ? 0.0f : MVa;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) acc[i] += f * s_o[w][y][part * (D / 8) + i];
-            }
-            const float f = exp2f(refv - ref);
+        for (int i = 0; i < D / 8; ++i) acc[i] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) acc[i] *= f;
-            const int tok = row / a.G;
-            store_row<D, HALF, 8>(a, (unit.row0 + tok) * a.Hq + unit.h * a.G + row - tok * a.G, part, acc, Ma, la);
+        for (int w = 0; w < W; ++w) {
+            la += s_o[w0 + w][yy][D + 2] * ex2(s_o[w0 + w][yy][D] - ref);
+            const float f = ex2(s_o[w0 + w][yy][D + 1] - refv);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) acc[i] += f * s_o[w0 + w][yy][part * (D / 8) + i];
         }
+        const float f = exp2f(refv - ref);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) acc[i] *= f;
+        const int tok = row / a.G;
+        store_row<D, HALF, 8>(a, (unit.row0 + tok) * a.Hq + unit.h * a.G + row - tok * a.G, part, acc, Ma, la);
     }
 }
 
-// The first blocks join the split kernel's units of 8 NT rows, at most 8 rows each;
-// the others the tile kernel's of 256 rows, 16 rows each.
+// The first blocks join the split kernel's units of 8 NT rows, 4 or 8 rows each; the
+// others the tile kernel's of 256 rows, 16 rows each.
 template <int D, int NT, bool HALF>
 __global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a, int split_ctas, int tc_ctas) {
-    __shared__ float s_o[4][16][D + 4];
     constexpr int JR = NT == 1 ? 4 : 8, JB = 8 * NT / JR;      // rows per block, blocks per unit
+    __shared__ float s_o[4][8][D + 4];
     pdl_wait();
     pdl_launch_dependents();
     const int x = blockIdx.x, n = JB * split_ctas;
-    if (x < n) join_unit<D, HALF, 8 * NT, JR>(a, a.join[x / JB], a.partial, x / JB, x % JB * JR, s_o);
-    else join_unit<D, HALF, kTcRows, 16>(a, a.join_tc[(x - n) / 16], a.partial_tc, (x - n) / 16, (x - n) % 16 * 16, s_o);
+    if (x < n)
+        join_unit<D, HALF, 8 * NT, JR, false>(a, a.join[x / JB], a.partial, x / JB, x % JB * JR,
+                                              reinterpret_cast<float (*)[JR][D + 4]>(s_o));
+    else
+        join_unit<D, HALF, kTcRows, 4, true>(a, a.join_tc[(x - n) / 16], a.partial_tc, (x - n) / 16, (x - n) % 16 * 16,
+                                             reinterpret_cast<float (*)[4][D + 4]>(s_o));
 }
 
 template <int D, int NT, bool HALF>
