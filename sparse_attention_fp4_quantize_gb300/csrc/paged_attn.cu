@@ -19,12 +19,15 @@
 namespace csa2 {
 namespace {
 
-constexpr int kAttnWarps = 4;
-constexpr int kTileKeys = kSplitKeys;   // keys per warp tile
+constexpr int kAttnWarps = kSplitWarps;
+constexpr int kHalf = 4096;             // bytes of a warp tile's keys, and of its values
 template <int D>
-constexpr int kStages = D == 64 ? 4 : 2;   // tiles in flight per warp: 16 KB
-// CTAs that an SM holds at once (registers; 3 x 64 KB of shared memory for 128 channels).
-constexpr int split_per_sm(int NT) { return NT == 4 ? 2 : 3; }
+constexpr int kTileKeys = kHalf / D;
+constexpr int kStages = 2;              // tiles in flight per warp
+// CTAs that an SM holds at once.  128 channels: two of 255 registers stream faster
+// than three of 168 (attn over 64 x 16k tokens, 8 heads: 195 against 203 us; 16 rows
+// per tile, 19 x 32k tokens: 60 against 88).
+constexpr int split_per_sm(int D, int NT) { return D == 128 ? 2 : (NT == 1 ? 4 : 3); }
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
@@ -32,9 +35,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
+template <int D>
 struct StageMeta {
-    float ks[2], vs[2];             // scales of the two 16-key halves
-    int stored[2];                  // keys of each half that are there
+    static constexpr int U = kTileKeys<D> / 16;
+    float ks[U], vs[U], lg[U], rv[U];   // scales of the 16-key groups; log2 and reciprocal of v's
+    int stored[U];                  // keys of each group that are there
 };
 
 // 8 x 8 halves, transposed across the warp.
@@ -60,9 +65,11 @@ template <int D, int NT>
 struct Tile {
     static constexpr int KS = D / 16;                // k-steps of q . k
     static constexpr int MO = D / 16;                // 16-channel tiles of O^T
+    static constexpr int U = kTileKeys<D> / 16;      // 16-key groups of a tile
     uint32_t q[NT][KS][2];
     float o[NT][MO][4];
-    float m[NT][2], mv[NT][2], l[NT][2];             // rows 2 t, 2 t + 1: running maxima (log2), sum of P of this lane's keys
+    float m[NT][2], mv[NT][2], l[NT][2];             // rows 2 t, 2 t + 1: references (log2), sum of P of this lane's keys
+    float back[NT][2], dmin, dmax;                   // 2^(mv - m); least and largest m - mv (-inf: a row without keys so far)
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -70,22 +77,64 @@ struct Tile {
 #pragma unroll
             for (int j = 0; j < MO; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.0f;
             m[x][0] = m[x][1] = mv[x][0] = mv[x][1] = __int_as_float(0xff800000);
-            l[x][0] = l[x][1] = 0.0f;
+            l[x][0] = l[x][1] = back[x][0] = back[x][1] = 0.0f;
         }
+        dmin = dmax = __int_as_float(0xff800000);
     }
 
-    // 32 keys from shared memory (codes at kb, vb).  zf: logit factor per row.  With
-    // MASK a row sees keys [lo, hi) of the 32, as far as they are stored; without,
-    // all of them.
-    template <bool MASK>
-    __device__ __forceinline__ void keys32(uint32_t kb, uint32_t vb, const StageMeta &meta, const float (&zf)[NT][2],
-                                           const int (&lo)[NT][2], const int (&hi)[NT][2]) {
+    // Weights of a tile whose keys every row sees, with the references as they are:
+    // one exponential per score and no maximum, P = 2^(s f + log2 vs - mv), and l
+    // gains sum P / vs 2^(mv - m).  False if a row's P may leave f16 or a scale is so
+    // far from the others that P would not carry its keys' part of l.
+    __device__ __forceinline__ bool weights(const float (&s)[NT][U][4], const StageMeta<D> &meta, const float (&zf)[NT][2],
+                                            uint32_t (&p)[NT][U][2]) {
+        float least = meta.lg[0], most = meta.lg[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) least = fminf(least, meta.lg[u]), most = fmaxf(most, meta.lg[u]);
+        bool ok = dmin + least > -64.0f && dmax + most < 64.0f;
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        float gain[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            float total[2] = {0.0f, 0.0f};
+            gain[x][0] = gain[x][1] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float e[2][2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float f = zf[x][r] * meta.ks[u], c = meta.lg[u] - mv[x][r];
+                    e[r][0] = ex2(fmaf(s[x][u][r], f, c)), e[r][1] = ex2(fmaf(s[x][u][2 + r], f, c));
+                    const float sum = e[r][0] + e[r][1];
+                    total[r] += sum;
+                    gain[x][r] = fmaf(sum, meta.rv[u], gain[x][r]);
+                }
+                p[x][u][0] = transpose8x8(pack_f16(e[0][0], e[1][0]));
+                p[x][u][1] = transpose8x8(pack_f16(e[0][1], e[1][1]));
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                gain[x][r] *= back[x][r];
+                ok = ok && total[r] < 16384.0f && gain[x][r] < 1e30f;        // (f16 ends at 65504)
+            }
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) l[x][0] += gain[x][0], l[x][1] += gain[x][1];
+        return true;
+    }
+
+    // A tile of keys from shared memory (codes at kb, vb), the first of them `key0`.  zf:
+    // logit factor per row.  If masked, a row sees keys [seen.x, seen.y] as far as
+    // they are stored; else all of them.
+    __device__ __forceinline__ void keys(uint32_t kb, uint32_t vb, const StageMeta<D> &meta, const float (&zf)[NT][2], bool masked,
+                                           int key0, const int2 *seen) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         constexpr uint32_t ALL = 0xFFFFFFFFu;
         const float NEG_INF = __int_as_float(0xff800000);
-        float s[NT][2][4];
+        float s[NT][U][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
             uint32_t kw[2][D / 16];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -105,72 +154,77 @@ struct Tile {
                 for (int x = 0; x < NT; ++x) mma_f16_16816(s[x][u], a0, a1, a2, a3, q[x][k][0], q[x][k][1]);
             }
         }
-        const float ve[2] = {(float)((int)((__float_as_uint(meta.vs[0]) >> 23) & 0xFFu) - 127),
-                             (float)((int)((__float_as_uint(meta.vs[1]) >> 23) & 0xFFu) - 127)};
-        uint32_t p[NT][2][2];
-        float grow[NT][2];
-        bool grew = false;
+        uint32_t p[NT][U][2];
+        if (masked || !weights(s, meta, zf, p)) {
+            float grow[NT][2];
+            bool grew = false;
+            dmin = __int_as_float(0x7f800000), dmax = NEG_INF;
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            float w[2][4];                           // [row][16 u + 8 h + g at 2 u + h]
+            for (int x = 0; x < NT; ++x) {
+                float w[2][2 * U];                       // [row][16 u + 8 h + g at 2 u + h]
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float z[4], top[2];
+                for (int r = 0; r < 2; ++r) {
+                    const int2 sees = seen[8 * x + 2 * t + r];
+                    float z[2 * U], tz = NEG_INF, tv = NEG_INF;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float f = zf[x][r] * meta.ks[u];
+                    for (int u = 0; u < U; ++u) {
+                        const float f = zf[x][r] * meta.ks[u];
+                        const float ve = (float)((int)((__float_as_uint(meta.vs[u]) >> 23) & 0xFFu) - 127);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int key = 16 * u + 8 * h + g;
-                        float v = s[x][u][2 * h + r] * f;
-                        if (MASK && !(key >= lo[x][r] && key < hi[x][r] && 8 * h + g < meta.stored[u])) v = NEG_INF;
-                        z[2 * u + h] = v;
+                        for (int h = 0; h < 2; ++h) {
+                            const int key = 16 * u + 8 * h + g;
+                            float v = s[x][u][2 * h + r] * f;
+                            if (masked && !(key0 + key >= sees.x && key0 + key <= sees.y && 8 * h + g < meta.stored[u])) v = NEG_INF;
+                            z[2 * u + h] = v;
+                            tz = fmaxf(tz, v);
+                            tv = fmaxf(tv, v + ve);
+                        }
                     }
-                    top[u] = fmaxf(z[2 * u], z[2 * u + 1]);
-                }
-                // the row's keys are spread over the 8 lanes of equal t
-                float tz = fmaxf(top[0], top[1]), tv = fmaxf(top[0] + ve[0], top[1] + ve[1]);
+                    // the row's keys are spread over the 8 lanes of equal t
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    tz = fmaxf(tz, __shfl_xor_sync(ALL, tz, d));
-                    if (ve[0] != ve[1]) tv = fmaxf(tv, __shfl_xor_sync(ALL, tv, d));
-                }
-                if (ve[0] == ve[1]) tv = tz + ve[0];
-                const float m1 = fmaxf(m[x][r], tz), mv1 = fmaxf(mv[x][r], tv);
-                const float ref = m1 == NEG_INF ? 0.0f : m1, refv = mv1 == NEG_INF ? 0.0f : mv1;
-                float sum = l[x][r] * ex2(m[x][r] - ref);
-                grow[x][r] = ex2(mv[x][r] - refv);
-                grew |= mv1 != mv[x][r];
-                m[x][r] = m1, mv[x][r] = mv1;
-                const float g2 = ex2(ref - refv);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float f = fminf(meta.vs[u] * g2, 1e38f);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float e = ex2(z[2 * u + h] - ref);
-                        sum += e;
-                        w[r][2 * u + h] = MASK && z[2 * u + h] == NEG_INF ? 0.0f : e * f;
+                    for (int d = 4; d < 32; d <<= 1) {
+                        tz = fmaxf(tz, __shfl_xor_sync(ALL, tz, d));
+                        tv = fmaxf(tv, __shfl_xor_sync(ALL, tv, d));
                     }
+                    const float m1 = fmaxf(m[x][r], tz), mv1 = fmaxf(mv[x][r], tv);
+                    const float ref = m1 == NEG_INF ? 0.0f : m1, refv = mv1 == NEG_INF ? 0.0f : mv1;
+                    float sum = l[x][r] * ex2(m[x][r] - ref);
+                    grow[x][r] = ex2(mv[x][r] - refv);
+                    grew |= mv1 != mv[x][r];
+                    m[x][r] = m1, mv[x][r] = mv1;
+                    const float g2 = ex2(ref - refv);
+                    back[x][r] = ex2(refv - ref);
+                    dmin = fminf(dmin, m1 == NEG_INF || mv1 == NEG_INF ? NEG_INF : m1 - mv1);
+                    dmax = fmaxf(dmax, ref - refv);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const float f = fminf(meta.vs[u] * g2, 1e38f);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float e = ex2(z[2 * u + h] - ref);
+                            sum += e;
+                            w[r][2 * u + h] = z[2 * u + h] == NEG_INF ? 0.0f : e * f;
+                        }
+                    }
+                    l[x][r] = sum;
                 }
-                l[x][r] = sum;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) p[x][u][h] = transpose8x8(pack_f16(w[0][2 * u + h], w[1][2 * u + h]));
             }
+            if (__any_sync(ALL, grew)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) p[x][u][h] = transpose8x8(pack_f16(w[0][2 * u + h], w[1][2 * u + h]));
-        }
-        if (__any_sync(ALL, grew)) {
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int j = 0; j < MO; ++j) {
-                    o[x][j][0] *= grow[x][0], o[x][j][1] *= grow[x][1];
-                    o[x][j][2] *= grow[x][0], o[x][j][3] *= grow[x][1];
-                }
+                    for (int j = 0; j < MO; ++j) {
+                        o[x][j][0] *= grow[x][0], o[x][j][1] *= grow[x][1];
+                        o[x][j][2] *= grow[x][0], o[x][j][3] *= grow[x][1];
+                    }
+            }
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
             constexpr int VW = D / 32;               // words of a value row per lane
             uint32_t vw[4][VW];
 #pragma unroll
@@ -217,28 +271,29 @@ struct Tile {
 
 template <int D, int NT>
 constexpr int attn_smem() {
-    constexpr int ring = kAttnWarps * kStages<D> * 2 * kTileKeys * D, merge = kAttnWarps * 8 * (D + 4) * 4;
+    constexpr int ring = kAttnWarps * kStages * 2 * kHalf, merge = kAttnWarps * 8 * (D + 4) * 4;
     return ring > merge ? ring : merge;
 }
 
 template <int D, int NT, bool HALF>
-__global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_split_kernel(PagedAttnArgs a) {
+__global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(D, NT)) paged_attn_split_kernel(PagedAttnArgs a) {
     constexpr int R = 8 * NT;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_st[kAttnWarps][8][3];
-    __shared__ StageMeta s_meta[kAttnWarps][kStages<D>];
+    __shared__ int2 s_seen[kAttnWarps][R];
+    __shared__ StageMeta<D> s_meta[kAttnWarps][kStages];
     __shared__ int64_t s_sum[kAttnWarps], s_found[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
     pdl_wait();
     pdl_launch_dependents();
-    using Work = SplitWork<R>;
+    using Work = SplitWork<R, kTileKeys<D>>;
     const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kAttnWarps, s_sum, s_found);
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
     if (tid == 0) a.join[blockIdx.x].last = -1;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages<D> * 2 * kTileKeys * D);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * 2 * kHalf);
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
         const Request rq = request_of(a, b);
@@ -252,45 +307,47 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                 a.join[blockIdx.x] = {rq.row0, h, r0, rows, (int)((at + pl.tiles - 1) / plan.share), {0, 0}};
             at += tb - ta;
 
-            // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / 2, half lane % 2) of 16 of them
-            const int count = tb - ta > warp ? (tb - ta - warp + kAttnWarps - 1) / kAttnWarps : 0;
+            // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / U, 16-key group lane % U) of 32 / U of them
+            constexpr int U = kTileKeys<D> / 16, BT = 32 / U;
+            const int todo = min(tb, Work::real_tiles(a, rq)) - ta;
+            const int count = todo > warp ? (todo - warp + kAttnWarps - 1) / kAttnWarps : 0;
             const int32_t *table = a.table + b * a.table_stride;
-            auto entry = [&](int i) -> int32_t {     // block of this lane's half of the 16 tiles from i on
-                const int key = key0 + (ta + warp + (i + (lane >> 1)) * kAttnWarps) * kTileKeys + 16 * (lane & 1);
-                return i + (lane >> 1) < count && key < rq.kv ? table[key / a.S] : -1;
-            };
-            int32_t block = entry(0), block_next = entry(16);
-            float ks = 0.0f, vs = 0.0f;
-            int64_t off = -1;                        // code offset of the half's first row, -1: not there
+            auto key_of = [&](int i) { return key0 + (ta + warp + (i + lane / U) * kAttnWarps) * kTileKeys<D> + 16 * (lane % U); };
+            auto there = [&](int i) { return i + lane / U < count && key_of(i) < rq.kv; };
+            auto entry = [&](int i) -> int32_t { return there(i) ? table[key_of(i) / a.S] : -1; };   // block of this lane's group
+            int32_t block = entry(0), block_next = entry(BT);
+            float ks = 0.0f, vs = 0.0f, lg = 0.0f, rv = 0.0f;
+            int64_t off = -1;                        // code offset of the group's first row, -1: not there
             auto scales = [&](int i) {
-                const int key = key0 + (ta + warp + (i + (lane >> 1)) * kAttnWarps) * kTileKeys + 16 * (lane & 1);
-                const bool there = i + (lane >> 1) < count && key < rq.kv, ok = there && block >= 0 && block < a.n_blocks;
-                if (there && !ok) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+                const bool ok = there(i) && block >= 0 && block < a.n_blocks;
+                if (there(i) && !ok) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
                 const int64_t bh = ok ? (int64_t)block * a.Hkv + h : 0;
                 ks = ok ? a.k_scale[bh] : 0.0f;
                 vs = ok ? a.v_scale[bh] : 0.0f;
-                off = ok ? (bh * a.S + (key & (a.S - 1))) * D : -1;
+                lg = lg2(vs), rv = rcp(vs);
+                off = ok ? (bh * a.S + (key_of(i) & (a.S - 1))) * D : -1;
             };
             scales(0);
             auto issue = [&](int i) {                // start the copy of this warp's tile i
                 if (i < count) {
-                    if (i && (i & 15) == 0) {
+                    if (i && i % BT == 0) {
                         block = block_next;
-                        block_next = entry(i + 16);
+                        block_next = entry(i + BT);
                         scales(i);
                     }
-                    const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
-                    const uint32_t dst = ring + (i % kStages<D>) * (2 * kTileKeys * D);
+                    const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys<D>;
+                    const uint32_t dst = ring + (i % kStages) * (2 * kHalf);
                     constexpr int CPR = D / 16, RPI = 32 / CPR;      // chunks per row, rows per instruction
                     const int c = lane % CPR, r1 = lane / CPR;
-                    const uint32_t who = 2 * (i & 15);
-                    if ((lane >> 1) == (i & 15)) {
-                        StageMeta &m = s_meta[warp][i % kStages<D>];
-                        m.ks[lane & 1] = ks, m.vs[lane & 1] = vs;
-                        m.stored[lane & 1] = off < 0 ? 0 : min(16, rq.kv - key - 16 * (lane & 1));
+                    const uint32_t who = U * (i % BT);
+                    if (lane / U == i % BT) {
+                        StageMeta<D> &m = s_meta[warp][i % kStages];
+                        const int u = lane % U;
+                        m.ks[u] = ks, m.vs[u] = vs, m.lg[u] = lg, m.rv[u] = rv;
+                        m.stored[u] = off < 0 ? 0 : min(16, rq.kv - key - 16 * u);
                     }
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < U; ++u) {
                         const int64_t from = __shfl_sync(ALL, off, who + u);
                         const int stored = from < 0 ? 0 : rq.kv - key - 16 * u;
                         const int64_t lane_at = (from < 0 ? 0 : from) + r1 * D + 16 * c;
@@ -300,7 +357,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                             for (int x = 0; x < 16 / RPI; ++x) {
                                 const uint32_t to = dst + chunk_at<D>(16 * u + x * RPI + r1, c);
                                 cp_async16(to, ksrc + x * RPI * D, 16);
-                                cp_async16(to + kTileKeys * D, vsrc + x * RPI * D, 16);
+                                cp_async16(to + kHalf, vsrc + x * RPI * D, 16);
                             }
                         } else {                     // rows that are not there read as zero
 #pragma unroll
@@ -308,7 +365,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                                 const bool there = x * RPI + r1 < stored;
                                 const uint32_t to = dst + chunk_at<D>(16 * u + x * RPI + r1, c);
                                 cp_async16(to, there ? ksrc + x * RPI * D : a.k_codes, there ? 16 : 0);
-                                cp_async16(to + kTileKeys * D, there ? vsrc + x * RPI * D : a.v_codes, there ? 16 : 0);
+                                cp_async16(to + kHalf, there ? vsrc + x * RPI * D : a.v_codes, there ? 16 : 0);
                             }
                         }
                     }
@@ -316,11 +373,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                 cp_async_commit();
             };
 #pragma unroll
-            for (int i = 0; i < kStages<D> - 1; ++i) issue(i);
+            for (int i = 0; i < kStages - 1; ++i) issue(i);
 
             Tile<D, NT> tile;
             tile.clear();
-            int pos[NT][2], first[NT][2];
             float zf[NT][2];
             int all_lo = 0, all_hi = 0x7FFFFFFF;     // keys that every real row of this lane sees
 #pragma unroll
@@ -362,27 +418,24 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(NT)) paged_attn_
                 for (int r = 0; r < 2; ++r) {        // the lane's rows of S^T and O^T
                     const int row = r0 + 8 * x + 2 * t + r;
                     const bool real = row < rows;
-                    pos[x][r] = real ? max(-1, rq.kv - rq.n + row / a.G) : -1;
-                    first[x][r] = a.window > 0 ? max(0, pos[x][r] - a.window + 1) : 0;
-                    if (real) all_lo = max(all_lo, first[x][r]), all_hi = min(all_hi, pos[x][r] + 1);
+                    // a row that is not there sees everything: it holds no other back, and is not stored
+                    const int pos = real ? max(-1, rq.kv - rq.n + row / a.G) : 0x7FFFFFF0;
+                    const int first = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                    if (g == 0) s_seen[warp][8 * x + 2 * t + r] = make_int2(first, pos);
+                    if (real) all_lo = max(all_lo, first), all_hi = min(all_hi, pos + 1);
                 }
             }
             for (int i = 0; i < count; ++i) {
-                issue(i + kStages<D> - 1);
-                cp_async_wait<kStages<D> - 1>();
+                issue(i + kStages - 1);
+                cp_async_wait<kStages - 1>();
                 __syncwarp();
-                const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys;
-                int lo[NT][2], hi[NT][2];
+                const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys<D>;
+                const uint32_t kb = ring + (i % kStages) * (2 * kHalf);
+                const StageMeta<D> &meta = s_meta[warp][i % kStages];
+                bool whole = key >= all_lo && key + kTileKeys<D> <= all_hi;
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) lo[x][r] = first[x][r] - key, hi[x][r] = pos[x][r] + 1 - key;
-                const uint32_t kb = ring + (i % kStages<D>) * (2 * kTileKeys * D);
-                const StageMeta &meta = s_meta[warp][i % kStages<D>];
-                // rows that are not there may see everything: they are not stored
-                const bool whole = key >= all_lo && key + kTileKeys <= all_hi && meta.stored[0] == 16 && meta.stored[1] == 16;
-                if (__all_sync(ALL, whole)) tile.template keys32<false>(kb, kb + kTileKeys * D, meta, zf, lo, hi);
-                else tile.template keys32<true>(kb, kb + kTileKeys * D, meta, zf, lo, hi);
+                for (int u = 0; u < U; ++u) whole = whole && meta.stored[u] == 16;
+                tile.keys(kb, kb + kHalf, meta, zf, !__all_sync(ALL, whole), key, s_seen[warp]);
                 __syncwarp();
             }
             cp_async_wait<0>();
@@ -535,12 +588,12 @@ __device__ __forceinline__ void join_unit(const PagedAttnArgs &a, const JoinUnit
     }
 }
 
-// The first blocks join the split kernel's units of 8 NT rows, 4 or 8 rows each; the
+// The first blocks join the split kernel's units of 8 NT rows, 4 rows each; the
 // others the tile kernel's of 256 rows, 16 rows each.
 template <int D, int NT, bool HALF>
 __global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a, int split_ctas, int tc_ctas) {
-    constexpr int JR = NT == 1 ? 4 : 8, JB = 8 * NT / JR;      // rows per block, blocks per unit
-    __shared__ float s_o[4][8][D + 4];
+    constexpr int JR = 4, JB = 8 * NT / JR;                    // rows per block, blocks per unit
+    __shared__ float s_o[4][4][D + 4];
     pdl_wait();
     pdl_launch_dependents();
     const int x = blockIdx.x, n = JB * split_ctas;
@@ -567,36 +620,33 @@ cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cud
         e = launch_paged_attn_tc(a, D, HALF, stream);
         if (e != cudaSuccess) return e;
     }
-    constexpr int JB = NT == 1 ? 2 : NT;
+    constexpr int JB = 2 * NT;
     return launch_pdl(paged_attn_join_kernel<D, NT, HALF>, dim3(JB * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
                       split_ctas, tc_ctas);
 }
 
 template <int D, bool HALF>
 cudaError_t launch_attn_nt(int NT, const PagedAttnArgs &a, int split_ctas, int tc_ctas, cudaStream_t stream) {
-    if (NT == 1) return launch_attn<D, 1, HALF>(a, split_ctas, tc_ctas, stream);
-    if (NT == 2) return launch_attn<D, 2, HALF>(a, split_ctas, tc_ctas, stream);
-    return launch_attn<D, 4, HALF>(a, split_ctas, tc_ctas, stream);
+    return NT == 1 ? launch_attn<D, 1, HALF>(a, split_ctas, tc_ctas, stream)
+                   : launch_attn<D, 2, HALF>(a, split_ctas, tc_ctas, stream);
 }
 
 // Which kernels a call launches.  Rows of one request that share a KV head are
-// G * max_new at most.  Up to 32 of them the split kernel takes every request, in
-// row tiles of 8, 16 or 32 that read the keys once for all.  Beyond, requests with
-// more rows than a single token's tile holds go to the tile kernel; the split
-// kernel then runs for the others, unless there is but one request.
+// G * max_new at most.  Up to 16 of them the split kernel takes every request, in
+// row tiles of 8 or 16 that read the keys once for all.  Beyond, requests with more
+// rows than a single token's tile holds go to the tile kernel; the split kernel
+// then runs for the others, if there can be any.
 struct Choice {
     int NT, split_ctas, tc_ctas, split_rows;
 };
-inline Choice choose(int B, int G, int max_new) {
+inline Choice choose(int B, int G, int D, int max_new) {
     const int64_t rows = (int64_t)G * max_new;
-    const int64_t tile = rows <= 32 ? rows : G;
-    Choice c = {tile <= 8 ? 1 : (tile <= 16 ? 2 : 4), 0, 0, 0x7FFFFFFF};
-    c.split_ctas = num_sms() * split_per_sm(c.NT);
-    if (rows > 32) {
+    Choice c = {(rows <= 16 ? rows : G) <= 8 ? 1 : 2, 0, 0, 0x7FFFFFFF};
+    if (rows > 16) {
         c.tc_ctas = paged_attn_tc_ctas();
-        c.split_rows = B > 1 ? 8 * c.NT : 0;
-        if (B == 1) c.split_ctas = 0;
+        c.split_rows = B > 1 && G <= 16 ? 8 * c.NT : 0;
     }
+    if (c.split_rows) c.split_ctas = num_sms() * split_per_sm(D, c.NT);
     return c;
 }
 inline size_t split_partial_floats(const Choice &c, int D) { return (size_t)2 * c.split_ctas * 8 * c.NT * (D + 4); }
@@ -608,7 +658,7 @@ using namespace csa2;
 
 extern "C" size_t csa2_paged_attn_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new) {
     if (B <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0 || max_new <= 0) return 0;
-    const Choice c = choose(B, Hq / Hkv, max_new);
+    const Choice c = choose(B, Hq / Hkv, D, max_new);
     return (c.split_ctas + c.tc_ctas) * sizeof(JoinUnit) +
            (split_partial_floats(c, D) + (size_t)2 * c.tc_ctas * kTcRows * (D + 4)) * sizeof(float);
 }
@@ -649,7 +699,7 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
         set_error("paged_attn: workspace of %zu bytes (16-byte aligned) needed, %zu given", need, ws_bytes);
         return CSA2_ERR_WORKSPACE;
     }
-    const Choice c = choose(B, Hq / Hkv, max_new);
+    const Choice c = choose(B, Hq / Hkv, D, max_new);
     JoinUnit *join = (JoinUnit *)workspace;
     float *partial = (float *)(join + c.split_ctas + c.tc_ctas);
     const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride,

@@ -60,6 +60,17 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -154,20 +165,24 @@ struct Place {
     int h, r0, tile, tiles;         // KV head, first row, key tile of the unit, the unit's key tiles
 };
 
-// The split kernel's work: units of R = 8 NT rows, key tiles of 32; every row
-// tile of a request has the same tiles, at least one so that each row gets its
-// output.
-constexpr int kSplitKeys = 32;
-template <int R>
+// The split kernel's work: units of R = 8 NT rows, key tiles of K keys (4 KB of
+// keys); every row tile of a request has the same tiles, at least one so that each row gets its
+// output, and counts as a whole number of rounds of the CTA's warps, so that short
+// units go to CTAs of their own.
+constexpr int kSplitWarps = 4;
+template <int R, int K>
 struct SplitWork {
     static constexpr int ROWS = R;
     static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r) {
         const int64_t p = (int64_t)r.kv - r.n - a.window + 1;      // lowest key of the first row's window
-        return a.window > 0 && p > 0 ? (int)p & ~(kSplitKeys - 1) : 0;
+        return a.window > 0 && p > 0 ? (int)p & ~(K - 1) : 0;
+    }
+    static __device__ __forceinline__ int real_tiles(const PagedAttnArgs &a, const Request &r) {
+        const int keys = r.kv - first_key(a, r);
+        return keys > 0 ? (keys + K - 1) / K : 1;
     }
     static __device__ __forceinline__ int unit_tiles(const PagedAttnArgs &a, const Request &r) {
-        const int keys = r.kv - first_key(a, r);
-        return keys > 0 ? (keys + kSplitKeys - 1) / kSplitKeys : 1;
+        return (real_tiles(a, r) + kSplitWarps - 1) / kSplitWarps * kSplitWarps;
     }
     static __device__ __forceinline__ int64_t tiles(const PagedAttnArgs &a, const Request &r) {
         const int rows = r.n * a.G;
@@ -187,7 +202,7 @@ struct SplitWork {
 
 // The tile kernel's work: units of 256 rows, key tiles of 128, for each row tile
 // those that its first to last row see.
-constexpr int kTcRows = 256, kTcKeys = 128, kTcRound = 2;
+constexpr int kTcRows = 256, kTcKeys = 128, kTcRound = 1;
 struct TcWork {
     static constexpr int ROWS = kTcRows;
     // A walk over the row tiles of a request, without a division per step.

@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 boff = ok ? (bh * a.S + (key & (a.S - 1))) * D : -1;
                 bks = ok ? a.k_scale[bh] : 0.0f;
                 bvs = ok ? a.v_scale[bh] : 0.0f;
-                blg = log2f(bvs);
-                brv = 1.0f / bvs;
+                blg = lg2(bvs);
+                brv = rcp(bvs);
                 bmiss = __ballot_sync(ALL, !ok);
             }
             cur = tile_ahead - batch;
