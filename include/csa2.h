@@ -378,10 +378,11 @@ size_t csa2_sparse_attn_noalloc_max_scratch_bytes(void);
  *
  *   k_codes, v_codes  uint8 [n_blocks, Hkv, S, D], a block's rows of one head
  *                     contiguous; S in {16, 32, 64, 128} tokens, D in {64, 128}
- *   k_scale, v_scale  fp32 [n_blocks, Hkv], not negative; a value is code * scale
+ *   k_scale, v_scale  fp32 [n_blocks, Hkv], finite, not negative; a value is code * scale
  *   block_table       int32 [B, M] (row stride table_stride): token position p
  *                     of request b is row p % S of block block_table[b][p / S]
  *   slot of a token   block * S + row, int64; -1: the token is not stored
+ * A block holds tokens of one request.
  *
  * One step of a serving loop is csa2_build_slots (which blocks the new tokens
  * go to), csa2_quantize_kv_fp8_paged (store them) per layer, then
@@ -473,8 +474,8 @@ csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, csa2_dtype 
  * q, out  bf16 or fp16 [T, Hq, D], q with token and head strides in elements
  *         (multiples of 8), out dense; 16-byte aligned.  Hq a multiple of Hkv.
  * lse     fp32 [T, Hq] or NULL.
- * kv_len int32 [B], cu_len int32 [B + 1] (clamped to [0, T]); tokens beyond
- *         M * S are not there.  A table entry outside [0, n_blocks) where a
+ * kv_len int32 [B] (after the step), cu_len int32 [B + 1] (clamped to [0, T]);
+ *         tokens beyond M * S are not there.  M * S <= 2^30, T * Hq / Hkv <= 2^30.  A table entry outside [0, n_blocks) where a
  *         visible key should be hides its keys (CSA2_FLAG_BAD_INDEX).
  * max_new upper bound (>= 1) of the rows of a request, known on the host: it only
  *         chooses among kernels, every value >= 1 gives right results.

@@ -24,10 +24,11 @@ constexpr int kHalf = 4096;             // bytes of a warp tile's keys, and of i
 template <int D>
 constexpr int kTileKeys = kHalf / D;
 constexpr int kStages = 2;              // tiles in flight per warp
-// CTAs that an SM holds at once.  128 channels: two of 255 registers stream faster
-// than three of 168 (attn over 64 x 16k tokens, 8 heads: 195 against 203 us; 16 rows
-// per tile, 19 x 32k tokens: 60 against 88).
-constexpr int split_per_sm(int D, int NT) { return D == 128 ? 2 : (NT == 1 ? 4 : 3); }
+// CTAs that an SM holds at once: two of 255 registers stream faster than three of
+// 168 (64 requests of up to 16k tokens, 8 heads of 128: 195 against 203 us; 16 rows
+// per tile, 19 of up to 32k: 60 against 88), and two tiles in flight per warp faster
+// than three (195 against 204).
+constexpr int kSplitPerSm = 2;
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
@@ -276,7 +277,7 @@ constexpr int attn_smem() {
 }
 
 template <int D, int NT, bool HALF>
-__global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(D, NT)) paged_attn_split_kernel(PagedAttnArgs a) {
+__global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split_kernel(PagedAttnArgs a) {
     constexpr int R = 8 * NT;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -364,8 +365,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, split_per_sm(D, NT)) paged_at
                             for (int x = 0; x < 16 / RPI; ++x) {
                                 const bool there = x * RPI + r1 < stored;
                                 const uint32_t to = dst + chunk_at<D>(16 * u + x * RPI + r1, c);
-                                cp_async16(to, there ? ksrc + x * RPI * D : a.k_codes, there ? 16 : 0);
-                                cp_async16(to + kHalf, there ? vsrc + x * RPI * D : a.v_codes, there ? 16 : 0);
+                                cp_async16(to, there ? (const void *)(ksrc + x * RPI * D) : a.q, there ? 16 : 0);
+                                cp_async16(to + kHalf, there ? (const void *)(vsrc + x * RPI * D) : a.q, there ? 16 : 0);
                             }
                         }
                     }
@@ -639,14 +640,14 @@ cudaError_t launch_attn_nt(int NT, const PagedAttnArgs &a, int split_ctas, int t
 struct Choice {
     int NT, split_ctas, tc_ctas, split_rows;
 };
-inline Choice choose(int B, int G, int D, int max_new) {
+inline Choice choose(int B, int G, int max_new) {
     const int64_t rows = (int64_t)G * max_new;
     Choice c = {(rows <= 16 ? rows : G) <= 8 ? 1 : 2, 0, 0, 0x7FFFFFFF};
     if (rows > 16) {
         c.tc_ctas = paged_attn_tc_ctas();
         c.split_rows = B > 1 && G <= 16 ? 8 * c.NT : 0;
     }
-    if (c.split_rows) c.split_ctas = num_sms() * split_per_sm(D, c.NT);
+    if (c.split_rows) c.split_ctas = num_sms() * kSplitPerSm;
     return c;
 }
 inline size_t split_partial_floats(const Choice &c, int D) { return (size_t)2 * c.split_ctas * 8 * c.NT * (D + 4); }
@@ -658,7 +659,7 @@ using namespace csa2;
 
 extern "C" size_t csa2_paged_attn_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new) {
     if (B <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0 || max_new <= 0) return 0;
-    const Choice c = choose(B, Hq / Hkv, D, max_new);
+    const Choice c = choose(B, Hq / Hkv, max_new);
     return (c.split_ctas + c.tc_ctas) * sizeof(JoinUnit) +
            (split_partial_floats(c, D) + (size_t)2 * c.tc_ctas * kTcRows * (D + 4)) * sizeof(float);
 }
@@ -678,7 +679,7 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
     CSA2_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536, "paged_attn: Hq=%d, Hkv=%d", Hq, Hkv);
     CSA2_REQUIRE(T * (Hq / Hkv) <= (1ll << 30), "paged_attn: T * Hq / Hkv = %lld rows", (long long)(T * (Hq / Hkv)));
     CSA2_REQUIRE(S == 16 || S == 32 || S == 64 || S == 128, "paged_attn: S=%d not in {16, 32, 64, 128}", S);
-    CSA2_REQUIRE(M >= 1 && (int64_t)M * S < (1ll << 31), "paged_attn: M=%d: need 1 <= M, M * S < 2^31", M);
+    CSA2_REQUIRE(M >= 1 && (int64_t)M * S <= (1ll << 30), "paged_attn: M=%d: need 1 <= M, M * S <= 2^30", M);
     CSA2_REQUIRE(table_stride >= M, "paged_attn: table_stride=%lld < M=%d", (long long)table_stride, M);
     CSA2_REQUIRE(n_blocks >= 0 && n_blocks < (1ll << 31), "paged_attn: n_blocks=%lld", (long long)n_blocks);
     CSA2_REQUIRE(max_new >= 1, "paged_attn: max_new=%d < 1", max_new);
@@ -699,7 +700,7 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
         set_error("paged_attn: workspace of %zu bytes (16-byte aligned) needed, %zu given", need, ws_bytes);
         return CSA2_ERR_WORKSPACE;
     }
-    const Choice c = choose(B, Hq / Hkv, D, max_new);
+    const Choice c = choose(B, Hq / Hkv, max_new);
     JoinUnit *join = (JoinUnit *)workspace;
     float *partial = (float *)(join + c.split_ctas + c.tc_ctas);
     const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride,

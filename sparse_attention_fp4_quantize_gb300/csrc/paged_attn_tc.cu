@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 for (int i = 0; i < N; ++i) {
                     const int u = i / (N / 2), r = (i % (N / 2)) * RPI + r0; // 16-key group, row of it
                     const bool there = r < rows[u];                          // rows that are not there read as zero
-                    cp_async16(stage + chunk_at<D>(16 * u + r, c), codes + (there ? off[u] + r * D + 16 * c : 0), there ? 16 : 0);
+                    cp_async16(stage + chunk_at<D>(16 * u + r, c), there ? (const void *)(codes + off[u] + r * D + 16 * c) : a.q, there ? 16 : 0);
                 }
             }
             cp_async_commit();

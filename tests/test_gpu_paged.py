@@ -545,3 +545,125 @@ def test_serving_loop(csa2, S, dtype):
     out, lse = _serve(csa2, S, dtype, False, 6)
     out2, lse2 = _serve(csa2, S, dtype, True, 6)                          # captured and replayed: the same bits
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+# ---------------------------------------------------------------- more of the attention
+@pytest.mark.parametrize("kv,new,Hq,H,D,S", [
+    ([3000, 17], [1, 1], 16, 1, 128, 32),          # 16 rows per KV head, one token
+    ([2000, 31], [1, 1], 32, 1, 64, 16),           # 32 rows: the tile kernel for single tokens
+    ([900, 1, 450], [2, 1, 2], 24, 3, 64, 64),     # 8 and 16 rows of one call
+    ([9000], [70], 2, 1, 64, 128),                 # a chunk behind a long prefix: parts joined over many CTAs
+    ([9000], [33], 8, 1, 128, 64),
+    ([129, 128, 127, 256, 257], [129, 128, 127, 256, 257], 1, 1, 128, 64),   # tile borders
+    ([5000], [1], 3, 3, 64, 64),
+])
+def test_more_layouts(csa2, kv, new, Hq, H, D, S):
+    for dtype in (torch.bfloat16, torch.float16):
+        inp = _attn_inputs(sum(kv) + Hq, kv, new, Hq, H, D, S, dtype)
+        out, lse = _attend(csa2, inp, 0.05, max(new))
+        ref.check_attention(out, lse, _reference(inp, 0.05))
+
+
+@pytest.mark.parametrize("new", [1, 80])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_that_grow_and_shrink(csa2, new, D):
+    """Scores whose scale rises or falls block by block, V scales against them: references move often, or never."""
+    for step in (0.5, -0.5, 3.0):
+        inp = list(_attn_inputs(31, [1000], [new], 4, 1, D, 16, torch.bfloat16))
+        at = torch.zeros(inp[3].shape[0])
+        used = inp[5][0, :63].long()
+        at[used] = torch.arange(63).float()
+        if abs(step) < 1:
+            inp[3] = torch.exp2(torch.round(step * at - 8 if step > 0 else step * at + 4)).clamp(2.0 ** -20, 2.0 ** 5)[:, None].contiguous()
+        else:
+            inp[3] = torch.full_like(inp[3], 2.0 ** -4)
+            inp[4] = torch.exp2((step * at) % 41 - 20).round()[:, None].clamp(2.0 ** -20, 2.0 ** 20).contiguous()
+        for sm in (0.02, 0.3):
+            out, lse = _attend(csa2, inp, sm, new)
+            ref.check_attention(out, lse, _reference(inp, sm))
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_sign_and_zero_of_the_scale(csa2, new):
+    inp = list(_attn_inputs(32, [700], [new], 4, 2, 64, 64, torch.float16))
+    for sm in (-0.2, 0.0):
+        out, lse = _attend(csa2, inp, sm, new)
+        ref.check_attention(out, lse, _reference(inp, sm))
+    inp[3], inp[4] = torch.zeros_like(inp[3]), torch.zeros_like(inp[4])       # a cache of zero scales: every value 0
+    out, lse = _attend(csa2, inp, 0.2, new)
+    ref.check_attention(out, lse, _reference(inp, 0.2))
+
+
+def test_many_short_requests(csa2):
+    rng = np.random.default_rng(5)
+    kv = rng.integers(0, 50, 700)
+    new = np.minimum(rng.choice([0, 1, 1, 1, 2, 30], 700), kv)
+    inp = _attn_inputs(33, list(kv), list(new), 4, 2, 64, 16, torch.bfloat16)
+    for hint in (1, 30):
+        out, lse = _attend(csa2, inp, 0.1, hint, pad=1)
+        ref.check_attention(out, lse, _reference(inp, 0.1))
+
+
+def test_a_cache_without_blocks(csa2):
+    q = torch.randn(3, 4, 64, device=DEV).to(torch.bfloat16)
+    planes = [torch.empty(0, 2, 16, 64, dtype=torch.uint8, device=DEV)] * 2 + [torch.empty(0, 2, device=DEV)] * 2
+    table = torch.full((2, 3), -1, dtype=I32, device=DEV)
+    for kv, flag in ([0, 0], 0), ([5, 0], 1):
+        for hint in (1, 100):
+            out, lse = torch.full_like(q, 3.0), torch.full((3, 4), 3.0, device=DEV)
+            err = torch.zeros(1, dtype=I32, device=DEV)
+            csa2.csa2_paged_attn_fp8(q, *planes, table, torch.tensor(kv, dtype=I32, device=DEV),
+                                     torch.tensor([0, 2, 3], dtype=I32, device=DEV), out, 0.1, hint, lse=lse, err_flag=err)
+            torch.cuda.synchronize()
+            assert (out == 0).all() and torch.isneginf(lse).all() and int(err) == flag
+
+
+def test_calls_on_two_streams_and_in_two_graphs(csa2):
+    """Calls that overlap have a workspace each; a graph replayed between eager calls gives the eager bits."""
+    a = _attn_inputs(34, [4000, 300], [1, 1], 8, 1, 128, 64, torch.bfloat16)
+    b = _attn_inputs(35, [600, 900], [300, 200], 8, 2, 128, 32, torch.bfloat16)
+    want = [_attend(csa2, x, 0.1, n) for x, n in ((a, 1), (b, 300))]
+    dev = [[t.to(DEV) for t in x] for x in (a, b)]
+    outs = [(torch.zeros_like(w[0]), torch.zeros_like(w[1])) for w in want]
+    ws = [csa2.workspace_for_paged_attn(2, x[0].shape[0], 8, x[1].shape[1], 128, n) for x, n in ((a, 1), (b, 300))]
+
+    def call(i, stream=None):
+        q, kc, vc, ks, vs, table, kv, cu = dev[i]
+        csa2.csa2_paged_attn_fp8(q, kc, vc, ks, vs, table, kv, cu, outs[i][0], 0.1, (1, 300)[i], lse=outs[i][1],
+                                 workspace=ws[i], stream=stream)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            call(i, streams[i])
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i)
+        graphs.append(g)
+    for i in range(2):
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+        outs[i][0].zero_(), outs[i][1].zero_()
+    for _ in range(3):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+
+
+def test_append_in_windows_of_many_rows(csa2):
+    """Enough rows that a warp looks at a window of them: runs that begin inside, end behind and span windows."""
+    H, D, S, T = 4, 64, 16, 9000
+    gen = torch.Generator().manual_seed(12)
+    counts = [1] * 40 + [5] * 30 + [S] * 20 + [S + 1] * 20 + [7000]
+    starts = [(7 * i) % (2 * S) for i in range(len(counts))]
+    slots, n = _request_slots(gen, starts, counts, S)
+    slots = torch.cat([slots, torch.full((T - slots.numel(),), -1)]).to(DEV)
+    k = torch.randn(T, H, D, generator=gen).to(torch.bfloat16).to(DEV)
+    v = torch.randn(T, H, D, generator=gen).to(torch.bfloat16).to(DEV)
+    _append_both(csa2, k, v, slots, _planes(13, n, H, S, D), S)
