@@ -12,11 +12,18 @@
 // entry n_free + k of that stack is block k - f_b of the ended request b that
 // holds k, found by bisection in f.
 //
-// One thread-block cluster does it in one launch: every CTA computes the
-// prefix sums of all requests itself (a few KB from L2, so no CTA waits for
-// another's sums), then the cluster's threads share the rows.  The results
-// kv_len_out, free_count_out are written after a cluster barrier, when every
-// CTA has read the inputs, so they may be the inputs themselves.
+// One launch: every CTA computes the prefix sums of all requests itself (a few KB
+// from L2, so no CTA waits for another's sums), then the CTAs share the rows, four
+// per thread and step.  Where the results go to the inputs themselves (a captured
+// step), the CTAs are one thread-block cluster and write them behind its barrier,
+// when every CTA has read what they replace.
+//
+// Bound by latency: a launch, two loads in a row, three prefix sums, a bisection
+// and a load.  On the GPU, from a cold L2: 32 requests decoding 7.7 us, 512 mixed
+// (16384 rows, blocks of 16, some ended) 12.1 us, 2000 prompts (65536 rows) 10.3 us;
+// a call from Python takes about 9 us of host time, so that only the last two show.
+// With one cluster for every call the prompts took 16 us: eight CTAs have 13 rows
+// per thread.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -38,6 +45,7 @@ struct SlotArgs {
     int64_t *slots;
     uint32_t *err_flag;
     bool wide;                       // slots and positions are 16-byte aligned
+    bool in_place;                   // the CTAs are a cluster
 };
 
 // Exclusive prefix sums over the block of N values per thread; totals to all.
@@ -96,9 +104,9 @@ __global__ void build_slots_kernel(SlotArgs a) {
     int32_t *s_kv = s_cu + a.B;            // tokens held
     int32_t *s_take = s_kv + a.B;          // first block taken, -1: waits
     int32_t *s_freed = s_take + a.B;       // first place among the freed blocks
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int rank = blockIdx.x, ranks = gridDim.x;
     const int tid = threadIdx.x, nt = blockDim.x;
+    const uint32_t S = a.S;
     const int per = (a.B + nt - 1) / nt, b0 = tid * per, b1 = min(a.B, b0 + per);
     const int64_t cap = (int64_t)a.M * a.S;
     uint32_t flags = 0;
@@ -114,7 +122,7 @@ __global__ void build_slots_kernel(SlotArgs a) {
         if (kv != k) flags |= CSA2_FLAG_BAD_INDEX;
         s_kv[b] = kv;
         if (n > 0) rows += n < a.T + 1 ? n : a.T + 1;
-        if (n < 0) freed += (kv + (int64_t)a.S - 1) / a.S;
+        if (n < 0) freed += (kv + S - 1) / S;
     }
     const int64_t fc = *a.free_count;
     int64_t sums[2] = {rows, freed}, totals[2];
@@ -126,41 +134,39 @@ __global__ void build_slots_kernel(SlotArgs a) {
     const int64_t size = n_free + n_freed;
 
     int64_t need = 0;
-    const int64_t cu0 = cu;
     for (int b = b0; b < b1; ++b) {
-        const int64_t n = a.new_len[b], kv = s_kv[b], held = (kv + a.S - 1) / a.S;
+        const int64_t n = a.new_len[b];
+        const uint32_t kv = s_kv[b], held = (kv + S - 1) / S;
         s_cu[b] = (int32_t)(cu < a.T ? cu : a.T);
         s_freed[b] = (int32_t)fr;
+        uint32_t more = 0;                 // blocks it asks for, if its tokens fit
         if (n > 0) {
             cu += n < a.T + 1 ? n : a.T + 1;
-            if (cu <= a.T && kv + n <= cap) need += (kv + n + a.S - 1) / a.S - held;
+            if (cu <= a.T && kv + n <= cap) need += more = (kv + (uint32_t)n + S - 1) / S - held;
+            else flags |= CSA2_FLAG_BAD_SLOT, more = 0xFFFFFFFFu;
         } else if (n < 0) {
             fr += held;
         }
+        s_take[b] = (int32_t)more;
     }
     int64_t wanted[1] = {need}, n_need[1];
     block_scan<1>(wanted, warp_sums + 2, n_need);
     int64_t take = wanted[0];
     int taken = 0;
-    cu = cu0;
     for (int b = b0; b < b1; ++b) {
-        const int64_t n = a.new_len[b], kv = s_kv[b], held = (kv + a.S - 1) / a.S;
-        int32_t first = -1;
-        if (n == 0) first = 0;
-        if (n > 0) {
-            cu += n < a.T + 1 ? n : a.T + 1;
-            if (cu <= a.T && kv + n <= cap) {
-                const int64_t more = (kv + n + a.S - 1) / a.S - held;
-                if (more == 0 || take + more <= size) {
-                    first = more ? (int32_t)take : 0;
-                    if (more) taken = (int)(take + more);
-                } else {
-                    flags |= CSA2_FLAG_NO_BLOCKS;
-                }
-                take += more;
+        const uint32_t more = (uint32_t)s_take[b];
+        int32_t first = 0;
+        if (more == 0xFFFFFFFFu) {
+            first = -1;
+        } else if (more) {
+            if (take + more <= size) {
+                first = (int32_t)take;
+                taken = (int)(take + more);
             } else {
-                flags |= CSA2_FLAG_BAD_SLOT;
+                first = -1;
+                flags |= CSA2_FLAG_NO_BLOCKS;
             }
+            take += more;
         }
         s_take[b] = first;
     }
@@ -179,7 +185,6 @@ __global__ void build_slots_kernel(SlotArgs a) {
     // four rows per thread and step: one search, and mostly one block, for all of them
     const int64_t step = (int64_t)ranks * nt;
     const int64_t end = n_rows < a.T ? n_rows : a.T;
-    const uint32_t S = a.S;
     for (int64_t t0 = ((int64_t)rank * nt + tid) * 4; t0 < a.T; t0 += step * 4) {
         int64_t slot[4];
         int32_t pos[4], b = 0, block = -1;
@@ -227,12 +232,12 @@ __global__ void build_slots_kernel(SlotArgs a) {
     for (int64_t k = (int64_t)rank * nt + tid; k < count - n_free; k += step) a.free_list[n_free + k] = freed_block(k);
     if (flags) flag_error(a.err_flag, flags);
 
-    cluster.sync();   // every CTA has read kv_len, new_len and free_count
+    if (a.in_place) cg::this_cluster().sync();   // every CTA has read kv_len and free_count
     if (rank == 0) {
         for (int b = tid; b < a.B; b += nt) {
             const int64_t n = a.new_len[b];
             const int32_t kv = s_kv[b];
-            a.kv_out[b] = n < 0 ? 0 : (s_take[b] >= 0 ? (int32_t)(kv + n) : kv);
+            a.kv_out[b] = n < 0 ? 0 : (n > 0 && s_take[b] >= 0 ? (int32_t)(kv + n) : kv);
             a.cu[b] = s_cu[b];
         }
         if (tid == 0) {
@@ -263,27 +268,30 @@ extern "C" csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int 
                  "build_slots: null pointer");
     CSA2_REQUIRE((free_list || free_cap == 0) && (slots || T == 0), "build_slots: null pointer");
     CSA2_REQUIRE(aligned(slots, 8), "build_slots: slots must be 8-byte aligned");
+    const bool in_place = kv_len_out == kv_len || free_count_out == free_count;
     const SlotArgs args = {B, M, S, table_stride, T, free_cap, kv_len, new_len, block_table, free_list, free_count,
                            kv_len_out, free_count_out, cu_len, positions, slots, err_flag,
-                           aligned(slots, 16) && aligned(positions, 16)};
+                           aligned(slots, 16) && aligned(positions, 16), in_place};
     const size_t smem = (size_t)B * 4 * sizeof(int32_t);
     static bool done[64];
     if (smem > 40 * 1024)
         CSA2_CUDA_CALL(ensure_smem_limit((const void *)build_slots_kernel, kMaxRequests * 16, done),
                        "build_slots: shared memory limit");
-    const int64_t work = (T + 3) / 4 > B ? (T + 3) / 4 : B;     // threads that have something to do
+    const int64_t quads = (T + 3) / 4, work = quads > B ? quads : B;     // threads that have something to do
+    // a CTA for 4096 rows or 32 requests (whose blocks may come back), whichever asks for more
+    const int64_t most = in_place ? 8 : num_sms(), want = quads / 1024 + 1 > B / 32 ? quads / 1024 + 1 : B / 32;
+    const int ctas = (int)(want < 1 ? 1 : (want < most ? want : most));
     cudaLaunchConfig_t cfg = {};
-    const int ctas = (T + 3) / 4 > 1024 ? 8 : 1;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(work <= 128 ? 128 : (work <= 512 ? 512 : 1024));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream_of(stream);
     cudaLaunchAttribute at[2] = {pdl_attribute(), {}};
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = ctas;
+    at[1].val.clusterDim.x = in_place ? ctas : 1;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = in_place ? 2 : 1;
     CSA2_CUDA_CALL(cudaLaunchKernelEx(&cfg, build_slots_kernel, args), "build_slots_kernel launch");
     CSA2_LAUNCH_CHECK("build_slots_kernel");
     return CSA2_OK;
