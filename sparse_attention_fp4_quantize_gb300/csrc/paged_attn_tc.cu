@@ -306,20 +306,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             };
             auto unlock = [&]() { *reinterpret_cast<volatile unsigned int *>(tensor_lock) = 0u; };
             auto issue_s = [&](uint32_t tile) {
-                const uint64_t k = tc::desc_at(dk, (tile & 1) * L::KV);
+                const uint32_t q = (uint32_t)dq, k = (uint32_t)dk + (tile & 1) * (L::KV / 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     if (ks == D / 32) unlock();
-                    tc::mma_f16(ts, tc::desc_at(dq, ks * 256), tc::desc_at(k, ks * 256), idesc_s, ks > 0);
+                    tc::mma_f16_lo(ts, q + ks * 16, k + ks * 16, (uint32_t)(dk >> 32), idesc_s, ks > 0);
                 }
                 tc::commit(sfull(sub));
                 tc::commit(kempty(tile & 1));
             };
             auto issue_o = [&](uint32_t tile, bool first) {
-                const uint64_t v = tc::desc_at(dv, (tile & 1) * L::KV);
+                const uint32_t v = (uint32_t)dv + (tile & 1) * (L::KV / 16);
 #pragma unroll
                 for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                    tc::mma_f16_ta(to, ts + ks * 8, tc::desc_at(v, ks * 2 * L::GROUP), idesc_o, !first || ks > 0);
+                    tc::mma_f16_ta_lo(to, ts + ks * 8, v + ks * (L::GROUP / 8), (uint32_t)(dv >> 32), idesc_o, !first || ks > 0);
                 tc::commit(ofull(sub));
                 tc::commit(vempty(tile & 1));
             };
