@@ -303,10 +303,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
         while (at < stop && at < end) {
             // segment: tiles [ta, tb) of one unit
             const Place pl = Work::place(a, rq, at - base);
-            const int h = pl.h, r0 = pl.r0, ta = pl.tile, tb = (int)min((int64_t)pl.tiles, ta + (stop - at));
-            if (tid == 0 && ta == 0 && tb < pl.tiles)
-                a.join[blockIdx.x] = {rq.row0, h, r0, rows, (int)((at + pl.tiles - 1) / plan.share), {0, 0}};
-            at += tb - ta;
+            const int64_t unit = at - pl.tile;       // its first place
+            at = min(stop, unit + pl.tiles);
+            const int h = pl.h, r0 = pl.r0, ta = max(0, pl.tile - kSplitCost), tb = (int)(at - unit) - kSplitCost;
+            if (tb <= 0) continue;
+            const bool first_part = ta == 0, whole = first_part && at == unit + pl.tiles;
+            if (tid == 0 && first_part && !whole)
+                a.join[blockIdx.x] = {rq.row0, h, r0, rows, (int)((unit + pl.tiles - 1) / plan.share), {0, 0}};
 
             // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / U, 16-key group lane % U) of 32 / U of them
             constexpr int U = kTileKeys<D> / 16, BT = 32 / U;
@@ -433,16 +436,15 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                 const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys<D>;
                 const uint32_t kb = ring + (i % kStages) * (2 * kHalf);
                 const StageMeta<D> &meta = s_meta[warp][i % kStages];
-                bool whole = key >= all_lo && key + kTileKeys<D> <= all_hi;
+                bool plain = key >= all_lo && key + kTileKeys<D> <= all_hi;
 #pragma unroll
-                for (int u = 0; u < U; ++u) whole = whole && meta.stored[u] == 16;
-                tile.keys(kb, kb + kHalf, meta, zf, !__all_sync(ALL, whole), key, s_seen[warp]);
+                for (int u = 0; u < U; ++u) plain = plain && meta.stored[u] == 16;
+                tile.keys(kb, kb + kHalf, meta, zf, !__all_sync(ALL, plain), key, s_seen[warp]);
                 __syncwarp();
             }
             cp_async_wait<0>();
 
             // the warps' shares meet in shared memory, 8 rows at a time
-            const bool whole = ta == 0 && tb == pl.tiles;
             float *s_o = reinterpret_cast<float *>(smem);
             constexpr int LD = D + 4;
 #pragma unroll
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                         const int tok = row / a.G;
                         store_row<D, HALF, 16>(a, (rq.row0 + tok) * a.Hq + h * a.G + row - tok * a.G, part, o, M, l);
                     } else {
-                        float *dst = a.partial + ((2 * (int64_t)blockIdx.x + (ta == 0)) * R + 8 * x + y) * LD;
+                        float *dst = a.partial + ((2 * (int64_t)blockIdx.x + first_part) * R + 8 * x + y) * LD;
 #pragma unroll
                         for (int c = 0; c < D / 16; c += 4)
                             *reinterpret_cast<float4 *>(dst + part * (D / 16) + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);

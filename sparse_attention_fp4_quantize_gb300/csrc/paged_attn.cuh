@@ -107,7 +107,9 @@ __device__ __forceinline__ Request request_of(const PagedAttnArgs &a, int b) {
 // and row tiles, are one long line that the CTAs cut into equal shares: a ragged
 // batch loads every SM alike, and a long context is split over as many CTAs as
 // it is worth.  A CTA's piece of a unit is a segment; only its first and its
-// last segment can be parts of a unit.
+// last segment can be parts of a unit.  A segment's fixed cost (its rows of Q, the
+// first loads, its output) counts too: a unit stands in the line with so many
+// places more, before its tiles, which nobody works on.
 struct Plan {
     int64_t share;                  // key tiles per CTA, a multiple of `round`
     int b;                          // request that holds the CTA's first tile (if there is one)
@@ -162,14 +164,17 @@ __device__ __forceinline__ Plan plan_of(const PagedAttnArgs &a, int cta, int cta
 
 // Where in a unit a place of the line is.
 struct Place {
-    int h, r0, tile, tiles;         // KV head, first row, key tile of the unit, the unit's key tiles
+    int h, r0, tile, tiles;         // KV head, first row, place in the unit, the unit's places
 };
 
 // The split kernel's work: units of R = 8 NT rows, key tiles of K keys (4 KB of
 // keys); every row tile of a request has the same tiles, at least one so that each row gets its
 // output, and counts as a whole number of rounds of the CTA's warps, so that short
 // units go to CTAs of their own.
-constexpr int kSplitWarps = 4;
+// kSplitCost: 64 requests of up to 16k tokens (8 heads of 128) 185 us with 16, 192 with
+// 0; 48 of up to 9k in a window of 4096 (5 heads of 64) 36.7, 42.0; 24: 187, 38.7.
+constexpr int kSplitWarps = 4, kSplitCost = 16;
+static_assert(kSplitCost % kSplitWarps == 0, "segments begin at whole rounds of the warps");
 template <int R, int K>
 struct SplitWork {
     static constexpr int ROWS = R;
@@ -181,15 +186,15 @@ struct SplitWork {
         const int keys = r.kv - first_key(a, r);
         return keys > 0 ? (keys + K - 1) / K : 1;
     }
-    static __device__ __forceinline__ int unit_tiles(const PagedAttnArgs &a, const Request &r) {
-        return (real_tiles(a, r) + kSplitWarps - 1) / kSplitWarps * kSplitWarps;
+    static __device__ __forceinline__ int unit_places(const PagedAttnArgs &a, const Request &r) {
+        return kSplitCost + (real_tiles(a, r) + kSplitWarps - 1) / kSplitWarps * kSplitWarps;
     }
     static __device__ __forceinline__ int64_t tiles(const PagedAttnArgs &a, const Request &r) {
         const int rows = r.n * a.G;
-        return rows > a.split_rows ? 0 : (int64_t)((rows + R - 1) / R) * a.Hkv * unit_tiles(a, r);
+        return rows > a.split_rows ? 0 : (int64_t)((rows + R - 1) / R) * a.Hkv * unit_places(a, r);
     }
     static __device__ __forceinline__ Place place(const PagedAttnArgs &a, const Request &r, int64_t off) {
-        const int row_tiles = (r.n * a.G + R - 1) / R, per = unit_tiles(a, r);
+        const int row_tiles = (r.n * a.G + R - 1) / R, per = unit_places(a, r);
         const int unit = (int)(off / per);
         Place p;
         p.h = unit / row_tiles;
@@ -202,7 +207,9 @@ struct SplitWork {
 
 // The tile kernel's work: units of 256 rows, key tiles of 128, for each row tile
 // those that its first to last row see.
-constexpr int kTcRows = 256, kTcKeys = 128, kTcRound = 1;
+// kTcCost: 3 prompts of up to 4096 tokens on up to 8192 (32 heads of 128) 854 us with 4 and
+// with 6, 905 with 0, 872 with 10.
+constexpr int kTcRows = 256, kTcKeys = 128, kTcRound = 1, kTcCost = 5;
 struct TcWork {
     static constexpr int ROWS = kTcRows;
     // A walk over the row tiles of a request, without a division per step.
@@ -223,15 +230,15 @@ struct TcWork {
         const int64_t p = (int64_t)r.kv - r.n + w.tok - a.window + 1;
         return a.window > 0 && p > 0 ? (int)p & ~(kTcKeys - 1) : 0;
     }
-    static __device__ __forceinline__ int unit_tiles(const PagedAttnArgs &a, const Request &r, const Rows &w) {
+    static __device__ __forceinline__ int unit_places(const PagedAttnArgs &a, const Request &r, const Rows &w) {
         const int last = min(w.last_tok(), r.n - 1);
         const int keys = min(r.kv, r.kv - r.n + last + 1) - first_key(a, r, w);
-        return keys > 0 ? (keys + kTcKeys - 1) / kTcKeys : 1;
+        return kTcCost + (keys > 0 ? (keys + kTcKeys - 1) / kTcKeys : 1);
     }
     static __device__ __forceinline__ bool mine(const PagedAttnArgs &a, const Request &r) { return r.n * a.G > a.split_rows; }
     static __device__ __forceinline__ int64_t head_tiles(const PagedAttnArgs &a, const Request &r) {
         int64_t n = 0;
-        for (Rows w(a.G); w.r0 < r.n * a.G; w.next()) n += unit_tiles(a, r, w);
+        for (Rows w(a.G); w.r0 < r.n * a.G; w.next()) n += unit_places(a, r, w);
         return n;
     }
     static __device__ __forceinline__ int64_t tiles(const PagedAttnArgs &a, const Request &r) {
@@ -244,7 +251,7 @@ struct TcWork {
         p.h = (int)(off / per);
         int64_t left = off - p.h * per;
         for (;; w.next()) {
-            p.tiles = unit_tiles(a, r, w);
+            p.tiles = unit_places(a, r, w);
             if (left < p.tiles) break;
             left -= p.tiles;
         }

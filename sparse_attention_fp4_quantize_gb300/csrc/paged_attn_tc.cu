@@ -48,7 +48,7 @@ constexpr int kSegs = 4;
 struct alignas(16) Segment {
     Request rq;
     Place pl;
-    int b, tb;                               // request, end of its key tiles [pl.tile, tb)
+    int b, tb;                               // request, end of its key tiles [pl.tile, tb) of pl.tiles
     int rows, key0;                          // rows of the request and KV head (0: no more segments); key of the unit's first tile
 };
 
@@ -141,7 +141,7 @@ __device__ __forceinline__ float factor(float zf, float ks) { return fmaxf(zf * 
 
 // The CTA's segments in order.
 struct Walk {
-    int64_t at, stop, base;
+    int64_t at, stop, base, unit;            // place of the line, its end; first places of the request, of the unit
     Request rq;
     TcWork::Rows rows;
     int b, h;                     // h < 0: before the first segment
@@ -168,14 +168,17 @@ struct Walk {
             s.pl.h = h;
             s.pl.r0 = rows.r0;
             s.pl.tile = 0;
-            s.pl.tiles = TcWork::unit_tiles(a, rq, rows);
+            s.pl.tiles = TcWork::unit_places(a, rq, rows);
         }
+        unit = at - s.pl.tile;
+        at = min(stop, unit + s.pl.tiles);
         s.rq = rq;
         s.b = b;
-        s.tb = (int)min((int64_t)s.pl.tiles, s.pl.tile + (stop - at));
+        s.tb = (int)(at - unit) - kTcCost;
+        s.pl.tile = max(0, s.pl.tile - kTcCost);             // from places to tiles
+        s.pl.tiles -= kTcCost;
         s.rows = rq.n * a.G;
         s.key0 = TcWork::first_key(a, rq, rows);
-        at += s.tb - s.pl.tile;
         return true;
     }
 };
@@ -278,10 +281,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             join->last = -1;
             for (bool more = true; more; ++n_seg) {
                 Segment s = {};
-                const int64_t at = walk.at;
-                more = walk.next(a, s);
+                do more = walk.next(a, s);
+                while (more && s.tb <= 0);
+                if (!more) s.rows = 0;
                 if (more && s.pl.tile == 0 && s.tb < s.pl.tiles)
-                    *join = {s.rq.row0, s.pl.h, s.pl.r0, s.rows, (int)((at + s.pl.tiles - 1) / plan.share), {0, 0}};
+                    *join = {s.rq.row0, s.pl.h, s.pl.r0, s.rows, (int)((walk.unit + kTcCost + s.pl.tiles - 1) / plan.share), {0, 0}};
                 const uint32_t i = n_seg % kSegs;
                 if (!wait_one(segempty(i), ((n_seg / kSegs) & 1) ^ 1, abort_word)) break;
                 segs[i] = s;
