@@ -708,7 +708,7 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
     const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride,
                              q_token_stride, q_head_stride, (const uint16_t *)q, k_codes, v_codes, k_scale, v_scale,
                              block_table, kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag,
-                             c.split_rows, join, join + c.split_ctas, partial, partial + split_partial_floats(c, D)};
+                             c.split_rows, c.split_ctas > 0, join, join + c.split_ctas, partial, partial + split_partial_floats(c, D)};
     auto go = dt == CSA2_FP16 ? (D == 64 ? launch_attn_nt<64, true> : launch_attn_nt<128, true>)
                               : (D == 64 ? launch_attn_nt<64, false> : launch_attn_nt<128, false>);
     CSA2_CUDA_CALL(go(c.NT, a, c.split_ctas, c.tc_ctas, stream_of(stream)), "paged_attn launch");
