@@ -10,19 +10,27 @@
 // for bits that fall below the subnormal step 2^-9 s.  Errors do not pile up
 // over the S appends that a decoding request makes to a block.
 //
-// One warp takes one (run, head, K or V).  A warp looks at a window of up to 32
-// rows with one load per lane: a run begins where the block changes, and its length
-// comes from ballots over the slots behind it.  First pass: the largest magnitude,
-// as an integer maximum of the sign-less bit patterns (order-preserving for both
-// formats).  Second pass, from L1: scale, round, store.  A row's D codes are
-// contiguous, a run's rows too, so loads and stores are 16 and 8 bytes per lane of
-// full lines, eight loads in flight per lane.
+// A CTA of four warps looks at a window of up to 64 rows for one head of K or V,
+// with two loads per lane: a run begins where the block changes, and its length
+// comes from ballots over the slots behind it.  Few runs (prompts) the warps take
+// together, up to eight loads in flight per lane, whose values stay in registers
+// from the maximum to the codes; many (decoding) they share out.  The largest
+// magnitude is an integer maximum of the sign-less bit patterns (order-preserving
+// for both formats).  A row's D codes are contiguous, a run's rows too, so loads
+// and stores are 16 and 8 bytes per lane of full lines.
+//
+// Bound by memory for prompts, by latency (slots, old scale, rows) and the launch
+// for decoding.  16384 tokens, 8 heads of 128, blocks of 64, K and V (94.5 MB):
+// 22.0 us, 4.3 TB/s, where a copy takes 13.9; 25 us with a warp per run, which has to
+// read its rows twice, 22.2 and 22.8 us with 8 and 6 CTAs per SM.  64 decoding
+// requests 6 us, 1501 tokens of 37 requests (5 heads of 64, blocks of 16) 11 us, both
+// less than the host takes for the call.
 #include "common.cuh"
 
 namespace csa2 {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4, kMostWindow = 64;
 
 struct PagedQuantArgs {
     const uint16_t *x[2];            // k, v
@@ -31,7 +39,7 @@ struct PagedQuantArgs {
     float *scale[2];
     const int64_t *slots;
     int64_t T, n_slots;
-    int H, S, shift, window;       // S = 1 << shift; rows per window (at most 32)
+    int H, S, shift, window;       // S = 1 << shift; rows per window
     uint32_t *err_flag;
 };
 
@@ -57,34 +65,46 @@ __device__ __forceinline__ float scale_of(float amax) {
 }
 
 template <int D, bool HALF>
-__global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQuantArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 7) quantize_fp8_paged_kernel(PagedQuantArgs a) {
     constexpr int LPR = D / 8;            // lanes per row: 8 channels each
     constexpr int RPW = 32 / LPR;         // rows per warp load
     constexpr uint32_t INF = HALF ? 0x7C00u : 0x7F80u;
     constexpr uint32_t ABS2 = 0x7FFF7FFFu, ALL = 0xFFFFFFFFu;
+    __shared__ uint32_t s_top[2][2][kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int unit = blockIdx.y * kWarps + warp;      // (head, K or V)
+    const int unit = blockIdx.x % (2 * a.H);          // (head, K or V)
     pdl_wait();
     pdl_launch_dependents();
-    if (unit >= 2 * a.H) return;
     const int h = unit >> 1;
     const bool is_v = unit & 1;
     const uint16_t *x = (is_v ? a.x[1] : a.x[0]) + h * (is_v ? a.head_stride[1] : a.head_stride[0]) + (lane % LPR) * 8;
     const int64_t ts = is_v ? a.token_stride[1] : a.token_stride[0];
     uint8_t *codes = is_v ? a.codes[1] : a.codes[0];
     float *scales = is_v ? a.scale[1] : a.scale[0];
-    const int64_t w0 = (int64_t)blockIdx.x * a.window;
+    const int64_t w0 = (int64_t)(blockIdx.x / (2 * a.H)) * a.window;
 
-    // lane = row of the window: its slot, the one before it
-    const int64_t mine = w0 + lane;
-    const bool in = lane < a.window && mine < a.T;
-    const int64_t slot = in ? a.slots[mine] : -1, prev = in && mine > 0 ? a.slots[mine - 1] : -1;
-    const bool valid = slot >= 0 && slot < a.n_slots;
-    const bool goes_on = valid && prev >= 0 && prev < a.n_slots && prev >> a.shift == slot >> a.shift;
-    if (unit == 0 && ((slot != -1 && !valid) || (goes_on && prev != slot - 1))) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
-    for (uint32_t leads = __ballot_sync(ALL, valid && !goes_on); leads; leads &= leads - 1) {
-        const int lead = __ffs(leads) - 1;
-        const int64_t i = w0 + lead, s0 = __shfl_sync(ALL, slot, lead), block = s0 >> a.shift;
+    // lane = rows lane, lane + 32 of the window: the slot, the one before it
+    int64_t slot[2];
+    uint64_t leads = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int64_t mine = w0 + 32 * k + lane;
+        const bool in = 32 * k + lane < a.window && mine < a.T;
+        slot[k] = in ? a.slots[mine] : -1;
+        const int64_t prev = in && mine > 0 ? a.slots[mine - 1] : -1;
+        const bool valid = slot[k] >= 0 && slot[k] < a.n_slots;
+        const bool goes_on = valid && prev >= 0 && prev < a.n_slots && prev >> a.shift == slot[k] >> a.shift;
+        if (unit == 0 && warp == 0 && ((slot[k] != -1 && !valid) || (goes_on && prev != slot[k] - 1)))
+            flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
+        leads |= (uint64_t)__ballot_sync(ALL, valid && !goes_on) << (32 * k);
+    }
+    const bool together = __popcll(leads) < kWarps;
+    const int parts = together ? kWarps : 1, part = together ? warp : 0;
+    const int row0 = part * RPW + lane / LPR, step = parts * RPW;    // this lane's first row of a run, and on from there
+    for (int turn = 0; leads; leads &= leads - 1, ++turn) {
+        if (!together && turn % kWarps != warp) continue;
+        const int lead = __ffsll(leads) - 1;
+        const int64_t i = w0 + lead, s0 = __shfl_sync(ALL, lead < 32 ? slot[0] : slot[1], lead & 31), block = s0 >> a.shift;
         const int start = (int)(s0 & (a.S - 1));
         float *scale = scales + block * a.H + h;
         const float old = start > 0 ? *scale : 0.0f;
@@ -96,27 +116,41 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQu
             n += ok == ALL ? 32 : __ffs(~ok) - 1;
             if (ok != ALL) break;
         }
-
-        uint32_t m2 = 0;                  // largest sign-less patterns of the even and odd channels
-        const uint16_t *row = x + (i + lane / LPR) * ts;
-        for (int r = lane / LPR; r < n; r += 8 * RPW, row += 8 * RPW * ts) {
-            uint4 v[8];
+        // the warps' maximum
+        auto of_all = [&](uint32_t v, int which) {
+            v = __reduce_max_sync(ALL, v);
+            if (together) {
+                uint32_t (&t)[kWarps] = s_top[turn & 1][which];
+                if (lane == 0) t[warp] = v;
+                __syncthreads();
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = r + q * RPW < n ? *reinterpret_cast<const uint4 *>(row + q * RPW * ts) : make_uint4(0, 0, 0, 0);
+                for (int w = 0; w < kWarps; ++w) v = max(v, t[w]);
+            }
+            return v;
+        };
+        uint4 v[8];
+        auto load = [&](int r) {          // rows r, r + step, ...
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = r + q * step < n ? *reinterpret_cast<const uint4 *>(x + (i + r + q * step) * ts) : make_uint4(0, 0, 0, 0);
+        };
+        uint32_t m2 = 0;                  // largest sign-less patterns of the even and odd channels
+        for (int r = row0; r < n; r += 8 * step) {
+            load(r);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
                 m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(v[q].x & ABS2, v[q].y & ABS2)), __vmaxu2(v[q].z & ABS2, v[q].w & ABS2));
         }
-        uint32_t top = __reduce_max_sync(ALL, max(m2 & 0xFFFFu, m2 >> 16));
+        uint32_t top = of_all(max(m2 & 0xFFFFu, m2 >> 16), 0);
         const bool bad = top >= INF;
         if (bad) {                        // infinities and NaN do not count
-            top = 0;
-            for (int r = lane / LPR; r < n; r += RPW)
+            uint32_t t = 0;
+            for (int r = row0; r < n; r += step)
                 for (int c = 0; c < 8; ++c) {
                     const uint32_t u = x[(i + r) * ts + c] & 0x7FFFu;
-                    if (u < INF) top = max(top, u);
+                    if (u < INF) t = max(t, u);
                 }
-            top = __reduce_max_sync(ALL, top);
+            top = of_all(t, 1);
             if (lane == 0) flag_error(a.err_flag, CSA2_FLAG_NONFINITE);
         }
         const float need = scale_of(unpack2(top, HALF).x);
@@ -126,7 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQu
             s = fmaxf(old, need);
             if (s != old) {               // re-encode the rows stored before
                 const float ratio = old > 0.0f ? old / s : 0.0f;
-                for (int r = lane / LPR - start; r < 0; r += RPW) {
+                for (int r = row0 - start; r < 0; r += step) {
                     uint2 *p = reinterpret_cast<uint2 *>(dst + (int64_t)r * D);
                     uint2 c = *p;
 #pragma unroll
@@ -141,14 +175,11 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQu
                 }
             }
         }
-        __syncwarp();
-        if (lane == 0) *scale = s;
+        __syncwarp();                     // every lane, and behind of_all's barrier every warp, has read the old scale
+        if (lane == 0 && part == 0) *scale = s;
         const float inv = 1.0f / s;       // exact: a power of two
-        row = x + (i + lane / LPR) * ts;
-        for (int r = lane / LPR; r < n; r += 8 * RPW, row += 8 * RPW * ts) {
-            uint4 v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = r + q * RPW < n ? *reinterpret_cast<const uint4 *>(row + q * RPW * ts) : make_uint4(0, 0, 0, 0);
+        for (int r = row0; r < n; r += 8 * step) {
+            if (n > 8 * step) load(r);    // else the values are at hand
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
@@ -162,8 +193,8 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_fp8_paged_kernel(PagedQu
                     }
                     c[k] = to_e4m3x2(f.x * inv, f.y * inv);
                 }
-                if (r + q * RPW < n)
-                    *reinterpret_cast<uint2 *>(dst + (int64_t)(r + q * RPW) * D) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+                if (r + q * step < n)
+                    *reinterpret_cast<uint2 *>(dst + (int64_t)(r + q * step) * D) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
             }
         }
         __syncwarp();
@@ -209,15 +240,16 @@ extern "C" csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, 
     a.scale[0] = k_scale, a.scale[1] = v_scale;
     a.slots = slots, a.T = T, a.n_slots = n_blocks * S, a.H = Hkv, a.S = S, a.err_flag = err_flag;
     a.shift = S == 16 ? 4 : (S == 32 ? 5 : (S == 64 ? 6 : 7));
-    // as many warps as run at once (48 per SM), each with at least one row to look at
-    const int64_t at_once = (int64_t)num_sms() * 48;
+    // as many CTAs as run at once (7 per SM), each with at least one row to look at
+    const int64_t at_once = (int64_t)num_sms() * 7;
     const int64_t window = (T * 2 * Hkv + at_once - 1) / at_once;
-    a.window = (int)(window < 1 ? 1 : (window > 32 ? 32 : window));
-    const dim3 grid((unsigned)((T + a.window - 1) / a.window), (unsigned)((2 * Hkv + kWarps - 1) / kWarps));
+    a.window = (int)(window < 1 ? 1 : (window > kMostWindow ? kMostWindow : window));
+    const int64_t ctas = (T + a.window - 1) / a.window * 2 * Hkv;
+    CSA2_REQUIRE(ctas < (1ll << 31), "quantize_paged: T * Hkv = %lld rows", (long long)(T * Hkv));
     void (*kern)(PagedQuantArgs);
     if (dt == CSA2_FP16) kern = D == 64 ? quantize_fp8_paged_kernel<64, true> : quantize_fp8_paged_kernel<128, true>;
     else kern = D == 64 ? quantize_fp8_paged_kernel<64, false> : quantize_fp8_paged_kernel<128, false>;
-    CSA2_CUDA_CALL(launch_pdl(kern, grid, dim3(kWarps * 32), 0, stream_of(stream), a),
+    CSA2_CUDA_CALL(launch_pdl(kern, dim3((unsigned)ctas), dim3(kWarps * 32), 0, stream_of(stream), a),
                    "quantize_fp8_paged_kernel launch");
     CSA2_LAUNCH_CHECK("quantize_fp8_paged_kernel");
     return CSA2_OK;
