@@ -414,7 +414,7 @@ size_t csa2_sparse_attn_noalloc_max_scratch_bytes(void);
  *            a negative one gives its tokens slot -1 (CSA2_FLAG_BAD_INDEX).
  * kv_len_out, free_count_out  int32 [B], [1]: the lengths and the count after
  *            the step; may be kv_len and free_count themselves (a captured
- *            step that is replayed).
+ *            step that is replayed).  No output overlaps another input (refused).
  * cu_len     int32 [B + 1]: the first row of each request among the step's
  *            tokens (those of waiting requests counted), clamped to T.
  * positions  int32 [T] or NULL, slots int64 [T]: position and slot of each
@@ -449,7 +449,8 @@ csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int S, int64_t 
  *         its run, as is a slot outside [-1, n_blocks * S) (CSA2_FLAG_BAD_SLOT).
  *         A block whose rows come in two separate runs is a data race.
  * Infinities are stored as +-448 s and NaN as 0, neither counts toward amax
- * (CSA2_FLAG_NONFINITE).  codes 16-byte, scales 4-byte aligned.
+ * (CSA2_FLAG_NONFINITE).  codes 16-byte, scales 4-byte aligned.  T <= 2^30,
+ * T * Hkv < 2^36.
  */
 csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, csa2_dtype dt, int64_t T, int Hkv, int D,
                                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
@@ -475,8 +476,11 @@ csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, csa2_dtype 
  *         (multiples of 8), out dense; 16-byte aligned.  Hq a multiple of Hkv.
  * lse     fp32 [T, Hq] or NULL.
  * kv_len int32 [B] (after the step), cu_len int32 [B + 1] (clamped to [0, T]);
- *         tokens beyond M * S are not there.  M * S <= 2^30, T * Hq / Hkv <= 2^30.  A table entry outside [0, n_blocks) where a
- *         visible key should be hides its keys (CSA2_FLAG_BAD_INDEX).
+ *         tokens beyond M * S are not there.  M * S <= 2^30, T * Hq / Hkv <= 2^30.
+ *         A table entry outside [0, n_blocks) where a visible key should be hides
+ *         its keys (CSA2_FLAG_BAD_INDEX).  The rows of a request that waits
+ *         (csa2_build_slots gave it slots of -1) get the output of the last tokens
+ *         that it holds: they mean nothing and are dropped.
  * max_new upper bound (>= 1) of the rows of a request, known on the host: it only
  *         chooses among kernels, every value >= 1 gives right results.
  * Stored rows must hold no NaN code (csa2_quantize_kv_fp8_paged writes none);

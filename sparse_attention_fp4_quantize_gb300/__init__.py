@@ -604,8 +604,11 @@ def csa2_paged_attn_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, kv_l
     shape = (T, Hq, D)
     qp, qt, qh = _rows_arg(q, "q", q.dtype, shape, dev)
     table, stride = _table_arg(block_table, (B, M), dev)
-    if workspace is None:
-        workspace = workspace_for_paged_attn(B, T, Hq, H, D, max_new, device=q.device)
+    if workspace is None:                         # of the stream that uses it, which may not be the current one
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+        with torch.cuda.stream(stream):
+            workspace = workspace_for_paged_attn(B, T, Hq, H, D, max_new, device=q.device)
     ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch(_lib.csa2_paged_attn_fp8, dev, stream, B, T, Hq, H, D, dt, qp, qt, qh, kc, vc, ks, vs, n, S, table, M,
             stride, _arg(kv_len, "kv_len", _I32, (B,), dev), _arg(cu_len, "cu_len", _I32, (B + 1,), dev), max_new,

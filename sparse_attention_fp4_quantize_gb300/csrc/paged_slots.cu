@@ -268,7 +268,16 @@ extern "C" csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int 
                  "build_slots: null pointer");
     CSA2_REQUIRE((free_list || free_cap == 0) && (slots || T == 0), "build_slots: null pointer");
     CSA2_REQUIRE(aligned(slots, 8), "build_slots: slots must be 8-byte aligned");
+    // every CTA reads the inputs: an output may take the place of its own, and overlap no other
     const bool in_place = kv_len_out == kv_len || free_count_out == free_count;
+    const struct { const void *p; int64_t n; } in[3] = {{kv_len, B}, {new_len, B}, {free_count, 1}},
+        out[5] = {{kv_len_out, B}, {cu_len, B + 1ll}, {free_count_out, 1}, {positions, positions ? T : 0}, {slots, 2 * T}};
+    for (int o = 0; o < 5; ++o)
+        for (int i = 0; i < 3; ++i) {
+            const uintptr_t x = (uintptr_t)out[o].p, y = (uintptr_t)in[i].p;
+            const bool own = o == i && o != 1 && x == y;
+            CSA2_REQUIRE(own || x + 4 * out[o].n <= y || y + 4 * in[i].n <= x, "build_slots: an output overlaps an input");
+        }
     const SlotArgs args = {B, M, S, table_stride, T, free_cap, kv_len, new_len, block_table, free_list, free_count,
                            kv_len_out, free_count_out, cu_len, positions, slots, err_flag,
                            aligned(slots, 16) && aligned(positions, 16), in_place};

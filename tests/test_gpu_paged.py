@@ -667,3 +667,39 @@ def test_append_in_windows_of_many_rows(csa2):
     k = torch.randn(T, H, D, generator=gen).to(torch.bfloat16).to(DEV)
     v = torch.randn(T, H, D, generator=gen).to(torch.bfloat16).to(DEV)
     _append_both(csa2, k, v, slots, _planes(13, n, H, S, D), S)
+
+
+@pytest.mark.parametrize("D,S", [(128, 16), (128, 32), (128, 128), (64, 64), (64, 128)])
+def test_append_runs_taken_together_and_dealt_out(csa2, D, S):
+    """Calls of so many rows that a window holds 64: whole blocks, which the warps take together, next to short
+    runs, which they share out; longer than a warp's and a window's loads; with infinities and NaN in both."""
+    H, T = 8, 5000
+    gen = torch.Generator().manual_seed(D + S)
+    counts = [1] * 70 + [3 * S + 1] + [S] * 6 + [2, S - 1] * 6
+    starts = [(5 * i) % S for i in range(len(counts))]
+    starts[-1] = 0
+    slots, n = _request_slots(gen, starts + [0], counts + [T - sum(counts)], S)
+    k = torch.randn(T, H, D, generator=gen).to(torch.bfloat16)
+    v = torch.randn(T, H, D, generator=gen).to(torch.bfloat16) * 2.0 ** 5
+    planes = _planes(21, n, H, S, D)
+    _append_both(csa2, k.to(DEV), v.to(DEV), slots.to(DEV), planes, S)
+    for r in (3, 75, 75 + S, T - 1):
+        k[r, 1, 5], v[r, 2, 7], v[r, 2, 9] = float("nan"), float("inf"), float("-inf")
+    _append_both(csa2, k.to(DEV), v.to(DEV), slots.to(DEV), planes, S, flags=0x20)
+
+
+def test_workspace_belongs_to_the_stream_that_uses_it(csa2, monkeypatch):
+    inp = _attn_inputs(36, [900, 40], [1, 1], 8, 2, 128, 64, torch.bfloat16)
+    want, _ = _attend(csa2, inp, 0.1, 1)
+    dev, side, made = [t.to(DEV) for t in inp], torch.cuda.Stream(), []
+    real = csa2.workspace_for_paged_attn
+    monkeypatch.setattr(csa2, "workspace_for_paged_attn", lambda *a, **k: made.append(torch.cuda.current_stream()) or real(*a, **k))
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, None):
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        q, kc, vc, ks, vs, table, kv, cu = dev
+        csa2.csa2_paged_attn_fp8(q, kc, vc, ks, vs, table, kv, cu, out, 0.1, 1, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert [s.cuda_stream for s in made] == [side.cuda_stream, side.cuda_stream, torch.cuda.current_stream().cuda_stream]

@@ -45,6 +45,25 @@ def test_build_slots_rejects_on_host(lib):
     _refused(call(slots=P(0x1004)), lib, 1, "8-byte")
 
 
+def test_build_slots_refuses_outputs_over_inputs(lib):
+    B, T = 4, 10
+    apart = dict(kv=0x10000, new=0x20000, count=0x30000, kv_out=0x40000, count_out=0x50000, cu=0x60000, pos=0x70000, slots=0x80000)
+
+    def call(**where):
+        w = {**apart, **where}
+        p = {n: P(x) for n, x in w.items()}
+        return lib.csa2_build_slots(B, 8, 8, 16, T, 32, p["kv"], p["new"], FAKE, FAKE, p["count"], p["kv_out"], p["count_out"],
+                                    p["cu"], p["pos"], p["slots"], NULL, NULL)
+    sizes = dict(kv_out=4 * B, count_out=4, cu=4 * B + 4, pos=4 * T, slots=8 * T)
+    for out, n in sizes.items():
+        for name, m in (("kv", 4 * B), ("new", 4 * B), ("count", 4)):
+            own = {"kv_out": "kv", "count_out": "count"}.get(out) == name
+            for off in (0, m - 4, 4 - n):
+                if (own and off == 0) or (out == "slots" and off % 8):
+                    continue
+                _refused(call(**{out: apart[name] + off}), lib, 1, "overlaps")
+
+
 def test_quantize_paged_rejects_on_host(lib):
     def call(dt=0, T=4, H=2, D=64, kt=128, kh=64, n=8, S=16, k=FAKE, kc=FAKE, slots=FAKE):
         return lib.csa2_quantize_kv_fp8_paged(k, FAKE, dt, T, H, D, kt, kh, 128, 64, slots, n, S, kc, FAKE, FAKE, FAKE, NULL,
@@ -58,6 +77,7 @@ def test_quantize_paged_rejects_on_host(lib):
     _refused(call(kh=-64), lib, 1, "strides")
     _refused(call(n=-1), lib, 1, "n_blocks")
     _refused(call(k=P(0x1008)), lib, 1, "16-byte")
+    _refused(call(T=1 << 30, H=1 << 16), lib, 1, "rows")
     _refused(call(kc=P(0x1008)), lib, 1, "16-byte")
     _refused(call(k=NULL), lib, 1, "null")
     _refused(call(kc=NULL), lib, 1, "null")
