@@ -703,3 +703,24 @@ def test_workspace_belongs_to_the_stream_that_uses_it(csa2, monkeypatch):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert [s.cuda_stream for s in made] == [side.cuda_stream, side.cuda_stream, torch.cuda.current_stream().cuda_stream]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_row_tiles_that_fill_half_a_unit(csa2, D):
+    """Units of 256 rows next to units of at most 128, many per CTA, whose last keys end inside a tile: every run
+    of the call gives the same bits, and the first is right."""
+    B, new, kv = 24, 96, [1100 + 37 * i for i in range(24)]
+    inp = _attn_inputs(40, kv, [new] * B, 32, 8, D, 32, torch.bfloat16)
+    q, kc, vc, ks, vs, table, kvl, cu = dev = [t.to(DEV) for t in inp]
+    runs = [(torch.zeros_like(q), torch.zeros(q.shape[:2], device=DEV)) for _ in range(30)]
+    for out, lse in runs:
+        csa2.csa2_paged_attn_fp8(*dev, out, 0.1, new, lse=lse)
+    torch.cuda.synchronize()
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+    some = [0, 7, 23]                                                  # requests, for the reference
+    rows = torch.cat([torch.arange(new) + new * b for b in some])
+    part = (inp[0][rows], kc.cpu(), vc.cpu(), ks.cpu(), vs.cpu(), table.cpu()[some], kvl.cpu()[some],
+            torch.tensor([0, new, 2 * new, 3 * new], dtype=I32))
+    for out, lse in (runs[0], runs[-1]):
+        ref.check_attention(out[rows.to(DEV)], lse[rows.to(DEV)], _reference(part, 0.1))
