@@ -656,38 +656,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 const TileMeta &m = metas[nt % kMetas];
                 const int key0 = seg.key0 + (seg.pl.tile + j) * kTcKeys;
                 const int lo = max(first - key0, 0), hi = min(pos + 1 - key0, kTcKeys);
-                uint32_t missing = 0;
-                bool mask = false;
-                auto look = [&]() {
-                    missing = m.missing[0] | m.missing[1] | m.missing[2] | m.missing[3];
-                    mask = lo > 0 || hi < kTcKeys || missing != 0;
-                };
                 // The common case, one exponential and no maximum: with the references as
                 // they are, P = 2^(s f + log2 vs - Mv), and l gains sum P / vs 2^(Mv - M).
                 // It stands unless the sum of a row's P shows that one may leave f16, or
                 // a scale is so far from the others that P would not carry its keys' part
                 // of l; P goes to TMEM when that is known.  What depends on the scales
-                // alone is settled before the scores arrive.
-                bool fast = false;
-                // For a segment's first tile only behind S: a sub-tile that had no part in the last
-                // segment may be here several tiles early, while its slot's barrier still counts
-                // an older round.  From the second on, S of the tile before says that the scales
-                // of all rounds before have arrived.
-                auto wait_scales = [&]() { return wait_bar(mfull(nt % kMetas), (nt / kMetas) & 1, abort_word); };
-                if (j > 0) {
-                    if (!(run = wait_scales())) break;
-                    look();
-                    const float4 lg0 = *reinterpret_cast<const float4 *>(m.lg), lg1 = *reinterpret_cast<const float4 *>(m.lg + 4);
-                    const float least = fminf(fminf(fminf(lg0.x, lg0.y), fminf(lg0.z, lg0.w)), fminf(fminf(lg1.x, lg1.y), fminf(lg1.z, lg1.w)));
-                    const float most = fmaxf(fmaxf(fmaxf(lg0.x, lg0.y), fmaxf(lg0.z, lg0.w)), fmaxf(fmaxf(lg1.x, lg1.y), fmaxf(lg1.z, lg1.w)));
-                    fast = __all_sync(ALL, !mask && M - MV + least > -kSpread && M - MV + most < kSpread);
-                }
-                if (!(run = wait_bar(sfull(sub), ns & 1, abort_word))) break;
+                // alone is settled before the scores arrive.  But a segment's first scores
+                // come first: a sub-tile that had no part in the last segment may be here
+                // several tiles early, while the barrier of the scales' slot still counts an
+                // older round.  From the second tile on, S of the tile before says that the
+                // scales of all rounds before have arrived.
+                auto wait_s = [&]() { return wait_bar(sfull(sub), ns & 1, abort_word); };
+                if (j == 0 && !(run = wait_s())) break;
+                if (!(run = wait_bar(mfull(nt % kMetas), (nt / kMetas) & 1, abort_word))) break;
+                const uint32_t missing = m.missing[0] | m.missing[1] | m.missing[2] | m.missing[3];
+                const bool mask = lo > 0 || hi < kTcKeys || missing != 0;
+                const float4 lg0 = *reinterpret_cast<const float4 *>(m.lg), lg1 = *reinterpret_cast<const float4 *>(m.lg + 4);
+                const float least = fminf(fminf(fminf(lg0.x, lg0.y), fminf(lg0.z, lg0.w)), fminf(fminf(lg1.x, lg1.y), fminf(lg1.z, lg1.w)));
+                const float most = fmaxf(fmaxf(fmaxf(lg0.x, lg0.y), fmaxf(lg0.z, lg0.w)), fmaxf(fmaxf(lg1.x, lg1.y), fmaxf(lg1.z, lg1.w)));
+                bool fast = __all_sync(ALL, !mask && M - MV + least > -kSpread && M - MV + most < kSpread);
+                if (j > 0 && !(run = wait_s())) break;
                 tc::fence_after();
-                if (j == 0) {
-                    if (!(run = wait_scales())) break;
-                    look();
-                }
                 // scores of the keys 32 c .. 32 c + 31 that the row does not see: -inf
                 auto hide = [&](int c, uint32_t (&r)[32]) {
                     const int l0 = max(lo - 32 * c, 0), h0 = min(hi - 32 * c, 32);
