@@ -116,7 +116,7 @@ struct Tile {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 gain[x][r] *= back[x][r];
-                ok = ok && total[r] < 16384.0f && gain[x][r] < 1e30f;        // (f16 ends at 65504)
+                ok = ok && total[r] < 65000.0f && gain[x][r] < 1e30f;        // (f16 ends at 65504)
             }
         }
         if (!__all_sync(0xFFFFFFFFu, ok)) return false;

@@ -34,7 +34,7 @@ constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after t
 constexpr uint32_t kLockPolls = 1u << 24;
 constexpr float kSlack = 8.0f;               // log2: how far a tile may exceed a reference before it moves
 constexpr float kSpread = 64.0f;             // log2: how far scales may lie apart in the common case
-constexpr float kMostP = 16384.0f, kMostL = 1e30f;   // its bounds on a tile's sum of P (f16 ends at 65504) and gain of l
+constexpr float kMostP = 65000.0f, kMostL = 1e30f;   // its bounds on a tile's sum of P (f16 ends at 65504) and gain of l
 constexpr int kMetas = 4;                    // key tiles whose scales are kept
 
 struct TileMeta {
@@ -744,9 +744,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                             tv = fmaxf(tv, t + (float)((int)((__float_as_uint(m.vs[2 * c + g]) >> 23) & 0xFFu) - 127));
                         }
                     }
-                    // a reference moves when the scores exceed it by more than the slack, or at the row's first key
-                    const bool up = tz > M + kSlack || (M == NEG_INF && tz > M);
-                    const bool upv = tv > MV + kSlack || (MV == NEG_INF && tv > MV);
+                    // The references move when a row's scores exceed one by more than the slack, or at a row's
+                    // first key; then those of all 32 rows do, as far as they are exceeded, so that the next
+                    // tiles are the less likely to need it.
+                    const bool due = tz > M + kSlack || tv > MV + kSlack || (M == NEG_INF && tz > M) || (MV == NEG_INF && tv > MV);
+                    const bool all = __any_sync(ALL, due), up = all && tz > M, upv = all && tv > MV;
                     if (up) {
                         l *= ex2(M - tz);
                         M = tz;
