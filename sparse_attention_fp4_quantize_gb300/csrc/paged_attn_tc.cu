@@ -9,15 +9,30 @@
 //   O += P . V       (M = 128 rows, N = D; A = P from TMEM, V tile in shared memory)
 // The E4M3 codes become f16 once per CTA and key tile; both sub-tiles use them.
 // K is read K-major and V MN-major from the same core-matrix layout, so one
-// conversion serves both.  Roles (13 warps):
+// conversion serves both.  Roles (16 warps, registers shared out by warpgroup):
 //   warps 0-3, 4-7   softmax of sub-tile 0, 1: thread = row (TMEM lane), so the
 //                    row's maximum and sum need no exchange; also load Q and
 //                    store the output
-//   warps 8-11       load codes (a key tile ahead, in registers), convert, store
-//   warp 12          issues every MMA
+//   warps 8-11       bring codes (a key tile ahead, into a staging buffer of their
+//                    own: the registers for them are the softmax's), convert, store
+//   warps 12, 13     issue the MMAs of sub-tile 0, 1, taking turns
+//   warp 14          works out the CTA's segments, a few ahead of the others
 // While one sub-tile's softmax runs, the tensor cores have the other's products.
 // The running references M, Mv (paged_attn.cu) move only when a tile's scores
-// exceed them far enough to matter to f16, so O in TMEM is rescaled rarely.
+// exceed them far enough to matter to f16, so most tiles need no maximum and O in
+// TMEM is rescaled rarely.
+//
+// Bound by the softmax and the hand-overs around it.  The products of a key tile
+// take 2048 cycles (64 per M 128 N 128 K 16), with their waits and the conversions
+// 2660 (measured without the softmax), all together about 3300: a sub-tile's softmax
+// (1000 cycles for 128 exponentials and what goes with them) and its products are one
+// chain, and the other sub-tile's products do not fill all of it.  3 prompts of up to
+// 4096 tokens on up to 8192, 32 heads of 128 over 8: 828 us, 936 TFLOP/s of the
+// visible pairs (cuBLAS bf16 1916).  Tried and slower there: P handed over in two
+// halves of 64 keys (1035 against 923 us: the MMA threads' waits and locks cost more
+// than the overlap gives), codes kept in registers instead of staged (934 against
+// 906), whole warps in place of one thread to issue (979 against 905), the lock given
+// up before S (956 against 905), Q asked for ahead by warp 14 (921 against 905).
 #include "paged_attn.cuh"
 #include "tc.cuh"
 

@@ -724,3 +724,17 @@ def test_row_tiles_that_fill_half_a_unit(csa2, D):
             torch.tensor([0, new, 2 * new, 3 * new], dtype=I32))
     for out, lse in (runs[0], runs[-1]):
         ref.check_attention(out[rows.to(DEV)], lse[rows.to(DEV)], _reference(part, 0.1))
+
+
+@pytest.mark.parametrize("kv,new,Hq,H,D,S,window", [
+    ([900, 70, 33], [5, 7, 8], 8, 2, 64, 16, 0),                       # 20, 28 and 32 rows per KV head: several row tiles
+    ([900, 70, 33], [5, 7, 8], 8, 2, 128, 64, 90),
+    ([4000, 1], [1, 1], 17, 1, 128, 32, 0),
+    ([500, 31, 200], [1, 1, 1], 64, 2, 64, 64, 0),                     # 32 heads of a group
+    ([500, 260, 31], [1, 250, 2], 20, 1, 128, 64, 0),                  # next to a prompt and to 40 rows
+    ([500, 260, 31], [1, 250, 2], 33, 1, 64, 32, 0),                   # one token's rows are too many already
+])
+def test_rows_of_several_row_tiles(csa2, kv, new, Hq, H, D, S, window):
+    inp = _attn_inputs(41, kv, new, Hq, H, D, S, torch.bfloat16)
+    out, lse = _attend(csa2, inp, 0.08, max(new), window, pad=2)
+    ref.check_attention(out, lse, _reference(inp, 0.08, window))
