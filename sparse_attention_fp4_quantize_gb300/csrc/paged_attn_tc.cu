@@ -742,19 +742,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 }
                 if (!fast) {
                     const bool masked = __any_sync(ALL, mask);
+                    // 64 scores at a time, read again for P: all 128 do not fit beside the rest
+                    uint32_t r[2][32];
                     float tz = NEG_INF, tv = NEG_INF;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        tc::tmem_ld32(ts + 32 * c, r);
+                    for (int c = 0; c < 4; c += 2) {
+                        tc::tmem_ld32(ts + 32 * c, r[0]);
+                        tc::tmem_ld32(ts + 32 * c + 32, r[1]);
                         tc::tmem_ld_wait();
-                        if (masked) hide(c, r);
+                        if (masked) hide(c, r[0]), hide(c + 1, r[1]);
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float t = __uint_as_float(r[16 * g]);
+                        for (int g = 0; g < 4; ++g) {
+                            const uint32_t (&x)[32] = r[g / 2];
+                            const int i0 = 16 * (g & 1);
+                            float t0 = __uint_as_float(x[i0]), t1 = __uint_as_float(x[i0 + 1]);
 #pragma unroll
-                            for (int i = 1; i < 15; i += 2) t = max3(t, __uint_as_float(r[16 * g + i]), __uint_as_float(r[16 * g + i + 1]));
-                            t = fmaxf(t, __uint_as_float(r[16 * g + 15])) * factor(zf, m.ks[2 * c + g]);
+                            for (int i = 2; i < 14; i += 4) {
+                                t0 = max3(t0, __uint_as_float(x[i0 + i]), __uint_as_float(x[i0 + i + 1]));
+                                t1 = max3(t1, __uint_as_float(x[i0 + i + 2]), __uint_as_float(x[i0 + i + 3]));
+                            }
+                            const float t = fmaxf(max3(t0, t1, __uint_as_float(x[i0 + 14])), __uint_as_float(x[i0 + 15])) * factor(zf, m.ks[2 * c + g]);
                             tz = fmaxf(tz, t);
                             tv = fmaxf(tv, t + (float)((int)((__float_as_uint(m.vs[2 * c + g]) >> 23) & 0xFFu) - 127));
                         }
@@ -770,45 +777,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     }
                     const float grow = upv ? ex2(MV - tv) : 1.0f;
                     if (upv) MV = tv;
-                    if (j > 0 && __any_sync(ALL, upv)) {             // O so far to the new reference, once P V is done
-                        if (!wait_bar(ofull(sub), (ns - 1) & 1, abort_word)) {
-                            run = false;
-                            break;
-                        }
-                        tc::fence_after();
+                    if (j > 0 && __any_sync(ALL, upv)) {             // O so far to the new reference; S followed its products
 #pragma unroll 1
-                        for (int x = 0; x < D / 16; ++x) {
-                            uint32_t o[16];
-                            tc::tmem_ld16(to + 16 * x, o);
+                        for (int x = 0; x < D; x += 64) {
+                            tc::tmem_ld32(to + x, r[0]);
+                            tc::tmem_ld32(to + x + 32, r[1]);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * grow);
-                            tc::tmem_st16(to + 16 * x, o);
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t o[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(r[c / 2][16 * (c & 1) + i]) * grow);
+                                tc::tmem_st16(to + x + 16 * c, o);
+                            }
                         }
                     }
                     const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(ref - (MV == NEG_INF ? 0.0f : MV));
                     const uint64_t nref = f2(-ref, -ref);
                     uint64_t sum = f2(0.0f, 0.0f);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32], p[16];
-                        tc::tmem_ld32(ts + 32 * c, r);
+                    for (int c = 0; c < 4; c += 2) {
+                        tc::tmem_ld32(ts + 32 * c, r[0]);
+                        tc::tmem_ld32(ts + 32 * c + 32, r[1]);
                         tc::tmem_ld_wait();
-                        if (masked) hide(c, r);
+                        if (masked) hide(c, r[0]), hide(c + 1, r[1]);
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float f = factor(zf, m.ks[2 * c + g]), w = fminf(m.vs[2 * c + g] * g2, 1e38f);
-                            const uint64_t ff = f2(f, f), ww = f2(w, w);
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t p[16];
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 z = un2(fma2(f2u(r[16 * g + i], r[16 * g + i + 1]), ff, nref));
-                                const uint64_t e = f2(ex2(z.x), ex2(z.y));
-                                sum = add2(sum, e);
-                                const float2 x = un2(mul2(e, ww));
-                                p[8 * g + i / 2] = pack_f16(x.x, x.y);
+                            for (int g = 0; g < 2; ++g) {
+                                const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2, 1e38f);
+                                const uint64_t ff = f2(f, f), ww = f2(w, w);
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    const float2 z = un2(fma2(f2u(r[k][16 * g + i], r[k][16 * g + i + 1]), ff, nref));
+                                    const uint64_t e = f2(ex2(z.x), ex2(z.y));
+                                    sum = add2(sum, e);
+                                    const float2 x = un2(mul2(e, ww));
+                                    p[8 * g + i / 2] = pack_f16(x.x, x.y);
+                                }
                             }
+                            tc::tmem_st16(ts + 16 * (c + k), p);
                         }
-                        tc::tmem_st16(ts + 16 * c, p);
                     }
                     const float2 s2 = un2(sum);
                     l += s2.x + s2.y;
