@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     uint32_t seen = h0 <= 0 || l0 >= 32 ? 0u : (0xFFFFFFFFu >> (32 - h0)) & (0xFFFFFFFFu << l0);
                     if ((missing >> (2 * c)) & 1) seen &= 0xFFFF0000u;
                     if ((missing >> (2 * c)) & 2) seen &= 0x0000FFFFu;
+                    if (__all_sync(ALL, seen == 0xFFFFFFFFu)) return;    // of a tile on the diagonal mostly two or three quarters
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (!((seen >> i) & 1)) r[i] = 0xff800000u;
