@@ -534,56 +534,63 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         Segment seg;
         float zf = 0.0f;
         // The warp's 32 rows of Q into shared memory; zf: the logit factor of this
-        // thread's row.  A load takes 64 bytes of 8 rows (lane % 8 the row), so that a
-        // quarter-warp's stores fill a core matrix.
+        // thread's row.  A copy takes 64 bytes of 8 rows (lane % 8 the row), so that a
+        // quarter-warp's pieces fill a core matrix; each lane then scales the pieces
+        // that it has copied, in place.  Rolled loops: the code is wanted once per
+        // segment, and fetching its instructions is what it would wait for.
         auto load_q = [&](const Segment &s) {
-            constexpr int CH = D / 32;                   // 16-byte chunks of a row per lane
+            constexpr int CH = D / 32;                   // 16-byte pieces of a row per lane
             const int r8 = lane & 7, c4 = lane >> 3, w0 = s.pl.r0 + 128 * sub + 32 * (warp & 3);
-            uint4 v[4][CH];
-#pragma unroll
+            const uint32_t dst = sb + L::OFF_Q + sub * L::Q + 4 * (warp & 3) * L::GROUP + c4 * 128 + r8 * 16;
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 const int row = w0 + 8 * i + r8;
                 const bool real = row < s.rows;
                 const int tok = real ? row / a.G : 0, hq = s.pl.h * a.G + (real ? row - tok * a.G : 0);
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (s.rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride) + c4;
+                const uint16_t *src = a.q + (s.rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride + 8 * c4;
 #pragma unroll
-                for (int c = 0; c < CH; ++c) v[i][c] = real ? src[4 * c] : make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < CH; ++c)             // rows that are not there are zero
+                    cp_async16(dst + i * L::GROUP + c * 512, real ? (const void *)(src + 32 * c) : a.q, real ? 16 : 0);
             }
-            const uint32_t flip = a.logit_scale < 0.0f ? 0x80008000u : 0u;   // the sign goes to q: factors are not negative
-            const uint32_t dst = sb + L::OFF_Q + sub * L::Q + 4 * (warp & 3) * L::GROUP + c4 * 128 + r8 * 16;
+            cp_async_commit();
+            cp_async_wait<0>();
+            const float sign = a.logit_scale < 0.0f ? -1.0f : 1.0f;      // goes to q: factors are not negative
+            if (HALF) zf = fabsf(a.logit_scale);
+            if (!HALF || a.logit_scale < 0.0f) {
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    uint4 v[CH];
+                    float top = 0.0f, mul = sign;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float mul = 1.0f;
-                if (!HALF) {
-                    float top = 0.0f;
+                    for (int c = 0; c < CH; ++c) v[c] = lds128(dst + i * L::GROUP + c * 512);
+                    if (!HALF) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float2 f = unpack_in<HALF>(w[x]);
+                                top = max3(top, fabsf(f.x), fabsf(f.y));
+                            }
+                        }
+                        top = fmaxf(top, __shfl_xor_sync(ALL, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(ALL, top, 16));
+                        // largest magnitude to [2^14, 2^15); a row below 2^-100 keeps that factor
+                        const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+                        mul = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                        if (i == c4) zf = fabsf(a.logit_scale) / mul;    // row 8 i + r8 is this thread's
+                        mul *= sign;
+                    }
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
-                        const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+                        uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             const float2 f = unpack_in<HALF>(w[x]);
-                            top = max3(top, fabsf(f.x), fabsf(f.y));
-                        }
-                    }
-                    top = fmaxf(top, __shfl_xor_sync(ALL, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(ALL, top, 16));
-                    // largest magnitude to [2^14, 2^15); a row below 2^-100 keeps that factor
-                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-                    mul = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                }
-                if (i == c4) zf = fabsf(a.logit_scale) / mul;    // row 8 i + r8 is this thread's
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if (!HALF) {
-                            const float2 f = unpack_in<HALF>(w[x]);
                             w[x] = pack_f16(f.x * mul, f.y * mul);
                         }
-                        w[x] ^= flip;
+                        sts128(dst + i * L::GROUP + c * 512, w[0], w[1], w[2], w[3]);
                     }
-                    sts128(dst + i * L::GROUP + c * 512, w[0], w[1], w[2], w[3]);
                 }
             }
             tc::fence_async_smem();
