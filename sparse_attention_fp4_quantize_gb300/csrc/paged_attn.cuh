@@ -178,7 +178,6 @@ constexpr int kSplitWarps = 4, kSplitCost = 16;
 static_assert(kSplitCost % kSplitWarps == 0, "segments begin at whole rounds of the warps");
 template <int R, int K>
 struct SplitWork {
-    static constexpr int ROWS = R;
     static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r) {
         const int64_t p = (int64_t)r.kv - r.n - a.window + 1;      // lowest key of the first row's window
         return a.window > 0 && p > 0 ? (int)p & ~(K - 1) : 0;
@@ -208,11 +207,10 @@ struct SplitWork {
 
 // The tile kernel's work: units of 256 rows, key tiles of 128, for each row tile
 // those that its first to last row see.
-// kTcCost: 3 prompts of up to 4096 tokens on up to 8192 (32 heads of 128) 854 us with 4 and
-// with 6, 905 with 0, 872 with 10.
-constexpr int kTcRows = 256, kTcKeys = 128, kTcRound = 1, kTcCost = 5;
+// kTcCost: 3 prompts of up to 4096 tokens on up to 8192 (32 heads of 128) 794 us, 801 with
+// 3, 796 with 7; before, 905 with 0, 854 with 4 and with 6, 872 with 10.
+constexpr int kTcRows = 256, kTcKeys = 128, kTcCost = 5;
 struct TcWork {
-    static constexpr int ROWS = kTcRows;
     // A walk over the row tiles of a request, without a division per step.
     struct Rows {
         int G, q256, m256, q255, m255;
@@ -259,10 +257,6 @@ struct TcWork {
         p.r0 = w.r0;
         p.tile = (int)left;
         return p;
-    }
-    static __device__ __forceinline__ Place place(const PagedAttnArgs &a, const Request &r, int64_t off) {
-        Rows w(a.G);
-        return place(a, r, off, w);
     }
 };
 

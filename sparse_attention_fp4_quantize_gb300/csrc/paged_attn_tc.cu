@@ -27,8 +27,8 @@
 // 2660 (measured without the softmax), all together about 3300: a sub-tile's softmax
 // (1000 cycles for 128 exponentials and what goes with them) and its products are one
 // chain, and the other sub-tile's products do not fill all of it.  3 prompts of up to
-// 4096 tokens on up to 8192, 32 heads of 128 over 8: 828 us, 936 TFLOP/s of the
-// visible pairs (cuBLAS bf16 1916).  Tried and slower there: P handed over in two
+// 4096 tokens on up to 8192, 32 heads of 128 over 8: 791 us, 980 TFLOP/s of the
+// visible pairs (cuBLAS bf16 1916).  Without the conversions' stores it would take 743.  Tried and slower there: P handed over in two
 // halves of 64 keys (1035 against 923 us: the MMA threads' waits and locks cost more
 // than the overlap gives), codes kept in registers instead of staged (934 against
 // 906), whole warps in place of one thread to issue (979 against 905), the lock given
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     // came before.  The wait at the end makes the join kernel's cover both.
     if (!a.after_split) pdl_wait();
     pdl_launch_dependents();
-    const Plan plan = plan_of<TcWork>(a, blockIdx.x, gridDim.x, kTcRound, s_sum, s_found);
+    const Plan plan = plan_of<TcWork>(a, blockIdx.x, gridDim.x, 1, s_sum, s_found);
     bool run = true;
     uint32_t n_seg = 0;
     // The next segment: of a whole warp, or of its one working thread.  False: none, or given up.
