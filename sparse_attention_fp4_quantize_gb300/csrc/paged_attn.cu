@@ -334,7 +334,19 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
             auto there = [&](int i) { return i + lane / U < count && key_of(i) < rq.kv; };
             auto entry = [&](int i) -> int32_t { return there(i) ? table[key_of(i) / a.S] : -1; };   // block of this lane's group
             int32_t block = entry(0), block_next = entry(BT);
-            float ks = 0.0f, vs = 0.0f, lg = 0.0f, rv = 0.0f;
+            // Q travels beside the chain of loads to the first codes: for a B operand row g,
+            // channels [t D/4, (t+1) D/4)
+            uint4 qv[NT][D / 32];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                const int row = r0 + 8 * x + g;
+                const bool real = row < rows;
+                const int tok = real ? row / a.G : 0, hq = h * a.G + (real ? row - tok * a.G : 0);
+                const uint16_t *src = a.q + (rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride + t * (D / 4);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) qv[x][c] = real ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+            }
+            float ks = 0.0f, vs = 0.0f;
             int64_t off = -1;                        // code offset of the group's first row, -1: not there
             auto scales = [&](int i) {
                 const bool ok = there(i) && block >= 0 && block < a.n_blocks;
@@ -342,7 +354,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                 const int64_t bh = ok ? (int64_t)block * a.Hkv + h : 0;
                 ks = ok ? a.k_scale[bh] : 0.0f;
                 vs = ok ? a.v_scale[bh] : 0.0f;
-                lg = lg2(vs), rv = rcp(vs);
                 off = ok ? (bh * a.S + (key_of(i) & (a.S - 1))) * D : -1;
             };
             scales(0);
@@ -358,12 +369,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                     constexpr int CPR = D / 16, RPI = 32 / CPR;      // chunks per row, rows per instruction
                     const int c = lane % CPR, r1 = lane / CPR;
                     const uint32_t who = U * (i % BT);
-                    if (lane / U == i % BT) {
-                        StageMeta<D> &m = s_meta[warp][i % kStages];
-                        const int u = lane % U;
-                        m.ks[u] = ks, m.vs[u] = vs, m.lg[u] = lg, m.rv[u] = rv;
-                        m.stored[u] = off < 0 ? 0 : min(16, rq.kv - key - 16 * u);
-                    }
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const int64_t from = __shfl_sync(ALL, off, who + u);
@@ -390,8 +395,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                 }
                 cp_async_commit();
             };
-#pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) issue(i);
+            // The scales of tile i, a tile after they were asked for: the codes' copies do not wait for them.
+            auto scales_of = [&](int i) {
+                if (lane / U == i % BT) {
+                    StageMeta<D> &m = s_meta[warp][i % kStages];
+                    const int u = lane % U, key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys<D>;
+                    m.ks[u] = ks, m.vs[u] = vs, m.lg[u] = lg2(vs), m.rv[u] = rcp(vs);
+                    m.stored[u] = off < 0 ? 0 : min(16, rq.kv - key - 16 * u);
+                }
+            };
+            static_assert(kStages == 2, "a tile's scales are kept until the next tile is asked for");
+            issue(0);
 
             Tile<D, NT> tile;
             tile.clear();
@@ -399,19 +413,12 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
             int all_lo = 0, all_hi = 0x7FFFFFFF;     // keys that every real row of this lane sees
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                {                                    // B operand: row g, channels [t D/4, (t+1) D/4)
-                    const int row = r0 + 8 * x + g;
-                    const bool real = row < rows;
-                    const int tok = real ? row / a.G : 0, hq = h * a.G + (real ? row - tok * a.G : 0);
-                    const uint16_t *src = a.q + (rq.row0 + tok) * a.q_token_stride + hq * a.q_head_stride + t * (D / 4);
+                {
                     uint32_t w[D / 8];
                     float top = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (real) v = *reinterpret_cast<const uint4 *>(src + 8 * c);
-                        w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
-                    }
+                    for (int c = 0; c < D / 32; ++c)
+                        w[4 * c] = qv[x][c].x, w[4 * c + 1] = qv[x][c].y, w[4 * c + 2] = qv[x][c].z, w[4 * c + 3] = qv[x][c].w;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
                         const float2 f = unpack_in<HALF>(w[c]);
@@ -444,8 +451,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                 }
             }
             for (int i = 0; i < count; ++i) {
-                issue(i + kStages - 1);
-                cp_async_wait<kStages - 1>();
+                scales_of(i);
+                issue(i + 1);
+                cp_async_wait<1>();
                 __syncwarp();
                 const int key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys<D>;
                 const uint32_t kb = ring + (i % kStages) * (2 * kHalf);
