@@ -23,11 +23,11 @@
 // parts of units that several CTAs shared.
 //
 // The split kernel, 64 requests of up to 16k tokens, 64 heads of 128 over 8 (1212 MB):
-// 185 us with the join, 6.6 TB/s, a copy's rate 6.8.  3 of up to 131k (257 MB): 53 us,
+// 184 us with the join, 6.6 TB/s, a copy's rate 6.8.  3 of up to 131k (257 MB): 52 us,
 // of which 10 are the launch, the first loads and the join.  48 with 5 new tokens in
-// a window of 4096, 15 heads of 64 over 5 (108 MB): 36 us, bound by latency: 1.8 warps
-// per scheduler, 0.35 instructions a cycle, a key costs as much as with 128 channels but
-// brings half the bytes.  One request of 1000 tokens: 8 us and 4.6 for the join.
+// a window of 4096, 15 heads of 64 over 5 (108 MB): 35 us, of which 8 go by before the
+// first tile (lengths, table, codes, each after the other), then the instructions: a key
+// costs as many as with 128 channels but brings half the bytes.  One request of 1000 tokens: 8 us and 4.6 for the join.
 #include "paged_attn.cuh"
 
 namespace csa2 {
@@ -39,9 +39,9 @@ template <int D>
 constexpr int kTileKeys = kHalf / D;
 constexpr int kStages = 2;              // tiles in flight per warp
 // CTAs that an SM holds at once: two of 255 registers stream faster than three of
-// 168 (64 requests of up to 16k tokens, 8 heads of 128: 195 against 203 us; 16 rows
-// per tile, 19 of up to 32k: 60 against 88), and two tiles in flight per warp faster
-// than three (195 against 204).
+// 168 (64 requests of up to 16k tokens, 8 heads of 128: 192 against 202 us; 16 rows
+// per tile, 19 of up to 32k: 60 against 88; 64 channels: 42 against 44.6), and two tiles
+// in flight per warp faster than three (195 against 204).
 constexpr int kSplitPerSm = 2;
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {

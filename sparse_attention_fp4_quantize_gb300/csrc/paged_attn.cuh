@@ -172,8 +172,9 @@ struct Place {
 // keys); every row tile of a request has the same tiles, at least one so that each row gets its
 // output, and counts as a whole number of rounds of the CTA's warps, so that short
 // units go to CTAs of their own.
-// kSplitCost: 64 requests of up to 16k tokens (8 heads of 128) 185 us with 16, 192 with
-// 0; 48 of up to 9k in a window of 4096 (5 heads of 64) 36.7, 42.0; 24: 187, 38.7.
+// kSplitCost: 64 requests of up to 16k tokens (8 heads of 128) 185 us with 16, 186 with
+// 8, 192 with 0; 48 of up to 9k in a window of 4096 (5 heads of 64) 35.0, 36.0 and
+// (before the segments' first loads were reordered) 42.0 against 36.7; 35.6 with 20.
 constexpr int kSplitWarps = 4, kSplitCost = 16;
 static_assert(kSplitCost % kSplitWarps == 0, "segments begin at whole rounds of the warps");
 template <int R, int K>
