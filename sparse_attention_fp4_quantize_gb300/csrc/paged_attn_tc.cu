@@ -253,10 +253,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
-    // Behind the split kernel, whose results it does not use, it starts while that one
-    // ends: the split kernel lets it start only when all its CTAs have waited for what
-    // came before.  The wait at the end makes the join kernel's cover both.
-    if (!a.after_split) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
     const Plan plan = plan_of<TcWork>(a, blockIdx.x, gridDim.x, 1, s_sum, s_found);
     bool run = true;
@@ -845,7 +842,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     tc::fence_after();
     if (tid == 0 && *abort_word) flag_error(a.err_flag, CSA2_FLAG_TIMEOUT);
     if (warp == 0) tc::tmem_dealloc(tmem, 512);
-    if (a.after_split) pdl_wait();
 }
 
 template <int D, bool HALF>
