@@ -27,7 +27,6 @@ struct PagedAttnArgs {
     float *lse;
     uint32_t *err_flag;
     int split_rows;                 // requests of more rows than this are the tile kernel's
-    bool after_tc;                  // the split kernel is launched behind the tile kernel
     JoinUnit *join, *join_tc;       // one per CTA of the split and of the tile kernel
     float *partial;                 // split kernel's [2 * CTAs][8 NT rows][D + 4]: o, m, mv, l
     float *partial_tc;              // tile kernel's [2 * CTAs][256 rows][D + 4]
