@@ -470,7 +470,8 @@ csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, csa2_dtype 
  * last request are not written.  Codes enter the tensor cores as exact f16, q
  * as f16 scaled per row by a power of two (bf16 values within 2^-31 of the
  * row's largest are exact); sums and softmax statistics are fp32, the weights
- * of the values are rounded to f16.
+ * of the values (P_j v_scale) are rounded to f16's 11 bits, those below 2^-22 of
+ * their sum to a step of 2^-32 of it.
  *
  * q, out  bf16 or fp16 [T, Hq, D], q with token and head strides in elements
  *         (multiples of 8), out dense; 16-byte aligned.  Hq a multiple of Hkv.

@@ -12,10 +12,11 @@
 // f16 range.  The weight of a value is P_j * v_scale: v_scale differs from
 // block to block, so each row keeps two references, the running maximum M of
 // z and the running maximum Mv of z + log2(v_scale) (its exponent), and feeds
-// P_j v_scale 2^(M - Mv) <= 2 to the product: no weight that matters is lost to
-// f16's range, whatever the ratio of the scales.  The weights are rounded to f16's 11
-// bits because the products' other operand, a code, has 4: sums and statistics stay
-// in 32.
+// P_j v_scale 2^(M - Mv) to the product, times 2^kUp (paged_attn.cuh) so that the many
+// small weights of a long tail are not lost to f16's range.  Both references may lag
+// behind the maxima as long as the weights stay below 65000, f16's end.  The weights are
+// rounded to f16's 11 bits because the products' other operand, a code, has 4: sums and
+// statistics stay in 32.
 //
 // Three kernels.  The split kernel (this file) takes rows as few as a decode step's,
 // 8 or 16 to a tile, whose time is the reading of the cache; the tile kernel
@@ -53,7 +54,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 template <int D>
 struct StageMeta {
     static constexpr int U = kTileKeys<D> / 16;
-    float ks[U], vs[U], lg[U], rv[U];   // scales of the 16-key groups; log2 and reciprocal of v's
+    float ks[U], vs[U], lg[U], rv[U];   // scales of the 16-key groups; log2 of 2^kUp v's, its reciprocal
     int stored[U];                  // keys of each group that are there
 };
 
@@ -98,8 +99,8 @@ struct Tile {
     }
 
     // Weights of a tile whose keys every row sees, with the references as they are:
-    // one exponential per score and no maximum, P = 2^(s f + log2 vs - mv), and l
-    // gains sum P / vs 2^(mv - m).  False if a row's P may leave f16 or a scale is so
+    // one exponential per score and no maximum, P = 2^(s f + log2(2^kUp vs) - mv), and l
+    // gains sum P / (2^kUp vs) 2^(mv - m).  False if a row's P may leave f16 or a scale is so
     // far from the others that P would not carry its keys' part of l.
     __device__ __forceinline__ bool weights(const float (&s)[NT][U][4], const StageMeta<D> &meta, const float (&zf)[NT][2],
                                             uint32_t (&p)[NT][U][2]) {
@@ -213,7 +214,7 @@ struct Tile {
                     dmax = fmaxf(dmax, ref - refv);
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const float f = fminf(meta.vs[u] * g2, 1e38f);
+                        const float f = fminf(meta.vs[u] * g2, kMostWeight) * kUpFactor;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float e = ex2(z[2 * u + h] - ref);
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                 if (lane / U == i % BT) {
                     StageMeta<D> &m = s_meta[warp][i % kStages];
                     const int u = lane % U, key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys<D>;
-                    m.ks[u] = ks, m.vs[u] = vs, m.lg[u] = lg2(vs), m.rv[u] = rcp(vs);
+                    m.ks[u] = ks, m.vs[u] = vs, m.lg[u] = lg2(vs) + kUp, m.rv[u] = rcp(vs) * kDownFactor;
                     m.stored[u] = off < 0 ? 0 : min(16, rq.kv - key - 16 * u);
                 }
             };

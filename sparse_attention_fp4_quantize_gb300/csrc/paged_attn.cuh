@@ -32,6 +32,18 @@ struct PagedAttnArgs {
     float *partial_tc;              // tile kernel's [2 * CTAs][256 rows][D + 4]
 };
 
+// The weights of the values go to f16 with 2^kUp above the reference Mv, the largest
+// of a row's z + log2(v_scale): f16 has 2^15 above 1 and 2^-14 (2^-24 with subnormals)
+// below.  Weights down to 2^-22 of all weights' sum keep their 11 bits; smaller ones are off
+// by 2^-33 of it at most, which a long tail of n keys adds up to n 2^-33 (2^-16 at 131k).
+// More room below leaves less above, by which scores may exceed the references before these
+// have to move: 3 prompts of up to 4096 tokens on up to 8192 take 841 us with 8 (803 with
+// 0, 820 with 4, 871 with 10), the windows of paged_attn.cu 36.5 (35.0 with 0), 64 requests of
+// up to 16k tokens the same with any.
+constexpr int kUp = 8;
+constexpr float kUpFactor = 1 << kUp, kDownFactor = 1.0f / kUpFactor;
+constexpr float kMostWeight = 0x1p118f;      // bound of v_scale 2^(M - Mv): finite times 2^kUp, for scales of keys that no row sees
+
 __device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
 }
@@ -260,10 +272,10 @@ struct TcWork {
     }
 };
 
-// P threads per row, D / P channels each: o = x / l in the output's type, lse.
+// P threads per row, D / P channels each: o = x / (2^kUp l) in the output's type, lse.
 template <int D, bool HALF, int P>
 __device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row, int part, const float *x, float M, float l) {
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    const float inv = l > 0.0f ? kDownFactor / l : (l == 0.0f ? 0.0f : l);
     constexpr int W = D / P / 2;
     uint32_t w[W];
 #pragma unroll

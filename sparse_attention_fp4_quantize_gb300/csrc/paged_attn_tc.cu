@@ -48,13 +48,14 @@ constexpr int kSoftRegs = 176, kConvRegs = 80, kMmaRegs = 80;
 static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * 128, "register shares exceed the launch's");
 constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after that many naps (ns, ended by the arrival)
 constexpr uint32_t kLockPolls = 1u << 24;
-constexpr float kSlack = 8.0f;               // log2: how far a tile may exceed a reference before it moves
+constexpr float kSlack = 14 - kUp;           // log2: how far a tile may exceed a reference before it moves (P < 2^(kUp + kSlack + 1))
 constexpr float kSpread = 64.0f;             // log2: how far scales may lie apart in the common case
 constexpr float kMostP = 65000.0f, kMostL = 1e30f;   // its bounds on a tile's sum of P (f16 ends at 65504) and gain of l
+constexpr float kMostRaise = 0x1p64f;        // and on the sum where a higher Mv is tried
 constexpr int kMetas = 4;                    // key tiles whose scales are kept
 
 struct TileMeta {
-    float ks[8], vs[8], lg[8], rv[8];        // scales of the 16-key groups; log2 and reciprocal of v's
+    float ks[8], vs[8], lg[8], rv[8];        // scales of the 16-key groups; log2 of 2^kUp v's, its reciprocal
     uint32_t missing[4];                     // per converting warp: its groups that are not stored (a bit each)
 };
 
@@ -431,8 +432,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 boff = ok ? (bh * a.S + (key & (a.S - 1))) * D : -1;
                 bks = ok ? a.k_scale[bh] : 0.0f;
                 bvs = ok ? a.v_scale[bh] : 0.0f;
-                blg = lg2(bvs);
-                brv = rcp(bvs);
+                blg = lg2(bvs) + kUp;
+                brv = rcp(bvs) * kDownFactor;
                 bmiss = __ballot_sync(ALL, !ok);
             }
             cur = tile_ahead - batch;
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 if (!wait_bar(ofull(sub), (ns - 1) & 1, abort_word)) break;
                 tc::fence_after();
                 const float ref = M == NEG_INF ? 0.0f : M, refv = MV == NEG_INF ? 0.0f : MV;
-                const float scale = exp2f(refv - ref), inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+                const float scale = exp2f(refv - ref), inv = l > 0.0f ? kDownFactor / l : (l == 0.0f ? 0.0f : l);
                 float *part = a.partial_tc + ((2 * (int64_t)blockIdx.x + first_part) * kTcRows + 128 * sub + rr) * (D + 4);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -677,10 +678,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 const int key0 = seg.key0 + (seg.pl.tile + j) * kTcKeys;
                 const int lo = max(first - key0, 0), hi = min(pos + 1 - key0, kTcKeys);
                 // The common case, one exponential and no maximum: with the references as
-                // they are, P = 2^(s f + log2 vs - Mv), and l gains sum P / vs 2^(Mv - M).
-                // It stands unless the sum of a row's P shows that one may leave f16, or
-                // a scale is so far from the others that P would not carry its keys' part
-                // of l; P goes to TMEM when that is known.  What depends on the scales
+                // they are, P = 2^(s f + log2(2^kUp vs) - Mv), and l gains sum P / (2^kUp vs) 2^(Mv - M).
+                // Where the sum of a row's P shows that one may leave f16, Mv is raised by a
+                // whole power of two and P computed once more; a scale so far from the others
+                // that P would not carry its keys' part of l takes the way with maxima.
+                // P goes to TMEM when that is known.  What depends on the scales
                 // alone is settled before the scores arrive.  But a segment's first scores
                 // come first: a sub-tile that had no part in the last segment may be here
                 // several tiles early, while the barrier of the scales' slot still counts an
@@ -708,7 +710,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     for (int i = 0; i < 32; ++i)
                         if (!((seen >> i) & 1)) r[i] = 0xff800000u;
                 };
-                if (fast) {
+                // O so far to another reference; S followed the products that it waited for
+                auto rescale = [&](float by) {
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 64) {
+                        uint32_t r[2][32];
+                        tc::tmem_ld32(to + x, r[0]);
+                        tc::tmem_ld32(to + x + 32, r[1]);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(r[c / 2][16 * (c & 1) + i]) * by);
+                            tc::tmem_st16(to + x + 16 * c, o);
+                        }
+                    }
+                };
+                while (fast) {
                     const float back = ex2(MV - M);
                     uint32_t p[4][16];
                     float gain = 0.0f, total = 0.0f;
@@ -739,11 +758,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                             gain += y * (g ? rv.y : rv.x);
                         }
                     }
-                    fast = __all_sync(ALL, total < kMostP && gain * back < kMostL);
-                    if (fast) {
+                    if (__all_sync(ALL, total < kMostP && gain * back < kMostL)) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tc::tmem_st16(ts + 16 * c, p[c]);
                         l += gain * back;
+                        break;
+                    }
+                    fast = __all_sync(ALL, total < kMostRaise && gain * back < kMostL);
+                    if (fast) {                          // all 32 rows' sums to 2^kUp, as far as they exceed it
+                        const int k = max(0, (int)(__float_as_uint(total) >> 23) - 127 - kUp);
+                        MV += k;
+                        rescale(__uint_as_float((uint32_t)(127 - k) << 23));
                     }
                 }
                 if (!fast) {
@@ -783,21 +808,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     }
                     const float grow = upv ? ex2(MV - tv) : 1.0f;
                     if (upv) MV = tv;
-                    if (j > 0 && __any_sync(ALL, upv)) {             // O so far to the new reference; S followed its products
-#pragma unroll 1
-                        for (int x = 0; x < D; x += 64) {
-                            tc::tmem_ld32(to + x, r[0]);
-                            tc::tmem_ld32(to + x + 32, r[1]);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t o[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(r[c / 2][16 * (c & 1) + i]) * grow);
-                                tc::tmem_st16(to + x + 16 * c, o);
-                            }
-                        }
-                    }
+                    if (j > 0 && __any_sync(ALL, upv)) rescale(grow);
                     const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(ref - (MV == NEG_INF ? 0.0f : MV));
                     const uint64_t nref = f2(-ref, -ref);
                     uint64_t sum = f2(0.0f, 0.0f);
@@ -812,7 +823,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                             uint32_t p[16];
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2, 1e38f);
+                                const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2, kMostWeight) * kUpFactor;
                                 const uint64_t ff = f2(f, f), ww = f2(w, w);
 #pragma unroll
                                 for (int i = 0; i < 16; i += 2) {

@@ -5,6 +5,8 @@ from __future__ import annotations
 import pytest
 import torch
 
+import paged_ref as ref
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 I32 = torch.int32
@@ -51,3 +53,51 @@ def test_mixed_steps_back_to_back_give_the_bits_of_steps_one_by_one(csa2):
     for _ in range(3):
         for a, b in zip(apart, _mixed_steps(False)):
             assert torch.equal(a, b)
+
+
+def _attend(csa2, inp, sm, max_new, window=0):
+    q, kc, vc, ks, vs, table, kv, cu = [t.to(DEV) for t in inp]
+    out, lse = torch.full_like(q, 9.0), torch.full(q.shape[:2], 9.0, device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    csa2.csa2_paged_attn_fp8(q, kc, vc, ks, vs, table, kv, cu, out, sm, max_new, window=window, lse=lse, err_flag=err)
+    torch.cuda.synchronize()
+    return out, lse, int(err)
+
+
+def _reference(inp, sm, window=0):
+    q, kc, vc, ks, vs, table, kv, cu = inp
+    return ref.attention(q.double(), ref.values_of(kc), ref.values_of(vc), ks.double(), vs.double(), table, kv, cu, sm,
+                         window)
+
+
+# ---------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("n,at,nats,D,H", [(16384, 0, 17, 128, 320), (16384, 9001, 18, 64, 320), (131072, 0, 18, 64, 160),
+                                           (131072, 5, 20, 64, 160)])
+def test_a_sink_of_small_value_leaves_the_tail_its_weight(csa2, dtype, new, n, at, nats, D, H):
+    """One key has nearly all the weight and no value: what comes out is the sum of many weights e^-nats.  A weight
+    is an f16 number of 11 bits whose reference lies 2^8 above 1, so those below 2^-14 2^-8 of the largest, and only
+    those, are off by up to half of f16's subnormal step, 2^-25 2^-8: n 2^-33 max|v| in place of the n 2^-25 max|v|
+    that ref.attention allows.  So many heads, all alike, that one CTA walks through most of a head's keys."""
+    gen = torch.Generator().manual_seed(n + nats)
+    S, G = 64, 2
+    table, pool = ref.ragged(gen, [n], S)
+    kc, vc = torch.zeros(pool, 1, S, D), 1 + torch.randn(pool, 1, S, D, generator=gen) / 8
+    kc[..., 1:] = torch.randn(pool, 1, S, D - 1, generator=gen)              # channels that q does not look at
+    sink = int(table[0, at // S])
+    kc[sink, 0, at % S, 0], vc[sink, 0, at % S] = 16.0, 0.0
+    kc, vc = [x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (kc, vc)]
+    q = torch.zeros(new, G, D)
+    q[:, :, 0] = torch.linspace(1.0, 1.04, G)[None]                         # two query heads, their tails not alike
+    ones = torch.ones(pool, 1)
+    inp = (q.to(dtype), kc, vc, ones, ones, table, torch.tensor([n], dtype=I32), torch.tensor([0, new], dtype=I32))
+    o, l, to, tl = _reference(inp, nats / 16)
+    seen = (n - new + 1 + torch.arange(new)).double()[:, None, None]
+    to = to - seen * (2.0 ** -25 - 2.0 ** -33) * ref.values_of(vc).abs().amax()
+    assert (to > 0).all()
+    all_heads = [x.to(DEV).expand(-1, H, *x.shape[2:]).contiguous() for x in inp[1:5]]
+    out, lse, err = _attend(csa2, (inp[0].repeat(1, H, 1), *all_heads, *inp[5:]), nats / 16, new)
+    assert err == 0
+    for h in range(0, H, 7):
+        ref.check_attention(out[:, G * h:G * h + G], lse[:, G * h:G * h + G], (o, l, to, tl))
