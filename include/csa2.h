@@ -479,7 +479,8 @@ csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, csa2_dtype 
  * kv_len int32 [B] (after the step), cu_len int32 [B + 1] (clamped to [0, T]);
  *         tokens beyond M * S are not there.  M * S <= 2^30, T * Hq / Hkv <= 2^30.
  *         A table entry outside [0, n_blocks) where a visible key should be hides
- *         its keys (CSA2_FLAG_BAD_INDEX).  The rows of a request that waits
+ *         its keys (CSA2_FLAG_BAD_INDEX); entries of blocks that end before every
+ *         row's window are not looked at.  The rows of a request that waits
  *         (csa2_build_slots gave it slots of -1) get the output of the last tokens
  *         that it holds: they mean nothing and are dropped.
  * max_new upper bound (>= 1) of the rows of a request, known on the host: it only

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
     for (int b = plan.b; at < stop && b < a.B; ++b) {
         const Request rq = request_of(a, b);
         const int64_t end = base + Work::tiles(a, rq);
-        const int key0 = Work::first_key(a, rq), rows = rq.n * a.G;
+        const int low = Work::low_key(a, rq), key0 = Work::first_key(a, rq), rows = rq.n * a.G;
         while (at < stop && at < end) {
             // segment: tiles [ta, tb) of one unit
             const Place pl = Work::place(a, rq, at - base);
@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
             const int count = todo > warp ? (todo - warp + kAttnWarps - 1) / kAttnWarps : 0;
             const int32_t *table = a.table + b * a.table_stride;
             auto key_of = [&](int i) { return key0 + (ta + warp + (i + lane / U) * kAttnWarps) * kTileKeys<D> + 16 * (lane % U); };
-            auto there = [&](int i) { return i + lane / U < count && key_of(i) < rq.kv; };
+            // groups that end before every row's window are not read: their blocks may be another request's by now
+            auto there = [&](int i) { return i + lane / U < count && key_of(i) < rq.kv && key_of(i) + 16 > low; };
             auto entry = [&](int i) -> int32_t { return there(i) ? table[key_of(i) / a.S] : -1; };   // block of this lane's group
             int32_t block = entry(0), block_next = entry(BT);
             // Q travels beside the chain of loads to the first codes: for a B operand row g,

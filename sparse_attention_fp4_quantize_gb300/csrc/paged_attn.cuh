@@ -190,10 +190,11 @@ constexpr int kSplitWarps = 4, kSplitCost = 16;
 static_assert(kSplitCost % kSplitWarps == 0, "segments begin at whole rounds of the warps");
 template <int R, int K>
 struct SplitWork {
-    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r) {
-        const int64_t p = (int64_t)r.kv - r.n - a.window + 1;      // lowest key of the first row's window
-        return a.window > 0 && p > 0 ? (int)p & ~(K - 1) : 0;
+    static __device__ __forceinline__ int low_key(const PagedAttnArgs &a, const Request &r) {       // of the first row's window
+        const int64_t p = (int64_t)r.kv - r.n - a.window + 1;
+        return a.window > 0 && p > 0 ? (int)p : 0;
     }
+    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r) { return low_key(a, r) & ~(K - 1); }
     static __device__ __forceinline__ int real_tiles(const PagedAttnArgs &a, const Request &r) {
         const int keys = r.kv - first_key(a, r);
         return keys > 0 ? (keys + K - 1) / K : 1;
@@ -237,9 +238,12 @@ struct TcWork {
         }
         __device__ __forceinline__ int last_tok() const { return tok + q255 + (rem + m255 >= G); }
     };
-    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r, const Rows &w) {
+    static __device__ __forceinline__ int low_key(const PagedAttnArgs &a, const Request &r, const Rows &w) {
         const int64_t p = (int64_t)r.kv - r.n + w.tok - a.window + 1;
-        return a.window > 0 && p > 0 ? (int)p & ~(kTcKeys - 1) : 0;
+        return a.window > 0 && p > 0 ? (int)p : 0;
+    }
+    static __device__ __forceinline__ int first_key(const PagedAttnArgs &a, const Request &r, const Rows &w) {
+        return low_key(a, r, w) & ~(kTcKeys - 1);
     }
     static __device__ __forceinline__ int unit_places(const PagedAttnArgs &a, const Request &r, const Rows &w) {
         const int last = min(w.last_tok(), r.n - 1);

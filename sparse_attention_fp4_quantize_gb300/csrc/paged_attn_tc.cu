@@ -66,7 +66,8 @@ struct alignas(16) Segment {
     Request rq;
     Place pl;
     int b, tb;                               // request, end of its key tiles [pl.tile, tb) of pl.tiles
-    int rows, key0;                          // rows of the request and KV head (0: no more segments); key of the unit's first tile
+    int rows, low;                           // rows of the request and KV head (0: no more segments); lowest key that the unit sees
+    __device__ __forceinline__ int key0() const { return low & ~(kTcKeys - 1); }               // of its first tile
 };
 
 template <int D>
@@ -195,7 +196,7 @@ struct Walk {
         s.pl.tile = max(0, s.pl.tile - kTcCost);             // from places to tiles
         s.pl.tiles -= kTcCost;
         s.rows = rq.n * a.G;
-        s.key0 = TcWork::first_key(a, rq, rows);
+        s.low = TcWork::low_key(a, rq, rows);
         return true;
     }
 };
@@ -423,8 +424,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         auto offsets = [&]() {
             if (batch < 0 || tile_ahead >= batch + 16) {
                 batch = tile_ahead;
-                const int key = ahead.key0 + (batch + (lane >> 1)) * kTcKeys + 32 * cw + 16 * (lane & 1);
-                const bool there = batch + (lane >> 1) < ahead.tb && key < ahead.rq.kv;
+                const int key = ahead.key0() + (batch + (lane >> 1)) * kTcKeys + 32 * cw + 16 * (lane & 1);
+                // groups that end before every row's window are not read: their blocks may be another request's by now
+                const bool there = batch + (lane >> 1) < ahead.tb && key < ahead.rq.kv && key + 16 > ahead.low;
                 const int32_t blk = there ? a.table[ahead.b * a.table_stride + key / a.S] : -1;
                 const bool ok = blk >= 0 && blk < a.n_blocks;
                 if (there && !ok) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int64_t at = __shfl_sync(ALL, boff, 2 * cur + u);
-                const int left = ahead.rq.kv - (ahead.key0 + tile_ahead * kTcKeys + 32 * cw + 16 * u);
+                const int left = ahead.rq.kv - (ahead.key0() + tile_ahead * kTcKeys + 32 * cw + 16 * u);
                 rows[u] = at < 0 ? 0 : min(left, 16);
                 off[u] = at < 0 ? 0 : at;
             }
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             l = 0.0f;
             for (int j = 0; j < n; ++j, ++nt, ++ns) {
                 const TileMeta &m = metas[nt % kMetas];
-                const int key0 = seg.key0 + (seg.pl.tile + j) * kTcKeys;
+                const int key0 = seg.key0() + (seg.pl.tile + j) * kTcKeys;
                 const int lo = max(first - key0, 0), hi = min(pos + 1 - key0, kTcKeys);
                 // The common case, one exponential and no maximum: with the references as
                 // they are, P = 2^(s f + log2(2^kUp vs) - Mv), and l gains sum P / (2^kUp vs) 2^(Mv - M).

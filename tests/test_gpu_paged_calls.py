@@ -2,6 +2,7 @@
 hold nothing where nothing is read, on the GPU."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -70,6 +71,16 @@ def _reference(inp, sm, window=0):
                          window)
 
 
+def _inputs(seed, kv, new, Hq, H, D, S, dtype=torch.bfloat16):
+    gen = torch.Generator().manual_seed(seed)
+    table, n = ref.ragged(gen, kv, S)
+    kc, ks = ref.random_planes(gen, n, H, S, D)
+    vc, vs = ref.random_planes(gen, n, H, S, D)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=I32)
+    q = torch.randn(int(cu[-1]), Hq, D, generator=gen).to(dtype)
+    return q, kc, vc, ks, vs, table, torch.tensor(kv, dtype=I32), cu
+
+
 # ---------------------------------------------------------------- weights far below the largest
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("new", [1, 40])
@@ -101,3 +112,22 @@ def test_a_sink_of_small_value_leaves_the_tail_its_weight(csa2, dtype, new, n, a
     assert err == 0
     for h in range(0, H, 7):
         ref.check_attention(out[:, G * h:G * h + G], lse[:, G * h:G * h + G], (o, l, to, tl))
+
+
+# ---------------------------------------------------------------- behind a window
+@pytest.mark.parametrize("new", [1, 3, 40, 200])
+@pytest.mark.parametrize("D,S,window", [(64, 16, 100), (128, 16, 1), (128, 32, 77), (64, 64, 300)])
+def test_nothing_is_read_before_the_window(csa2, new, D, S, window):
+    """Blocks wholly before every row's window: given back (-1, no flag), or another request's, with rows that are not written."""
+    inp = list(_inputs(new + S, [2050, 130], [new, min(new, 130)], 8, 2, D, S))
+    want = _reference(inp, 0.1, window)
+    q, kc, vc, ks, vs, table, kv, cu = inp
+    for entry in (-1, kc.shape[0]):
+        x = [t.clone() for t in inp]
+        for b in range(2):
+            x[5][b, :max(0, int(kv[b]) - int(cu[b + 1] - cu[b]) - window + 1) // S] = entry
+        x[1], x[2] = [torch.cat([t, torch.full_like(t[:1], 0x7F)]) for t in (kc, vc)]
+        x[3], x[4] = torch.cat([ks, torch.full_like(ks[:1], float("nan"))]), torch.cat([vs, torch.full_like(vs[:1], float("inf"))])
+        out, lse, err = _attend(csa2, x, 0.1, new, window)
+        ref.check_attention(out, lse, want)
+        assert err == 0
