@@ -208,13 +208,13 @@ struct Tile {
                     grow[x][r] = ex2(mv[x][r] - refv);
                     grew |= mv1 != mv[x][r];
                     m[x][r] = m1, mv[x][r] = mv1;
-                    const float g2 = ex2(ref - refv);
+                    const float g2 = ex2(0.5f * (ref - refv));          // 2^(m - mv) in two steps: it need not be an fp32 number
                     back[x][r] = ex2(refv - ref);
                     dmin = fminf(dmin, m1 == NEG_INF || mv1 == NEG_INF ? NEG_INF : m1 - mv1);
                     dmax = fmaxf(dmax, ref - refv);
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const float f = fminf(meta.vs[u] * g2, kMostWeight) * kUpFactor;
+                        const float f = fminf(meta.vs[u] * g2 * g2, kMostWeight) * kUpFactor;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float e = ex2(z[2 * u + h] - ref);
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                 if (lane / U == i % BT) {
                     StageMeta<D> &m = s_meta[warp][i % kStages];
                     const int u = lane % U, key = key0 + (ta + warp + i * kAttnWarps) * kTileKeys<D>;
-                    m.ks[u] = ks, m.vs[u] = vs, m.lg[u] = lg2(vs) + kUp, m.rv[u] = rcp(vs) * kDownFactor;
+                    m.ks[u] = ks, m.vs[u] = vs, m.lg[u] = log_scale(vs), m.rv[u] = rcp(vs) * kDownFactor;
                     m.stored[u] = off < 0 ? 0 : min(16, rq.kv - key - 16 * u);
                 }
             };
@@ -514,11 +514,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
                         }
                     }
                     if (whole) {
-                        const float f = exp2f(refv - ref);
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) o[c] *= f;
                         const int tok = row / a.G;
-                        store_row<D, HALF, 16>(a, (rq.row0 + tok) * a.Hq + h * a.G + row - tok * a.G, part, o, M, l);
+                        store_row<D, HALF, 16>(a, (rq.row0 + tok) * a.Hq + h * a.G + row - tok * a.G, part, o, exp2f(refv - ref), M, l);
                     } else {
                         float *dst = a.partial + ((2 * (int64_t)blockIdx.x + first_part) * R + 8 * x + y) * LD;
 #pragma unroll
@@ -607,11 +604,8 @@ __device__ __forceinline__ void join_unit(const PagedAttnArgs &a, const JoinUnit
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) acc[i] += f * s_o[w0 + w][yy][part * (D / 8) + i];
         }
-        const float f = exp2f(refv - ref);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) acc[i] *= f;
         const int tok = row / a.G;
-        store_row<D, HALF, 8>(a, (unit.row0 + tok) * a.Hq + unit.h * a.G + row - tok * a.G, part, acc, Ma, la);
+        store_row<D, HALF, 8>(a, (unit.row0 + tok) * a.Hq + unit.h * a.G + row - tok * a.G, part, acc, exp2f(refv - ref), Ma, la);
     }
 }
 

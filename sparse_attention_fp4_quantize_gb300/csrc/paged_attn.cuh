@@ -83,6 +83,13 @@ __device__ __forceinline__ float rcp(float x) {
     return r;
 }
 
+// log2 of 2^kUp v_scale for the common case of both kernels, whose factors 2^(Mv - M) and
+// 1 / v_scale stay normal fp32 numbers for scales within 2^+-40; -inf for others (and 0),
+// which take the way with maxima.
+__device__ __forceinline__ float log_scale(float vs) {
+    return vs >= 0x1p-40f && vs <= 0x1p40f ? lg2(vs) + kUp : __int_as_float(0xff800000);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -276,14 +283,14 @@ struct TcWork {
     }
 };
 
-// P threads per row, D / P channels each: o = x / (2^kUp l) in the output's type, lse.
+// P threads per row, D / P channels each: o = x / (2^kUp l) f in the output's type (f = 2^(Mv - M)), lse.
 template <int D, bool HALF, int P>
-__device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row, int part, const float *x, float M, float l) {
+__device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row, int part, const float *x, float f, float M, float l) {
     const float inv = l > 0.0f ? kDownFactor / l : (l == 0.0f ? 0.0f : l);
     constexpr int W = D / P / 2;
     uint32_t w[W];
 #pragma unroll
-    for (int c = 0; c < W; ++c) w[c] = pack_out<HALF>(x[2 * c] * inv, x[2 * c + 1] * inv);
+    for (int c = 0; c < W; ++c) w[c] = pack_out<HALF>(x[2 * c] * inv * f, x[2 * c + 1] * inv * f);
     uint16_t *dst = a.out + o_row * D + part * (D / P);
     if constexpr (W == 2) {
         *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 boff = ok ? (bh * a.S + (key & (a.S - 1))) * D : -1;
                 bks = ok ? a.k_scale[bh] : 0.0f;
                 bvs = ok ? a.v_scale[bh] : 0.0f;
-                blg = lg2(bvs) + kUp;
+                blg = log_scale(bvs);
                 brv = rcp(bvs) * kDownFactor;
                 bmiss = __ballot_sync(ALL, !ok);
             }
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                         uint32_t w[4][4];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            w[i / 4][i % 4] = pack_out<HALF>(__uint_as_float(r[2 * i]) * scale * inv, __uint_as_float(r[2 * i + 1]) * scale * inv);
+                            w[i / 4][i % 4] = pack_out<HALF>(__uint_as_float(r[2 * i]) * inv * scale, __uint_as_float(r[2 * i + 1]) * inv * scale);
 #pragma unroll
                         for (int d = 1; d < 4; d *= 2)
 #pragma unroll
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     const float grow = upv ? ex2(MV - tv) : 1.0f;
                     if (upv) MV = tv;
                     if (j > 0 && __any_sync(ALL, upv)) rescale(grow);
-                    const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(ref - (MV == NEG_INF ? 0.0f : MV));
+                    const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(0.5f * (ref - (MV == NEG_INF ? 0.0f : MV)));     // 2^(M - Mv) in two steps
                     const uint64_t nref = f2(-ref, -ref);
                     uint64_t sum = f2(0.0f, 0.0f);
 #pragma unroll 1
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                             uint32_t p[16];
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2, kMostWeight) * kUpFactor;
+                                const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2 * g2, kMostWeight) * kUpFactor;
                                 const uint64_t ff = f2(f, f), ww = f2(w, w);
 #pragma unroll
                                 for (int i = 0; i < 16; i += 2) {

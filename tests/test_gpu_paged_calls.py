@@ -131,3 +131,16 @@ def test_nothing_is_read_before_the_window(csa2, new, D, S, window):
         out, lse, err = _attend(csa2, x, 0.1, new, window)
         ref.check_attention(out, lse, want)
         assert err == 0
+
+
+# ---------------------------------------------------------------- scales at the ends of fp32
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("exponent", [127, 126, 120, 61, 41, 39, -39, -41, -61, -126, -130])
+def test_value_scales_at_the_ends_of_fp32(csa2, new, exponent):
+    """V scales that have no fp32 reciprocal or are subnormal, codes that keep the values finite."""
+    inp = list(_inputs(200 + exponent, [1500], [new], 4, 2, 64, 16))
+    vc = (ref.values_of(inp[2]) / 448).float().clamp(-0.9, 0.9).to(torch.float8_e4m3fn).view(torch.uint8)
+    inp[2], inp[4] = vc, torch.full_like(inp[4], 2.0 ** exponent)
+    out, lse, err = _attend(csa2, inp, 0.05, new)
+    ref.check_attention(out, lse, _reference(inp, 0.05))
+    assert err == 0
