@@ -414,7 +414,8 @@ size_t csa2_sparse_attn_noalloc_max_scratch_bytes(void);
  *            a negative one gives its tokens slot -1 (CSA2_FLAG_BAD_INDEX).
  * kv_len_out, free_count_out  int32 [B], [1]: the lengths and the count after
  *            the step; may be kv_len and free_count themselves (a captured
- *            step that is replayed).  No output overlaps another input (refused).
+ *            step that is replayed).  Nothing that is written (outputs, block_table,
+ *            free_list) overlaps any other argument otherwise (refused).
  * cu_len     int32 [B + 1]: the first row of each request among the step's
  *            tokens (those of waiting requests counted), clamped to T.
  * positions  int32 [T] or NULL, slots int64 [T]: position and slot of each

@@ -247,6 +247,14 @@ __global__ void build_slots_kernel(SlotArgs a) {
     }
 }
 
+// Whether n words at p share one with the table's rows (B of M words, `stride` words apart).
+bool rows_meet(const int32_t *table, int64_t B, int64_t M, int64_t stride, const void *p, int64_t n) {
+    const int64_t x = (int64_t)((uintptr_t)p - (uintptr_t)table), end = x + 4 * n, pitch = 4 * stride;      // bytes from the table's begin
+    if (n == 0 || end <= 0 || x / pitch >= B) return false;
+    const int64_t row = x < 4 * M ? 0 : (x - 4 * M) / pitch + 1;           // the first row that ends behind x
+    return row < B && row * pitch < end;
+}
+
 }  // namespace
 }  // namespace csa2
 
@@ -262,22 +270,31 @@ extern "C" csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int 
     CSA2_REQUIRE(S >= 1 && M >= 1 && (int64_t)M * S < (1ll << 31), "build_slots: S=%d, M=%d: need M * S < 2^31", S, M);
     CSA2_REQUIRE((int64_t)B * M < (1ll << 31), "build_slots: B * M = %lld entries", (long long)B * M);
     CSA2_REQUIRE(table_stride >= M, "build_slots: table_stride=%lld < M=%d", (long long)table_stride, M);
+    CSA2_REQUIRE(table_stride < (1ll << 40), "build_slots: table_stride=%lld", (long long)table_stride);
     CSA2_REQUIRE(T >= 0 && T <= (1ll << 30), "build_slots: T=%lld not in [0, 2^30]", (long long)T);
     CSA2_REQUIRE(free_cap >= 0 && free_cap < (1ll << 31), "build_slots: free_cap=%lld", (long long)free_cap);
     CSA2_REQUIRE(kv_len && new_len && block_table && free_count && kv_len_out && free_count_out && cu_len,
                  "build_slots: null pointer");
     CSA2_REQUIRE((free_list || free_cap == 0) && (slots || T == 0), "build_slots: null pointer");
     CSA2_REQUIRE(aligned(slots, 8), "build_slots: slots must be 8-byte aligned");
-    // every CTA reads the inputs: an output may take the place of its own, and overlap no other
+    // The CTAs read and write side by side: only the lengths' and the count's outputs may take
+    // the place of their inputs, all else stands apart.  Inputs first, then what is written.
     const bool in_place = kv_len_out == kv_len || free_count_out == free_count;
-    const struct { const void *p; int64_t n; } in[3] = {{kv_len, B}, {new_len, B}, {free_count, 1}},
-        out[5] = {{kv_len_out, B}, {cu_len, B + 1ll}, {free_count_out, 1}, {positions, positions ? T : 0}, {slots, 2 * T}};
-    for (int o = 0; o < 5; ++o)
-        for (int i = 0; i < 3; ++i) {
-            const uintptr_t x = (uintptr_t)out[o].p, y = (uintptr_t)in[i].p;
-            const bool own = o == i && o != 1 && x == y;
-            CSA2_REQUIRE(own || x + 4 * out[o].n <= y || y + 4 * in[i].n <= x, "build_slots: an output overlaps an input");
+    const struct Span { const void *p; int64_t n; } span[10] = {           // 4-byte words
+        {kv_len, B}, {free_count, 1}, {new_len, B}, {kv_len_out, B}, {free_count_out, 1}, {cu_len, B + 1ll},
+        {positions, positions ? T : 0}, {slots, 2 * T}, {free_list, free_cap},
+        {err_flag, err_flag != nullptr}};
+    auto apart = [](const Span &x, const Span &y) {
+        return !x.n || !y.n || (uintptr_t)x.p + 4 * x.n <= (uintptr_t)y.p || (uintptr_t)y.p + 4 * y.n <= (uintptr_t)x.p;
+    };
+    for (int i = 0; i < 10; ++i) {
+        for (int o = i < 3 ? 3 : i + 1; o < 10; ++o) {
+            const bool own = o == i + 3 && i < 2 && span[o].p == span[i].p;
+            CSA2_REQUIRE(own || apart(span[i], span[o]), i < 3 ? "build_slots: an output overlaps an input"
+                                                               : "build_slots: an output overlaps another");
         }
+        CSA2_REQUIRE(!rows_meet(block_table, B, M, table_stride, span[i].p, span[i].n), "build_slots: block_table overlaps another tensor");
+    }
     const SlotArgs args = {B, M, S, table_stride, T, free_cap, kv_len, new_len, block_table, free_list, free_count,
                            kv_len_out, free_count_out, cu_len, positions, slots, err_flag,
                            aligned(slots, 16) && aligned(positions, 16), in_place};

@@ -144,3 +144,21 @@ def test_value_scales_at_the_ends_of_fp32(csa2, new, exponent):
     out, lse, err = _attend(csa2, inp, 0.05, new)
     ref.check_attention(out, lse, _reference(inp, 0.05))
     assert err == 0
+
+
+# ---------------------------------------------------------------- slot maps
+def test_slots_with_lengths_in_the_gap_between_table_rows(csa2):
+    """Nothing that is written may overlap anything else; a strided table's gaps are nobody's."""
+    B, M, S, T = 3, 4, 16, 40
+    wide = torch.full((B, M + B), -1, dtype=I32, device=DEV)
+    kv, new = wide[0, M:], wide[1, M:]
+    kv.copy_(torch.tensor([0, 16, 5])), new.copy_(torch.tensor([20, 1, 0]))
+    wide[1, 0], wide[2, 0] = 6, 7
+    free, count = torch.arange(6, dtype=I32, device=DEV), torch.tensor([6], dtype=I32, device=DEV)
+    kv_out, cu = torch.zeros(B, dtype=I32, device=DEV), torch.zeros(B + 1, dtype=I32, device=DEV)
+    slots = torch.zeros(T, dtype=torch.int64, device=DEV)
+    csa2.csa2_build_slots(kv, new, wide[:, :M], free, count, S, kv_out, count, cu, None, slots)
+    torch.cuda.synchronize()
+    assert kv_out.tolist() == [20, 17, 5] and kv.tolist() == [0, 16, 5] and int(count) == 3
+    assert wide[:, :M].tolist() == [[5, 4, -1, -1], [6, 3, -1, -1], [7, -1, -1, -1]]
+    assert slots.tolist() == [5 * S + i for i in range(16)] + [4 * S + i for i in range(4)] + [3 * S] + [-1] * 19

@@ -1,0 +1,58 @@
+"""Calls of the paged 8-bit cache that the C ABI or the class refuse or keep apart, on the CPU."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+import sparse_attention_fp4_quantize_gb300 as csa2
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__._build_module().build()
+    return csa2._lib
+
+
+def _refused(rc, lib, word):
+    assert rc == 1, (rc, lib.csa2_last_error())
+    assert word in lib.csa2_last_error().decode()
+
+
+# ---------------------------------------------------------------- slot maps
+B, M, STRIDE, T, CAP = 4, 8, 20, 10, 32
+APART = dict(kv=0x10000, new=0x20000, count=0x30000, kv_out=0x40000, count_out=0x50000, cu=0x60000, pos=0x70000, slots=0x80000,
+             free=0x90000, table=0xA0000, err=0xB0000)
+BYTES = dict(kv=4 * B, new=4 * B, count=4, kv_out=4 * B, count_out=4, cu=4 * B + 4, pos=4 * T, slots=8 * T, free=4 * CAP, err=4)
+
+
+def _build_slots(lib, **where):
+    p = {n: P(x) for n, x in {**APART, **where}.items()}
+    return lib.csa2_build_slots(B, M, STRIDE, 8, T, CAP, p["kv"], p["new"], p["table"], p["free"], p["count"], p["kv_out"],
+                                p["count_out"], p["cu"], p["pos"], p["slots"], p["err"], None)
+
+
+WRITTEN = ["kv_out", "count_out", "cu", "pos", "slots", "free", "err"]
+
+
+@pytest.mark.parametrize("one", WRITTEN)
+def test_build_slots_refuses_what_is_written_over_anything_else(lib, one):
+    for other, n in BYTES.items():
+        if other == one:
+            continue
+        own = {"kv_out": "kv", "count_out": "count"}.get(one) == other
+        for off in (0, n - 4, 4 - BYTES[one]):
+            if (own and off == 0) or (one == "slots" and off % 8):
+                continue
+            _refused(_build_slots(lib, **{one: APART[other] + off}), lib, "overlaps")
+
+
+@pytest.mark.parametrize("one", list(BYTES))
+def test_build_slots_refuses_the_table_over_anything_else(lib, one):
+    row, last, step = 4 * STRIDE, (B - 1) * 4 * STRIDE, 8 if one == "slots" else 4
+    for begin in (0, row, last):
+        for at in (begin, begin + 4 * M - step, begin + step - BYTES[one]):
+            _refused(_build_slots(lib, **{one: APART["table"] + at}), lib, "overlaps")
