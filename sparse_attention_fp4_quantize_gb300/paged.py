@@ -62,7 +62,9 @@ class PagedCache:
         self.out = torch.zeros(s.layers, s.tokens, s.heads, s.dim, dtype=s.dtype, device=dev)
         self.lse = torch.zeros(s.layers, s.tokens, s.heads, dtype=torch.float32, device=dev)
         self.err = torch.zeros(1, dtype=i32, device=dev)
-        self.ws = workspace_for_paged_attn(s.requests, s.tokens, s.heads, s.kv_heads, s.dim, s.max_new, device=dev)
+        # one per layer: layers may be attended side by side, on streams of their own or in graphs of their own
+        self.ws = [workspace_for_paged_attn(s.requests, s.tokens, s.heads, s.kv_heads, s.dim, s.max_new, device=dev)
+                   for _ in range(s.layers)]
         self.sm_scale = 1.0 / float(s.dim) ** 0.5
 
     def plan(self, stream=None):
@@ -77,9 +79,10 @@ class PagedCache:
                                    self.v_scale[layer], err_flag=self.err, stream=stream)
 
     def attend(self, layer: int, q, window: int = 0, stream=None):
-        """Attention of q [tokens, heads, dim] over the layer's cache; returns (out, lse), the cache's buffers."""
+        """Attention of q [tokens, heads, dim] over the layer's cache; returns (out, lse), the cache's buffers.  Calls for
+        several layers may overlap; calls for one layer, which share its buffers, must follow one another."""
         csa2_paged_attn_fp8(q, self.k_codes[layer], self.v_codes[layer], self.k_scale[layer], self.v_scale[layer],
                             self.block_table, self.kv_len, self.cu_len, self.out[layer], self.sm_scale,
                             self.shape.max_new, window=window, lse=self.lse[layer], err_flag=self.err,
-                            workspace=self.ws, stream=stream)
+                            workspace=self.ws[layer], stream=stream)
         return self.out[layer], self.lse[layer]

@@ -162,3 +162,29 @@ def test_slots_with_lengths_in_the_gap_between_table_rows(csa2):
     assert kv_out.tolist() == [20, 17, 5] and kv.tolist() == [0, 16, 5] and int(count) == 3
     assert wide[:, :M].tolist() == [[5, 4, -1, -1], [6, 3, -1, -1], [7, -1, -1, -1]]
     assert slots.tolist() == [5 * S + i for i in range(16)] + [4 * S + i for i in range(4)] + [3 * S] + [-1] * 19
+
+
+# ---------------------------------------------------------------- layers side by side
+def test_layers_attended_on_streams_of_their_own(csa2):
+    """The same bits as one behind the other: long contexts, whose parts are joined through the workspace."""
+    from sparse_attention_fp4_quantize_gb300.paged import PagedCache, PagedShape
+    B, H, Hq, D, L, n = 2, 2, 8, 128, 2, 3000
+    cache = PagedCache(PagedShape(requests=B, tokens=2 * n, max_context=n + 1, n_blocks=100, heads=Hq, kv_heads=H, dim=D,
+                                  layers=L, max_new=1))
+    gen = torch.Generator(DEV).manual_seed(3)
+    q, k, v = [torch.randn(L, 2 * n, h, D, generator=gen, device=DEV).to(torch.bfloat16) for h in (Hq, H, H)]
+    for new in (n, 1):
+        cache.new_len.fill_(new)
+        cache.plan()
+        for layer in range(L):
+            cache.append(layer, k[layer], v[layer])
+    want = [[t.clone() for t in cache.attend(layer, q[layer])] for layer in range(L)]
+    streams = [torch.cuda.Stream() for _ in range(L)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for layer in range(L):
+            cache.attend(layer, q[layer], stream=streams[layer])
+    torch.cuda.synchronize()
+    for layer in range(L):
+        assert torch.equal(cache.out[layer][:B], want[layer][0][:B]) and torch.equal(cache.lse[layer][:B], want[layer][1][:B])
+    assert int(cache.err) == 0

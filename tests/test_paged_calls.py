@@ -4,6 +4,7 @@ from __future__ import annotations
 import ctypes
 
 import pytest
+import torch
 
 import sparse_attention_fp4_quantize_gb300 as csa2
 
@@ -56,3 +57,36 @@ def test_build_slots_refuses_the_table_over_anything_else(lib, one):
     for begin in (0, row, last):
         for at in (begin, begin + 4 * M - step, begin + step - BYTES[one]):
             _refused(_build_slots(lib, **{one: APART["table"] + at}), lib, "overlaps")
+
+
+# ---------------------------------------------------------------- the class
+class _Calls:
+    """A stand-in for the library that keeps the calls' arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def csa2_paged_attn_workspace_bytes(self, *a):
+        return 4096
+
+    def __getattr__(self, name):
+        def call(*a):
+            self.calls.append((name, a))
+            return 0
+        return call
+
+
+def test_layers_of_a_cache_share_no_workspace(monkeypatch):
+    """attend takes a stream: layers that run side by side, on two streams or in two graphs, join their own parts."""
+    from sparse_attention_fp4_quantize_gb300.paged import PagedCache, PagedShape
+    fake = _Calls()
+    monkeypatch.setattr(csa2, "_lib", fake)
+    monkeypatch.setattr(csa2, "_on_device", lambda t: True)
+    monkeypatch.setattr(csa2, "_stream", lambda s: s)
+    cache = PagedCache(PagedShape(requests=2, tokens=4, max_context=64, n_blocks=4, heads=4, kv_heads=2, dim=64, block_size=16,
+                                  layers=3), device="cpu")
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)
+    for layer in range(3):
+        cache.attend(layer, q, stream=layer + 1)
+    used = sorted(a[-3] for name, a in fake.calls if name == "csa2_paged_attn_fp8")
+    assert len(used) == 3 and all(y - x >= 4096 for x, y in zip(used, used[1:]))
