@@ -44,8 +44,13 @@ constexpr int kSoftWarps = 8, kConvWarps = 4, kMmaWarp = kSoftWarps + kConvWarps
 constexpr int kTcThreads = 512;              // four warpgroups, as the register shares go by warpgroup
 // Registers per thread: 512 x 128 at launch; the softmax warpgroups, which hold
 // a row's 128 scores, take what the others give up.
-constexpr int kSoftRegs = 176, kConvRegs = 80, kMmaRegs = 80;
-static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * 128, "register shares exceed the launch's");
+constexpr int kLaunchRegs = 128, kSoftRegs = 176, kConvRegs = 80, kMmaRegs = 80;
+static_assert(kLaunchRegs * kTcThreads == 65536, "the launch's registers are an SM's");
+static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * kLaunchRegs, "register shares exceed the launch's");
+static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs,
+              "setmaxnreg.inc may not ask for fewer than the launch's, .dec not for more (an illegal instruction)");
+static_assert(kSoftRegs % 8 == 0 && kConvRegs % 8 == 0 && kMmaRegs % 8 == 0 && kConvRegs >= 24 && kMmaRegs >= 24 && kSoftRegs <= 256,
+              "setmaxnreg takes multiples of 8 from 24 to 256");
 constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after that many naps (ns, ended by the arrival)
 constexpr uint32_t kLockPolls = 1u << 24;
 constexpr float kSlack = 14 - kUp;           // log2: how far a tile may exceed a reference before it moves (P < 2^(kUp + kSlack + 1))
