@@ -382,7 +382,8 @@ size_t csa2_sparse_attn_noalloc_max_scratch_bytes(void);
  *   block_table       int32 [B, M] (row stride table_stride): token position p
  *                     of request b is row p % S of block block_table[b][p / S]
  *   slot of a token   block * S + row, int64; -1: the token is not stored
- * A block holds tokens of one request.
+ * A block holds tokens of one request.  Arrays of int32 and fp32 are 4-byte
+ * aligned, others as the calls say (anything else is refused).
  *
  * One step of a serving loop is csa2_build_slots (which blocks the new tokens
  * go to), csa2_quantize_kv_fp8_paged (store them) per layer, then

@@ -722,6 +722,9 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
     CSA2_REQUIRE((k_codes && v_codes && k_scale && v_scale) || n_blocks == 0, "paged_attn: null pointer");
     CSA2_REQUIRE(aligned(q, 16) && aligned(out, 16) && aligned(k_codes, 16) && aligned(v_codes, 16),
                  "paged_attn: q, out and codes must be 16-byte aligned");
+    CSA2_REQUIRE(aligned(k_scale, 4) && aligned(v_scale, 4) && aligned(block_table, 4) && aligned(kv_len, 4) &&
+                     aligned(cu_len, 4) && aligned(lse, 4) && aligned(err_flag, 4),
+                 "paged_attn: scales, table, lengths, lse and flag must be 4-byte aligned");
     const size_t need = csa2_paged_attn_workspace_bytes(B, T, Hq, Hkv, D, max_new);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) {
         set_error("paged_attn: workspace of %zu bytes (16-byte aligned) needed, %zu given", need, ws_bytes);

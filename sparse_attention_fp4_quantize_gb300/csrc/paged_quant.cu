@@ -231,7 +231,8 @@ extern "C" csa2_status csa2_quantize_kv_fp8_paged(const void *k, const void *v, 
     CSA2_REQUIRE((k_codes && v_codes && k_scale && v_scale) || n_blocks == 0, "quantize_paged: null pointer");
     CSA2_REQUIRE(aligned(k, 16) && aligned(v, 16), "quantize_paged: k and v must be 16-byte aligned");
     CSA2_REQUIRE(aligned(k_codes, 16) && aligned(v_codes, 16), "quantize_paged: codes must be 16-byte aligned");
-    CSA2_REQUIRE(aligned(k_scale, 4) && aligned(v_scale, 4) && aligned(slots, 8), "quantize_paged: misaligned scales / slots");
+    CSA2_REQUIRE(aligned(k_scale, 4) && aligned(v_scale, 4) && aligned(slots, 8) && aligned(err_flag, 4),
+                 "quantize_paged: misaligned scales / slots / flag (4-, 8- and 4-byte aligned)");
     PagedQuantArgs a = {};
     a.x[0] = (const uint16_t *)k, a.x[1] = (const uint16_t *)v;
     a.token_stride[0] = k_token_stride, a.token_stride[1] = v_token_stride;

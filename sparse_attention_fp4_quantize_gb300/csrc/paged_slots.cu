@@ -277,6 +277,10 @@ extern "C" csa2_status csa2_build_slots(int B, int M, int64_t table_stride, int 
                  "build_slots: null pointer");
     CSA2_REQUIRE((free_list || free_cap == 0) && (slots || T == 0), "build_slots: null pointer");
     CSA2_REQUIRE(aligned(slots, 8), "build_slots: slots must be 8-byte aligned");
+    for (const void *p : {(const void *)kv_len, (const void *)new_len, (const void *)block_table, (const void *)free_list,
+                          (const void *)free_count, (const void *)kv_len_out, (const void *)free_count_out,
+                          (const void *)cu_len, (const void *)positions, (const void *)err_flag})
+        CSA2_REQUIRE(aligned(p, 4), "build_slots: int32 arguments must be 4-byte aligned");
     // The CTAs read and write side by side: only the lengths' and the count's outputs may take
     // the place of their inputs, all else stands apart.  Inputs first, then what is written.
     const bool in_place = kv_len_out == kv_len || free_count_out == free_count;

@@ -59,6 +59,28 @@ def test_build_slots_refuses_the_table_over_anything_else(lib, one):
             _refused(_build_slots(lib, **{one: APART["table"] + at}), lib, "overlaps")
 
 
+@pytest.mark.parametrize("one", ["kv", "new", "count", "kv_out", "count_out", "cu", "pos", "free", "table", "err"])
+def test_build_slots_refuses_misaligned_words(lib, one):
+    for off in (1, 2):
+        _refused(_build_slots(lib, **{one: APART[one] + 0x4000 + off}), lib, "aligned")
+
+
+@pytest.mark.parametrize("one", ["k_scale", "v_scale", "table", "kv_len", "cu_len", "lse", "err"])
+def test_attention_refuses_misaligned_words(lib, one):
+    at = {n: P(0x10000 * i) for i, n in enumerate(["q", "k", "v", "k_scale", "v_scale", "table", "kv_len", "cu_len", "out", "lse",
+                                                   "err", "ws"], 1)}
+    for off in (1, 2):
+        p = {**at, one: P(at[one].value + off)}
+        _refused(lib.csa2_paged_attn_fp8(2, 4, 8, 2, 64, 0, p["q"], 512, 64, p["k"], p["v"], p["k_scale"], p["v_scale"], 9, 64,
+                                         p["table"], 4, 4, p["kv_len"], p["cu_len"], 1, 0, 0.1, p["out"], p["lse"], p["err"],
+                                         p["ws"], 1 << 30, None), lib, "aligned")
+
+
+def test_append_refuses_a_misaligned_flag(lib):
+    _refused(lib.csa2_quantize_kv_fp8_paged(P(0x1000), P(0x2000), 0, 4, 2, 64, 128, 64, 128, 64, P(0x3000), 8, 16, P(0x4000),
+                                            P(0x5000), P(0x6000), P(0x7000), P(0x8002), None), lib, "aligned")
+
+
 # ---------------------------------------------------------------- the class
 class _Calls:
     """A stand-in for the library that keeps the calls' arguments."""
