@@ -37,7 +37,7 @@ struct PagedAttnArgs {
 // below.  Weights down to 2^-22 of all weights' sum keep their 11 bits; smaller ones are off
 // by 2^-33 of it at most, which a long tail of n keys adds up to n 2^-33 (2^-16 at 131k).
 // More room below leaves less above, by which scores may exceed the references before these
-// have to move: 3 prompts of up to 4096 tokens on up to 8192 take 841 us with 8 (803 with
+// have to move: 3 prompts of up to 4096 tokens on up to 8192 took 841 us with 8 (803 with
 // 0, 820 with 4, 871 with 10), the windows of paged_attn.cu 36.5 (35.0 with 0), 64 requests of
 // up to 16k tokens the same with any.
 constexpr int kUp = 8;

@@ -720,21 +720,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 // O so far to another reference; S followed the products that it waited for
                 auto rescale = [&](float by) {
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 64) {
-                        uint32_t r[2][32];
-                        tc::tmem_ld32(to + x, r[0]);
-                        tc::tmem_ld32(to + x + 32, r[1]);
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t r[32];
+                        tc::tmem_ld32(to + x, r);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < 2; ++c) {
                             uint32_t o[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(r[c / 2][16 * (c & 1) + i]) * by);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(r[16 * c + i]) * by);
                             tc::tmem_st16(to + x + 16 * c, o);
                         }
                     }
                 };
-                while (fast) {
+                for (bool raised = false; fast; raised = true) {
                     const float back = ex2(MV - M);
                     uint32_t p[4][16];
                     float gain = 0.0f, total = 0.0f;
@@ -771,11 +770,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                         l += gain * back;
                         break;
                     }
-                    fast = __all_sync(ALL, total < kMostRaise && gain * back < kMostL);
+                    // once: of scores beyond 2^24 a higher Mv may round to the same, or further up
+                    fast = !raised && __all_sync(ALL, total < kMostRaise && gain * back < kMostL);
                     if (fast) {                          // all 32 rows' sums to 2^kUp, as far as they exceed it
-                        const int k = max(0, (int)(__float_as_uint(total) >> 23) - 127 - kUp);
-                        MV += k;
-                        rescale(__uint_as_float((uint32_t)(127 - k) << 23));
+                        const float mv1 = MV + max(0, (int)(__float_as_uint(total) >> 23) - 127 - kUp);
+                        rescale(ex2(MV - mv1));
+                        MV = mv1;
                     }
                 }
                 if (!fast) {
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     // The references move when a row's scores exceed one by more than the slack, or at a row's
                     // first key; then those of all 32 rows do, as far as they are exceeded, so that the next
                     // tiles are the less likely to need it.
-                    const bool due = tz > M + kSlack || tv > MV + kSlack || (M == NEG_INF && tz > M) || (MV == NEG_INF && tv > MV);
+                    const bool due = tz - M > kSlack || tv - MV > kSlack;
                     const bool all = __any_sync(ALL, due), up = all && tz > M, upv = all && tv > MV;
                     if (up) {
                         l *= ex2(M - tz);
@@ -817,7 +817,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     if (upv) MV = tv;
                     if (j > 0 && __any_sync(ALL, upv)) rescale(grow);
                     const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(0.5f * (ref - (MV == NEG_INF ? 0.0f : MV)));     // 2^(M - Mv) in two steps
-                    const uint64_t nref = f2(-ref, -ref);
                     uint64_t sum = f2(0.0f, 0.0f);
 #pragma unroll 1
                     for (int c = 0; c < 4; c += 2) {
@@ -831,11 +830,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
                                 const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2 * g2, kMostWeight) * kUpFactor;
-                                const uint64_t ff = f2(f, f), ww = f2(w, w);
+                                const uint64_t ww = f2(w, w);
 #pragma unroll
                                 for (int i = 0; i < 16; i += 2) {
-                                    const float2 z = un2(fma2(f2u(r[k][16 * g + i], r[k][16 * g + i + 1]), ff, nref));
-                                    const uint64_t e = f2(ex2(z.x), ex2(z.y));
+                                    // rounded as the maxima were, before the reference is taken off, so that none is beyond
+                                    // them (a packed product and sum would be joined again, without that rounding)
+                                    const float z0 = __fmul_rn(__uint_as_float(r[k][16 * g + i]), f), z1 = __fmul_rn(__uint_as_float(r[k][16 * g + i + 1]), f);
+                                    const uint64_t e = f2(ex2(__fadd_rn(z0, -ref)), ex2(__fadd_rn(z1, -ref)));
                                     sum = add2(sum, e);
                                     const float2 x = un2(mul2(e, ww));
                                     p[8 * g + i / 2] = pack_f16(x.x, x.y);

@@ -188,3 +188,17 @@ def test_layers_attended_on_streams_of_their_own(csa2):
     for layer in range(L):
         assert torch.equal(cache.out[layer][:B], want[layer][0][:B]) and torch.equal(cache.lse[layer][:B], want[layer][1][:B])
     assert int(cache.err) == 0
+
+
+# ---------------------------------------------------------------- scores beyond fp32's whole numbers
+@pytest.mark.parametrize("new", [1, 80])
+def test_scores_of_any_size_come_to_an_end(csa2, new):
+    """Scores of 2^20 to 2^40, whose steps in fp32 are larger than the references' moves: one key has all the weight, or
+    keys that fp32 cannot tell apart share it, so a row lies between the values' ends."""
+    for seed, exponent in enumerate((20, 24, 26, 28, 30, 40)):
+        inp = list(_inputs(90 + seed, [1500], [new], 4, 2, 64, 16))
+        inp[4] = torch.full_like(inp[4], 1.75)
+        out, lse, err = _attend(csa2, inp, 2.0 ** exponent, new)
+        assert err == 0 and torch.isfinite(lse).all()
+        v = ref.values_of(inp[2]).abs().amax() * 1.75
+        assert (out.double().abs().cpu() <= v * 1.01).all()
