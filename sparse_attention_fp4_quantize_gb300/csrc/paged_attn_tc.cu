@@ -51,7 +51,10 @@ static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kMmaRegs <
               "setmaxnreg.inc may not ask for fewer than the launch's, .dec not for more (an illegal instruction)");
 static_assert(kSoftRegs % 8 == 0 && kConvRegs % 8 == 0 && kMmaRegs % 8 == 0 && kConvRegs >= 24 && kMmaRegs >= 24 && kSoftRegs <= 256,
               "setmaxnreg takes multiples of 8 from 24 to 256");
-constexpr uint32_t kPolls = 4096, kNap = 500000;      // a wait gives up after that many naps (ns, ended by the arrival)
+// A wait gives up after that many naps, which an arrival ends; the hardware cuts them to 6 us
+// whatever is asked for (measured).  Within a key tile, of 2 us, 26 ms; for a segment, which may be 2^23 tiles
+// (2^30 keys) long, 50 s: where something is lost the waits within a tile end all others.
+constexpr uint32_t kPolls = 4096, kSegPolls = 1u << 23, kNap = 500000;
 constexpr uint32_t kLockPolls = 1u << 24;
 constexpr float kSlack = 14 - kUp;           // log2: how far a tile may exceed a reference before it moves (P < 2^(kUp + kSlack + 1))
 constexpr float kSpread = 64.0f;             // log2: how far scales may lie apart in the common case
@@ -134,7 +137,7 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 
 // Bounded wait of one thread that also gives up once another has raised the
 // abort word; and of a whole warp, every lane of which gets the same answer.
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int *abort_word) {
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int *abort_word, uint32_t polls = kPolls) {
     uint32_t ok;                             // most waits are over before they begin: asked without going to sleep
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -142,7 +145,7 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile
         : "r"(bar), "r"(parity)
         : "memory");
     if (ok) return true;
-    for (uint32_t i = 0; i < kPolls; ++i) {
+    for (uint32_t i = 0; i < polls; ++i) {
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
@@ -155,8 +158,8 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile
     *abort_word = 1;
     return false;
 }
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_word) {
-    return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, abort_word));
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_word, uint32_t polls = kPolls) {
+    return __all_sync(0xFFFFFFFFu, wait_one(bar, parity, abort_word, polls));
 }
 
 // Logit factor of a key: not 0, so that a hidden score of -inf stays -inf.
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     auto next_seg = [&](Segment &s) -> bool {
         const uint32_t i = n_seg % kSegs, par = (n_seg / kSegs) & 1;
         ++n_seg;
-        if (!wait_bar(segfull(i), par, abort_word)) return false;
+        if (!wait_bar(segfull(i), par, abort_word, kSegPolls)) return false;
         s = segs[i];
         __syncwarp();
         if (lane == 0) arrive(segempty(i));
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     auto next_seg_one = [&](Segment &s) -> bool {
         const uint32_t i = n_seg % kSegs, par = (n_seg / kSegs) & 1;
         ++n_seg;
-        if (!wait_one(segfull(i), par, abort_word)) return false;
+        if (!wait_one(segfull(i), par, abort_word, kSegPolls)) return false;
         s = segs[i];
         arrive(segempty(i));
         return s.rows > 0;
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 if (more && s.pl.tile == 0 && s.tb < s.pl.tiles)
                     *join = {s.rq.row0, s.pl.h, s.pl.r0, s.rows, (int)((walk.unit + kTcCost + s.pl.tiles - 1) / plan.share), {0, 0}};
                 const uint32_t i = n_seg % kSegs;
-                if (!wait_one(segempty(i), ((n_seg / kSegs) & 1) ^ 1, abort_word)) break;
+                if (!wait_one(segempty(i), ((n_seg / kSegs) & 1) ^ 1, abort_word, kSegPolls)) break;
                 segs[i] = s;
                 arrive(segfull(i));
             }

@@ -202,3 +202,21 @@ def test_scores_of_any_size_come_to_an_end(csa2, new):
         assert err == 0 and torch.isfinite(lse).all()
         v = ref.values_of(inp[2]).abs().amax() * 1.75
         assert (out.double().abs().cpu() <= v * 1.01).all()
+
+
+# ---------------------------------------------------------------- long segments
+def test_units_that_a_cta_works_on_for_long(csa2):
+    """Five row tiles and more per CTA against 4 million keys each, some 50 ms: whoever works a segment ahead waits for that
+    long.  All keys are alike and all values 1 (one block, over and over): out = 1, lse = log of the keys seen."""
+    S, D, kv, T = 128, 64, 1 << 22, 200000
+    kc, vc = torch.zeros(1, 1, S, D, dtype=torch.uint8, device=DEV), torch.full((1, 1, S, D), 0x38, dtype=torch.uint8, device=DEV)
+    one, table = torch.ones(1, 1, device=DEV), torch.zeros(1, kv // S, dtype=I32, device=DEV)
+    q = torch.randn(T, 1, D, generator=torch.Generator(DEV).manual_seed(1), device=DEV).to(torch.bfloat16)
+    out, lse, err = torch.zeros_like(q), torch.zeros(T, 1, device=DEV), torch.zeros(1, dtype=I32, device=DEV)
+    csa2.csa2_paged_attn_fp8(q, kc, vc, one, one, table, torch.tensor([kv], dtype=I32, device=DEV),
+                             torch.tensor([0, T], dtype=I32, device=DEV), out, 0.1, T, lse=lse, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    assert (out == 1).all()
+    want = torch.log((kv - T + 1 + torch.arange(T, device=DEV)).double())
+    assert ((lse[:, 0].double() - want).abs() <= 4 * 2.0 ** -24 * want).all()
