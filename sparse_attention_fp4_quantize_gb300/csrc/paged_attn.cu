@@ -26,9 +26,10 @@
 // The split kernel, 64 requests of up to 16k tokens, 64 heads of 128 over 8 (1212 MB):
 // 184 us with the join, 6.6 TB/s, a copy's rate 6.8.  3 of up to 131k (257 MB): 52 us,
 // of which 10 are the launch, the first loads and the join.  48 with 5 new tokens in
-// a window of 4096, 15 heads of 64 over 5 (108 MB): 35 us, of which 8 go by before the
-// first tile (lengths, table, codes, each after the other), then the instructions: a key
-// costs as many as with 128 channels but brings half the bytes.  One request of 1000 tokens: 8 us and 4.6 for the join.
+// a window of 4096, 15 heads of 64 over 5 (108 MB): 36.5 us, of which 8 go by before the
+// first tile (lengths, table, codes, each after the other), then latency: 1.8 warps per
+// scheduler issue 0.35 instructions a cycle, and a key takes as many as with 128 channels
+// but brings half the bytes.  One request of 1000 tokens: 8 us and 4.6 for the join.
 #include "paged_attn.cuh"
 
 namespace csa2 {
@@ -633,7 +634,7 @@ cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cud
     cudaError_t e = cudaSuccess;
     // Neither kernel uses the other's results, but each waits for the one before it: what
     // was written before both is visible to a grid only once it has waited itself.  The
-    // split kernel first: a mixed batch of 17 takes 217 us, 221 the other way round.
+    // split kernel first: a mixed batch of 17 took 217 us, 221 the other way round.
     if (split_ctas) {
         e = ensure_smem_limit((const void *)paged_attn_split_kernel<D, NT, HALF>, smem, done);
         if (e != cudaSuccess) return e;

@@ -227,8 +227,8 @@ struct SplitWork {
 
 // The tile kernel's work: units of 256 rows, key tiles of 128, for each row tile
 // those that its first to last row see.
-// kTcCost: 3 prompts of up to 4096 tokens on up to 8192 (32 heads of 128) 794 us, 801 with
-// 3, 796 with 7; before, 905 with 0, 854 with 4 and with 6, 872 with 10.
+// kTcCost, when it was chosen: 3 prompts of up to 4096 tokens on up to 8192 (32 heads of
+// 128) 794 us, 801 with 3, 796 with 7; before, 905 with 0, 854 with 4 and with 6, 872 with 10.
 constexpr int kTcRows = 256, kTcKeys = 128, kTcCost = 5;
 struct TcWork {
     // A walk over the row tiles of a request, without a division per step.

@@ -27,9 +27,10 @@
 // 2660 (measured without the softmax), all together about 3300: a sub-tile's softmax
 // (1000 cycles for 128 exponentials and what goes with them) and its products are one
 // chain, and the other sub-tile's products do not fill all of it.  3 prompts of up to
-// 4096 tokens on up to 8192, 32 heads of 128 over 8: 786 us, 986 TFLOP/s of the
-// visible pairs (cuBLAS bf16 1916).  Without the conversions' stores it would take
-// about 740.  Tried and slower there: P handed over in two
+// 4096 tokens on up to 8192, 32 heads of 128 over 8: 851 us in the mean of ten inputs
+// (678 to 1028: wide scores move the references more often), 993 TFLOP/s of the
+// visible pairs (cuBLAS bf16 1916).  Tried and slower there, as first built (the
+// figures are of then): P handed over in two
 // halves of 64 keys (1035 against 923 us: the MMA threads' waits and locks cost more
 // than the overlap gives), codes kept in registers instead of staged (934 against
 // 906), whole warps in place of one thread to issue (979 against 905), the lock given
