@@ -28,8 +28,8 @@
 // (1000 cycles for 128 exponentials and what goes with them) and its products are one
 // chain, and the other sub-tile's products do not fill all of it.  3 prompts of up to
 // 4096 tokens on up to 8192, 32 heads of 128 over 8: 851 us in the mean of ten inputs
-// (678 to 1028: wide scores move the references more often), 993 TFLOP/s of the
-// visible pairs (cuBLAS bf16 1916).  Tried and slower there, as first built (the
+// (678 to 1028: wide scores move the references more often), 0.99 to 1.13 PFLOP/s of the
+// visible pairs (cuBLAS bf16 1.92).  Tried and slower there, as first built (the
 // figures are of then): P handed over in two
 // halves of 64 keys (1035 against 923 us: the MMA threads' waits and locks cost more
 // than the overlap gives), codes kept in registers instead of staged (934 against
