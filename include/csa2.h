@@ -60,6 +60,9 @@ typedef enum {
 
 typedef enum { CSA2_BF16 = 0, CSA2_FP8_E4M3 = 1, CSA2_FP32 = 2, CSA2_FP16 = 3 } csa2_dtype;
 
+/* Which channels of a head rotary positions turn together: 2i and 2i + 1, or i and i + rope_dim/2. */
+typedef enum { CSA2_ROPE_INTERLEAVED = 0, CSA2_ROPE_HALF = 1 } csa2_rope_layout;
+
 /* Bits OR-ed into *err_flag by the kernels. */
 #define CSA2_FLAG_BAD_INDEX 0x1u  /* attention idx outside [-1, kv_len)              */
 #define CSA2_FLAG_BAD_POOL 0x2u   /* pool block id outside [-1, ceil(N/8))           */
@@ -500,6 +503,124 @@ csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, int D, csa2_d
                                 const int32_t *cu_len, int max_new, int window, float sm_scale, void *out, float *lse,
                                 uint32_t *err_flag, void *workspace, size_t ws_bytes, csa2_stream_t stream);
 size_t csa2_paged_attn_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new);
+
+/*
+ * Rotary positions of query and key rows.  The pages name a fused RoPE kernel but
+ * fix neither layout nor table; these rules are this library's own.
+ *
+ * csa2_rope_table -- the table of cosines and sines that csa2_rope,
+ * csa2_quantize_kv_fp4_paged and csa2_rope_quantize_kv_fp4 read:
+ *     cos_sin[n][i] = amplitude * (cos, sin)((start + n) * inv_freq[i])
+ * in fp32, the angle kept modulo one turn in 64-bit fixed point, so that a far
+ * position is as exact as a near one.  Frequencies stretched for long contexts
+ * (and the amplitude that goes with them) come from the caller.
+ *
+ * inv_freq  double [half], radians per position, 8-byte aligned; one that is not
+ *           finite or beyond 2^20 gives NaN.  1 <= half <= 512.
+ * start, n_pos  0..2^31.  cos_sin float [n_pos, half, 2], 8-byte aligned.
+ */
+csa2_status csa2_rope_table(const double *inv_freq, int half, int64_t start, int64_t n_pos, float amplitude,
+                            float *cos_sin, csa2_stream_t stream);
+
+/*
+ * csa2_rope -- rotate rope_dim channels of every head of q and k, from channel
+ * `first` on; the channels beside them are copied.  With (c, s) =
+ * cos_sin[pos[t]][i], pair i of a row becomes
+ *     a' = (a*c) - (b*s),  b' = (a*s) + (b*c)
+ * in fp32, every product and sum rounded (no fused multiply-add), then rounded
+ * to the rows' type (nearest even): the steps of csa2_rope_quantize_kv_fp4.
+ *
+ * q, q_out  bf16 or fp16 [T, Hq, D]; k, k_out [T, Hk, D]; Hq or Hk may be 0 (and
+ *           its pointers NULL).  Token and head strides in elements (multiples of
+ *           8, below 2^32), channels contiguous, 16-byte aligned.  An output is its
+ *           own input (pointer and strides) or shares no element with either input
+ *           or the other output; slices of one projection's output fit.
+ * D         multiple of 8, 16..1024; rope_dim multiple of 16, 16..D; first multiple
+ *           of 8, 0..D - rope_dim.
+ * pos       int32 [T], -1: a row without a token, whose output is left as it was;
+ *           so is that of a position outside [0, n_pos) (CSA2_FLAG_BAD_INDEX).
+ * cos_sin   float [n_pos, rope_dim/2, 2], 16-byte aligned.
+ */
+csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_token_stride, int64_t q_head_stride,
+                      int64_t qo_token_stride, int64_t qo_head_stride, const void *k, void *k_out, int Hk,
+                      int64_t k_token_stride, int64_t k_head_stride, int64_t ko_token_stride, int64_t ko_head_stride,
+                      csa2_dtype dt, int64_t T, int D, const int32_t *pos, const float *cos_sin, int64_t n_pos,
+                      int rope_dim, int first, csa2_rope_layout layout, uint32_t *err_flag, csa2_stream_t stream);
+
+/*
+ * The paged 4-bit cache: the paged cache above in the FP4 format of the main
+ * cache, E2M1 codes with one E4M3 scale per 16 channels of a row and no other
+ * scale.
+ *
+ *   k_codes, v_codes    uint8 [n_blocks, Hkv, S, D/2], channel 2i in the low nibble of byte i
+ *   k_scales, v_scales  uint8 [n_blocks, Hkv, S, D/16], E4M3; a value is code * scale
+ * all 16-byte aligned; S in {16, 32, 64, 128}, D in {64, 128}.  Block tables, slots
+ * and lengths are those of csa2_build_slots.  A row needs 9/16 of the 8-bit cache's bytes
+ * and is stored for good: later rows do not move its scales.
+ */
+
+/*
+ * csa2_quantize_kv_fp4_paged -- store new key and value rows.  Row t goes to
+ * slots[t] by the rule of csa2_quantize_kv_fp4 (scale = E4M3(amax/6), codes to
+ * nearest, ties to the even one).  With cos_sin the keys are rotated first, to the bits that
+ * csa2_rope writes.
+ *
+ * k, v    bf16 or fp16 [T, Hkv, D], 16-byte aligned, D contiguous; token and head
+ *         strides in elements, multiples of 8 below 2^32.  T <= 2^30, Hkv <= 32767.
+ * slots   int64 [T]; -1 skips a row, as does a slot outside [-1, n_blocks * S)
+ *         (CSA2_FLAG_BAD_SLOT).  A slot given twice is a data race: its row is a mixture.
+ * pos, cos_sin, n_pos, rope_dim, first, layout  as csa2_rope; both pointers NULL: no
+ *         rotation.  A token to be stored whose position is outside [0, n_pos) is not,
+ *         neither key nor value (CSA2_FLAG_BAD_INDEX).
+ * k_values, v_values  NULL, or [T, Hkv, D] of the rows' type, dense, 16-byte aligned: what the
+ *         codes stand for (exact), so that a prompt may attend to the values that later
+ *         steps will see.  Rows that are not stored are left as they were.
+ * Infinities are stored as +-6 scale and NaN as 0, neither counts toward amax
+ * (CSA2_FLAG_NONFINITE).
+ */
+csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, csa2_dtype dt, int64_t T, int Hkv, int D,
+                                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                       int64_t v_head_stride, const int64_t *slots, int64_t n_blocks, int S,
+                                       uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_scales, uint8_t *v_scales,
+                                       const int32_t *pos, const float *cos_sin, int64_t n_pos, int rope_dim, int first,
+                                       csa2_rope_layout layout, void *k_values, void *v_values, uint32_t *err_flag,
+                                       csa2_stream_t stream);
+
+/*
+ * csa2_dequantize_kv_fp4_paged -- read rows back: k[t], v[t] = the values at
+ * slots[t], exact in bf16 and fp16.  A slot may be given any number of times; -1 leaves its
+ * row as it was, as does a slot outside [-1, n_blocks * S) (CSA2_FLAG_BAD_SLOT).
+ * k, v bf16 or fp16 [T, Hkv, D], 16-byte aligned, D contiguous, token and head
+ * strides in elements (multiples of 8 below 2^32); no two rows share elements.
+ */
+csa2_status csa2_dequantize_kv_fp4_paged(const int64_t *slots, int64_t T, int64_t n_blocks, int Hkv, int S, int D,
+                                         const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_scales,
+                                         const uint8_t *v_scales, csa2_dtype dt, void *k, void *v, int64_t k_token_stride,
+                                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                                         uint32_t *err_flag, csa2_stream_t stream);
+
+/*
+ * csa2_paged_attn_fp4 -- causal attention of a ragged batch over the paged 4-bit
+ * cache: csa2_paged_attn_fp8's rows, masks, errors and limits, with
+ *   z_j = sm_scale * q . k_j,  out = sum_j softmax(z)_j v_j,  lse = log sum_j exp(z_j).
+ * Keys and values enter the tensor cores as exact f16, q as f16 scaled per row by a
+ * power of two (bf16 values within 2^-31 of the row's largest are exact); sums and
+ * softmax statistics are fp32, the weights P_j are rounded to f16's 11 bits, those
+ * below 2^-22 of the row's largest to a step of 2^-32 of it.
+ * Stored scales must be no NaN (csa2_quantize_kv_fp4_paged writes none); rows at or
+ * beyond kv_len may hold anything.
+ * workspace csa2_paged_attn_fp4_workspace_bytes() bytes, 16-byte aligned (at most 64 MiB).
+ *         Calls that may overlap need one each.
+ * err_flag  CSA2_FLAG_BAD_INDEX; CSA2_FLAG_TIMEOUT if a bounded on-chip wait gave up.
+ */
+csa2_status csa2_paged_attn_fp4(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, const void *q,
+                                int64_t q_token_stride, int64_t q_head_stride, const uint8_t *k_codes,
+                                const uint8_t *v_codes, const uint8_t *k_scales, const uint8_t *v_scales,
+                                int64_t n_blocks, int S, const int32_t *block_table, int M, int64_t table_stride,
+                                const int32_t *kv_len, const int32_t *cu_len, int max_new, int window, float sm_scale,
+                                void *out, float *lse, uint32_t *err_flag, void *workspace, size_t ws_bytes,
+                                csa2_stream_t stream);
+size_t csa2_paged_attn_fp4_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new);
 
 /*
  * csa2_selftest_bounded_wait -- exercises the library's bounded wait on an

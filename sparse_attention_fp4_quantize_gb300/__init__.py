@@ -17,7 +17,10 @@ Names follow the C ABI: ``csa2_quantize_kv_fp4``, ``csa2_rope_quantize_kv_fp4``
 ``csa2_swa_attn_fp8`` (sliding-window branch and merge), the paged 8-bit
 cache's ``csa2_build_slots`` (block tables and slot maps),
 ``csa2_quantize_kv_fp8_paged`` (append) and ``csa2_paged_attn_fp8`` (attention;
-``paged.PagedCache`` keeps the buffers and calls the three in order),
+``paged.PagedCache`` keeps the buffers and calls the three in order), the
+same cache in 4 bits (``csa2_quantize_kv_fp4_paged``,
+``csa2_dequantize_kv_fp4_paged``, ``csa2_paged_attn_fp4``), rotary positions
+(``csa2_rope_table``, ``csa2_rope``; ``rope.Rope`` makes the frequencies),
 ``csa2_selftest_bounded_wait`` and the ``*_workspace_bytes`` helpers.
 """
 from __future__ import annotations
@@ -32,6 +35,7 @@ LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
 BF16, FP8_E4M3, FP32, FP16 = 0, 1, 2, 3
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 FLAG_BAD_INDEX, FLAG_BAD_POOL, FLAG_BAD_SLOT, FLAG_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 FLAG_NO_BLOCKS, FLAG_NONFINITE = 0x10, 0x20
 INDEX_HEADS, INDEX_DIM, POOL_BLOCK, MAX_POOL, MAX_K = 4, 64, 8, 2048, 2048
@@ -78,6 +82,16 @@ def _load() -> ctypes.CDLL:
         "csa2_paged_attn_fp8": ([i32, i64, i32, i32, i32, i32, P, i64, i64, P, P, P, P, i64, i32, P, i32, i64, P, P,
                                  i32, i32, f32, P, P, P, P, u64, P], i32),
         "csa2_paged_attn_workspace_bytes": ([i32, i64, i32, i32, i32, i32], u64),
+        "csa2_rope_table": ([P, i32, i64, i64, f32, P, P], i32),
+        "csa2_rope": ([P, P, i32, i64, i64, i64, i64, P, P, i32, i64, i64, i64, i64, i32, i64, i32, P, P, i64, i32, i32,
+                       i32, P, P], i32),
+        "csa2_quantize_kv_fp4_paged": ([P, P, i32, i64, i32, i32, i64, i64, i64, i64, P, i64, i32, P, P, P, P, P, P, i64,
+                                        i32, i32, i32, P, P, P, P], i32),
+        "csa2_dequantize_kv_fp4_paged": ([P, i64, i64, i32, i32, i32, P, P, P, P, i32, P, P, i64, i64, i64, i64, P, P],
+                                         i32),
+        "csa2_paged_attn_fp4": ([i32, i64, i32, i32, i32, i32, P, i64, i64, P, P, P, P, i64, i32, P, i32, i64, P, P,
+                                 i32, i32, f32, P, P, P, P, u64, P], i32),
+        "csa2_paged_attn_fp4_workspace_bytes": ([i32, i64, i32, i32, i32, i32], u64),
         "csa2_selftest_bounded_wait": ([ctypes.c_uint32, P, P], i32),
         "csa2_status_string": ([i32], ctypes.c_char_p),
         "csa2_last_error": ([], ctypes.c_char_p),
@@ -100,7 +114,8 @@ def exported_symbols():
             "csa2_sparse_attn_fp4_prefetch", "csa2_swa_attn_fp8",
             "csa2_sparse_attn_fp4_noalloc", "csa2_sparse_attn_noalloc_max_scratch_bytes",
             "csa2_build_slots", "csa2_quantize_kv_fp8_paged", "csa2_paged_attn_fp8",
-            "csa2_paged_attn_workspace_bytes",
+            "csa2_paged_attn_workspace_bytes", "csa2_rope_table", "csa2_rope", "csa2_quantize_kv_fp4_paged",
+            "csa2_dequantize_kv_fp4_paged", "csa2_paged_attn_fp4", "csa2_paged_attn_fp4_workspace_bytes",
             "csa2_selftest_bounded_wait", "csa2_status_string", "csa2_last_error", "csa2_version"]
 
 
@@ -611,6 +626,151 @@ def csa2_paged_attn_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, kv_l
             workspace = workspace_for_paged_attn(B, T, Hq, H, D, max_new, device=q.device)
     ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch(_lib.csa2_paged_attn_fp8, dev, stream, B, T, Hq, H, D, dt, qp, qt, qh, kc, vc, ks, vs, n, S, table, M,
+            stride, _arg(kv_len, "kv_len", _I32, (B,), dev), _arg(cu_len, "cu_len", _I32, (B + 1,), dev), max_new,
+            window, sm_scale, _arg(out, "out", q.dtype, shape, dev), _opt(lse, "lse", _F32, (T, Hq), dev),
+            _flag_arg(err_flag, dev),
+            None if workspace is None else _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev), ws)
+
+
+# ------------------------------------------------------------------ rotary positions
+def csa2_rope_table(inv_freq, cos_sin, start=0, amplitude=1.0, stream=None):
+    """inv_freq float64 [half], radians per position -> cos_sin fp32 [n_pos,
+    half, 2]: amplitude * (cos, sin) of positions start, start + 1, ..."""
+    dev = _device_of(cos_sin)
+    half = inv_freq.numel()
+    if cos_sin.dim() != 3:
+        raise ValueError("cos_sin must be [n_pos, half, 2], got %s" % (tuple(cos_sin.shape),))
+    _launch(_lib.csa2_rope_table, dev, stream, _arg(inv_freq, "inv_freq", torch.float64, (half,), dev), half, start,
+            cos_sin.shape[0], amplitude, _arg(cos_sin, "cos_sin", _F32, (cos_sin.shape[0], half, 2), dev))
+
+
+def _table_of(cos_sin, dev):
+    """(pointer, positions, rope_dim) of a table of cosines and sines."""
+    if cos_sin.dim() != 3 or cos_sin.shape[2] != 2:
+        raise ValueError("cos_sin must be [n_pos, rope_dim/2, 2], got %s" % (tuple(cos_sin.shape),))
+    return _arg(cos_sin, "cos_sin", _F32, cos_sin.shape, dev), cos_sin.shape[0], 2 * cos_sin.shape[1]
+
+
+def csa2_rope(q, pos, cos_sin, k=None, q_out=None, k_out=None, first=0, layout=ROPE_HALF, err_flag=None, stream=None):
+    """Rotate q [T, Hq, D] and k [T, Hk, D] (or None), bf16 (or int16 bits) or
+    fp16 with any token and head strides that are multiples of 8, by
+    cos_sin fp32 [n_pos, rope_dim/2, 2] at pos int32 [T] (-1: the row is left
+    out): the rope_dim channels from `first` on, in pairs of `layout`.  Into q_out
+    and k_out, or in place where they are None."""
+    dev = _device_of(q)
+    T, Hq, D = q.shape
+    dt = _ROWS.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be bf16 (or int16 bits) or fp16, got %s" % q.dtype)
+    qp, qt, qh = _rows_arg(q, "q", q.dtype, (T, Hq, D), dev)
+    op, ot, oh = (qp, qt, qh) if q_out is None else _rows_arg(q_out, "q_out", q.dtype, (T, Hq, D), dev)
+    kp, kt, kh, pp, pt, ph, Hk = None, 0, 0, None, 0, 0, 0
+    if k is not None:
+        Hk = k.shape[1]
+        kp, kt, kh = _rows_arg(k, "k", q.dtype, (T, Hk, D), dev)
+        pp, pt, ph = (kp, kt, kh) if k_out is None else _rows_arg(k_out, "k_out", q.dtype, (T, Hk, D), dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    table, n_pos, rope_dim = _table_of(cos_sin, dev)
+    _launch(_lib.csa2_rope, dev, stream, qp, op, Hq, qt, qh, ot, oh, kp, pp, Hk, kt, kh, pt, ph, dt, T, D,
+            _arg(pos, "pos", _I32, (T,), dev), table, n_pos, rope_dim, first, layout, _flag_arg(err_flag, dev))
+
+
+# ------------------------------------------------------------------ paged 4-bit cache
+_U8 = torch.uint8
+
+
+def _planes4_args(k_codes, v_codes, k_scales, v_scales, dev):
+    """(pointers..., n_blocks, Hkv, S, D) of the planes of a 4-bit cache."""
+    shape = k_codes.shape
+    if len(shape) != 4:
+        raise ValueError("k_codes must be [n_blocks, Hkv, S, D/2], got %s" % (tuple(shape),))
+    n, H, S, half = shape
+    at, sd = (n, H, S, half // 8), k_scales.dtype
+    if not (sd is _U8 or sd is torch.float8_e4m3fn) or v_scales.dtype is not sd:
+        raise TypeError("k_scales and v_scales must be E4M3 (both uint8 or both float8_e4m3fn), got %s and %s" % (sd, v_scales.dtype))
+    return (_arg(k_codes, "k_codes", _U8, shape, dev), _arg(v_codes, "v_codes", _U8, shape, dev),
+            _arg(k_scales, "k_scales", sd, at, dev), _arg(v_scales, "v_scales", sd, at, dev), n, H, S, 2 * half)
+
+
+def csa2_quantize_kv_fp4_paged(k, v, slots, k_codes, v_codes, k_scales, v_scales, pos=None, cos_sin=None, first=0,
+                               layout=ROPE_HALF, k_values=None, v_values=None, err_flag=None, stream=None):
+    """k, v bf16 (or int16 bits) or fp16 [T, Hkv, D] (any token and head
+    strides that are multiples of 8), slots int64 [T] -> k_codes, v_codes
+    uint8 [n_blocks, Hkv, S, D/2], k_scales, v_scales uint8 or float8_e4m3fn
+    [n_blocks, Hkv, S, D/16], updated in place; with pos and cos_sin the keys
+    are rotated first, as csa2_rope does.  k_values, v_values [T, Hkv, D] of
+    k's type, or None: what the codes stand for."""
+    dev = _device_of(k)
+    kc, vc, ks, vs, n, H, S, D = _planes4_args(k_codes, v_codes, k_scales, v_scales, dev)
+    (T,) = slots.shape
+    dt = _ROWS.get(k.dtype)
+    if dt is None:
+        raise TypeError("k and v must be bf16 (or int16 bits) or fp16, got %s" % k.dtype)
+    shape = (T, H, D)
+    kp, kt, kh = _rows_arg(k, "k", k.dtype, shape, dev)
+    vp, vt, vh = _rows_arg(v, "v", k.dtype, shape, dev)
+    if (pos is None) != (cos_sin is None):
+        raise ValueError("pos and cos_sin go together")
+    table, n_pos, rope_dim = (None, 0, 0) if cos_sin is None else _table_of(cos_sin, dev)
+    _launch(_lib.csa2_quantize_kv_fp4_paged, dev, stream, kp, vp, dt, T, H, D, kt, kh, vt, vh,
+            _arg(slots, "slots", _I64, (T,), dev), n, S, kc, vc, ks, vs, _opt(pos, "pos", _I32, (T,), dev), table, n_pos,
+            rope_dim, first, layout, _opt(k_values, "k_values", k.dtype, shape, dev),
+            _opt(v_values, "v_values", k.dtype, shape, dev), _flag_arg(err_flag, dev))
+
+
+def csa2_dequantize_kv_fp4_paged(slots, k_codes, v_codes, k_scales, v_scales, k, v, err_flag=None, stream=None):
+    """Read rows back: the values at slots int64 [T] (-1: the row is left as
+    it was) of planes as csa2_quantize_kv_fp4_paged writes them -> k, v bf16
+    (or int16 bits) or fp16 [T, Hkv, D] (any token and head strides that are
+    multiples of 8)."""
+    dev = _device_of(k)
+    kc, vc, ks, vs, n, H, S, D = _planes4_args(k_codes, v_codes, k_scales, v_scales, dev)
+    (T,) = slots.shape
+    dt = _ROWS.get(k.dtype)
+    if dt is None:
+        raise TypeError("k and v must be bf16 (or int16 bits) or fp16, got %s" % k.dtype)
+    kp, kt, kh = _rows_arg(k, "k", k.dtype, (T, H, D), dev)
+    vp, vt, vh = _rows_arg(v, "v", k.dtype, (T, H, D), dev)
+    _launch(_lib.csa2_dequantize_kv_fp4_paged, dev, stream, _arg(slots, "slots", _I64, (T,), dev), T, n, H, S, D, kc, vc,
+            ks, vs, dt, kp, vp, kt, kh, vt, vh, _flag_arg(err_flag, dev))
+
+
+def csa2_paged_attn_fp4_workspace_bytes(B, T, Hq, Hkv, D, max_new) -> int:
+    return int(_lib.csa2_paged_attn_fp4_workspace_bytes(B, T, Hq, Hkv, D, max_new))
+
+
+def workspace_for_paged_attn_fp4(B, T, Hq, Hkv, D, max_new, device="cuda"):
+    """Allocate (through torch) the scratch csa2_paged_attn_fp4 needs, or None."""
+    n = csa2_paged_attn_fp4_workspace_bytes(B, T, Hq, Hkv, D, max_new)
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def csa2_paged_attn_fp4(q, k_codes, v_codes, k_scales, v_scales, block_table, kv_len, cu_len, out, sm_scale, max_new,
+                        window=0, lse=None, err_flag=None, workspace=None, stream=None):
+    """Causal attention of a ragged batch over the paged 4-bit cache: the
+    arguments of csa2_paged_attn_fp8, with planes as
+    csa2_quantize_kv_fp4_paged writes them.  workspace: a CUDA byte tensor of at
+    least csa2_paged_attn_fp4_workspace_bytes bytes (allocated here when None)."""
+    dev = _device_of(q)
+    kc, vc, ks, vs, n, H, S, D = _planes4_args(k_codes, v_codes, k_scales, v_scales, dev)
+    T, Hq = q.shape[:2]
+    B, M = block_table.shape
+    dt = _ROWS.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be bf16 (or int16 bits) or fp16, got %s" % q.dtype)
+    if H < 1 or Hq % H:
+        raise ValueError("%d query heads do not divide over %d KV heads" % (Hq, H))
+    shape = (T, Hq, D)
+    qp, qt, qh = _rows_arg(q, "q", q.dtype, shape, dev)
+    table, stride = _table_arg(block_table, (B, M), dev)
+    if workspace is None:                         # of the stream that uses it, which may not be the current one
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+        with torch.cuda.stream(stream):
+            workspace = workspace_for_paged_attn_fp4(B, T, Hq, H, D, max_new, device=q.device)
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch(_lib.csa2_paged_attn_fp4, dev, stream, B, T, Hq, H, D, dt, qp, qt, qh, kc, vc, ks, vs, n, S, table, M,
             stride, _arg(kv_len, "kv_len", _I32, (B,), dev), _arg(cu_len, "cu_len", _I32, (B + 1,), dev), max_new,
             window, sm_scale, _arg(out, "out", q.dtype, shape, dev), _opt(lse, "lse", _F32, (T, Hq), dev),
             _flag_arg(err_flag, dev),

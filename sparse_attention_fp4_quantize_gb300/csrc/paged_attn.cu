@@ -628,6 +628,13 @@ __global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a, i
 }
 
 template <int D, int NT, bool HALF>
+cudaError_t launch_join(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cudaStream_t stream) {
+    constexpr int JB = 2 * NT;
+    return launch_pdl(paged_attn_join_kernel<D, NT, HALF>, dim3(JB * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
+                      split_ctas, tc_ctas);
+}
+
+template <int D, int NT, bool HALF>
 cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cudaStream_t stream) {
     static bool done[64];
     constexpr int smem = attn_smem<D, NT>();
@@ -645,9 +652,7 @@ cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cud
         e = launch_paged_attn_tc(a, D, HALF, stream);
         if (e != cudaSuccess) return e;
     }
-    constexpr int JB = 2 * NT;
-    return launch_pdl(paged_attn_join_kernel<D, NT, HALF>, dim3(JB * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
-                      split_ctas, tc_ctas);
+    return launch_join<D, NT, HALF>(a, split_ctas, tc_ctas, stream);
 }
 
 template <int D, bool HALF>
@@ -681,6 +686,37 @@ inline Choice choose(int B, int G, int max_new) {
 inline size_t split_partial_floats(const Choice &c, int D) { return (size_t)2 * c.split_ctas * 8 * c.NT * (D + 4); }
 
 }  // namespace
+
+cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, int D, int NT, bool half, int split_ctas, int tc_ctas, cudaStream_t stream) {
+    auto go = D == 64 ? (NT == 1 ? (half ? launch_join<64, 1, true> : launch_join<64, 1, false>)
+                                 : (half ? launch_join<64, 2, true> : launch_join<64, 2, false>))
+                      : (NT == 1 ? (half ? launch_join<128, 1, true> : launch_join<128, 1, false>)
+                                 : (half ? launch_join<128, 2, true> : launch_join<128, 2, false>));
+    return go(a, split_ctas, tc_ctas, stream);
+}
+
+csa2_status check_paged_attn(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, int64_t q_token_stride,
+                             int64_t q_head_stride, int64_t n_blocks, int S, int M, int64_t table_stride, int max_new, int window) {
+    CSA2_REQUIRE(dt == CSA2_BF16 || dt == CSA2_FP16, "paged_attn: q must be bf16 or fp16");
+    CSA2_REQUIRE(B >= 0 && B <= 65536, "paged_attn: B=%d not in [0, 65536]", B);
+    CSA2_REQUIRE(T >= 0 && T <= (1ll << 30), "paged_attn: T=%lld not in [0, 2^30]", (long long)T);
+    CSA2_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536, "paged_attn: Hq=%d, Hkv=%d", Hq, Hkv);
+    CSA2_REQUIRE(T * (Hq / Hkv) <= (1ll << 30), "paged_attn: T * Hq / Hkv = %lld rows", (long long)(T * (Hq / Hkv)));
+    CSA2_REQUIRE(S == 16 || S == 32 || S == 64 || S == 128, "paged_attn: S=%d not in {16, 32, 64, 128}", S);
+    CSA2_REQUIRE(M >= 1 && (int64_t)M * S <= (1ll << 30), "paged_attn: M=%d: need 1 <= M, M * S <= 2^30", M);
+    CSA2_REQUIRE(table_stride >= M, "paged_attn: table_stride=%lld < M=%d", (long long)table_stride, M);
+    CSA2_REQUIRE(n_blocks >= 0 && n_blocks < (1ll << 31), "paged_attn: n_blocks=%lld", (long long)n_blocks);
+    CSA2_REQUIRE(max_new >= 1, "paged_attn: max_new=%d < 1", max_new);
+    CSA2_REQUIRE(window >= 0, "paged_attn: window=%d < 0", window);
+    CSA2_REQUIRE(q_token_stride >= 0 && q_head_stride >= 0 && q_token_stride % 8 == 0 && q_head_stride % 8 == 0,
+                 "paged_attn: q strides must be multiples of 8, not negative");
+    if (D != 64 && D != 128) {
+        set_error("paged_attn: D=%d not in {64, 128}", D);
+        return CSA2_ERR_UNSUPPORTED;
+    }
+    return CSA2_OK;
+}
+
 }  // namespace csa2
 
 using namespace csa2;
@@ -701,23 +737,9 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
                                            uint32_t *err_flag, void *workspace, size_t ws_bytes,
                                            csa2_stream_t stream) {
     clear_error();
-    CSA2_REQUIRE(dt == CSA2_BF16 || dt == CSA2_FP16, "paged_attn: q must be bf16 or fp16");
-    CSA2_REQUIRE(B >= 0 && B <= 65536, "paged_attn: B=%d not in [0, 65536]", B);
-    CSA2_REQUIRE(T >= 0 && T <= (1ll << 30), "paged_attn: T=%lld not in [0, 2^30]", (long long)T);
-    CSA2_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 65536, "paged_attn: Hq=%d, Hkv=%d", Hq, Hkv);
-    CSA2_REQUIRE(T * (Hq / Hkv) <= (1ll << 30), "paged_attn: T * Hq / Hkv = %lld rows", (long long)(T * (Hq / Hkv)));
-    CSA2_REQUIRE(S == 16 || S == 32 || S == 64 || S == 128, "paged_attn: S=%d not in {16, 32, 64, 128}", S);
-    CSA2_REQUIRE(M >= 1 && (int64_t)M * S <= (1ll << 30), "paged_attn: M=%d: need 1 <= M, M * S <= 2^30", M);
-    CSA2_REQUIRE(table_stride >= M, "paged_attn: table_stride=%lld < M=%d", (long long)table_stride, M);
-    CSA2_REQUIRE(n_blocks >= 0 && n_blocks < (1ll << 31), "paged_attn: n_blocks=%lld", (long long)n_blocks);
-    CSA2_REQUIRE(max_new >= 1, "paged_attn: max_new=%d < 1", max_new);
-    CSA2_REQUIRE(window >= 0, "paged_attn: window=%d < 0", window);
-    CSA2_REQUIRE(q_token_stride >= 0 && q_head_stride >= 0 && q_token_stride % 8 == 0 && q_head_stride % 8 == 0,
-                 "paged_attn: q strides must be multiples of 8, not negative");
-    if (D != 64 && D != 128) {
-        set_error("paged_attn: D=%d not in {64, 128}", D);
-        return CSA2_ERR_UNSUPPORTED;
-    }
+    const csa2_status st = check_paged_attn(B, T, Hq, Hkv, D, dt, q_token_stride, q_head_stride, n_blocks, S, M, table_stride,
+                                            max_new, window);
+    if (st != CSA2_OK) return st;
     if (B == 0 || T == 0) return CSA2_OK;
     CSA2_REQUIRE(q && out && block_table && kv_len && cu_len, "paged_attn: null pointer");
     CSA2_REQUIRE((k_codes && v_codes && k_scale && v_scale) || n_blocks == 0, "paged_attn: null pointer");
@@ -736,7 +758,7 @@ extern "C" csa2_status csa2_paged_attn_fp8(int B, int64_t T, int Hq, int Hkv, in
     float *partial = (float *)(join + c.split_ctas + c.tc_ctas);
     const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride,
                              q_token_stride, q_head_stride, (const uint16_t *)q, k_codes, v_codes, k_scale, v_scale,
-                             block_table, kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag,
+                             nullptr, nullptr, block_table, kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse, err_flag,
                              c.split_rows, join, join + c.split_ctas, partial, partial + split_partial_floats(c, D)};
     auto go = dt == CSA2_FP16 ? (D == 64 ? launch_attn_nt<64, true> : launch_attn_nt<128, true>)
                               : (D == 64 ? launch_attn_nt<64, false> : launch_attn_nt<128, false>);

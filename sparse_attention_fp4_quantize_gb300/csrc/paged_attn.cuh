@@ -21,6 +21,7 @@ struct PagedAttnArgs {
     const uint16_t *q;
     const uint8_t *k_codes, *v_codes;
     const float *k_scale, *v_scale;
+    const uint8_t *k_scale4, *v_scale4;      // of the 4-bit cache: E4M3, 16 channels each
     const int32_t *table, *kv_len, *cu_len;
     float logit_scale;              // sm_scale * log2(e)
     uint16_t *out;
@@ -300,6 +301,14 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row,
     }
     if (a.lse && part == 0) a.lse[o_row] = l > 0.0f || l != l ? (M + log2f(l)) * 0.69314718055994531f : __int_as_float(0xff800000);
 }
+
+// What both calls refuse, whatever the cache holds.
+csa2_status check_paged_attn(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, int64_t q_token_stride,
+                             int64_t q_head_stride, int64_t n_blocks, int S, int M, int64_t table_stride, int max_new, int window);
+
+// The join kernel (paged_attn.cu): adds up the parts of the units that split_ctas CTAs of a
+// split kernel with row tiles of 8 NT and tc_ctas of the tile kernel shared.
+cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, int D, int NT, bool half, int split_ctas, int tc_ctas, cudaStream_t stream);
 
 // The tile kernel (paged_attn_tc.cu): one CTA per SM.
 int paged_attn_tc_ctas();

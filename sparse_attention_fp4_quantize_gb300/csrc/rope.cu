@@ -1,0 +1,224 @@
+// csa2_rope_table and csa2_rope: rotary positions, the table of cosines and sines
+// from (scaled) frequencies, and the rotation of query and key rows by it.
+#include "fp4.cuh"
+
+namespace csa2 {
+namespace {
+
+// ---- the table.  The angle of position p and pair i is p f_i radians.  At far
+// positions it is many turns, of which only the fraction counts: f_i becomes a
+// fraction of a turn in 64-bit fixed point once per thread, and its product with p
+// wraps at whole turns by itself, with an error below p 2^-65 turns.  What is left of
+// the nearest quarter turn goes to sinpi / cospi in fp32 with all its leading bits.
+constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;   // 1 / (2 pi) in two parts
+constexpr double kMostFreq = 1048576.0;      // radians per position
+
+struct TableArgs {
+    const double *freq;
+    float2 *table;
+    int64_t start, n_pos;
+    int half;
+    float amplitude;
+};
+
+__global__ void __launch_bounds__(1024) rope_table_kernel(TableArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int i = threadIdx.x;
+    const double f = a.freq[i];
+    const bool fine = fabs(f) <= kMostFreq;  // no NaN either
+    const double t = f * kTurn, low = fma(f, kTurn, -t) + f * kTurnLow, r = t - rint(t);
+    const double hi = rint(r * 0x1p32);
+    const uint64_t step = fine ? ((uint64_t)(int64_t)hi << 32) + (uint64_t)llrint((fma(hi, -0x1p-32, r) + low) * 0x1p64) : 0;
+    const bool slow = fabs(f) < 0x1p-30;     // fixed point would cost it leading bits; its angles fit fp64
+    const float amp = fine ? a.amplitude : __int_as_float(0x7FC00000);
+    for (int64_t n = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; n < a.n_pos; n += (int64_t)gridDim.x * blockDim.y) {
+        const int64_t p = a.start + n;
+        float s, c;
+        if (slow) {
+            const double x = 2.0 * (t * (double)p);
+            s = (float)sinpi(x), c = (float)cospi(x);
+        } else {
+            const uint64_t phase = step * (uint64_t)p, quarter = (phase + (1ull << 61)) >> 62;
+            const float x = (float)(int64_t)(phase - (quarter << 62)) * 0x1p-63f;
+            float s0, c0;
+            sincospif(x, &s0, &c0);
+            s = quarter & 1 ? c0 : s0, c = quarter & 1 ? s0 : c0;
+            if (quarter & 2) s = -s;
+            if ((quarter + 1) & 2) c = -c;
+        }
+        a.table[n * a.half + i] = make_float2(amp * c, amp * s);
+    }
+}
+
+// ---- the rotation.  A thread takes 8 channels of a head (with the 8 that are their
+// partners, in the layout of halves), holds their cosines and sines and walks over heads.
+struct RotateArgs {
+    const uint16_t *in[2];                   // q, k
+    uint16_t *out[2];
+    int64_t in_token[2], in_head[2], out_token[2], out_head[2];
+    int heads[2], per;                       // heads; heads per thread
+    int64_t T, n_pos;
+    const int32_t *pos;
+    const float *table;
+    int pairs, first, turned;                // rotated pairs and first rotated channel of a head; units that rotate
+    uint32_t *err_flag;
+};
+
+constexpr int kBatch = 4;                    // heads whose loads are in flight together
+
+template <bool HALF, bool SPLIT>
+__global__ void __launch_bounds__(256) rope_kernel(RotateArgs a) {
+    constexpr int P = SPLIT ? 8 : 4;         // pairs of a thread
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= a.T) return;
+    const int64_t p = a.pos[t];
+    if (p < 0 || p >= a.n_pos) {             // -1: a row without a token
+        if (p != -1 && threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+        return;
+    }
+    const int u = threadIdx.x, H = a.heads[0] + a.heads[1];
+    const bool turns = u < a.turned;
+    int c0 = a.first + 8 * u, c1 = c0 + a.pairs;
+    float2 cs[P];
+    if (turns) {
+        const float4 *row = reinterpret_cast<const float4 *>(a.table + 2 * (p * a.pairs + P * u));
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+            const float4 v = row[i];
+            cs[2 * i] = make_float2(v.x, v.y), cs[2 * i + 1] = make_float2(v.z, v.w);
+        }
+    } else {                                 // a piece that is copied as it is
+        c0 = 8 * (u - a.turned);
+        if (c0 >= a.first) c0 += 2 * a.pairs;
+        c1 = c0;
+    }
+    const int end = min(H, (int)(blockIdx.y + 1) * a.per);
+    for (int h0 = blockIdx.y * a.per; h0 < end; h0 += kBatch) {
+        uint4 x[kBatch], y[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int h = h0 + k, w = h >= a.heads[0];
+            if (h >= end) continue;
+            const uint16_t *src = (w ? a.in[1] : a.in[0]) + t * (w ? a.in_token[1] : a.in_token[0]) +
+                                  (w ? h - a.heads[0] : h) * (w ? a.in_head[1] : a.in_head[0]);
+            x[k] = *reinterpret_cast<const uint4 *>(src + c0);
+            if (SPLIT && turns) y[k] = *reinterpret_cast<const uint4 *>(src + c1);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int h = h0 + k, w = h >= a.heads[0];
+            if (h >= end) continue;
+            uint16_t *dst = (w ? a.out[1] : a.out[0]) + t * (w ? a.out_token[1] : a.out_token[0]) +
+                            (w ? h - a.heads[0] : h) * (w ? a.out_head[1] : a.out_head[0]);
+            if (turns) {
+                uint32_t *xw = reinterpret_cast<uint32_t *>(&x[k]), *yw = reinterpret_cast<uint32_t *>(&y[k]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = unpack16<HALF>(xw[i]);
+                    if (SPLIT) {
+                        const float2 z = unpack16<HALF>(yw[i]), r0 = rotate(v.x, z.x, cs[2 * i].x, cs[2 * i].y),
+                                     r1 = rotate(v.y, z.y, cs[(2 * i + 1) % P].x, cs[(2 * i + 1) % P].y);
+                        xw[i] = pack16<HALF>(r0.x, r1.x), yw[i] = pack16<HALF>(r0.y, r1.y);
+                    } else {
+                        const float2 r = rotate(v.x, v.y, cs[i].x, cs[i].y);
+                        xw[i] = pack16<HALF>(r.x, r.y);
+                    }
+                }
+                if (SPLIT) *reinterpret_cast<uint4 *>(dst + c1) = y[k];
+            }
+            *reinterpret_cast<uint4 *>(dst + c0) = x[k];
+        }
+    }
+}
+
+}  // namespace
+}  // namespace csa2
+
+using namespace csa2;
+
+extern "C" csa2_status csa2_rope_table(const double *inv_freq, int half, int64_t start, int64_t n_pos, float amplitude,
+                                       float *cos_sin, csa2_stream_t stream) {
+    clear_error();
+    CSA2_REQUIRE(half >= 1 && half <= 512, "rope_table: half=%d not in [1, 512]", half);
+    CSA2_REQUIRE(n_pos >= 0 && n_pos <= (1ll << 31), "rope_table: n_pos=%lld not in [0, 2^31]", (long long)n_pos);
+    CSA2_REQUIRE(start >= 0 && start <= (1ll << 31), "rope_table: start=%lld not in [0, 2^31]", (long long)start);
+    if (n_pos == 0) return CSA2_OK;
+    CSA2_REQUIRE(inv_freq && cos_sin, "rope_table: null pointer");
+    CSA2_REQUIRE(aligned(inv_freq, 8) && aligned(cos_sin, 8), "rope_table: inv_freq and cos_sin must be 8-byte aligned");
+    const uintptr_t f0 = (uintptr_t)inv_freq, t0 = (uintptr_t)cos_sin;
+    CSA2_REQUIRE(f0 + 8 * half <= t0 || t0 + 8 * n_pos * half <= f0, "rope_table: cos_sin overlaps inv_freq");
+    const int rows = half >= 256 ? 1 : 256 / half;
+    const int64_t want = (n_pos + rows - 1) / rows, most = (int64_t)num_sms() * 8;
+    const TableArgs a = {inv_freq, (float2 *)cos_sin, start, n_pos, half, amplitude};
+    CSA2_CUDA_CALL(launch_pdl(rope_table_kernel, dim3((unsigned)(want < most ? want : most)), dim3(half, rows), 0,
+                              stream_of(stream), a),
+                   "rope_table_kernel launch");
+    CSA2_LAUNCH_CHECK("rope_table_kernel");
+    return CSA2_OK;
+}
+
+extern "C" csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_token_stride, int64_t q_head_stride,
+                                 int64_t qo_token_stride, int64_t qo_head_stride, const void *k, void *k_out, int Hk,
+                                 int64_t k_token_stride, int64_t k_head_stride, int64_t ko_token_stride,
+                                 int64_t ko_head_stride, csa2_dtype dt, int64_t T, int D, const int32_t *pos,
+                                 const float *cos_sin, int64_t n_pos, int rope_dim, int first, csa2_rope_layout layout,
+                                 uint32_t *err_flag, csa2_stream_t stream) {
+    clear_error();
+    CSA2_REQUIRE(dt == CSA2_BF16 || dt == CSA2_FP16, "rope: rows must be bf16 or fp16");
+    CSA2_REQUIRE(T >= 0 && T <= (1ll << 30), "rope: T=%lld not in [0, 2^30]", (long long)T);
+    CSA2_REQUIRE(Hq >= 0 && Hk >= 0 && Hq <= 32768 && Hk <= 32767, "rope: Hq=%d, Hk=%d not in [0, 32768], [0, 32767]", Hq, Hk);
+    CSA2_REQUIRE(D >= 16 && D <= 1024 && D % 8 == 0, "rope: D=%d must be a multiple of 8 in [16, 1024]", D);
+    CSA2_REQUIRE(layout == CSA2_ROPE_INTERLEAVED || layout == CSA2_ROPE_HALF, "rope: layout=%d", (int)layout);
+    CSA2_REQUIRE(rope_dim >= 16 && rope_dim <= D && rope_dim % 16 == 0, "rope: rope_dim=%d must be a multiple of 16 in [16, D]",
+                 rope_dim);
+    CSA2_REQUIRE(first >= 0 && first % 8 == 0 && first + rope_dim <= D, "rope: first=%d must be a multiple of 8 in [0, D - rope_dim]",
+                 first);
+    CSA2_REQUIRE(n_pos >= 1 && n_pos <= (1ll << 31), "rope: n_pos=%lld not in [1, 2^31]", (long long)n_pos);
+    if (T == 0 || Hq + Hk == 0) return CSA2_OK;
+    CSA2_REQUIRE(pos && cos_sin && (Hq == 0 || (q && q_out)) && (Hk == 0 || (k && k_out)), "rope: null pointer");
+    CSA2_REQUIRE(aligned(pos, 4) && aligned(err_flag, 4) && aligned(cos_sin, 16),
+                 "rope: pos and flag must be 4-byte aligned, cos_sin 16-byte");
+    RotateArgs a = {{(const uint16_t *)q, (const uint16_t *)k}, {(uint16_t *)q_out, (uint16_t *)k_out},
+                    {q_token_stride, k_token_stride}, {q_head_stride, k_head_stride}, {qo_token_stride, ko_token_stride},
+                    {qo_head_stride, ko_head_stride}, {Hq, Hk}, 1, T, n_pos, pos, cos_sin, rope_dim / 2, first, 0, err_flag};
+    bool in_place = true;
+    Rows in[2] = {}, out[2] = {};
+    for (int i = 0; i < 2; ++i) {
+        if (a.heads[i] == 0) continue;
+        in[i] = {a.in[i], T, a.heads[i], D, a.in_token[i], a.in_head[i]};
+        out[i] = {a.out[i], T, a.heads[i], D, a.out_token[i], a.out_head[i]};
+        for (int64_t s : {a.in_token[i], a.in_head[i], a.out_token[i], a.out_head[i]})
+            CSA2_REQUIRE(s >= 0 && s % 8 == 0 && s < (1ll << 32), "rope: strides must be multiples of 8 in [0, 2^32)");
+        CSA2_REQUIRE(aligned(a.in[i], 16) && aligned(a.out[i], 16), "rope: rows must be 16-byte aligned");
+        CSA2_REQUIRE(out[i].apart(), "rope: rows of an output share elements");
+        const bool same = a.in[i] == a.out[i] && (T == 1 || a.in_token[i] == a.out_token[i]) &&
+                          (a.heads[i] == 1 || a.in_head[i] == a.out_head[i]);
+        CSA2_REQUIRE(same || !meet(in[i].p, in[i].bytes(), out[i].p, out[i].bytes()), "rope: an output overlaps its input");
+        CSA2_REQUIRE(!meet(out[i].p, out[i].bytes(), pos, 4 * T) && !meet(out[i].p, out[i].bytes(), cos_sin, 4 * n_pos * rope_dim) &&
+                         !meet(out[i].p, out[i].bytes(), err_flag, err_flag ? 4 : 0),
+                     "rope: an output overlaps pos, cos_sin or the flag");
+        in_place = in_place && same;
+    }
+    CSA2_REQUIRE(!share(out[0], out[1]), "rope: q_out and k_out share elements");
+    CSA2_REQUIRE(!share(out[0], in[1]) && !share(out[1], in[0]), "rope: an output overlaps the other input");
+    const int vectors = D / 8, turned = layout == CSA2_ROPE_HALF ? rope_dim / 16 : rope_dim / 8;
+    const int units = in_place ? turned : turned + vectors - rope_dim / 8;
+    a.turned = turned;
+    const int rows = 256 / units, H = Hq + Hk;
+    const int64_t blocks = (T + rows - 1) / rows;
+    // Cosines and sines are loaded once for all heads of a thread, as many as leave work for every SM.
+    int per = kBatch;
+    while (per < H && blocks * ((H + 2 * per - 1) / (2 * per)) >= (int64_t)num_sms() * 8) per *= 2;
+    if (blocks * ((H + per - 1) / per) < (int64_t)num_sms() * 4) per = 1;
+    a.per = per;
+    const dim3 grid((unsigned)blocks, (H + per - 1) / per);
+    const bool half_type = dt == CSA2_FP16;
+    void (*kern)(RotateArgs) = layout == CSA2_ROPE_HALF ? (half_type ? rope_kernel<true, true> : rope_kernel<false, true>)
+                                                        : (half_type ? rope_kernel<true, false> : rope_kernel<false, false>);
+    CSA2_CUDA_CALL(launch_pdl(kern, grid, dim3(units, rows), 0, stream_of(stream), a), "rope_kernel launch");
+    CSA2_LAUNCH_CHECK("rope_kernel");
+    return CSA2_OK;
+}
