@@ -649,7 +649,7 @@ cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cud
         if (e != cudaSuccess) return e;
     }
     if (tc_ctas) {
-        e = launch_paged_attn_tc(a, D, HALF, stream);
+        e = launch_paged_attn_tc(a, D, HALF, false, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_join<D, NT, HALF>(a, split_ctas, tc_ctas, stream);

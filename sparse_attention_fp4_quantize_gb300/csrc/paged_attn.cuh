@@ -312,6 +312,6 @@ cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, int D, int NT, bool h
 
 // The tile kernel (paged_attn_tc.cu): one CTA per SM.
 int paged_attn_tc_ctas();
-cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, int D, bool half, cudaStream_t stream);
+cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, int D, bool half, bool fp4, cudaStream_t stream);
 
 }  // namespace csa2

@@ -498,12 +498,19 @@ cudaError_t launch_split4(const PagedAttnArgs &a, int ctas, cudaStream_t stream)
     return launch_pdl(paged_attn4_split_kernel<D, NT, HALF>, dim3(ctas), dim3(kWarps4 * 32), split4_smem<D>(), stream, a);
 }
 
+constexpr int kSplitRows4 = 32;
 struct Choice4 {
     int NT, split_ctas, tc_ctas, split_rows;
 };
 inline Choice4 choose4(int B, int G, int max_new) {
     const int64_t rows = (int64_t)G * max_new;
-    return {rows <= 8 ? 1 : 2, num_sms() * kPerSm4, 0, 0x7FFFFFFF};
+    Choice4 c = {(rows <= kSplitRows4 ? rows : G) <= 8 ? 1 : 2, 0, 0, 0x7FFFFFFF};
+    if (rows > kSplitRows4) {
+        c.tc_ctas = paged_attn_tc_ctas();
+        c.split_rows = B == 1 || G > kSplitRows4 ? 0 : (c.NT == 1 ? 8 : kSplitRows4);
+    }
+    if (c.split_rows) c.split_ctas = num_sms() * kPerSm4;
+    return c;
 }
 inline size_t partial4_floats(const Choice4 &c, int D) { return (size_t)2 * c.split_ctas * 8 * c.NT * (D + 4); }
 
@@ -555,7 +562,8 @@ extern "C" csa2_status csa2_paged_attn_fp4(int B, int64_t T, int Hq, int Hkv, in
                                    : (half ? launch_split4<64, 2, true> : launch_split4<64, 2, false>))
                       : (c.NT == 1 ? (half ? launch_split4<128, 1, true> : launch_split4<128, 1, false>)
                                    : (half ? launch_split4<128, 2, true> : launch_split4<128, 2, false>));
-    CSA2_CUDA_CALL(go(a, c.split_ctas, stream_of(stream)), "paged_attn launch");
+    if (c.split_ctas) CSA2_CUDA_CALL(go(a, c.split_ctas, stream_of(stream)), "paged_attn launch");
+    if (c.tc_ctas) CSA2_CUDA_CALL(launch_paged_attn_tc(a, D, half, true, stream_of(stream)), "paged_attn tile launch");
     CSA2_CUDA_CALL(launch_paged_attn_join(a, D, c.NT, half, c.split_ctas, c.tc_ctas, stream_of(stream)), "paged_attn join launch");
     CSA2_LAUNCH_CHECK("paged_attn kernels");
     return CSA2_OK;

@@ -35,6 +35,7 @@
 // than the overlap gives), codes kept in registers instead of staged (934 against
 // 906), whole warps in place of one thread to issue (979 against 905), the lock given
 // up before S (956 against 905), Q asked for ahead by warp 14 (921 against 905).
+#include "fp4.cuh"
 #include "paged_attn.cuh"
 #include "tc.cuh"
 
@@ -90,6 +91,19 @@ struct Lay {
     static constexpr uint32_t SMEM = USED + 128 > 120 * 1024 ? USED + 128 : 120 * 1024;   // one CTA per SM (TMEM)
     static constexpr uint32_t COL_S = 0, COL_O = 256;    // TMEM columns: S0, S1 (P over them), O0, O1
 };
+
+// Copy of N (4 or 8) bytes, or N zeros.
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t smem, const void *gmem, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem), "l"(gmem), "n"(N), "r"(there ? N : 0) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r in a staged tile of the 4-bit cache's rows,
+// swizzled so that 8 rows' loads of one chunk meet every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t chunk4_at(int r, int c) {
+    return D == 128 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+}
 
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
     uint64_t d;
@@ -210,7 +224,7 @@ struct Walk {
     }
 };
 
-template <int D, bool HALF>
+template <int D, bool HALF, bool FP4>
 __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnArgs a) {
     using L = Lay<D>;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
@@ -423,7 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         Segment ahead;
         int tile_ahead = 0;
         bool have = next_seg(ahead);
-        // lane = (tile lane / 2, 16-key group lane % 2) of 16 tiles: code offset (-1: not stored) and scales
+        // lane = (tile lane / 2, 16-key group lane % 2) of 16 tiles: its first row among the cache's (-1: not stored) and scales
         int64_t boff = -1;
         float bks = 0.0f, bvs = 0.0f, blg = 0.0f, brv = 0.0f;
         uint32_t bmiss = 0;
@@ -440,11 +454,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 const bool ok = blk >= 0 && blk < a.n_blocks;
                 if (there && !ok) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
                 const int64_t bh = ok ? (int64_t)blk * a.Hkv + ahead.pl.h : 0;
-                boff = ok ? (bh * a.S + (key & (a.S - 1))) * D : -1;
-                bks = ok ? a.k_scale[bh] : 0.0f;
-                bvs = ok ? a.v_scale[bh] : 0.0f;
-                blg = log_scale(bvs);
-                brv = rcp(bvs) * kDownFactor;
+                boff = ok ? bh * a.S + (key & (a.S - 1)) : -1;
+                if constexpr (!FP4) {
+                    bks = ok ? a.k_scale[bh] : 0.0f;
+                    bvs = ok ? a.v_scale[bh] : 0.0f;
+                    blg = log_scale(bvs);
+                    brv = rcp(bvs) * kDownFactor;
+                }
                 bmiss = __ballot_sync(ALL, !ok);
             }
             cur = tile_ahead - batch;
@@ -453,15 +469,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 const int64_t at = __shfl_sync(ALL, boff, 2 * cur + u);
                 const int left = ahead.rq.kv - (ahead.key0() + tile_ahead * kTcKeys + 32 * cw + 16 * u);
                 rows[u] = at < 0 ? 0 : min(left, 16);
-                off[u] = at < 0 ? 0 : at;
+                off[u] = at < 0 ? 0 : at * (FP4 ? 1 : D);
             }
         };
         // The next tile's rows travel into the warp's own part of shared memory
         // (registers would do, but the softmax has them): whole rows per copy, chunks
         // swizzled, so that copies touch full lines and the reads below every bank.
         const uint32_t stage_k = sb + L::OFF_STAGE + cw * 32 * D, stage_v = stage_k + L::KV / 2;
-        auto fetch = [&](uint32_t stage, const uint8_t *codes) {
-            if (have) {
+        auto fetch = [&](uint32_t stage, const uint8_t *codes, const uint8_t *scales) {
+            if constexpr (FP4) {
+                if (have) {
+                    constexpr int CPR = D / 32, RPI = 32 / CPR, SB = D / 16; // chunks per row, rows per copy, bytes of a row's scales
+                    const int c = lane % CPR, r0 = lane / CPR;
+#pragma unroll
+                    for (int i = 0; i < CPR; ++i) {
+                        const int r = i * RPI + r0, u = r >> 4;              // row, its 16-key group
+                        const bool there = (r & 15) < (u ? rows[1] : rows[0]);       // rows that are not there read as zero
+                        const int64_t at = (u ? off[1] : off[0]) + (r & 15);
+                        cp_async16(stage + chunk4_at<D>(r, c), there ? (const void *)(codes + at * (D / 2) + 16 * c) : a.q, there ? 16 : 0);
+                    }
+                    const bool there = (lane & 15) < (lane >> 4 ? rows[1] : rows[0]);
+                    const int64_t at = (lane >> 4 ? off[1] : off[0]) + (lane & 15);
+                    cp_async_small<SB>(stage + 16 * D + lane * SB, there ? (const void *)(scales + at * SB) : a.q, there);
+                }
+            } else if (have) {
                 constexpr int CPR = D / 16, RPI = 32 / CPR;                  // chunks per row, rows per copy
                 const int c = lane % CPR, r0 = lane / CPR;
 #pragma unroll
@@ -476,20 +507,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         auto store = [&](uint32_t dst, uint32_t stage) {
             cp_async_wait<1>();                          // all but the newest of the copies
             __syncwarp();
-            uint4 c[N];
+            if constexpr (FP4) {
+                // lane = (row of 8, piece of 32 channels, for 64 channels every other 8 rows)
+                constexpr int PIECES = D / 32, STEP = 4 / PIECES;
+                const int piece = chunk % PIECES, g0 = chunk / PIECES;
+                uint4 c[4 / STEP];
+                uint32_t sc[4 / STEP];
 #pragma unroll
-            for (int i = 0; i < N; ++i) c[i] = lds128(stage + chunk_at<D>(8 * (i / CH) + row, 4 * (i % CH) + chunk));
+                for (int i = 0; i < 4 / STEP; ++i) {
+                    const int r = 8 * (i * STEP + g0) + row;
+                    c[i] = lds128(stage + chunk4_at<D>(r, piece));
+                    uint16_t two;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(two) : "r"(stage + 16 * D + r * (D / 16) + 2 * piece));
+                    sc[i] = e4m3x2_to_f16x2(two);
+                }
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int g = i / CH;
-                const uint32_t to = dst + (4 * cw + g) * L::GROUP + (8 * (i % CH) + 2 * chunk) * 128 + row * 16;
-                uint32_t h[8];
-                e4m3x4_to_f16x2x2(c[i].x, h[0], h[1]);
-                e4m3x4_to_f16x2x2(c[i].y, h[2], h[3]);
-                e4m3x4_to_f16x2x2(c[i].z, h[4], h[5]);
-                e4m3x4_to_f16x2x2(c[i].w, h[6], h[7]);
-                sts128(to, h[0], h[1], h[2], h[3]);
-                sts128(to + 128, h[4], h[5], h[6], h[7]);
+                for (int i = 0; i < 4 / STEP; ++i) {
+                    const uint32_t to = dst + (4 * cw + i * STEP + g0) * L::GROUP + 4 * piece * 128 + row * 16;
+                    const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t h[4];
+                        e2m1x8_to_f16(w[k], __byte_perm(sc[i], 0, k < 2 ? 0x1010 : 0x3232), h);
+                        sts128(to + k * 128, h[0], h[1], h[2], h[3]);
+                    }
+                }
+            } else {
+                uint4 c[N];
+    #pragma unroll
+                for (int i = 0; i < N; ++i) c[i] = lds128(stage + chunk_at<D>(8 * (i / CH) + row, 4 * (i % CH) + chunk));
+    #pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int g = i / CH;
+                    const uint32_t to = dst + (4 * cw + g) * L::GROUP + (8 * (i % CH) + 2 * chunk) * 128 + row * 16;
+                    uint32_t h[8];
+                    e4m3x4_to_f16x2x2(c[i].x, h[0], h[1]);
+                    e4m3x4_to_f16x2x2(c[i].y, h[2], h[3]);
+                    e4m3x4_to_f16x2x2(c[i].z, h[4], h[5]);
+                    e4m3x4_to_f16x2x2(c[i].w, h[6], h[7]);
+                    sts128(to, h[0], h[1], h[2], h[3]);
+                    sts128(to + 128, h[4], h[5], h[6], h[7]);
+                }
             }
         };
         tile_ahead = ahead.pl.tile;
@@ -501,7 +559,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 TileMeta &m = metas[nt % kMetas];
                 if ((lane >> 1) == cur) {                // the lanes with the tile's scales
                     const int u = 2 * cw + (lane & 1);
-                    m.ks[u] = bks, m.vs[u] = bvs, m.lg[u] = blg, m.rv[u] = brv;
+                    if constexpr (!FP4) m.ks[u] = bks, m.vs[u] = bvs, m.lg[u] = blg, m.rv[u] = brv;
                     if (!(lane & 1)) m.missing[cw] = ((bmiss >> lane) & 3) << (2 * cw);
                 }
                 __syncwarp();
@@ -515,7 +573,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 __syncwarp();
                 if (lane == 0) arrive(kfull(buf));
             }
-            fetch(stage_k, a.k_codes);
+            fetch(stage_k, a.k_codes, a.k_scale4);
             if (loaded) {
                 if (!wait_bar(vempty(buf), par, abort_word)) break;
                 store(sb + L::OFF_V + buf * L::KV, stage_v);
@@ -525,7 +583,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 ++nt;
             }
             loaded = have;
-            fetch(stage_v, a.v_codes);
+            fetch(stage_v, a.v_codes, a.v_scale4);
             if (have) {
                 if (++tile_ahead >= ahead.tb) {          // the tile after the one that travels
                     have = next_seg(ahead);
@@ -619,6 +677,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             if (busy) {                                  // O of the segment before
                 if (!wait_bar(ofull(sub), (ns - 1) & 1, abort_word)) break;
                 tc::fence_after();
+                if (FP4) MV = M;
                 const float ref = M == NEG_INF ? 0.0f : M, refv = MV == NEG_INF ? 0.0f : MV;
                 const float scale = exp2f(refv - ref), inv = l > 0.0f ? kDownFactor / l : (l == 0.0f ? 0.0f : l);
                 float *part = a.partial_tc + ((2 * (int64_t)blockIdx.x + first_part) * kTcRows + 128 * sub + rr) * (D + 4);
@@ -704,10 +763,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 if (!(run = wait_bar(mfull(nt % kMetas), (nt / kMetas) & 1, abort_word))) break;
                 const uint32_t missing = m.missing[0] | m.missing[1] | m.missing[2] | m.missing[3];
                 const bool mask = lo > 0 || hi < kTcKeys || missing != 0;
-                const float4 lg0 = *reinterpret_cast<const float4 *>(m.lg), lg1 = *reinterpret_cast<const float4 *>(m.lg + 4);
-                const float least = fminf(fminf(fminf(lg0.x, lg0.y), fminf(lg0.z, lg0.w)), fminf(fminf(lg1.x, lg1.y), fminf(lg1.z, lg1.w)));
-                const float most = fmaxf(fmaxf(fmaxf(lg0.x, lg0.y), fmaxf(lg0.z, lg0.w)), fmaxf(fmaxf(lg1.x, lg1.y), fmaxf(lg1.z, lg1.w)));
-                bool fast = __all_sync(ALL, !mask && M - MV + least > -kSpread && M - MV + most < kSpread);
+                bool fast;
+                if constexpr (FP4) {
+                    fast = __all_sync(ALL, !mask && M > NEG_INF);
+                } else {
+                    const float4 lg0 = *reinterpret_cast<const float4 *>(m.lg), lg1 = *reinterpret_cast<const float4 *>(m.lg + 4);
+                    const float least = fminf(fminf(fminf(lg0.x, lg0.y), fminf(lg0.z, lg0.w)), fminf(fminf(lg1.x, lg1.y), fminf(lg1.z, lg1.w)));
+                    const float most = fmaxf(fmaxf(fmaxf(lg0.x, lg0.y), fmaxf(lg0.z, lg0.w)), fmaxf(fmaxf(lg1.x, lg1.y), fmaxf(lg1.z, lg1.w)));
+                    fast = __all_sync(ALL, !mask && M - MV + least > -kSpread && M - MV + most < kSpread);
+                }
                 if (j > 0 && !(run = wait_s())) break;
                 tc::fence_after();
                 // scores of the keys 32 c .. 32 c + 31 that the row does not see: -inf
@@ -737,120 +801,217 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                         }
                     }
                 };
-                for (bool raised = false; fast; raised = true) {
-                    const float back = ex2(MV - M);
-                    uint32_t p[4][16];
-                    float gain = 0.0f, total = 0.0f;
-                    uint32_t r[2][32];
-                    tc::tmem_ld32(ts, r[0]);
+                if constexpr (FP4) {
+                    // No scales between scores and weights: one reference, P = 2^(s f + kUp - M).
+                    const float f = fmaxf(zf, 1e-38f);       // not 0, so that a hidden score of -inf stays -inf
+                    const uint64_t ff = f2(f, f);
+                    for (bool raised = false; fast; raised = true) {
+                        const float at = kUp - M;
+                        const uint64_t aa = f2(at, at);
+                        uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
+                        uint32_t p[4][16], r[2][32];
+                        tc::tmem_ld32(ts, r[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tc::tmem_ld_wait();
-                        if (c < 3) tc::tmem_ld32(ts + 32 * (c + 1), r[(c + 1) & 1]);
-                        const float2 ks = *reinterpret_cast<const float2 *>(&m.ks[2 * c]), lg = *reinterpret_cast<const float2 *>(&m.lg[2 * c]),
-                                     rv = *reinterpret_cast<const float2 *>(&m.rv[2 * c]);
+                        for (int c = 0; c < 4; ++c) {
+                            tc::tmem_ld_wait();
+                            if (c < 3) tc::tmem_ld32(ts + 32 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float f = factor(zf, g ? ks.y : ks.x), at = (g ? lg.y : lg.x) - MV;
-                            const uint64_t ff = f2(f, f), aa = f2(at, at);
-                            uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 z = un2(fma2(f2u(r[c & 1][16 * g + i], r[c & 1][16 * g + i + 1]), ff, aa));
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 z = un2(fma2(f2u(r[c & 1][i], r[c & 1][i + 1]), ff, aa));
                                 const float e0 = ex2(z.x), e1 = ex2(z.y);
                                 if (i & 2) sum1 = add2(sum1, f2(e0, e1));
                                 else sum0 = add2(sum0, f2(e0, e1));
-                                p[c][8 * g + i / 2] = pack_f16(e0, e1);
+                                p[c][i / 2] = pack_f16(e0, e1);
                             }
-                            const float2 x = un2(add2(sum0, sum1));
-                            const float y = x.x + x.y;
-                            total += y;
-                            gain += y * (g ? rv.y : rv.x);
+                        }
+                        const float2 x = un2(add2(sum0, sum1));
+                        const float total = x.x + x.y;
+                        if (__all_sync(ALL, total < kMostP)) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) tc::tmem_st16(ts + 16 * c, p[c]);
+                            l = fmaf(total, kDownFactor, l);
+                            break;
+                        }
+                        // once: of scores beyond 2^24 a higher M may round to the same, or further up
+                        fast = !raised && __all_sync(ALL, total < kMostRaise);
+                        if (fast) {                          // all 32 rows' sums to 2^kUp, as far as they exceed it
+                            const float m1 = M + max(0, (int)(__float_as_uint(total) >> 23) - 127 - kUp), by = ex2(M - m1);
+                            rescale(by);
+                            l *= by;
+                            M = m1;
                         }
                     }
-                    if (__all_sync(ALL, total < kMostP && gain * back < kMostL)) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tc::tmem_st16(ts + 16 * c, p[c]);
-                        l += gain * back;
-                        break;
-                    }
-                    // once: of scores beyond 2^24 a higher Mv may round to the same, or further up
-                    fast = !raised && __all_sync(ALL, total < kMostRaise && gain * back < kMostL);
-                    if (fast) {                          // all 32 rows' sums to 2^kUp, as far as they exceed it
-                        const float mv1 = MV + max(0, (int)(__float_as_uint(total) >> 23) - 127 - kUp);
-                        rescale(ex2(MV - mv1));
-                        MV = mv1;
-                    }
-                }
-                if (!fast) {
-                    const bool masked = __any_sync(ALL, mask);
-                    // 64 scores at a time, read again for P: all 128 do not fit beside the rest
-                    uint32_t r[2][32];
-                    float tz = NEG_INF, tv = NEG_INF;
+                    if (!fast) {
+                        const bool masked = __any_sync(ALL, mask);
+                        uint32_t r[2][32];
+                        float tz = NEG_INF;
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        tc::tmem_ld32(ts + 32 * c, r[0]);
-                        tc::tmem_ld32(ts + 32 * c + 32, r[1]);
-                        tc::tmem_ld_wait();
-                        if (masked) hide(c, r[0]), hide(c + 1, r[1]);
+                        for (int c = 0; c < 4; c += 2) {
+                            tc::tmem_ld32(ts + 32 * c, r[0]);
+                            tc::tmem_ld32(ts + 32 * c + 32, r[1]);
+                            tc::tmem_ld_wait();
+                            if (masked) hide(c, r[0]), hide(c + 1, r[1]);
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint32_t (&x)[32] = r[g / 2];
-                            const int i0 = 16 * (g & 1);
-                            float t0 = __uint_as_float(x[i0]), t1 = __uint_as_float(x[i0 + 1]);
+                            for (int k = 0; k < 2; ++k) {
+                                float t0 = __uint_as_float(r[k][0]), t1 = __uint_as_float(r[k][1]);
 #pragma unroll
-                            for (int i = 2; i < 14; i += 4) {
-                                t0 = max3(t0, __uint_as_float(x[i0 + i]), __uint_as_float(x[i0 + i + 1]));
-                                t1 = max3(t1, __uint_as_float(x[i0 + i + 2]), __uint_as_float(x[i0 + i + 3]));
-                            }
-                            const float t = fmaxf(max3(t0, t1, __uint_as_float(x[i0 + 14])), __uint_as_float(x[i0 + 15])) * factor(zf, m.ks[2 * c + g]);
-                            tz = fmaxf(tz, t);
-                            tv = fmaxf(tv, t + (float)((int)((__float_as_uint(m.vs[2 * c + g]) >> 23) & 0xFFu) - 127));
-                        }
-                    }
-                    // The references move when a row's scores exceed one by more than the slack, or at a row's
-                    // first key; then those of all 32 rows do, as far as they are exceeded, so that the next
-                    // tiles are the less likely to need it.
-                    const bool due = tz - M > kSlack || tv - MV > kSlack;
-                    const bool all = __any_sync(ALL, due), up = all && tz > M, upv = all && tv > MV;
-                    if (up) {
-                        l *= ex2(M - tz);
-                        M = tz;
-                    }
-                    const float grow = upv ? ex2(MV - tv) : 1.0f;
-                    if (upv) MV = tv;
-                    if (j > 0 && __any_sync(ALL, upv)) rescale(grow);
-                    const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(0.5f * (ref - (MV == NEG_INF ? 0.0f : MV)));     // 2^(M - Mv) in two steps
-                    uint64_t sum = f2(0.0f, 0.0f);
-#pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        tc::tmem_ld32(ts + 32 * c, r[0]);
-                        tc::tmem_ld32(ts + 32 * c + 32, r[1]);
-                        tc::tmem_ld_wait();
-                        if (masked) hide(c, r[0]), hide(c + 1, r[1]);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t p[16];
-#pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2 * g2, kMostWeight) * kUpFactor;
-                                const uint64_t ww = f2(w, w);
-#pragma unroll
-                                for (int i = 0; i < 16; i += 2) {
-                                    // rounded as the maxima were, before the reference is taken off, so that none is beyond
-                                    // them (a packed product and sum would be joined again, without that rounding)
-                                    const float z0 = __fmul_rn(__uint_as_float(r[k][16 * g + i]), f), z1 = __fmul_rn(__uint_as_float(r[k][16 * g + i + 1]), f);
-                                    const uint64_t e = f2(ex2(__fadd_rn(z0, -ref)), ex2(__fadd_rn(z1, -ref)));
-                                    sum = add2(sum, e);
-                                    const float2 x = un2(mul2(e, ww));
-                                    p[8 * g + i / 2] = pack_f16(x.x, x.y);
+                                for (int i = 2; i < 30; i += 4) {
+                                    t0 = max3(t0, __uint_as_float(r[k][i]), __uint_as_float(r[k][i + 1]));
+                                    t1 = max3(t1, __uint_as_float(r[k][i + 2]), __uint_as_float(r[k][i + 3]));
                                 }
+                                tz = fmaxf(tz, fmaxf(max3(t0, t1, __uint_as_float(r[k][30])), __uint_as_float(r[k][31])));
                             }
-                            tc::tmem_st16(ts + 16 * (c + k), p);
+                        }
+                        tz = __fmul_rn(tz, f);
+                        // The references move when a row's scores exceed one by more than the slack, or at a row's
+                        // first key; then those of all 32 rows do, as far as they are exceeded, so that the next
+                        // tiles are the less likely to need it.
+                        const bool up = __any_sync(ALL, tz - M > kSlack) && tz > M;
+                        const float grow = up ? ex2(M - tz) : 1.0f;
+                        l *= grow;
+                        if (up) M = tz;
+                        if (j > 0 && __any_sync(ALL, up)) rescale(grow);
+                        const float ref = M == NEG_INF ? 0.0f : M;
+                        uint64_t sum = f2(0.0f, 0.0f);
+#pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            tc::tmem_ld32(ts + 32 * c, r[0]);
+                            tc::tmem_ld32(ts + 32 * c + 32, r[1]);
+                            tc::tmem_ld_wait();
+                            if (masked) hide(c, r[0]), hide(c + 1, r[1]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t p[16];
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) {
+                                    // rounded as the maximum was, before the reference is taken off, so that none is beyond it
+                                    const float z0 = __fmul_rn(__uint_as_float(r[k][i]), f), z1 = __fmul_rn(__uint_as_float(r[k][i + 1]), f);
+                                    const float e0 = ex2(__fadd_rn(z0, -ref) + kUp), e1 = ex2(__fadd_rn(z1, -ref) + kUp);
+                                    sum = add2(sum, f2(e0, e1));
+                                    p[i / 2] = pack_f16(e0, e1);
+                                }
+                                tc::tmem_st16(ts + 16 * (c + k), p);
+                            }
+                        }
+                        const float2 s2 = un2(sum);
+                        l = fmaf(s2.x + s2.y, kDownFactor, l);
+                    }
+                } else {
+                    for (bool raised = false; fast; raised = true) {
+                        const float back = ex2(MV - M);
+                        uint32_t p[4][16];
+                        float gain = 0.0f, total = 0.0f;
+                        uint32_t r[2][32];
+                        tc::tmem_ld32(ts, r[0]);
+    #pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tc::tmem_ld_wait();
+                            if (c < 3) tc::tmem_ld32(ts + 32 * (c + 1), r[(c + 1) & 1]);
+                            const float2 ks = *reinterpret_cast<const float2 *>(&m.ks[2 * c]), lg = *reinterpret_cast<const float2 *>(&m.lg[2 * c]),
+                                         rv = *reinterpret_cast<const float2 *>(&m.rv[2 * c]);
+    #pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const float f = factor(zf, g ? ks.y : ks.x), at = (g ? lg.y : lg.x) - MV;
+                                const uint64_t ff = f2(f, f), aa = f2(at, at);
+                                uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
+    #pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    const float2 z = un2(fma2(f2u(r[c & 1][16 * g + i], r[c & 1][16 * g + i + 1]), ff, aa));
+                                    const float e0 = ex2(z.x), e1 = ex2(z.y);
+                                    if (i & 2) sum1 = add2(sum1, f2(e0, e1));
+                                    else sum0 = add2(sum0, f2(e0, e1));
+                                    p[c][8 * g + i / 2] = pack_f16(e0, e1);
+                                }
+                                const float2 x = un2(add2(sum0, sum1));
+                                const float y = x.x + x.y;
+                                total += y;
+                                gain += y * (g ? rv.y : rv.x);
+                            }
+                        }
+                        if (__all_sync(ALL, total < kMostP && gain * back < kMostL)) {
+    #pragma unroll
+                            for (int c = 0; c < 4; ++c) tc::tmem_st16(ts + 16 * c, p[c]);
+                            l += gain * back;
+                            break;
+                        }
+                        // once: of scores beyond 2^24 a higher Mv may round to the same, or further up
+                        fast = !raised && __all_sync(ALL, total < kMostRaise && gain * back < kMostL);
+                        if (fast) {                          // all 32 rows' sums to 2^kUp, as far as they exceed it
+                            const float mv1 = MV + max(0, (int)(__float_as_uint(total) >> 23) - 127 - kUp);
+                            rescale(ex2(MV - mv1));
+                            MV = mv1;
                         }
                     }
-                    const float2 s2 = un2(sum);
-                    l += s2.x + s2.y;
+                    if (!fast) {
+                        const bool masked = __any_sync(ALL, mask);
+                        // 64 scores at a time, read again for P: all 128 do not fit beside the rest
+                        uint32_t r[2][32];
+                        float tz = NEG_INF, tv = NEG_INF;
+    #pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            tc::tmem_ld32(ts + 32 * c, r[0]);
+                            tc::tmem_ld32(ts + 32 * c + 32, r[1]);
+                            tc::tmem_ld_wait();
+                            if (masked) hide(c, r[0]), hide(c + 1, r[1]);
+    #pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint32_t (&x)[32] = r[g / 2];
+                                const int i0 = 16 * (g & 1);
+                                float t0 = __uint_as_float(x[i0]), t1 = __uint_as_float(x[i0 + 1]);
+    #pragma unroll
+                                for (int i = 2; i < 14; i += 4) {
+                                    t0 = max3(t0, __uint_as_float(x[i0 + i]), __uint_as_float(x[i0 + i + 1]));
+                                    t1 = max3(t1, __uint_as_float(x[i0 + i + 2]), __uint_as_float(x[i0 + i + 3]));
+                                }
+                                const float t = fmaxf(max3(t0, t1, __uint_as_float(x[i0 + 14])), __uint_as_float(x[i0 + 15])) * factor(zf, m.ks[2 * c + g]);
+                                tz = fmaxf(tz, t);
+                                tv = fmaxf(tv, t + (float)((int)((__float_as_uint(m.vs[2 * c + g]) >> 23) & 0xFFu) - 127));
+                            }
+                        }
+                        // The references move when a row's scores exceed one by more than the slack, or at a row's
+                        // first key; then those of all 32 rows do, as far as they are exceeded, so that the next
+                        // tiles are the less likely to need it.
+                        const bool due = tz - M > kSlack || tv - MV > kSlack;
+                        const bool all = __any_sync(ALL, due), up = all && tz > M, upv = all && tv > MV;
+                        if (up) {
+                            l *= ex2(M - tz);
+                            M = tz;
+                        }
+                        const float grow = upv ? ex2(MV - tv) : 1.0f;
+                        if (upv) MV = tv;
+                        if (j > 0 && __any_sync(ALL, upv)) rescale(grow);
+                        const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(0.5f * (ref - (MV == NEG_INF ? 0.0f : MV)));     // 2^(M - Mv) in two steps
+                        uint64_t sum = f2(0.0f, 0.0f);
+    #pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            tc::tmem_ld32(ts + 32 * c, r[0]);
+                            tc::tmem_ld32(ts + 32 * c + 32, r[1]);
+                            tc::tmem_ld_wait();
+                            if (masked) hide(c, r[0]), hide(c + 1, r[1]);
+    #pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t p[16];
+    #pragma unroll
+                                for (int g = 0; g < 2; ++g) {
+                                    const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2 * g2, kMostWeight) * kUpFactor;
+                                    const uint64_t ww = f2(w, w);
+    #pragma unroll
+                                    for (int i = 0; i < 16; i += 2) {
+                                        // rounded as the maxima were, before the reference is taken off, so that none is beyond
+                                        // them (a packed product and sum would be joined again, without that rounding)
+                                        const float z0 = __fmul_rn(__uint_as_float(r[k][16 * g + i]), f), z1 = __fmul_rn(__uint_as_float(r[k][16 * g + i + 1]), f);
+                                        const uint64_t e = f2(ex2(__fadd_rn(z0, -ref)), ex2(__fadd_rn(z1, -ref)));
+                                        sum = add2(sum, e);
+                                        const float2 x = un2(mul2(e, ww));
+                                        p[8 * g + i / 2] = pack_f16(x.x, x.y);
+                                    }
+                                }
+                                tc::tmem_st16(ts + 16 * (c + k), p);
+                            }
+                        }
+                        const float2 s2 = un2(sum);
+                        l += s2.x + s2.y;
+                    }
                 }
                 tc::tmem_st_wait();
                 tc::fence_before();
@@ -868,21 +1029,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool HALF>
+template <int D, bool HALF, bool FP4>
 cudaError_t go(const PagedAttnArgs &a, cudaStream_t stream) {
     static bool done[64];
-    cudaError_t e = ensure_smem_limit((const void *)paged_attn_tc_kernel<D, HALF>, Lay<D>::SMEM, done);
+    cudaError_t e = ensure_smem_limit((const void *)paged_attn_tc_kernel<D, HALF, FP4>, Lay<D>::SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attn_tc_kernel<D, HALF>, dim3(paged_attn_tc_ctas()), dim3(kTcThreads), Lay<D>::SMEM, stream, a);
+    return launch_pdl(paged_attn_tc_kernel<D, HALF, FP4>, dim3(paged_attn_tc_ctas()), dim3(kTcThreads), Lay<D>::SMEM, stream, a);
+}
+
+template <bool FP4>
+cudaError_t go_for(const PagedAttnArgs &a, int D, bool half, cudaStream_t stream) {
+    if (half) return D == 64 ? go<64, true, FP4>(a, stream) : go<128, true, FP4>(a, stream);
+    return D == 64 ? go<64, false, FP4>(a, stream) : go<128, false, FP4>(a, stream);
 }
 
 }  // namespace
 
 int paged_attn_tc_ctas() { return num_sms(); }
 
-cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, int D, bool half, cudaStream_t stream) {
-    if (half) return D == 64 ? go<64, true>(a, stream) : go<128, true>(a, stream);
-    return D == 64 ? go<64, false>(a, stream) : go<128, false>(a, stream);
+cudaError_t launch_paged_attn_tc(const PagedAttnArgs &a, int D, bool half, bool fp4, cudaStream_t stream) {
+    return fp4 ? go_for<true>(a, D, half, stream) : go_for<false>(a, D, half, stream);
 }
 
 }  // namespace csa2
