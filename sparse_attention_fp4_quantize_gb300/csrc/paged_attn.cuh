@@ -195,9 +195,9 @@ struct Place {
 // 8, 192 with 0; 48 of up to 9k in a window of 4096 (5 heads of 64) 35.0, 36.0 and
 // (before the segments' first loads were reordered) 42.0 against 36.7; 35.6 with 20.
 constexpr int kSplitWarps = 4, kSplitCost = 16;
-static_assert(kSplitCost % kSplitWarps == 0, "segments begin at whole rounds of the warps");
-template <int R, int K>
+template <int R, int K, int COST = kSplitCost>
 struct SplitWork {
+    static_assert(COST % kSplitWarps == 0, "segments begin at whole rounds of the warps");
     static __device__ __forceinline__ int low_key(const PagedAttnArgs &a, const Request &r) {       // of the first row's window
         const int64_t p = (int64_t)r.kv - r.n - a.window + 1;
         return a.window > 0 && p > 0 ? (int)p : 0;
@@ -208,7 +208,7 @@ struct SplitWork {
         return keys > 0 ? (keys + K - 1) / K : 1;
     }
     static __device__ __forceinline__ int unit_places(const PagedAttnArgs &a, const Request &r) {
-        return kSplitCost + (real_tiles(a, r) + kSplitWarps - 1) / kSplitWarps * kSplitWarps;
+        return COST + (real_tiles(a, r) + kSplitWarps - 1) / kSplitWarps * kSplitWarps;
     }
     static __device__ __forceinline__ int64_t tiles(const PagedAttnArgs &a, const Request &r) {
         const int rows = r.n * a.G;

@@ -18,14 +18,17 @@ namespace {
 
 constexpr int kWarps4 = kSplitWarps;
 constexpr int kPerSm4 = 3;              // CTAs that an SM holds at once
-constexpr int kStages4 = 3;             // tiles in flight per warp
-constexpr int kCodes4 = 2048, kScales4 = kCodes4 / 8;        // bytes of a tile's keys: codes, scales; of its values the same
-constexpr int kStage4 = 2 * (kCodes4 + kScales4);
+constexpr int kKeys4 = 64;              // keys of a warp's tile
+constexpr int kCost4 = 8;               // tiles that a unit's fixed cost counts as
+template <int D>
+struct Stage4 {                         // a tile in shared memory: codes and scales of its keys and of its values
+    static constexpr int CODES = kKeys4 * D / 2, SCALES = kKeys4 * D / 16;
+    static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = KS + SCALES, BYTES = VS + SCALES;
+    static constexpr int N = D == 128 ? 2 : 4;               // of them per warp
+    static constexpr int AT_ONCE = D == 128 ? 32 : 64;       // keys whose scores a warp holds together
+};
 constexpr uint32_t kPolls4 = 1u << 20;  // a copy that has not arrived by then never will
 constexpr float kMostP4 = 65000.0f;     // bound of a row's weights in a tile (f16 ends at 65504)
-template <int D>
-constexpr int kTileKeys4 = 2 * kCodes4 / D;
-
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -78,7 +81,7 @@ __device__ __forceinline__ int key_at(int i) { return (i & 8) + (i & 1 ? 4 + (((
 //        g + 8 of MMA j; C: those channels of query rows 2 t, 2 t + 1.
 template <int D, int NT>
 struct Tile4 {
-    static constexpr int KS = D / 16, MO = D / 16, U = kTileKeys4<D> / 16, ROW = D / 2, SROW = D / 16;
+    static constexpr int KS = D / 16, MO = D / 16, U = Stage4<D>::AT_ONCE / 16, ROW = D / 2, SROW = D / 16;
     uint32_t q[NT][KS][2];
     float o[NT][MO][4];
     float m[NT][2], l[NT][2];                // rows 2 t, 2 t + 1: reference (log2), sum of P of this lane's keys
@@ -121,15 +124,16 @@ struct Tile4 {
         return true;
     }
 
-    // A tile of keys from shared memory, the first of them `key0`.  zf: logit factor per
-    // row.  If masked, a row sees the keys [seen.x, seen.y] of the first `stored` of the
-    // tile in the 16-key groups of `there`; else all of them.
-    __device__ __forceinline__ void keys(uint32_t kb, const float (&zf)[NT][2], bool masked, int key0, int stored, uint32_t there,
-                                         const int2 *seen) {
+    // Keys [first, first + 16 U) of a tile in shared memory, whose own first is `key0`.  zf:
+    // logit factor per row.  If masked, a row sees the keys [seen.x, seen.y] of the first
+    // `stored` of the tile in its 16-key groups of `there`; else all of them.
+    __device__ __forceinline__ void keys(uint32_t kb, int first, const float (&zf)[NT][2], bool masked, int key0, int stored,
+                                         uint32_t there, const int2 *seen) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         constexpr uint32_t ALL = 0xFFFFFFFFu;
         const float NEG_INF = __int_as_float(0xff800000);
-        const uint32_t vb = kb + kCodes4, ksb = kb + 2 * kCodes4, vsb = ksb + kScales4;
+        const uint32_t vb = kb + Stage4<D>::V + first * ROW, ksb = kb + Stage4<D>::KS + first * SROW, vsb = kb + Stage4<D>::VS + first * SROW;
+        kb += first * ROW, key0 += first, stored -= first, there >>= first / 16;
         const int kg = key_at(g);
         float s[NT][U][4];
 #pragma unroll
@@ -258,37 +262,39 @@ struct Tile4 {
 
 template <int D>
 constexpr int split4_smem() {
-    constexpr int ring = kWarps4 * kStages4 * kStage4, merge = kWarps4 * 8 * (D + 4) * 4;
+    constexpr int ring = kWarps4 * Stage4<D>::N * Stage4<D>::BYTES, merge = kWarps4 * 8 * (D + 4) * 4;
     return ring > merge ? ring : merge;
 }
 
 template <int D, int NT, bool HALF>
 __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kernel(PagedAttnArgs a) {
-    constexpr int R = 8 * NT, K = kTileKeys4<D>, ROW = D / 2, SROW = D / 16;
+    using St = Stage4<D>;
+    constexpr int R = 8 * NT, K = kKeys4, ROW = D / 2, SROW = D / 16, N = St::N;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_st[kWarps4][8][2];
     __shared__ int2 s_seen[kWarps4][R];
-    __shared__ uint32_t s_info[kWarps4][kStages4];
-    __shared__ __align__(8) uint64_t s_bar[kWarps4][kStages4];
+    __shared__ uint32_t s_info[kWarps4][N];
+    __shared__ __align__(8) uint64_t s_bar[kWarps4][N];
     __shared__ int64_t s_sum[kWarps4], s_found[2];
     __shared__ int s_dead;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
     // A copy takes the tile's rows of one block: GR rows, GU copies (of codes and of scales) to a tile.
-    const int GR = min(a.S, K), GU = K / GR;
-    if (lane < kStages4) tc::mbar_init(tc::smem_u32(&s_bar[warp][lane]), GU);
+    const int lgGU = a.S >= K ? 0 : (a.S == 32 ? 1 : 2), GU = 1 << lgGU, GR = K >> lgGU;
+    static_assert(K == 64, "copies to a tile: 1, 2 or 4, as blocks are 64 and more, 32 or 16 tokens");
+    if (lane < N) tc::mbar_init(tc::smem_u32(&s_bar[warp][lane]), GU);
     if (tid == 0) s_dead = 0;
     tc::mbar_init_fence();
     pdl_wait();
     pdl_launch_dependents();
-    using Work = SplitWork<R, K>;
+    using Work = SplitWork<R, K, kCost4>;
     const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kWarps4, s_sum, s_found);
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
     if (tid == 0) a.join[blockIdx.x].last = -1;
-    const uint32_t ring = tc::smem_u32(smem) + warp * (kStages4 * kStage4), bar0 = tc::smem_u32(&s_bar[warp][0]);
-    uint32_t n_issued = 0, n_read = 0;       // this warp's tiles so far
+    const uint32_t ring = tc::smem_u32(smem) + warp * (N * St::BYTES), bar0 = tc::smem_u32(&s_bar[warp][0]);
+    uint32_t to_fill = 0, to_read = 0, phase = 0;    // this warp's next stages, the latter's parity
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
         const Request rq = request_of(a, b);
@@ -299,20 +305,20 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
             const Place pl = Work::place(a, rq, at - base);
             const int64_t unit = at - pl.tile;       // its first place
             at = min(stop, unit + pl.tiles);
-            const int h = pl.h, r0 = pl.r0, ta = max(0, pl.tile - kSplitCost), tb = (int)(at - unit) - kSplitCost;
+            const int h = pl.h, r0 = pl.r0, ta = max(0, pl.tile - kCost4), tb = (int)(at - unit) - kCost4;
             if (tb <= 0) continue;
             const bool first_part = ta == 0, whole = first_part && at == unit + pl.tiles;
             if (tid == 0 && first_part && !whole)
                 a.join[blockIdx.x] = {rq.row0, h, r0, rows, (int)((unit + pl.tiles - 1) / plan.share), {0, 0}};
 
             // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / GU, copy lane % GU) of BT of them
-            const int BT = 32 / GU;
+            const int BT = 32 >> lgGU, my_tile = lane >> lgGU, my_copy = lane & (GU - 1);
             const int todo = min(tb, Work::real_tiles(a, rq)) - ta;
             const int count = todo > warp ? (todo - warp + kWarps4 - 1) / kWarps4 : 0;
             const int32_t *table = a.table + b * a.table_stride;
-            auto key_of = [&](int i) { return key0 + (ta + warp + (i + lane / GU) * kWarps4) * K + GR * (lane % GU); };
+            auto key_of = [&](int i) { return key0 + (ta + warp + (i + my_tile) * kWarps4) * K + GR * my_copy; };
             // rows that end before every row's window are not read: their blocks may be another request's by now
-            auto asked = [&](int i) { return i + lane / GU < count && key_of(i) < rq.kv && key_of(i) + GR > low; };
+            auto asked = [&](int i) { return i + my_tile < count && key_of(i) < rq.kv && key_of(i) + GR > low; };
             auto entry = [&](int i) -> int32_t { return asked(i) ? table[key_of(i) / a.S] : -1; };
             int32_t block = entry(0), block_next = entry(BT);
             // Q travels beside the chain of loads to the first codes: for a B operand row g,
@@ -339,30 +345,28 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
             locate(0);
             auto issue = [&](int i) {                // start the copies of this warp's tile i
                 if (i >= count || s_dead) return;
-                if (i && i % BT == 0) {
+                const int in = i & (BT - 1);         // its place in the batch
+                if (i && in == 0) {
                     block = block_next;
                     block_next = entry(i + BT);
                     locate(i);
                 }
-                const int who = GU * (i % BT), stage = n_issued++ % kStages4;
-                const uint32_t dst = ring + stage * kStage4, bar = bar0 + 8 * stage;
-                const uint32_t mine = (1u << GU) - 1;
-                if (lane - who >= 0 && lane - who < GU) {
-                    const int u = lane - who;
-                    if (u == 0) s_info[warp][stage] = ((have >> who) & mine) | (((whole_rows >> who) & mine) << 8);
+                if (my_tile == in) {
+                    const uint32_t dst = ring + to_fill * St::BYTES, bar = bar0 + 8 * to_fill, mine = (1u << GU) - 1;
+                    if (my_copy == 0) s_info[warp][to_fill] = ((have >> lane) & mine) | (((whole_rows >> lane) & mine) << 8);
                     arrive_expect(bar, off < 0 ? 0 : 2 * GR * (ROW + SROW));
                     if (off >= 0) {
-                        const uint32_t to = dst + u * GR * ROW, tos = dst + 2 * kCodes4 + u * GR * SROW;
-                        bulk_load(to, a.k_codes + off * ROW, GR * ROW, bar);
-                        bulk_load(tos, a.k_scale4 + off * SROW, GR * SROW, bar);
-                        bulk_load(to + kCodes4, a.v_codes + off * ROW, GR * ROW, bar);
-                        bulk_load(tos + kScales4, a.v_scale4 + off * SROW, GR * SROW, bar);
+                        const uint32_t to = dst + my_copy * GR * ROW, tos = dst + my_copy * GR * SROW;
+                        bulk_load(to + St::K, a.k_codes + off * ROW, GR * ROW, bar);
+                        bulk_load(tos + St::KS, a.k_scale4 + off * SROW, GR * SROW, bar);
+                        bulk_load(to + St::V, a.v_codes + off * ROW, GR * ROW, bar);
+                        bulk_load(tos + St::VS, a.v_scale4 + off * SROW, GR * SROW, bar);
                     }
                 }
-                __syncwarp();
+                if (++to_fill == N) to_fill = 0;
             };
 #pragma unroll 1
-            for (int i = 0; i < kStages4 - 1; ++i) issue(i);
+            for (int i = 0; i < N - 1; ++i) issue(i);
 
             Tile4<D, NT> tile;
             tile.clear();
@@ -409,10 +413,10 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
             }
             __syncwarp();
             for (int i = 0; i < count; ++i) {
-                issue(i + kStages4 - 1);
-                const int stage = n_read % kStages4;
-                const bool ok = tc::mbar_wait(bar0 + 8 * stage, (n_read / kStages4) & 1, s_dead ? 1024 : kPolls4);
-                ++n_read;
+                issue(i + N - 1);
+                const uint32_t stage = to_read;
+                const bool ok = tc::mbar_wait(bar0 + 8 * stage, phase, s_dead ? 1024 : kPolls4);
+                if (++to_read == N) to_read = 0, phase ^= 1;
                 if (!__all_sync(ALL, ok)) {
                     s_dead = 1;                      // no more copies; those that travel are waited for once more each
                     continue;
@@ -424,7 +428,9 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
                 if (masked)
                     for (int u = 0; u < GU; ++u)
                         if ((info >> u) & 1) there |= ((1u << (GR / 16)) - 1) << (u * (GR / 16));
-                tile.keys(ring + stage * kStage4, zf, masked, key, rq.kv - key, there, s_seen[warp]);
+#pragma unroll 1
+                for (int first = 0; first < K; first += St::AT_ONCE)
+                    tile.keys(ring + stage * St::BYTES, first, zf, masked, key, rq.kv - key, there, s_seen[warp]);
                 __syncwarp();
             }
 
