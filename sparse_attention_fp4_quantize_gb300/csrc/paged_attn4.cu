@@ -11,7 +11,6 @@
 // stay below f16's end.
 #include "fp4.cuh"
 #include "paged_attn.cuh"
-#include "tc.cuh"
 
 namespace csa2 {
 namespace {
@@ -27,7 +26,6 @@ struct Stage4 {                         // a tile in shared memory: codes and sc
     static constexpr int N = D == 128 ? 2 : 4;               // of them per warp
     static constexpr int AT_ONCE = D == 128 ? 32 : 64;       // keys whose scores a warp holds together
 };
-constexpr uint32_t kPolls4 = 1u << 20;  // a copy that has not arrived by then never will
 constexpr float kMostP4 = 65000.0f;     // bound of a row's weights in a tile (f16 ends at 65504)
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
@@ -49,16 +47,6 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
-// One bulk copy, global -> shared, counted on an mbarrier (16-byte boundaries and size).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
 // 8 x 8 halves, transposed across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
@@ -66,10 +54,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return r;
 }
 
-// Row i of S^T, which is place i of P V's contraction, is key key_of(i) of its 16: so a
-// lane's four keys of V lie in rows of either parity, and a warp's loads meet a bank
-// twice where the plain order would four times (a row is 64 bytes).
-__device__ __forceinline__ int key_at(int i) { return (i & 8) + (i & 1 ? 4 + (((i & 7) >> 1) ^ 1) : (i & 7) >> 1); }
+// Row i of S^T, which is place i of P V's contraction, is key key_at(i) of its 16: the
+// four keys that the lanes of a quarter read together lie next to one another, so that
+// with the staged chunks' order (chunk4_at) every load of codes meets a bank once.
+__device__ __forceinline__ int key_at(int i) { return (i & 8) + (i & 1 ? 7 - ((i & 7) >> 1) : (i & 7) >> 1); }
+
+// Byte offset of 16-byte chunk c of row r of codes in a staged tile.
+template <int D>
+__device__ __forceinline__ uint32_t chunk4_at(int r, int c) { return D == 128 ? r * 64 + ((c ^ (r & 2)) << 4) : r * 32 + (c << 4); }
 
 // A warp's share of the softmax over keys for 8 NT rows, transposed as in paged_attn.cu:
 // keys and channels on the 16 rows of an MMA, query rows on its 8 columns.  Lane
@@ -144,7 +136,7 @@ struct Tile4 {
             for (int h = 0; h < 2; ++h) {
                 const int row = 16 * u + 8 * h + kg;
                 if constexpr (D == 128) {
-                    const uint4 v = lds128(kb + row * ROW + 16 * t);
+                    const uint4 v = lds128(kb + chunk4_at<D>(row, t));
                     c[h][0] = v.x, c[h][1] = v.y, c[h][2] = v.z, c[h][3] = v.w;
                     const uint32_t two = e4m3x2_to_f16x2(lds16(ksb + row * SROW + 2 * t));
                     sc[h][0] = sc[h][1] = __byte_perm(two, 0, 0x1010);
@@ -228,9 +220,9 @@ struct Tile4 {
             uint32_t v[4][W], sc[4];                 // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the contraction
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = 16 * u + 8 * (i >> 1) + (i & 1 ? 4 + (t ^ 1) : t);
+                const int row = 16 * u + 8 * (i >> 1) + (i & 1 ? 7 - t : t);
                 if constexpr (D == 128) {
-                    const uint2 x = lds64(vb + row * ROW + 8 * g);
+                    const uint2 x = lds64(vb + chunk4_at<D>(row, g >> 1) + 8 * (g & 1));
                     v[i][0] = x.x, v[i][1] = x.y;
                     sc[i] = lds8(vsb + row * SROW + g);
                 } else {
@@ -275,17 +267,12 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
     __shared__ float s_st[kWarps4][8][2];
     __shared__ int2 s_seen[kWarps4][R];
     __shared__ uint32_t s_info[kWarps4][N];
-    __shared__ __align__(8) uint64_t s_bar[kWarps4][N];
     __shared__ int64_t s_sum[kWarps4], s_found[2];
-    __shared__ int s_dead;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
-    // A copy takes the tile's rows of one block: GR rows, GU copies (of codes and of scales) to a tile.
-    const int lgGU = a.S >= K ? 0 : (a.S == 32 ? 1 : 2), GU = 1 << lgGU, GR = K >> lgGU;
-    static_assert(K == 64, "copies to a tile: 1, 2 or 4, as blocks are 64 and more, 32 or 16 tokens");
-    if (lane < N) tc::mbar_init(tc::smem_u32(&s_bar[warp][lane]), GU);
-    if (tid == 0) s_dead = 0;
-    tc::mbar_init_fence();
+    // A tile's rows of one block are a piece: GR rows, GU pieces to a tile.
+    const int lgGU = a.S >= K ? 0 : (a.S == 32 ? 1 : 2), lgGR = 6 - lgGU, GU = 1 << lgGU, GR = 1 << lgGR;
+    static_assert(K == 64, "pieces of a tile: 1, 2 or 4, as blocks are 64 and more, 32 or 16 tokens");
     pdl_wait();
     pdl_launch_dependents();
     using Work = SplitWork<R, K, kCost4>;
@@ -293,8 +280,11 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
     if (tid == 0) a.join[blockIdx.x].last = -1;
-    const uint32_t ring = tc::smem_u32(smem) + warp * (N * St::BYTES), bar0 = tc::smem_u32(&s_bar[warp][0]);
-    uint32_t to_fill = 0, to_read = 0, phase = 0;    // this warp's next stages, the latter's parity
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (N * St::BYTES);
+    // this lane's chunk of a copy by the warp, 512 bytes: 8 or 16 rows
+    constexpr int CPR = D / 32, RPC = 32 / CPR;
+    const uint32_t lane_to = chunk4_at<D>(lane / CPR, lane % CPR);
+    static_assert(RPC % 4 == 0 && RPC <= 16, "the order of a row's chunks goes by its number modulo 4");
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
         const Request rq = request_of(a, b);
@@ -311,12 +301,12 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
             if (tid == 0 && first_part && !whole)
                 a.join[blockIdx.x] = {rq.row0, h, r0, rows, (int)((unit + pl.tiles - 1) / plan.share), {0, 0}};
 
-            // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / GU, copy lane % GU) of BT of them
-            const int BT = 32 >> lgGU, my_tile = lane >> lgGU, my_copy = lane & (GU - 1);
+            // this warp's tiles are ta + warp + 4 i; lane holds (tile lane / GU, piece lane % GU) of BT of them
+            const int BT = 32 >> lgGU, my_tile = lane >> lgGU, my_piece = lane & (GU - 1);
             const int todo = min(tb, Work::real_tiles(a, rq)) - ta;
             const int count = todo > warp ? (todo - warp + kWarps4 - 1) / kWarps4 : 0;
             const int32_t *table = a.table + b * a.table_stride;
-            auto key_of = [&](int i) { return key0 + (ta + warp + (i + my_tile) * kWarps4) * K + GR * my_copy; };
+            auto key_of = [&](int i) { return key0 + (ta + warp + (i + my_tile) * kWarps4) * K + GR * my_piece; };
             // rows that end before every row's window are not read: their blocks may be another request's by now
             auto asked = [&](int i) { return i + my_tile < count && key_of(i) < rq.kv && key_of(i) + GR > low; };
             auto entry = [&](int i) -> int32_t { return asked(i) ? table[key_of(i) / a.S] : -1; };
@@ -333,8 +323,8 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) qv[x][c] = real ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0, 0, 0, 0);
             }
-            int64_t off = -1;                        // first row of this lane's copy among the cache's, -1: not there
-            uint32_t have = 0, whole_rows = 0;       // lanes whose copy is there; whose rows all are keys
+            int64_t off = -1;                        // first row of this lane's piece among the cache's, -1: not there
+            uint32_t have = 0, whole_rows = 0;       // lanes whose piece is there; whose rows all are keys
             auto locate = [&](int i) {
                 const bool ok = asked(i) && block >= 0 && block < a.n_blocks;
                 if (asked(i) && !ok) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
@@ -343,27 +333,50 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
                 whole_rows = __ballot_sync(ALL, ok && key_of(i) + GR <= rq.kv);
             };
             locate(0);
+            uint32_t fill = 0, take = 0;             // next stages
             auto issue = [&](int i) {                // start the copies of this warp's tile i
-                if (i >= count || s_dead) return;
-                const int in = i & (BT - 1);         // its place in the batch
-                if (i && in == 0) {
-                    block = block_next;
-                    block_next = entry(i + BT);
-                    locate(i);
-                }
-                if (my_tile == in) {
-                    const uint32_t dst = ring + to_fill * St::BYTES, bar = bar0 + 8 * to_fill, mine = (1u << GU) - 1;
-                    if (my_copy == 0) s_info[warp][to_fill] = ((have >> lane) & mine) | (((whole_rows >> lane) & mine) << 8);
-                    arrive_expect(bar, off < 0 ? 0 : 2 * GR * (ROW + SROW));
-                    if (off >= 0) {
-                        const uint32_t to = dst + my_copy * GR * ROW, tos = dst + my_copy * GR * SROW;
-                        bulk_load(to + St::K, a.k_codes + off * ROW, GR * ROW, bar);
-                        bulk_load(tos + St::KS, a.k_scale4 + off * SROW, GR * SROW, bar);
-                        bulk_load(to + St::V, a.v_codes + off * ROW, GR * ROW, bar);
-                        bulk_load(tos + St::VS, a.v_scale4 + off * SROW, GR * SROW, bar);
+                if (i < count) {
+                    const int in = i & (BT - 1), who = in << lgGU;               // its place in the batch, its first lane
+                    if (i && in == 0) {
+                        block = block_next;
+                        block_next = entry(i + BT);
+                        locate(i);
                     }
+                    const uint32_t dst = ring + fill * St::BYTES, mine = (1u << GU) - 1;
+                    if (lane == 0) s_info[warp][fill] = ((have >> who) & mine) | (((whole_rows >> who) & mine) << 8);
+                    if (lgGU == 0) {                 // all rows from one place
+                        const int64_t row = __shfl_sync(ALL, off, who);
+                        if (row >= 0) {
+                            const uint8_t *kc = a.k_codes + row * ROW + 16 * lane, *vc = a.v_codes + row * ROW + 16 * lane;
+#pragma unroll
+                            for (int x = 0; x < K / RPC; ++x) {
+                                cp_async16(dst + St::K + lane_to + 512 * x, kc + 512 * x, 16);
+                                cp_async16(dst + St::V + lane_to + 512 * x, vc + 512 * x, 16);
+                            }
+                            const uint8_t *sc = (D == 64 && lane >= 16 ? a.v_scale4 : a.k_scale4) + row * SROW + 16 * (D == 64 ? lane & 15 : lane);
+                            cp_async16(dst + St::KS + 16 * lane, sc, 16);        // of 64 channels both planes' at once
+                            if (D == 128) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + row * SROW + 16 * lane, 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < K / RPC; ++x) {
+                            const int64_t row = __shfl_sync(ALL, off, who + ((x * RPC + lane / CPR) >> lgGR));
+                            if (row >= 0) {
+                                const int64_t at = row * ROW + ((x * RPC + lane / CPR) & (GR - 1)) * ROW + 16 * (lane % CPR);
+                                cp_async16(dst + St::K + lane_to + 512 * x, a.k_codes + at, 16);
+                                cp_async16(dst + St::V + lane_to + 512 * x, a.v_codes + at, 16);
+                            }
+                        }
+                        const int r = (D == 64 ? lane & 15 : lane) * (16 / SROW);       // first row of this lane's scales
+                        const int64_t row = __shfl_sync(ALL, off, who + (r >> lgGR)), at = (row + (r & (GR - 1))) * SROW;
+                        if (row >= 0) {
+                            cp_async16(dst + St::KS + 16 * lane, (D == 64 && lane >= 16 ? a.v_scale4 : a.k_scale4) + at, 16);
+                            if (D == 128) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + at, 16);
+                        }
+                    }
+                    if (++fill == N) fill = 0;
                 }
-                if (++to_fill == N) to_fill = 0;
+                cp_async_commit();
             };
 #pragma unroll 1
             for (int i = 0; i < N - 1; ++i) issue(i);
@@ -414,13 +427,10 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
             __syncwarp();
             for (int i = 0; i < count; ++i) {
                 issue(i + N - 1);
-                const uint32_t stage = to_read;
-                const bool ok = tc::mbar_wait(bar0 + 8 * stage, phase, s_dead ? 1024 : kPolls4);
-                if (++to_read == N) to_read = 0, phase ^= 1;
-                if (!__all_sync(ALL, ok)) {
-                    s_dead = 1;                      // no more copies; those that travel are waited for once more each
-                    continue;
-                }
+                cp_async_wait<N - 1>();
+                __syncwarp();
+                const uint32_t stage = take;
+                if (++take == N) take = 0;
                 const int key = key0 + (ta + warp + i * kWarps4) * K;
                 const uint32_t info = s_info[warp][stage], full = (1u << GU) - 1;
                 const bool masked = !__all_sync(ALL, key >= all_lo && key + K <= all_hi && (info >> 8) == full);
@@ -433,6 +443,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
                     tile.keys(ring + stage * St::BYTES, first, zf, masked, key, rq.kv - key, there, s_seen[warp]);
                 __syncwarp();
             }
+            cp_async_wait<0>();
 
             // the warps' shares meet in shared memory, 8 rows at a time
             float *s_o = reinterpret_cast<float *>(smem);
@@ -487,13 +498,10 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
                     }
                 }
             }
-            tc::fence_async_smem();                  // what was written here lies before the next copies
             __syncthreads();
         }
         base = end;
     }
-    __syncthreads();
-    if (tid == 0 && s_dead) flag_error(a.err_flag, CSA2_FLAG_TIMEOUT);
 }
 
 template <int D, int NT, bool HALF>
