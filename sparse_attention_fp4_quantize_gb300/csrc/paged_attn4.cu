@@ -17,11 +17,11 @@ namespace {
 
 constexpr int kWarps4 = kSplitWarps;
 constexpr int kPerSm4 = 3;              // CTAs that an SM holds at once
-constexpr int kKeys4 = 64;              // keys of a warp's tile
 constexpr int kCost4 = 8;               // tiles that a unit's fixed cost counts as
 template <int D>
 struct Stage4 {                         // a tile in shared memory: codes and scales of its keys and of its values
-    static constexpr int CODES = kKeys4 * D / 2, SCALES = kKeys4 * D / 16;
+    static constexpr int KEYS = 64;                          // of a warp's tile
+    static constexpr int CODES = KEYS * D / 2, SCALES = KEYS * D / 16;
     static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = KS + SCALES, BYTES = VS + SCALES;
     static constexpr int N = D == 128 ? 2 : 4;               // of them per warp
     static constexpr int AT_ONCE = D == 128 ? 32 : 64;       // keys whose scores a warp holds together
@@ -261,7 +261,7 @@ constexpr int split4_smem() {
 template <int D, int NT, bool HALF>
 __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kernel(PagedAttnArgs a) {
     using St = Stage4<D>;
-    constexpr int R = 8 * NT, K = kKeys4, ROW = D / 2, SROW = D / 16, N = St::N;
+    constexpr int R = 8 * NT, K = St::KEYS, ROW = D / 2, SROW = D / 16, N = St::N;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_st[kWarps4][8][2];
@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
     // A tile's rows of one block are a piece: GR rows, GU pieces to a tile.
-    const int lgGU = a.S >= K ? 0 : (a.S == 32 ? 1 : 2), lgGR = 6 - lgGU, GU = 1 << lgGU, GR = 1 << lgGR;
-    static_assert(K == 64, "pieces of a tile: 1, 2 or 4, as blocks are 64 and more, 32 or 16 tokens");
+    const int lgGR = min(a.S, K) == 16 ? 4 : (min(a.S, K) == 32 ? 5 : 6), lgGU = (K == 64 ? 6 : 5) - lgGR, GU = 1 << lgGU, GR = 1 << lgGR;
+    static_assert(K == 64 || K == 32, "pieces of a tile: blocks are 16, 32, 64 or 128 tokens");
     pdl_wait();
     pdl_launch_dependents();
     using Work = SplitWork<R, K, kCost4>;
@@ -284,6 +284,8 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
     // this lane's chunk of a copy by the warp, 512 bytes: 8 or 16 rows
     constexpr int CPR = D / 32, RPC = 32 / CPR;
     const uint32_t lane_to = chunk4_at<D>(lane / CPR, lane % CPR);
+    constexpr bool BOTH = St::SCALES == 256;         // one copy takes the keys' and the values' scales
+    static_assert(BOTH || St::SCALES == 512, "a lane's chunk of each plane's scales, or of one's");
     static_assert(RPC % 4 == 0 && RPC <= 16, "the order of a row's chunks goes by its number modulo 4");
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
@@ -353,9 +355,9 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
                                 cp_async16(dst + St::K + lane_to + 512 * x, kc + 512 * x, 16);
                                 cp_async16(dst + St::V + lane_to + 512 * x, vc + 512 * x, 16);
                             }
-                            const uint8_t *sc = (D == 64 && lane >= 16 ? a.v_scale4 : a.k_scale4) + row * SROW + 16 * (D == 64 ? lane & 15 : lane);
-                            cp_async16(dst + St::KS + 16 * lane, sc, 16);        // of 64 channels both planes' at once
-                            if (D == 128) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + row * SROW + 16 * lane, 16);
+                            const uint8_t *sc = (BOTH && lane >= 16 ? a.v_scale4 : a.k_scale4) + row * SROW + 16 * (BOTH ? lane & 15 : lane);
+                            cp_async16(dst + St::KS + 16 * lane, sc, 16);
+                            if (!BOTH) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + row * SROW + 16 * lane, 16);
                         }
                     } else {
 #pragma unroll
@@ -367,11 +369,11 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
                                 cp_async16(dst + St::V + lane_to + 512 * x, a.v_codes + at, 16);
                             }
                         }
-                        const int r = (D == 64 ? lane & 15 : lane) * (16 / SROW);       // first row of this lane's scales
+                        const int r = (BOTH ? lane & 15 : lane) * (16 / SROW);          // first row of this lane's scales
                         const int64_t row = __shfl_sync(ALL, off, who + (r >> lgGR)), at = (row + (r & (GR - 1))) * SROW;
                         if (row >= 0) {
-                            cp_async16(dst + St::KS + 16 * lane, (D == 64 && lane >= 16 ? a.v_scale4 : a.k_scale4) + at, 16);
-                            if (D == 128) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + at, 16);
+                            cp_async16(dst + St::KS + 16 * lane, (BOTH && lane >= 16 ? a.v_scale4 : a.k_scale4) + at, 16);
+                            if (!BOTH) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + at, 16);
                         }
                     }
                     if (++fill == N) fill = 0;

@@ -18,7 +18,7 @@
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 
 struct Rope4 {
     const int32_t *pos;
@@ -35,7 +35,8 @@ struct Quant4Args {
     uint16_t *values[2];             // what the codes stand for [T, H, D], or NULL
     const int64_t *slots;
     int64_t T, n_slots;
-    int H, S, shift, per, chunks;    // heads per thread, threads' shares of a token's heads
+    int H, S, shift, per;
+    uint32_t chunks;                 // heads per thread, threads' shares of a token's heads
     Rope4 rope;
     uint32_t *err_flag;
 };
@@ -54,6 +55,26 @@ __device__ __forceinline__ uint32_t to_e4m3(float v) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
     return r & 0xFFu;
+}
+
+// The keys' or the values' member of a pair among a kernel's arguments.  A select: an index
+// would have every thread copy the arguments to local memory first (65536 tokens read back, 8
+// heads of 128: 79 us).
+template <typename X>
+__device__ __forceinline__ X of(const X (&pair)[2], bool is_v) { return is_v ? pair[1] : pair[0]; }
+
+// The values of eight codes, of either 16-bit type.
+template <bool HALF>
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t scale2) {
+    uint32_t r[4];
+    e2m1x8_to_f16(codes, scale2, r);
+    if (!HALF)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 z = unpack16<true>(r[k]);
+            r[k] = pack16<false>(z.x, z.y);
+        }
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // The rotation of 8 channels of a key: their cosines and sines, and the channels that
@@ -83,120 +104,170 @@ __device__ __forceinline__ void turn8(uint4 &x, const uint4 &y, const Turn &t, b
     }
 }
 
+// 16 values w of row (t, h), a group g of its channels: their codes, scale and, if asked
+// for, the values that these stand for.
 template <bool HALF>
-__global__ void __launch_bounds__(kThreads) quantize_fp4_paged_kernel(Quant4Args a) {
+__device__ __forceinline__ void store_group(const Quant4Args &a, bool is_v, int D, int64_t t, int h, int64_t row, int g, uint32_t (&w)[8]) {
     constexpr uint32_t INF = HALF ? 0x7C00u : 0x7F80u, ABS2 = 0x7FFF7FFFu;
+    uint32_t m2 = 0;                 // largest sign-less patterns of the even and odd channels
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & ABS2);
+    uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+    if (top >= INF) {                // infinities and NaN do not count: the one becomes the largest value, the other 0
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t both = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t u = (w[i] >> (16 * k)) & 0xFFFFu;
+                const uint32_t mag = u & 0x7FFFu;
+                if (mag < INF) top = max(top, mag);
+                else u = mag > INF ? 0u : u - 1;
+                both |= u << (16 * k);
+            }
+            w[i] = both;
+        }
+        flag_error(a.err_flag, CSA2_FLAG_NONFINITE);
+    }
+    const uint32_t s8 = to_e4m3(round16(unpack16<HALF>(top).x * (1.0f / 6.0f)));
+    const uint32_t s2 = e4m3x2_to_f16x2(s8 | s8 << 8);
+    const float inv = s8 ? rcp_of(__half2float(__ushort_as_half((unsigned short)(s2 & 0xFFFFu)))) : 0.0f;
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 z = unpack16<HALF>(w[4 * i + k]);
+            f[2 * k] = round16(z.x * inv), f[2 * k + 1] = round16(z.y * inv);
+        }
+        c[i] = to_e2m1x8(f);
+    }
+    *reinterpret_cast<uint2 *>(of(a.codes, is_v) + row * (D / 2) + 8 * g) = make_uint2(c[0], c[1]);
+    of(a.scales, is_v)[row * (D / 16) + g] = (uint8_t)s8;
+    if (of(a.values, is_v)) {
+        uint4 *dst = reinterpret_cast<uint4 *>(of(a.values, is_v) + (t * a.H + h) * D + 16 * g);
+        dst[0] = values8<HALF>(c[0], s2);
+        dst[1] = values8<HALF>(c[1], s2);
+    }
+}
+
+// Where a token's row goes: false, and a flag if that is an error, if it is not stored.
+__device__ __forceinline__ bool place_of(const Quant4Args &a, int64_t t, bool first_thread, int64_t &row0, int64_t &p) {
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.n_slots) {
+        if (slot != -1 && first_thread) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
+        return false;
+    }
+    if (a.rope.table) {              // a token without a position is not stored
+        p = a.rope.pos[t];
+        if (p < 0 || p >= a.rope.n_pos) {
+            if (first_thread) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+            return false;
+        }
+    }
+    row0 = (slot >> a.shift) * a.H * a.S + (slot & (a.S - 1));       // of head 0; the others S rows apart
+    return true;
+}
+
+// Any rotation: a thread takes one group of a row and reads its partners beside it.
+template <bool HALF>
+__global__ void __launch_bounds__(kThreads) quantize_fp4_paged_any_kernel(Quant4Args a) {
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const int g = threadIdx.x, D = blockDim.x * 16;
-    const int chunk = blockIdx.y % a.chunks;
-    const bool is_v = blockIdx.y >= a.chunks, first_thread = g == 0 && blockIdx.y == 0;
-    const int64_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.n_slots) {
-        if (slot != -1 && first_thread) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
-        return;
-    }
+    const bool is_v = blockIdx.y >= a.chunks;
+    const int chunk = is_v ? blockIdx.y - a.chunks : blockIdx.y;
+    int64_t row0, p;
+    if (!place_of(a, t, g == 0 && blockIdx.y == 0, row0, p)) return;
     Turn turn[2];
     turn[0].on = turn[1].on = false;
-    if (a.rope.table) {              // a token without a position is not stored
-        const int64_t p = a.rope.pos[t];
-        if (p < 0 || p >= a.rope.n_pos) {
-            if (first_thread) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
-            return;
-        }
-        if (!is_v) {
-            const float *row = a.rope.table + 2 * p * a.rope.pairs;
+    if (!is_v) {
+        const float *row = a.rope.table + 2 * p * a.rope.pairs;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = 16 * g + 8 * i - a.rope.first;         // of the rotated channels
-                Turn &u = turn[i];
-                if (c < 0 || c >= 2 * a.rope.pairs) continue;
-                u.on = true;
-                u.low = c < a.rope.pairs;
-                u.partner = u.low ? a.rope.pairs : -a.rope.pairs;
-                const float4 *src = reinterpret_cast<const float4 *>(row + (a.rope.split ? 2 * (u.low ? c : c - a.rope.pairs) : c));
+        for (int i = 0; i < 2; ++i) {
+            const int c = 16 * g + 8 * i - a.rope.first;             // of the rotated channels
+            Turn &u = turn[i];
+            if (c < 0 || c >= 2 * a.rope.pairs) continue;
+            u.on = true;
+            u.low = c < a.rope.pairs;
+            u.partner = u.low ? a.rope.pairs : -a.rope.pairs;
+            const float4 *src = reinterpret_cast<const float4 *>(row + (a.rope.split ? 2 * (u.low ? c : c - a.rope.pairs) : c));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= 2 && !a.rope.split) continue;
-                    const float4 v = src[k];
-                    u.cs[2 * k] = make_float2(v.x, v.y), u.cs[2 * k + 1] = make_float2(v.z, v.w);
-                }
+            for (int k = 0; k < 4; ++k) {
+                if (k >= 2 && !a.rope.split) continue;
+                const float4 v = src[k];
+                u.cs[2 * k] = make_float2(v.x, v.y), u.cs[2 * k + 1] = make_float2(v.z, v.w);
             }
         }
     }
-    const int64_t hs = a.head_stride[is_v];
-    const uint16_t *x = a.x[is_v] + t * a.token_stride[is_v] + 16 * g;
-    const int64_t block = slot >> a.shift;
-    const int64_t row0 = block * a.H * a.S + (slot & (a.S - 1));     // of head 0; the others S rows apart
+    const int64_t hs = of(a.head_stride, is_v);
+    const uint16_t *x = of(a.x, is_v) + t * of(a.token_stride, is_v) + 16 * g;
     const int h0 = chunk * a.per, h1 = min(a.H, h0 + a.per);
     for (int h = h0; h < h1; ++h) {
-        uint4 v[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<const uint4 *>(x + h * hs + 8 * i);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (turn[i].on) {
-                uint4 y = v[i];
-                if (a.rope.split) y = *reinterpret_cast<const uint4 *>(x + h * hs + 8 * i + turn[i].partner);
-                turn8<HALF>(v[i], y, turn[i], a.rope.split);
-            }
-        uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-        uint32_t m2 = 0;             // largest sign-less patterns of the even and odd channels
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & ABS2);
-        uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
-        const bool bad = top >= INF;
-        if (bad) {                   // infinities and NaN do not count: the one becomes the largest value, the other 0
-            top = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t both = 0;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t u = (w[i] >> (16 * k)) & 0xFFFFu;
-                    const uint32_t mag = u & 0x7FFFu;
-                    if (mag < INF) top = max(top, mag);
-                    else u = mag > INF ? 0u : u - 1;
-                    both |= u << (16 * k);
-                }
-                w[i] = both;
-            }
-            flag_error(a.err_flag, CSA2_FLAG_NONFINITE);
-        }
-        const uint32_t s8 = to_e4m3(round16(unpack16<HALF>(top).x * (1.0f / 6.0f)));
-        const uint32_t s2 = e4m3x2_to_f16x2(s8 | s8 << 8);
-        const float inv = s8 ? rcp_of(__half2float(__ushort_as_half((unsigned short)(s2 & 0xFFFFu)))) : 0.0f;
-        uint32_t c[2];
+        uint4 v[2], y[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float f[8];
+            y[i] = v[i] = *reinterpret_cast<const uint4 *>(x + h * hs + 8 * i);
+            if (turn[i].on && a.rope.split) y[i] = *reinterpret_cast<const uint4 *>(x + h * hs + 8 * i + turn[i].partner);
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 z = unpack16<HALF>(w[4 * i + k]);
-                f[2 * k] = round16(z.x * inv), f[2 * k + 1] = round16(z.y * inv);
+        for (int i = 0; i < 2; ++i)
+            if (turn[i].on) turn8<HALF>(v[i], y[i], turn[i], a.rope.split);
+        uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        store_group<HALF>(a, is_v, D, t, h, row0 + (int64_t)h * a.S, g, w);
+    }
+}
+
+// No rotation, or one of halves over the whole head: a thread takes a group and the one
+// half a row behind it, which are each other's partners.
+template <bool HALF>
+__global__ void __launch_bounds__(kThreads) quantize_fp4_paged_kernel(Quant4Args a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= a.T) return;
+    const int g = threadIdx.x, far = blockDim.x, D = far * 32;
+    const bool is_v = blockIdx.y >= a.chunks, turns = a.rope.table && !is_v;
+    const int chunk = is_v ? blockIdx.y - a.chunks : blockIdx.y;
+    int64_t row0, p;
+    if (!place_of(a, t, g == 0 && blockIdx.y == 0, row0, p)) return;
+    float2 cs[16];
+    if (turns) {
+        const float4 *src = reinterpret_cast<const float4 *>(a.rope.table + p * D + 32 * g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 v = src[k];
+            cs[2 * k] = make_float2(v.x, v.y), cs[2 * k + 1] = make_float2(v.z, v.w);
+        }
+    }
+    const int64_t hs = of(a.head_stride, is_v);
+    const uint16_t *x = of(a.x, is_v) + t * of(a.token_stride, is_v) + 16 * g;
+    const int h0 = chunk * a.per, h1 = min(a.H, h0 + a.per);
+    uint4 next[4];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const uint4 *>(x + h * hs + (i >> 1) * (D / 2) + (i & 1) * 8);
+    };
+    load(h0);
+    for (int h = h0; h < h1; ++h) {
+        uint32_t w[2][8] = {{next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w},
+                            {next[2].x, next[2].y, next[2].z, next[2].w, next[3].x, next[3].y, next[3].z, next[3].w}};
+        if (h + 1 < h1) load(h + 1);
+        if (turns) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 u = unpack16<HALF>(w[0][i]), v = unpack16<HALF>(w[1][i]);
+                const float2 r0 = rotate(u.x, v.x, cs[2 * i].x, cs[2 * i].y), r1 = rotate(u.y, v.y, cs[2 * i + 1].x, cs[2 * i + 1].y);
+                w[0][i] = pack16<HALF>(r0.x, r1.x), w[1][i] = pack16<HALF>(r0.y, r1.y);
             }
-            c[i] = to_e2m1x8(f);
         }
         const int64_t row = row0 + (int64_t)h * a.S;
-        *reinterpret_cast<uint2 *>(a.codes[is_v] + row * (D / 2) + 8 * g) = make_uint2(c[0], c[1]);
-        a.scales[is_v][row * (D / 16) + g] = (uint8_t)s8;
-        if (a.values[is_v]) {
-            uint4 *dst = reinterpret_cast<uint4 *>(a.values[is_v] + (t * a.H + h) * D + 16 * g);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t r[4];
-                e2m1x8_to_f16(c[i], s2, r);
-                if (!HALF)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 z = unpack16<true>(r[k]);
-                        r[k] = pack16<false>(z.x, z.y);
-                    }
-                dst[i] = make_uint4(r[0], r[1], r[2], r[3]);
-            }
-        }
+        store_group<HALF>(a, is_v, D, t, h, row, g, w[0]);
+        store_group<HALF>(a, is_v, D, t, h, row, g + far, w[1]);
     }
 }
 
@@ -206,42 +277,47 @@ struct Read4Args {
     int64_t token_stride[2], head_stride[2];
     const int64_t *slots;
     int64_t T, n_slots;
-    int H, S, shift, per, chunks;
+    int H, S, shift;
     uint32_t *err_flag;
 };
 
-template <bool HALF>
-__global__ void __launch_bounds__(kThreads) dequantize_fp4_paged_kernel(Read4Args a) {
+// A thread writes 16 bytes of every head of a token, so that a warp's store fills whole sectors
+// and the row's place is worked out once.  65536 tokens, 8 heads of 128, to bf16 (344 MB): 55 us,
+// 6.3 TB/s of a copy's 6.8; 57.4 with the loads of four heads on their way together in place
+// of eight, 60 with the heads dealt out to two threads, 67 with a thread per row.
+constexpr int kReadThreads = 64, kReadBatch = 8;         // heads whose loads are on their way together
+
+template <int D, bool HALF>
+__global__ void __launch_bounds__(kReadThreads) dequantize_fp4_paged_kernel(Read4Args a) {
+    constexpr int TOKENS = kReadThreads / (D / 8);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool is_v = blockIdx.x & 1;                    // side by side, as the two read the same slots
+    const int64_t t = (int64_t)(blockIdx.x >> 1) * TOKENS + threadIdx.x / (D / 8);
     if (t >= a.T) return;
-    const int g = threadIdx.x, D = blockDim.x * 16;
-    const int chunk = blockIdx.y % a.chunks;
-    const bool is_v = blockIdx.y >= a.chunks;
+    const int c = threadIdx.x % (D / 8);                 // 8 channels
     const int64_t slot = a.slots[t];
     if (slot < 0 || slot >= a.n_slots) {
-        if (slot != -1 && g == 0 && blockIdx.y == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
+        if (slot != -1 && !is_v && c == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
         return;
     }
-    const int64_t row0 = (slot >> a.shift) * a.H * a.S + (slot & (a.S - 1));
-    uint16_t *x = a.x[is_v] + t * a.token_stride[is_v] + 16 * g;
-    const int h0 = chunk * a.per, h1 = min(a.H, h0 + a.per);
-    for (int h = h0; h < h1; ++h) {
-        const int64_t row = row0 + (int64_t)h * a.S;
-        const uint2 c = *reinterpret_cast<const uint2 *>(a.codes[is_v] + row * (D / 2) + 8 * g);
-        const uint32_t s8 = a.scales[is_v][row * (D / 16) + g], s2 = e4m3x2_to_f16x2(s8 | s8 << 8);
+    const int64_t row = (slot >> a.shift) * a.H * a.S + (slot & (a.S - 1)), hs = of(a.head_stride, is_v);    // of head 0; the others S rows apart
+    const uint8_t *codes = of(a.codes, is_v) + row * (D / 2) + 4 * c, *scales = of(a.scales, is_v) + row * (D / 16) + (c >> 1);
+    uint16_t *x = of(a.x, is_v) + t * of(a.token_stride, is_v) + 8 * c;
+    for (int h = 0; h < a.H; h += kReadBatch) {
+        uint32_t w[kReadBatch], s8[kReadBatch];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t r[4];
-            e2m1x8_to_f16(i ? c.y : c.x, s2, r);
-            if (!HALF)
+        for (int k = 0; k < kReadBatch; ++k) {
+            if (h + k < a.H) {
+                w[k] = *reinterpret_cast<const uint32_t *>(codes);
+                s8[k] = *scales;
+            }
+            codes += (int64_t)a.S * (D / 2), scales += (int64_t)a.S * (D / 16);
+        }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 z = unpack16<true>(r[k]);
-                    r[k] = pack16<false>(z.x, z.y);
-                }
-            *reinterpret_cast<uint4 *>(x + h * a.head_stride[is_v] + 8 * i) = make_uint4(r[0], r[1], r[2], r[3]);
+        for (int k = 0; k < kReadBatch; ++k) {
+            if (h + k < a.H) *reinterpret_cast<uint4 *>(x) = values8<HALF>(w[k], e4m3x2_to_f16x2(s8[k] | s8[k] << 8));
+            x += hs;
         }
     }
 }
@@ -252,8 +328,8 @@ struct Shape4 {
     dim3 grid, block;
     int per, chunks;
 };
-Shape4 shape_of(int64_t T, int H, int D) {
-    const int groups = D / 16, rows = kThreads / groups;
+Shape4 shape_of(int64_t T, int H, int groups) {
+    const int rows = kThreads / groups;
     const int64_t blocks = (T + rows - 1) / rows;
     int per = 1;
     while (per < 8 && per < H && blocks * 2 * ((H + 2 * per - 1) / (2 * per)) >= (int64_t)num_sms() * 8) per *= 2;
@@ -325,7 +401,8 @@ extern "C" csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, 
         CSA2_REQUIRE(!over, "quantize_fp4_paged: values overlap another argument");
     }
     CSA2_REQUIRE(!k_values || !v_values || !meet(k_values, dense, v_values, dense), "quantize_fp4_paged: k_values and v_values overlap");
-    const Shape4 sh = shape_of(T, Hkv, D);
+    const bool any = cos_sin && (layout != CSA2_ROPE_HALF || rope_dim != D);
+    const Shape4 sh = shape_of(T, Hkv, any ? D / 16 : D / 32);
     Quant4Args a = {};
     a.x[0] = (const uint16_t *)k, a.x[1] = (const uint16_t *)v;
     a.token_stride[0] = k_token_stride, a.token_stride[1] = v_token_stride;
@@ -336,9 +413,10 @@ extern "C" csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, 
     a.shift = S == 16 ? 4 : (S == 32 ? 5 : (S == 64 ? 6 : 7));
     a.per = sh.per, a.chunks = sh.chunks;
     a.rope = {pos, cos_sin, n_pos, rope_dim / 2, first, layout == CSA2_ROPE_HALF};
-    CSA2_CUDA_CALL(launch_pdl(dt == CSA2_FP16 ? quantize_fp4_paged_kernel<true> : quantize_fp4_paged_kernel<false>, sh.grid,
-                              sh.block, 0, stream_of(stream), a),
-                   "quantize_fp4_paged_kernel launch");
+    const bool half = dt == CSA2_FP16;
+    void (*kern)(Quant4Args) = any ? (half ? quantize_fp4_paged_any_kernel<true> : quantize_fp4_paged_any_kernel<false>)
+                                   : (half ? quantize_fp4_paged_kernel<true> : quantize_fp4_paged_kernel<false>);
+    CSA2_CUDA_CALL(launch_pdl(kern, sh.grid, sh.block, 0, stream_of(stream), a), "quantize_fp4_paged_kernel launch");
     CSA2_LAUNCH_CHECK("quantize_fp4_paged_kernel");
     return CSA2_OK;
 }
@@ -364,7 +442,8 @@ extern "C" csa2_status csa2_dequantize_kv_fp4_paged(const int64_t *slots, int64_
         CSA2_REQUIRE(!over, "dequantize_fp4_paged: an output overlaps another argument");
     }
     CSA2_REQUIRE(!share(out[0], out[1]), "dequantize_fp4_paged: k and v share elements");
-    const Shape4 sh = shape_of(T, Hkv, D);
+    const int tokens = kReadThreads / (D / 8);
+    const int64_t blocks = (T + tokens - 1) / tokens * 2;           // T <= 2^30, tokens >= 4
     Read4Args a = {};
     a.codes[0] = k_codes, a.codes[1] = v_codes, a.scales[0] = k_scales, a.scales[1] = v_scales;
     a.x[0] = (uint16_t *)k, a.x[1] = (uint16_t *)v;
@@ -372,9 +451,10 @@ extern "C" csa2_status csa2_dequantize_kv_fp4_paged(const int64_t *slots, int64_
     a.head_stride[0] = k_head_stride, a.head_stride[1] = v_head_stride;
     a.slots = slots, a.T = T, a.n_slots = n_blocks * S, a.H = Hkv, a.S = S, a.err_flag = err_flag;
     a.shift = S == 16 ? 4 : (S == 32 ? 5 : (S == 64 ? 6 : 7));
-    a.per = sh.per, a.chunks = sh.chunks;
-    CSA2_CUDA_CALL(launch_pdl(dt == CSA2_FP16 ? dequantize_fp4_paged_kernel<true> : dequantize_fp4_paged_kernel<false>, sh.grid,
-                              sh.block, 0, stream_of(stream), a),
+    const bool half = dt == CSA2_FP16;
+    void (*kern)(Read4Args) = D == 64 ? (half ? dequantize_fp4_paged_kernel<64, true> : dequantize_fp4_paged_kernel<64, false>)
+                                      : (half ? dequantize_fp4_paged_kernel<128, true> : dequantize_fp4_paged_kernel<128, false>);
+    CSA2_CUDA_CALL(launch_pdl(kern, dim3((unsigned)blocks), dim3(kReadThreads), 0, stream_of(stream), a),
                    "dequantize_fp4_paged_kernel launch");
     CSA2_LAUNCH_CHECK("dequantize_fp4_paged_kernel");
     return CSA2_OK;

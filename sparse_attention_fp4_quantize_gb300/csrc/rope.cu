@@ -9,7 +9,9 @@ namespace {
 // positions it is many turns, of which only the fraction counts: f_i becomes a
 // fraction of a turn in 64-bit fixed point once per thread, and its product with p
 // wraps at whole turns by itself, with an error below p 2^-65 turns.  What is left of
-// the nearest quarter turn goes to sinpi / cospi in fp32 with all its leading bits.
+// the nearest quarter turn becomes an fp32 angle of at most pi / 4 with all its leading
+// bits, and the Taylor series around 0 end with its 9th and 10th power (the next terms
+// are 2^-28 and 2^-31 of the results).
 constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;   // 1 / (2 pi) in two parts
 constexpr double kMostFreq = 1048576.0;      // radians per position
 
@@ -21,7 +23,21 @@ struct TableArgs {
     float amplitude;
 };
 
-__global__ void __launch_bounds__(1024) rope_table_kernel(TableArgs a) {
+// Cosine and sine of phase 2^-64 turns.
+__device__ __forceinline__ float2 cos_sin_of(uint64_t phase) {
+    const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
+    const int64_t rest = (int64_t)(phase << 2) >> 2;             // of the nearest quarter: its two leading bits are the sign's now
+    constexpr float UNIT = 3.14159265358979f * 0x1p-31f;         // radians of 2^-32 turns
+    const float x = fmaf((float)(int32_t)(rest >> 32), UNIT, (float)(uint32_t)rest * (UNIT * 0x1p-32f)), y = x * x;
+    float s = fmaf(y, fmaf(y, fmaf(y, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6);
+    float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f);
+    s = fmaf(x * y, s, x);
+    c = fmaf(y, c, 1.0f);
+    const float u = quarter & 1 ? s : c, v = quarter & 1 ? c : s;
+    return make_float2((quarter + 1) & 2 ? -u : u, quarter & 2 ? -v : v);
+}
+
+__global__ void __launch_bounds__(512) rope_table_kernel(TableArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int i = threadIdx.x;
@@ -30,24 +46,21 @@ __global__ void __launch_bounds__(1024) rope_table_kernel(TableArgs a) {
     const double t = f * kTurn, low = fma(f, kTurn, -t) + f * kTurnLow, r = t - rint(t);
     const double hi = rint(r * 0x1p32);
     const uint64_t step = fine ? ((uint64_t)(int64_t)hi << 32) + (uint64_t)llrint((fma(hi, -0x1p-32, r) + low) * 0x1p64) : 0;
-    const bool slow = fabs(f) < 0x1p-30;     // fixed point would cost it leading bits; its angles fit fp64
     const float amp = fine ? a.amplitude : __int_as_float(0x7FC00000);
-    for (int64_t n = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; n < a.n_pos; n += (int64_t)gridDim.x * blockDim.y) {
-        const int64_t p = a.start + n;
-        float s, c;
-        if (slow) {
-            const double x = 2.0 * (t * (double)p);
-            s = (float)sinpi(x), c = (float)cospi(x);
-        } else {
-            const uint64_t phase = step * (uint64_t)p, quarter = (phase + (1ull << 61)) >> 62;
-            const float x = (float)(int64_t)(phase - (quarter << 62)) * 0x1p-63f;
-            float s0, c0;
-            sincospif(x, &s0, &c0);
-            s = quarter & 1 ? c0 : s0, c = quarter & 1 ? s0 : c0;
-            if (quarter & 2) s = -s;
-            if ((quarter + 1) & 2) c = -c;
+    const int64_t n0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, ahead = (int64_t)gridDim.x * blockDim.y;
+    float2 *out = a.table + n0 * a.half + i;
+    if (fabs(f) < 0x1p-30) {                 // fixed point would cost it leading bits; its angles fit fp64
+        for (int64_t n = n0; n < a.n_pos; n += ahead, out += ahead * a.half) {
+            const double x = 2.0 * (t * (double)(a.start + n));
+            *out = make_float2(amp * (float)cospi(x), amp * (float)sinpi(x));
         }
-        a.table[n * a.half + i] = make_float2(amp * c, amp * s);
+        return;
+    }
+    uint64_t phase = step * (uint64_t)(a.start + n0);
+    const uint64_t phases = step * (uint64_t)ahead;
+    for (int64_t n = n0; n < a.n_pos; n += ahead, out += ahead * a.half, phase += phases) {
+        const float2 v = cos_sin_of(phase);
+        *out = make_float2(amp * v.x, amp * v.y);
     }
 }
 
@@ -62,21 +75,24 @@ struct RotateArgs {
     const int32_t *pos;
     const float *table;
     int pairs, first, turned;                // rotated pairs and first rotated channel of a head; units that rotate
+    uint32_t shares;                         // threads' shares of a token's heads
     uint32_t *err_flag;
 };
 
-constexpr int kBatch = 4;                    // heads whose loads are in flight together
+constexpr int kBatch = 2;                    // heads whose loads are in flight together
 
 template <bool HALF, bool SPLIT>
-__global__ void __launch_bounds__(256) rope_kernel(RotateArgs a) {
+__global__ void __launch_bounds__(128) rope_kernel(RotateArgs a) {
     constexpr int P = SPLIT ? 8 : 4;         // pairs of a thread
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    // the blocks that share the heads of some tokens stand side by side
+    const uint32_t tokens = blockIdx.x / a.shares, share = blockIdx.x - tokens * a.shares;
+    const int64_t t = (int64_t)tokens * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const int64_t p = a.pos[t];
     if (p < 0 || p >= a.n_pos) {             // -1: a row without a token
-        if (p != -1 && threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
+        if (p != -1 && threadIdx.x == 0 && share == 0) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
         return;
     }
     const int u = threadIdx.x, H = a.heads[0] + a.heads[1];
@@ -95,8 +111,8 @@ __global__ void __launch_bounds__(256) rope_kernel(RotateArgs a) {
         if (c0 >= a.first) c0 += 2 * a.pairs;
         c1 = c0;
     }
-    const int end = min(H, (int)(blockIdx.y + 1) * a.per);
-    for (int h0 = blockIdx.y * a.per; h0 < end; h0 += kBatch) {
+    const int end = min(H, (int)(share + 1) * a.per);
+    for (int h0 = share * a.per; h0 < end; h0 += kBatch) {
         uint4 x[kBatch], y[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -183,7 +199,7 @@ extern "C" csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_t
                  "rope: pos and flag must be 4-byte aligned, cos_sin 16-byte");
     RotateArgs a = {{(const uint16_t *)q, (const uint16_t *)k}, {(uint16_t *)q_out, (uint16_t *)k_out},
                     {q_token_stride, k_token_stride}, {q_head_stride, k_head_stride}, {qo_token_stride, ko_token_stride},
-                    {qo_head_stride, ko_head_stride}, {Hq, Hk}, 1, T, n_pos, pos, cos_sin, rope_dim / 2, first, 0, err_flag};
+                    {qo_head_stride, ko_head_stride}, {Hq, Hk}, 1, T, n_pos, pos, cos_sin, rope_dim / 2, first, 0, 1, err_flag};
     bool in_place = true;
     Rows in[2] = {}, out[2] = {};
     for (int i = 0; i < 2; ++i) {
@@ -207,18 +223,19 @@ extern "C" csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_t
     const int vectors = D / 8, turned = layout == CSA2_ROPE_HALF ? rope_dim / 16 : rope_dim / 8;
     const int units = in_place ? turned : turned + vectors - rope_dim / 8;
     a.turned = turned;
-    const int rows = 256 / units, H = Hq + Hk;
+    const int rows = 128 / units, H = Hq + Hk;
     const int64_t blocks = (T + rows - 1) / rows;
     // Cosines and sines are loaded once for all heads of a thread, as many as leave work for every SM.
     int per = kBatch;
-    while (per < H && blocks * ((H + 2 * per - 1) / (2 * per)) >= (int64_t)num_sms() * 8) per *= 2;
+    while (per < H && blocks * ((H + 2 * per - 1) / (2 * per)) >= (int64_t)num_sms() * 32) per *= 2;
     if (blocks * ((H + per - 1) / per) < (int64_t)num_sms() * 4) per = 1;
     a.per = per;
-    const dim3 grid((unsigned)blocks, (H + per - 1) / per);
+    a.shares = (H + per - 1) / per;
+    CSA2_REQUIRE(blocks * a.shares < (1ll << 31), "rope: T * (Hq + Hk) = %lld rows", (long long)(T * H));
     const bool half_type = dt == CSA2_FP16;
     void (*kern)(RotateArgs) = layout == CSA2_ROPE_HALF ? (half_type ? rope_kernel<true, true> : rope_kernel<false, true>)
                                                         : (half_type ? rope_kernel<true, false> : rope_kernel<false, false>);
-    CSA2_CUDA_CALL(launch_pdl(kern, grid, dim3(units, rows), 0, stream_of(stream), a), "rope_kernel launch");
+    CSA2_CUDA_CALL(launch_pdl(kern, dim3((unsigned)(blocks * a.shares)), dim3(units, rows), 0, stream_of(stream), a), "rope_kernel launch");
     CSA2_LAUNCH_CHECK("rope_kernel");
     return CSA2_OK;
 }
