@@ -89,21 +89,9 @@ struct Lay {
     static constexpr int BARS = 29;
     static constexpr uint32_t USED = OFF_BAR + BARS * 8 + 12;
     static constexpr uint32_t SMEM = USED + 128 > 120 * 1024 ? USED + 128 : 120 * 1024;   // one CTA per SM (TMEM)
-    static constexpr uint32_t COL_S = 0, COL_O = 256;    // TMEM columns: S0, S1 (P over them), O0, O1
+    static constexpr uint32_t COL_S = 0, COL_O = 256, COL_Q = COL_O + 2 * D;   // TMEM columns: S0, S1 (P over them), O0, O1, and Q0, Q1 where there is room
+    static constexpr bool TMEM_Q = COL_Q + D <= 512;
 };
-
-// Copy of N (4 or 8) bytes, or N zeros.
-template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t smem, const void *gmem, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem), "l"(gmem), "n"(N), "r"(there ? N : 0) : "memory");
-}
-
-// Byte offset of 16-byte chunk c of row r in a staged tile of the 4-bit cache's rows,
-// swizzled so that 8 rows' loads of one chunk meet every bank once.
-template <int D>
-__device__ __forceinline__ uint32_t chunk4_at(int r, int c) {
-    return D == 128 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
-}
 
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
     uint64_t d;
@@ -227,11 +215,12 @@ struct Walk {
 template <int D, bool HALF, bool FP4>
 __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnArgs a) {
     using L = Lay<D>;
+    constexpr bool TMEM_Q = FP4 && L::TMEM_Q;            // S reads Q from tensor memory, which halves what it asks of shared memory
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((128u - (tc::smem_u32(smem_raw) & 127u)) & 127u);
     __shared__ int64_t s_sum[kTcThreads / 32], s_found[2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(ALL, tid >> 5, 0), lane = tid & 31;
     const uint32_t sb = tc::smem_u32(smem);
     TileMeta *metas = reinterpret_cast<TileMeta *>(smem + L::OFF_META);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_BAR + L::BARS * 8);
@@ -278,13 +267,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(ALL, *tmem_slot, 0);
     pdl_wait();
     pdl_launch_dependents();
     const Plan plan = plan_of<TcWork>(a, blockIdx.x, gridDim.x, 1, s_sum, s_found);
     bool run = true;
     uint32_t n_seg = 0;
-    // The next segment: of a whole warp, or of its one working thread.  False: none, or given up.
+    // The next segment, of a whole warp.  False: none, or given up.
     auto next_seg = [&](Segment &s) -> bool {
         const uint32_t i = n_seg % kSegs, par = (n_seg / kSegs) & 1;
         ++n_seg;
@@ -292,15 +281,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         s = segs[i];
         __syncwarp();
         if (lane == 0) arrive(segempty(i));
-        return s.rows > 0;
-    };
-    auto next_seg_one = [&](Segment &s) -> bool {
-        const uint32_t i = n_seg % kSegs, par = (n_seg / kSegs) & 1;
-        ++n_seg;
-        if (!wait_one(segfull(i), par, abort_word, kSegPolls)) return false;
-        s = segs[i];
-        arrive(segempty(i));
-        return s.rows > 0;
+        return __shfl_sync(ALL, s.rows, 0) > 0;
     };
 
     if (warp >= kMmaWarp) {
@@ -333,7 +314,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                 arrive(segfull(i));
             }
         }
-        if (lane == 0 && sub < 2) {
+        if (sub < 2) {
             constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, kTcKeys, false, false);
             constexpr uint32_t idesc_o = tc::idesc_f16_f32(128, D, false, true);
             const uint64_t dq = tc::desc_noswizzle(sb + L::OFF_Q + sub * L::Q, 128, L::GROUP);
@@ -343,8 +324,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             uint32_t nk = 0, nq = 0, np = 0;             // key tiles, segments with this sub-tile, its P tiles so far
             auto lock = [&]() -> bool {
                 for (uint32_t i = 0; i < kLockPolls; ++i) {
-                    if (atomicCAS(tensor_lock, 0u, 1u) == 0u) return true;
-                    if (*abort_word) break;
+                    uint32_t got = 0;
+                    if (lane == 0) got = atomicCAS(tensor_lock, 0u, 1u) == 0u;
+                    if (__any_sync(ALL, got)) return true;
+                    if (__any_sync(ALL, *abort_word)) break;
                 }
                 *abort_word = 1;
                 return false;
@@ -352,42 +335,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             auto unlock = [&]() { *reinterpret_cast<volatile unsigned int *>(tensor_lock) = 0u; };
             auto issue_s = [&](uint32_t tile) {
                 const uint32_t q = (uint32_t)dq, k = (uint32_t)dk + (tile & 1) * (L::KV / 16);
+                if (tc::elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    if (ks == D / 32) unlock();
-                    tc::mma_f16_lo(ts, q + ks * 16, k + ks * 16, (uint32_t)(dk >> 32), idesc_s, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        if (ks == D / 32) unlock();
+                        if constexpr (TMEM_Q) tc::mma_f16_ta_lo(ts, tmem + L::COL_Q + sub * (D / 2) + ks * 8, k + ks * 16, (uint32_t)(dk >> 32), idesc_s, ks > 0);
+                        else tc::mma_f16_lo(ts, q + ks * 16, k + ks * 16, (uint32_t)(dk >> 32), idesc_s, ks > 0);
+                    }
+                    tc::commit(sfull(sub));
+                    tc::commit(kempty(tile & 1));
                 }
-                tc::commit(sfull(sub));
-                tc::commit(kempty(tile & 1));
             };
             auto issue_o = [&](uint32_t tile, bool first) {
                 const uint32_t v = (uint32_t)dv + (tile & 1) * (L::KV / 16);
+                if (tc::elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                    tc::mma_f16_ta_lo(to, ts + ks * 8, v + ks * (L::GROUP / 8), (uint32_t)(dv >> 32), idesc_o, !first || ks > 0);
-                tc::commit(ofull(sub));
-                tc::commit(vempty(tile & 1));
+                    for (int ks = 0; ks < kTcKeys / 16; ++ks)
+                        tc::mma_f16_ta_lo(to, ts + ks * 8, v + ks * (L::GROUP / 8), (uint32_t)(dv >> 32), idesc_o, !first || ks > 0);
+                    tc::commit(ofull(sub));
+                    tc::commit(vempty(tile & 1));
+                }
             };
-            auto wait_k = [&](uint32_t tile) { return wait_one(kfull(tile & 1), (tile >> 1) & 1, abort_word); };
-            auto wait_v = [&](uint32_t tile) { return wait_one(vfull(tile & 1), (tile >> 1) & 1, abort_word); };
-            auto wait_q = [&]() { return wait_one(qfull(sub), nq++ & 1, abort_word); };
-            auto wait_p = [&]() { return wait_one(pfull(sub), np++ & 1, abort_word); };
+            auto wait_k = [&](uint32_t tile) { return wait_bar(kfull(tile & 1), (tile >> 1) & 1, abort_word); };
+            auto wait_v = [&](uint32_t tile) { return wait_bar(vfull(tile & 1), (tile >> 1) & 1, abort_word); };
+            auto wait_q = [&]() { return wait_bar(qfull(sub), nq++ & 1, abort_word); };
+            auto wait_p = [&]() { return wait_bar(pfull(sub), np++ & 1, abort_word); };
             // a segment without this sub-tile: its buffers count as read once they are filled
             auto pass_k = [&](uint32_t tile) -> bool {
                 if (!wait_k(tile)) return false;
-                arrive(kempty(tile & 1));
+                if (lane == 0) arrive(kempty(tile & 1));
                 return true;
             };
             auto pass_v = [&](uint32_t tile) -> bool {
                 if (!wait_v(tile)) return false;
-                arrive(vempty(tile & 1));
+                if (lane == 0) arrive(vempty(tile & 1));
                 return true;
             };
             Segment seg;
-            bool more = next_seg_one(seg);
+            bool more = next_seg(seg);
             while (run && more) {
-                const int n = seg.tb - seg.pl.tile;
-                const bool takes = sub == 0 || seg.rows - seg.pl.r0 > 128;
+                const int n = __shfl_sync(ALL, seg.tb - seg.pl.tile, 0);
+                const bool takes = __shfl_sync(ALL, sub == 0 || seg.rows - seg.pl.r0 > 128, 0);
                 // S of the first key tile (P V of the segment before is on its way)
                 if (takes) {
                     run = wait_q() && wait_k(nk) && lock();
@@ -414,14 +402,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     if (!run) break;
                     tc::fence_after();
                     issue_o(nk, n == 1);
-                    unlock();
+                    __syncwarp();
+                    if (lane == 0) unlock();
                 } else if (!(run = pass_v(nk))) {
                     break;
                 }
                 ++nk;
-                more = next_seg_one(seg);
+                more = next_seg(seg);
             }
-            tc::commit(drain);                           // products still in flight end before the tensor memory is given back
+            if (tc::elect_one()) tc::commit(drain);                           // products still in flight end before the tensor memory is given back
         }
         __syncwarp();
     } else if (warp >= kSoftWarps) {
@@ -476,23 +465,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         // (registers would do, but the softmax has them): whole rows per copy, chunks
         // swizzled, so that copies touch full lines and the reads below every bank.
         const uint32_t stage_k = sb + L::OFF_STAGE + cw * 32 * D, stage_v = stage_k + L::KV / 2;
-        auto fetch = [&](uint32_t stage, const uint8_t *codes, const uint8_t *scales) {
-            if constexpr (FP4) {
-                if (have) {
-                    constexpr int CPR = D / 32, RPI = 32 / CPR, SB = D / 16; // chunks per row, rows per copy, bytes of a row's scales
-                    const int c = lane % CPR, r0 = lane / CPR;
+        // Half as many bytes, the 4-bit cache's codes stay in registers: the products are
+        // near what shared memory can feed them, and staging would ask it for a tenth more.
+        // A lane holds, of every piece of 32 channels that it converts (row of 8, piece; of 64
+        // channels every other 8 rows), the codes and the two scales.
+        constexpr int PIECES = D / 32, STEP = 4 / PIECES, HELD = 4 / STEP;
+        struct Held {
+            uint4 c[HELD];
+            uint32_t sc[HELD];
+        } held_k, held_v;
+        const int piece = chunk % PIECES, g0 = chunk / PIECES;
+        auto hold = [&](Held &x, const uint8_t *codes, const uint8_t *scales) {
+            if (have) {
 #pragma unroll
-                    for (int i = 0; i < CPR; ++i) {
-                        const int r = i * RPI + r0, u = r >> 4;              // row, its 16-key group
-                        const bool there = (r & 15) < (u ? rows[1] : rows[0]);       // rows that are not there read as zero
-                        const int64_t at = (u ? off[1] : off[0]) + (r & 15);
-                        cp_async16(stage + chunk4_at<D>(r, c), there ? (const void *)(codes + at * (D / 2) + 16 * c) : a.q, there ? 16 : 0);
-                    }
-                    const bool there = (lane & 15) < (lane >> 4 ? rows[1] : rows[0]);
-                    const int64_t at = (lane >> 4 ? off[1] : off[0]) + (lane & 15);
-                    cp_async_small<SB>(stage + 16 * D + lane * SB, there ? (const void *)(scales + at * SB) : a.q, there);
+                for (int i = 0; i < HELD; ++i) {
+                    const int r = 8 * (i * STEP + g0) + row;                 // of the warp's 32
+                    const bool there = (r & 15) < (r >> 4 ? rows[1] : rows[0]);      // rows that are not there read as zero
+                    const int64_t at = (r >> 4 ? off[1] : off[0]) + (r & 15);
+                    x.c[i] = there ? *reinterpret_cast<const uint4 *>(codes + at * (D / 2) + 16 * piece) : make_uint4(0, 0, 0, 0);
+                    x.sc[i] = there ? *reinterpret_cast<const uint16_t *>(scales + at * (D / 16) + 2 * piece) : 0;
                 }
-            } else if (have) {
+            }
+        };
+        auto convert = [&](uint32_t dst, const Held &x) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                const uint32_t to = dst + (4 * cw + i * STEP + g0) * L::GROUP + 4 * piece * 128 + row * 16;
+                const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w}, sc = e4m3x2_to_f16x2(x.sc[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t h[4];
+                    e2m1x8_to_f16(w[k], __byte_perm(sc, 0, k < 2 ? 0x1010 : 0x3232), h);
+                    sts128(to + k * 128, h[0], h[1], h[2], h[3]);
+                }
+            }
+        };
+        auto fetch = [&](uint32_t stage, const uint8_t *codes) {
+            if (have) {
                 constexpr int CPR = D / 16, RPI = 32 / CPR;                  // chunks per row, rows per copy
                 const int c = lane % CPR, r0 = lane / CPR;
 #pragma unroll
@@ -507,47 +516,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         auto store = [&](uint32_t dst, uint32_t stage) {
             cp_async_wait<1>();                          // all but the newest of the copies
             __syncwarp();
-            if constexpr (FP4) {
-                // lane = (row of 8, piece of 32 channels, for 64 channels every other 8 rows)
-                constexpr int PIECES = D / 32, STEP = 4 / PIECES;
-                const int piece = chunk % PIECES, g0 = chunk / PIECES;
-                uint4 c[4 / STEP];
-                uint32_t sc[4 / STEP];
+            uint4 c[N];
 #pragma unroll
-                for (int i = 0; i < 4 / STEP; ++i) {
-                    const int r = 8 * (i * STEP + g0) + row;
-                    c[i] = lds128(stage + chunk4_at<D>(r, piece));
-                    uint16_t two;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(two) : "r"(stage + 16 * D + r * (D / 16) + 2 * piece));
-                    sc[i] = e4m3x2_to_f16x2(two);
-                }
+            for (int i = 0; i < N; ++i) c[i] = lds128(stage + chunk_at<D>(8 * (i / CH) + row, 4 * (i % CH) + chunk));
 #pragma unroll
-                for (int i = 0; i < 4 / STEP; ++i) {
-                    const uint32_t to = dst + (4 * cw + i * STEP + g0) * L::GROUP + 4 * piece * 128 + row * 16;
-                    const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t h[4];
-                        e2m1x8_to_f16(w[k], __byte_perm(sc[i], 0, k < 2 ? 0x1010 : 0x3232), h);
-                        sts128(to + k * 128, h[0], h[1], h[2], h[3]);
-                    }
-                }
-            } else {
-                uint4 c[N];
-    #pragma unroll
-                for (int i = 0; i < N; ++i) c[i] = lds128(stage + chunk_at<D>(8 * (i / CH) + row, 4 * (i % CH) + chunk));
-    #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int g = i / CH;
-                    const uint32_t to = dst + (4 * cw + g) * L::GROUP + (8 * (i % CH) + 2 * chunk) * 128 + row * 16;
-                    uint32_t h[8];
-                    e4m3x4_to_f16x2x2(c[i].x, h[0], h[1]);
-                    e4m3x4_to_f16x2x2(c[i].y, h[2], h[3]);
-                    e4m3x4_to_f16x2x2(c[i].z, h[4], h[5]);
-                    e4m3x4_to_f16x2x2(c[i].w, h[6], h[7]);
-                    sts128(to, h[0], h[1], h[2], h[3]);
-                    sts128(to + 128, h[4], h[5], h[6], h[7]);
-                }
+            for (int i = 0; i < N; ++i) {
+                const int g = i / CH;
+                const uint32_t to = dst + (4 * cw + g) * L::GROUP + (8 * (i % CH) + 2 * chunk) * 128 + row * 16;
+                uint32_t h[8];
+                e4m3x4_to_f16x2x2(c[i].x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(c[i].y, h[2], h[3]);
+                e4m3x4_to_f16x2x2(c[i].z, h[4], h[5]);
+                e4m3x4_to_f16x2x2(c[i].w, h[6], h[7]);
+                sts128(to, h[0], h[1], h[2], h[3]);
+                sts128(to + 128, h[4], h[5], h[6], h[7]);
             }
         };
         tile_ahead = ahead.pl.tile;
@@ -568,22 +550,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             if (have) offsets();
             if (loaded) {
                 if (!wait_bar(kempty(buf), par, abort_word)) break;
-                store(sb + L::OFF_K + buf * L::KV, stage_k);
+                if constexpr (FP4) convert(sb + L::OFF_K + buf * L::KV, held_k);
+                else store(sb + L::OFF_K + buf * L::KV, stage_k);
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive(kfull(buf));
             }
-            fetch(stage_k, a.k_codes, a.k_scale4);
+            if constexpr (FP4) hold(held_k, a.k_codes, a.k_scale4);
+            else fetch(stage_k, a.k_codes);
             if (loaded) {
                 if (!wait_bar(vempty(buf), par, abort_word)) break;
-                store(sb + L::OFF_V + buf * L::KV, stage_v);
+                if constexpr (FP4) convert(sb + L::OFF_V + buf * L::KV, held_v);
+                else store(sb + L::OFF_V + buf * L::KV, stage_v);
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive(vfull(buf));
                 ++nt;
             }
             loaded = have;
-            fetch(stage_v, a.v_codes, a.v_scale4);
+            if constexpr (FP4) hold(held_v, a.v_codes, a.v_scale4);
+            else fetch(stage_v, a.v_codes);
             if (have) {
                 if (++tile_ahead >= ahead.tb) {          // the tile after the one that travels
                     have = next_seg(ahead);
@@ -661,7 +647,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                     }
                 }
             }
-            tc::fence_async_smem();
+            if constexpr (TMEM_Q) {                      // this thread's row to its lane
+                __syncwarp();
+                const uint32_t src = sb + L::OFF_Q + sub * L::Q + (4 * (warp & 3) + c4) * L::GROUP + r8 * 16;
+#pragma unroll
+                for (int c = 0; c < D / 8; c += 4) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 v = lds128(src + (c + x) * 128);
+                        w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
+                    }
+                    tc::tmem_st16(tmem + lanes + L::COL_Q + sub * (D / 2) + 4 * c, w);
+                }
+                tc::tmem_st_wait();
+                tc::fence_before();
+            } else {
+                tc::fence_async_smem();
+            }
             __syncwarp();
             if (lane == 0) arrive(qfull(sub));
         };
