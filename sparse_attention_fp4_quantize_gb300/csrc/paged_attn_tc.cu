@@ -1,40 +1,45 @@
-// The tile kernel of csa2_paged_attn_fp8: prompts, and whatever else brings more
-// rows per KV head than the split kernel's row tiles hold.
+// The tile kernel of csa2_paged_attn_fp8 and csa2_paged_attn_fp4: prompts, and whatever else
+// brings more rows per KV head than the split kernels' row tiles hold.
 //
 // A unit is 256 rows of one (request, KV head), two sub-tiles of 128, against
 // tiles of 128 keys: 2 x 2 x 128 x 128 x D MACs per key tile on tcgen05 in f16
 // with fp32 accumulators in TMEM.  Per key tile and sub-tile
-//   S = Q . K^T      (M = 128 rows, N = 128 keys; Q and K tiles in shared memory)
+//   S = Q . K^T      (M = 128 rows, N = 128 keys; Q and K tiles in shared memory, Q of 64
+//                    channels over the 4-bit cache in TMEM)
 //   P = f16 of the softmax weights, written over S in TMEM
 //   O += P . V       (M = 128 rows, N = D; A = P from TMEM, V tile in shared memory)
-// The E4M3 codes become f16 once per CTA and key tile; both sub-tiles use them.
+// The codes become f16 once per CTA and key tile; both sub-tiles use them.
 // K is read K-major and V MN-major from the same core-matrix layout, so one
 // conversion serves both.  Roles (16 warps, registers shared out by warpgroup):
 //   warps 0-3, 4-7   softmax of sub-tile 0, 1: thread = row (TMEM lane), so the
 //                    row's maximum and sum need no exchange; also load Q and
 //                    store the output
-//   warps 8-11       bring codes (a key tile ahead, into a staging buffer of their
-//                    own: the registers for them are the softmax's), convert, store
+//   warps 8-11       bring codes (a key tile ahead; E4M3 into a staging buffer of their own,
+//                    as the registers for them are the softmax's), convert, store
 //   warps 12, 13     issue the MMAs of sub-tile 0, 1, taking turns
 //   warp 14          works out the CTA's segments, a few ahead of the others
 // While one sub-tile's softmax runs, the tensor cores have the other's products.
-// The running references M, Mv (paged_attn.cu) move only when a tile's scores
-// exceed them far enough to matter to f16, so most tiles need no maximum and O in
-// TMEM is rescaled rarely.
+// The running references M, Mv (paged_attn.cu; the 4-bit cache has no Mv) move only when a
+// tile's scores exceed them far enough to matter to f16, so most tiles need no maximum and O
+// in TMEM is rescaled rarely.
 //
-// Bound by the softmax and the hand-overs around it.  The products of a key tile
-// take 2048 cycles (64 per M 128 N 128 K 16), with their waits and the conversions
-// 2660 (measured without the softmax), all together about 3300: a sub-tile's softmax
-// (1000 cycles for 128 exponentials and what goes with them) and its products are one
-// chain, and the other sub-tile's products do not fill all of it.  3 prompts of up to
-// 4096 tokens on up to 8192, 32 heads of 128 over 8: 851 us in the mean of ten inputs
-// (678 to 1028: wide scores move the references more often), 0.99 to 1.13 PFLOP/s of the
-// visible pairs (cuBLAS bf16 1.92).  Tried and slower there, as first built (the
-// figures are of then): P handed over in two
-// halves of 64 keys (1035 against 923 us: the MMA threads' waits and locks cost more
-// than the overlap gives), codes kept in registers instead of staged (934 against
-// 906), whole warps in place of one thread to issue (979 against 905), the lock given
-// up before S (956 against 905), Q asked for ahead by warp 14 (921 against 905).
+// Bound by the chain softmax -> hand-over -> products -> hand-over of a sub-tile, which the
+// other sub-tile's fills only in part.  The products of a key tile take 2048 cycles (64 per
+// M 128 N 128 K 16); of the 3500 that it takes (clock64 in a copy), a sub-tile's softmax
+// 1340 (128 exponentials, at 4 cycles per warp, are 512), waking the issuing warp 110, the
+// lock 340 (an atomic behind the converters' stores), its 16 products 1050 to issue and
+// 450 more until S is seen.  Of 64 channels, with half the products: 1280, 110, 390, 520, 440.
+// 3 prompts of up to 4096 tokens on up to 8192, 32 heads of 128 over 8: 773 us over 8 bits,
+// 735 over 4, 64 channels over 4 bits 637.
+// The issuing warps run with all lanes and elect one for the products, so that descriptors
+// stay in uniform registers: as one thread's work each product waited for them to be moved
+// there, 94 cycles a product instead of 42 of 64 channels (845 against 783 us over 8 bits, 818
+// against 761 over 4; 730 against 654 of 64 channels).  Tried and slower: P handed over in
+// two halves of 64 keys (1035 against 923 us as first built), E4M3 codes kept in
+// registers instead of staged (934 against 906 then; over 4 bits the same), the lock given up
+// with half of S to go (750 against 741), before S (772 against 760) or left out (792
+// against 745), strict turns by mbarriers in its place (771 against 745), waits that poll
+// before they sleep (828 against 753 with 16 polls).
 #include "fp4.cuh"
 #include "paged_attn.cuh"
 #include "tc.cuh"
@@ -45,14 +50,19 @@ namespace {
 constexpr int kSoftWarps = 8, kConvWarps = 4, kMmaWarp = kSoftWarps + kConvWarps;
 constexpr int kTcThreads = 512;              // four warpgroups, as the register shares go by warpgroup
 // Registers per thread: 512 x 128 at launch; the softmax warpgroups, which hold
-// a row's 128 scores, take what the others give up.
-constexpr int kLaunchRegs = 128, kSoftRegs = 176, kConvRegs = 80, kMmaRegs = 80;
-static_assert(kLaunchRegs * kTcThreads == 65536, "the launch's registers are an SM's");
-static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs <= 4 * kLaunchRegs, "register shares exceed the launch's");
-static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs,
-              "setmaxnreg.inc may not ask for fewer than the launch's, .dec not for more (an illegal instruction)");
-static_assert(kSoftRegs % 8 == 0 && kConvRegs % 8 == 0 && kMmaRegs % 8 == 0 && kConvRegs >= 24 && kMmaRegs >= 24 && kSoftRegs <= 256,
-              "setmaxnreg takes multiples of 8 from 24 to 256");
+// a row's 128 scores, take what the others give up (over the 8-bit cache the converters give up
+// less: with 72 its softmax spills).
+constexpr int kLaunchRegs = 128;
+template <bool FP4>
+struct Regs {
+    static constexpr int SOFT = FP4 ? 184 : 176, CONV = FP4 ? 72 : 80, MMA = CONV;
+    static_assert(kLaunchRegs * kTcThreads == 65536, "the launch's registers are an SM's");
+    static_assert(2 * SOFT + CONV + MMA <= 4 * kLaunchRegs, "register shares exceed the launch's");
+    static_assert(SOFT >= kLaunchRegs && CONV <= kLaunchRegs && MMA <= kLaunchRegs,
+                  "setmaxnreg.inc may not ask for fewer than the launch's, .dec not for more (an illegal instruction)");
+    static_assert(SOFT % 8 == 0 && CONV % 8 == 0 && MMA % 8 == 0 && CONV >= 24 && MMA >= 24 && SOFT <= 256,
+                  "setmaxnreg takes multiples of 8 from 24 to 256");
+};
 // A wait gives up after that many naps, which an arrival ends; the hardware cuts them to 6 us
 // whatever is asked for (measured).  Within a key tile, of 2 us, 26 ms; for a segment, which may be 2^23 tiles
 // (2^30 keys) long, 50 s: where something is lost the waits within a tile end all others.
@@ -285,16 +295,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     };
 
     if (warp >= kMmaWarp) {
-        // ---- the MMAs, one warp (one thread of it) per sub-tile: the waits of one,
-        // each worth 1.5 products of idle tensor cores, overlap the other's
-        // products.  S of the next key tile goes out behind P V of this one, which it
-        // may only overwrite then: the products of one thread run in order.  The two
-        // take turns by a lock, P V and S at a time: interleaved, both sub-tiles would
-        // get their scores late and at once, and the softmaxes would run side by side
-        // and then the tensor cores alone.  The lock is given up with half of S to
-        // go, so that the other's first product is there when they end.  A sub-tile
+        // ---- the MMAs, one warp per sub-tile: the waits of one, each worth 1.5 products
+        // of idle tensor cores, overlap the other's products.  S of the next key tile goes
+        // out behind P V of this one, which it may only overwrite then: the products of one
+        // thread run in order.  The two take turns by a lock, P V and S at a time:
+        // interleaved, both sub-tiles would get their scores late and at once, and the
+        // softmaxes would run side by side and then the tensor cores alone.  A sub-tile
         // without rows in the segment only hands the buffers on.
-        fewer_regs<kMmaRegs>();
+        fewer_regs<Regs<FP4>::MMA>();
         const int sub = warp - kMmaWarp;
         if (warp == kMmaWarp + 2 && lane == 0) {
             // ---- the segments, and one of no rows behind the last
@@ -321,29 +329,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             const uint64_t dk = tc::desc_noswizzle(sb + L::OFF_K, 128, L::GROUP);
             const uint64_t dv = tc::desc_noswizzle(sb + L::OFF_V, L::GROUP, 128);
             const uint32_t ts = tmem + L::COL_S + sub * 128, to = tmem + L::COL_O + sub * D;
+            const uint32_t lock_at = tc::smem_u32(tensor_lock);
             uint32_t nk = 0, nq = 0, np = 0;             // key tiles, segments with this sub-tile, its P tiles so far
             auto lock = [&]() -> bool {
                 for (uint32_t i = 0; i < kLockPolls; ++i) {
-                    uint32_t got = 0;
-                    if (lane == 0) got = atomicCAS(tensor_lock, 0u, 1u) == 0u;
-                    if (__any_sync(ALL, got)) return true;
+                    uint32_t held = 1;
+                    if (lane == 0)
+                        asm volatile("atom.relaxed.cta.shared::cta.cas.b32 %0, [%1], 0, 1;" : "=r"(held) : "r"(lock_at));
+                    if (__any_sync(ALL, held == 0)) return true;
                     if (__any_sync(ALL, *abort_word)) break;
                 }
                 *abort_word = 1;
                 return false;
             };
-            auto unlock = [&]() { *reinterpret_cast<volatile unsigned int *>(tensor_lock) = 0u; };
+            auto unlock = [&]() { asm volatile("st.relaxed.cta.shared::cta.b32 [%0], 0;" ::"r"(lock_at)); };
             auto issue_s = [&](uint32_t tile) {
                 const uint32_t q = (uint32_t)dq, k = (uint32_t)dk + (tile & 1) * (L::KV / 16);
                 if (tc::elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        if (ks == D / 32) unlock();
                         if constexpr (TMEM_Q) tc::mma_f16_ta_lo(ts, tmem + L::COL_Q + sub * (D / 2) + ks * 8, k + ks * 16, (uint32_t)(dk >> 32), idesc_s, ks > 0);
                         else tc::mma_f16_lo(ts, q + ks * 16, k + ks * 16, (uint32_t)(dk >> 32), idesc_s, ks > 0);
                     }
                     tc::commit(sfull(sub));
                     tc::commit(kempty(tile & 1));
+                    unlock();
                 }
             };
             auto issue_o = [&](uint32_t tile, bool first) {
@@ -419,7 +429,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
         // Scales go to a ring of kMetas: tile j + 4's are written once V of tile j + 3
         // is, for which P V of tile j + 1 had to be done, so both softmaxes are past
         // tile j and its slot is free.
-        fewer_regs<kConvRegs>();
+        fewer_regs<Regs<FP4>::CONV>();
         constexpr int CH = D / 64, N = 4 * CH;           // 64-byte column groups, 16-byte pieces per thread and operand
         const int cw = warp - kSoftWarps, row = lane & 7, chunk = lane >> 3;
         uint32_t nt = 0;
@@ -579,7 +589,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
             }
         }
     } else {
-        more_regs<kSoftRegs>();
+        more_regs<Regs<FP4>::SOFT>();
         // ---- softmax: thread = row
         const int sub = warp >> 2, rr = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -812,21 +822,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                         const float at = kUp - M;
                         const uint64_t aa = f2(at, at);
                         uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
+                        // 16 scores at a time, their sums and halves behind the exponentials of the next
                         uint32_t p[4][16], r[2][32];
-                        tc::tmem_ld32(ts, r[0]);
+                        float e[2][16];
+                        auto take = [&](int g) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            tc::tmem_ld_wait();
-                            if (c < 3) tc::tmem_ld32(ts + 32 * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float2 z = un2(fma2(f2u(r[c & 1][i], r[c & 1][i + 1]), ff, aa));
-                                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                            for (int i = 0; i < 16; i += 2) {
+                                const float e0 = e[g & 1][i], e1 = e[g & 1][i + 1];
                                 if (i & 2) sum1 = add2(sum1, f2(e0, e1));
                                 else sum0 = add2(sum0, f2(e0, e1));
-                                p[c][i / 2] = pack_f16(e0, e1);
+                                p[g / 2][8 * (g & 1) + i / 2] = pack_f16(e0, e1);
                             }
+                        };
+                        tc::tmem_ld32(ts, r[0]);
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            const int c = g / 2, at16 = 16 * (g & 1);
+                            if (at16 == 0) {
+                                tc::tmem_ld_wait();
+                                if (c < 3) tc::tmem_ld32(ts + 32 * (c + 1), r[(c + 1) & 1]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 z = un2(fma2(f2u(r[c & 1][at16 + i], r[c & 1][at16 + i + 1]), ff, aa));
+                                e[g & 1][i] = ex2(z.x), e[g & 1][i + 1] = ex2(z.y);
+                            }
+                            if (g) take(g - 1);
                         }
+                        take(7);
                         const float2 x = un2(add2(sum0, sum1));
                         const float total = x.x + x.y;
                         if (__all_sync(ALL, total < kMostP)) {
@@ -906,18 +929,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                         float gain = 0.0f, total = 0.0f;
                         uint32_t r[2][32];
                         tc::tmem_ld32(ts, r[0]);
-    #pragma unroll
+#pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             tc::tmem_ld_wait();
                             if (c < 3) tc::tmem_ld32(ts + 32 * (c + 1), r[(c + 1) & 1]);
                             const float2 ks = *reinterpret_cast<const float2 *>(&m.ks[2 * c]), lg = *reinterpret_cast<const float2 *>(&m.lg[2 * c]),
                                          rv = *reinterpret_cast<const float2 *>(&m.rv[2 * c]);
-    #pragma unroll
+#pragma unroll
                             for (int g = 0; g < 2; ++g) {
                                 const float f = factor(zf, g ? ks.y : ks.x), at = (g ? lg.y : lg.x) - MV;
                                 const uint64_t ff = f2(f, f), aa = f2(at, at);
                                 uint64_t sum0 = f2(0.0f, 0.0f), sum1 = sum0;
-    #pragma unroll
+#pragma unroll
                                 for (int i = 0; i < 16; i += 2) {
                                     const float2 z = un2(fma2(f2u(r[c & 1][16 * g + i], r[c & 1][16 * g + i + 1]), ff, aa));
                                     const float e0 = ex2(z.x), e1 = ex2(z.y);
@@ -932,7 +955,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                             }
                         }
                         if (__all_sync(ALL, total < kMostP && gain * back < kMostL)) {
-    #pragma unroll
+#pragma unroll
                             for (int c = 0; c < 4; ++c) tc::tmem_st16(ts + 16 * c, p[c]);
                             l += gain * back;
                             break;
@@ -950,18 +973,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                         // 64 scores at a time, read again for P: all 128 do not fit beside the rest
                         uint32_t r[2][32];
                         float tz = NEG_INF, tv = NEG_INF;
-    #pragma unroll 1
+#pragma unroll 1
                         for (int c = 0; c < 4; c += 2) {
                             tc::tmem_ld32(ts + 32 * c, r[0]);
                             tc::tmem_ld32(ts + 32 * c + 32, r[1]);
                             tc::tmem_ld_wait();
                             if (masked) hide(c, r[0]), hide(c + 1, r[1]);
-    #pragma unroll
+#pragma unroll
                             for (int g = 0; g < 4; ++g) {
                                 const uint32_t (&x)[32] = r[g / 2];
                                 const int i0 = 16 * (g & 1);
                                 float t0 = __uint_as_float(x[i0]), t1 = __uint_as_float(x[i0 + 1]);
-    #pragma unroll
+#pragma unroll
                                 for (int i = 2; i < 14; i += 4) {
                                     t0 = max3(t0, __uint_as_float(x[i0 + i]), __uint_as_float(x[i0 + i + 1]));
                                     t1 = max3(t1, __uint_as_float(x[i0 + i + 2]), __uint_as_float(x[i0 + i + 3]));
@@ -985,20 +1008,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
                         if (j > 0 && __any_sync(ALL, upv)) rescale(grow);
                         const float ref = M == NEG_INF ? 0.0f : M, g2 = ex2(0.5f * (ref - (MV == NEG_INF ? 0.0f : MV)));     // 2^(M - Mv) in two steps
                         uint64_t sum = f2(0.0f, 0.0f);
-    #pragma unroll 1
+#pragma unroll 1
                         for (int c = 0; c < 4; c += 2) {
                             tc::tmem_ld32(ts + 32 * c, r[0]);
                             tc::tmem_ld32(ts + 32 * c + 32, r[1]);
                             tc::tmem_ld_wait();
                             if (masked) hide(c, r[0]), hide(c + 1, r[1]);
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 uint32_t p[16];
-    #pragma unroll
+#pragma unroll
                                 for (int g = 0; g < 2; ++g) {
                                     const float f = factor(zf, m.ks[2 * c + 2 * k + g]), w = fminf(m.vs[2 * c + 2 * k + g] * g2 * g2, kMostWeight) * kUpFactor;
                                     const uint64_t ww = f2(w, w);
-    #pragma unroll
+#pragma unroll
                                     for (int i = 0; i < 16; i += 2) {
                                         // rounded as the maxima were, before the reference is taken off, so that none is beyond
                                         // them (a packed product and sum would be joined again, without that rounding)
