@@ -16,15 +16,18 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps4 = kSplitWarps;
-constexpr int kPerSm4 = 3;              // CTAs that an SM holds at once
+// CTAs that an SM holds at once: 16 rows of 128 channels need the registers of two (24
+// requests of up to 16k tokens, 8 heads, 16 rows each: 77 us, 84 with three), others run
+// fastest with three (8 rows of 128 channels, 64 requests: 130 us, 141 with two, 148 with four;
+// of 64 channels 82, 91 with two).
+constexpr int per_sm4(int D, int NT) { return D == 128 && NT == 2 ? 2 : 3; }
 constexpr int kCost4 = 8;               // tiles that a unit's fixed cost counts as
 template <int D>
 struct Stage4 {                         // a tile in shared memory: codes and scales of its keys and of its values
-    static constexpr int KEYS = 64;                          // of a warp's tile
+    static constexpr int LOG_KEYS = 6, KEYS = 1 << LOG_KEYS;  // of a warp's tile
     static constexpr int CODES = KEYS * D / 2, SCALES = KEYS * D / 16;
     static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = KS + SCALES, BYTES = VS + SCALES;
-    static constexpr int N = D == 128 ? 2 : 4;               // of them per warp
-    static constexpr int AT_ONCE = D == 128 ? 32 : 64;       // keys whose scores a warp holds together
+    static constexpr int N = 2;                              // of them per warp
 };
 constexpr float kMostP4 = 65000.0f;     // bound of a row's weights in a tile (f16 ends at 65504)
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -73,7 +76,8 @@ __device__ __forceinline__ uint32_t chunk4_at(int r, int c) { return D == 128 ? 
 //        g + 8 of MMA j; C: those channels of query rows 2 t, 2 t + 1.
 template <int D, int NT>
 struct Tile4 {
-    static constexpr int KS = D / 16, MO = D / 16, U = Stage4<D>::AT_ONCE / 16, ROW = D / 2, SROW = D / 16;
+    static constexpr int KS = D / 16, MO = D / 16, ROW = D / 2, SROW = D / 16;
+    static constexpr int AT_ONCE = D == 128 && NT == 2 ? 32 : 64, U = AT_ONCE / 16;      // keys whose scores a warp holds together
     uint32_t q[NT][KS][2];
     float o[NT][MO][4];
     float m[NT][2], l[NT][2];                // rows 2 t, 2 t + 1: reference (log2), sum of P of this lane's keys
@@ -259,9 +263,9 @@ constexpr int split4_smem() {
 }
 
 template <int D, int NT, bool HALF>
-__global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kernel(PagedAttnArgs a) {
+__global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_split_kernel(PagedAttnArgs a) {
     using St = Stage4<D>;
-    constexpr int R = 8 * NT, K = St::KEYS, ROW = D / 2, SROW = D / 16, N = St::N;
+    constexpr int R = 8 * NT, K = St::KEYS, ROW = D / 2, SROW = D / 16, N = St::N, LGK = St::LOG_KEYS;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_st[kWarps4][8][2];
@@ -271,8 +275,8 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
     // A tile's rows of one block are a piece: GR rows, GU pieces to a tile.
-    const int lgGR = min(a.S, K) == 16 ? 4 : (min(a.S, K) == 32 ? 5 : 6), lgGU = (K == 64 ? 6 : 5) - lgGR, GU = 1 << lgGU, GR = 1 << lgGR;
-    static_assert(K == 64 || K == 32, "pieces of a tile: blocks are 16, 32, 64 or 128 tokens");
+    const int lgGR = 31 - __clz(min(a.S, K)), lgGU = LGK - lgGR, GU = 1 << lgGU, GR = 1 << lgGR;
+    static_assert(K == 1 << LGK && LGK >= 5 && LGK <= 7, "pieces of a tile: blocks are 16, 32, 64 or 128 tokens");
     pdl_wait();
     pdl_launch_dependents();
     using Work = SplitWork<R, K, kCost4>;
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, kPerSm4) paged_attn4_split_kerne
                     for (int u = 0; u < GU; ++u)
                         if ((info >> u) & 1) there |= ((1u << (GR / 16)) - 1) << (u * (GR / 16));
 #pragma unroll 1
-                for (int first = 0; first < K; first += St::AT_ONCE)
+                for (int first = 0; first < K; first += Tile4<D, NT>::AT_ONCE)
                     tile.keys(ring + stage * St::BYTES, first, zf, masked, key, rq.kv - key, there, s_seen[warp]);
                 __syncwarp();
             }
@@ -518,14 +522,14 @@ constexpr int kSplitRows4 = 32;
 struct Choice4 {
     int NT, split_ctas, tc_ctas, split_rows;
 };
-inline Choice4 choose4(int B, int G, int max_new) {
+inline Choice4 choose4(int B, int G, int D, int max_new) {
     const int64_t rows = (int64_t)G * max_new;
     Choice4 c = {(rows <= kSplitRows4 ? rows : G) <= 8 ? 1 : 2, 0, 0, 0x7FFFFFFF};
     if (rows > kSplitRows4) {
         c.tc_ctas = paged_attn_tc_ctas();
         c.split_rows = B == 1 || G > kSplitRows4 ? 0 : (c.NT == 1 ? 8 : kSplitRows4);
     }
-    if (c.split_rows) c.split_ctas = num_sms() * kPerSm4;
+    if (c.split_rows) c.split_ctas = num_sms() * per_sm4(D, c.NT);
     return c;
 }
 inline size_t partial4_floats(const Choice4 &c, int D) { return (size_t)2 * c.split_ctas * 8 * c.NT * (D + 4); }
@@ -537,7 +541,7 @@ using namespace csa2;
 
 extern "C" size_t csa2_paged_attn_fp4_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int D, int max_new) {
     if (B <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0 || max_new <= 0) return 0;
-    const Choice4 c = choose4(B, Hq / Hkv, max_new);
+    const Choice4 c = choose4(B, Hq / Hkv, D, max_new);
     return (c.split_ctas + c.tc_ctas) * sizeof(JoinUnit) +
            (partial4_floats(c, D) + (size_t)2 * c.tc_ctas * kTcRows * (D + 4)) * sizeof(float);
 }
@@ -566,7 +570,7 @@ extern "C" csa2_status csa2_paged_attn_fp4(int B, int64_t T, int Hq, int Hkv, in
         set_error("paged_attn: workspace of %zu bytes (16-byte aligned) needed, %zu given", need, ws_bytes);
         return CSA2_ERR_WORKSPACE;
     }
-    const Choice4 c = choose4(B, Hq / Hkv, max_new);
+    const Choice4 c = choose4(B, Hq / Hkv, D, max_new);
     JoinUnit *join = (JoinUnit *)workspace;
     float *partial = (float *)(join + c.split_ctas + c.tc_ctas);
     const PagedAttnArgs a = {B, Hq, Hkv, Hq / Hkv, S, M, window < M * S ? window : 0, T, n_blocks, table_stride,
