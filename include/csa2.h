@@ -532,7 +532,7 @@ csa2_status csa2_rope_table(const double *inv_freq, int half, int64_t start, int
  *
  * q, q_out  bf16 or fp16 [T, Hq, D]; k, k_out [T, Hk, D]; Hq or Hk may be 0 (and
  *           its pointers NULL).  Token and head strides in elements (multiples of
- *           8, below 2^32), channels contiguous, 16-byte aligned.  An output is its
+ *           8, below 2^31), channels contiguous, 16-byte aligned.  An output is its
  *           own input (pointer and strides) or shares no element with either input
  *           or the other output; slices of one projection's output fit.
  * D         multiple of 8, 16..1024; rope_dim multiple of 16, 16..D; first multiple
@@ -566,7 +566,7 @@ csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_token_stride
  * csa2_rope writes.
  *
  * k, v    bf16 or fp16 [T, Hkv, D], 16-byte aligned, D contiguous; token and head
- *         strides in elements, multiples of 8 below 2^32.  T <= 2^30, Hkv <= 32767.
+ *         strides in elements, multiples of 8 below 2^31.  T <= 2^30, Hkv <= 32767.
  * slots   int64 [T]; -1 skips a row, as does a slot outside [-1, n_blocks * S)
  *         (CSA2_FLAG_BAD_SLOT).  A slot given twice is a data race: its row is a mixture.
  * pos, cos_sin, n_pos, rope_dim, first, layout  as csa2_rope; both pointers NULL: no
@@ -591,7 +591,7 @@ csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, csa2_dtype 
  * slots[t], exact in bf16 and fp16.  A slot may be given any number of times; -1 leaves its
  * row as it was, as does a slot outside [-1, n_blocks * S) (CSA2_FLAG_BAD_SLOT).
  * k, v bf16 or fp16 [T, Hkv, D], 16-byte aligned, D contiguous, token and head
- * strides in elements (multiples of 8 below 2^32); no two rows share elements.
+ * strides in elements (multiples of 8 below 2^31); no two rows share elements.
  */
 csa2_status csa2_dequantize_kv_fp4_paged(const int64_t *slots, int64_t T, int64_t n_blocks, int Hkv, int S, int D,
                                          const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_scales,

@@ -346,8 +346,8 @@ csa2_status check4(const char *who, csa2_dtype dt, int64_t T, int H, int D, int6
     CSA2_REQUIRE(n_blocks >= 0 && n_blocks < (1ll << 31), "%s: n_blocks=%lld", who, (long long)n_blocks);
     CSA2_REQUIRE(S == 16 || S == 32 || S == 64 || S == 128, "%s: S=%d not in {16, 32, 64, 128}", who, S);
     for (int i = 0; i < 4; ++i)
-        CSA2_REQUIRE(stride[i] >= 0 && stride[i] % 8 == 0 && stride[i] < (1ll << 32),
-                     "%s: strides must be multiples of 8 in [0, 2^32)", who);
+        CSA2_REQUIRE(stride[i] >= 0 && stride[i] % 8 == 0 && stride[i] < (1ll << 31),
+                     "%s: strides must be multiples of 8 in [0, 2^31)", who);
     if (D != 64 && D != 128) {
         set_error("%s: D=%d not in {64, 128}", who, D);
         return CSA2_ERR_UNSUPPORTED;

@@ -167,7 +167,7 @@ extern "C" csa2_status csa2_rope_table(const double *inv_freq, int half, int64_t
     const uintptr_t f0 = (uintptr_t)inv_freq, t0 = (uintptr_t)cos_sin;
     CSA2_REQUIRE(f0 + 8 * half <= t0 || t0 + 8 * n_pos * half <= f0, "rope_table: cos_sin overlaps inv_freq");
     const int rows = half >= 256 ? 1 : 256 / half;
-    const int64_t want = (n_pos + rows - 1) / rows, most = (int64_t)num_sms() * 8;
+    const int64_t want = (n_pos + rows - 1) / rows, most = (int64_t)num_sms() * 4;
     const TableArgs a = {inv_freq, (float2 *)cos_sin, start, n_pos, half, amplitude};
     CSA2_CUDA_CALL(launch_pdl(rope_table_kernel, dim3((unsigned)(want < most ? want : most)), dim3(half, rows), 0,
                               stream_of(stream), a),
@@ -207,7 +207,7 @@ extern "C" csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_t
         in[i] = {a.in[i], T, a.heads[i], D, a.in_token[i], a.in_head[i]};
         out[i] = {a.out[i], T, a.heads[i], D, a.out_token[i], a.out_head[i]};
         for (int64_t s : {a.in_token[i], a.in_head[i], a.out_token[i], a.out_head[i]})
-            CSA2_REQUIRE(s >= 0 && s % 8 == 0 && s < (1ll << 32), "rope: strides must be multiples of 8 in [0, 2^32)");
+            CSA2_REQUIRE(s >= 0 && s % 8 == 0 && s < (1ll << 31), "rope: strides must be multiples of 8 in [0, 2^31)");
         CSA2_REQUIRE(aligned(a.in[i], 16) && aligned(a.out[i], 16), "rope: rows must be 16-byte aligned");
         CSA2_REQUIRE(out[i].apart(), "rope: rows of an output share elements");
         const bool same = a.in[i] == a.out[i] && (T == 1 || a.in_token[i] == a.out_token[i]) &&
