@@ -576,7 +576,7 @@ csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_token_stride
  *         codes stand for (exact), so that a prompt may attend to the values that later
  *         steps will see.  Rows that are not stored are left as they were.
  * Infinities are stored as +-6 scale and NaN as 0, neither counts toward amax
- * (CSA2_FLAG_NONFINITE).
+ * (CSA2_FLAG_NONFINITE).  Codes, scales and values overlap nothing else.
  */
 csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, csa2_dtype dt, int64_t T, int Hkv, int D,
                                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,

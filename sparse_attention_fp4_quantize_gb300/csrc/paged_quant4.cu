@@ -393,14 +393,19 @@ extern "C" csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, 
     CSA2_REQUIRE(aligned(k_values, 16) && aligned(v_values, 16), "quantize_fp4_paged: values must be 16-byte aligned");
     const Rows in[2] = {{k, T, Hkv, D, k_token_stride, k_head_stride}, {v, T, Hkv, D, v_token_stride, v_head_stride}};
     const int64_t dense = 2 * T * Hkv * D, plane = n_blocks * Hkv * S * (D / 2);
-    for (const void *x : {k_values, v_values}) {
-        bool over = x && (meet(x, dense, slots, 8 * T) || (cos_sin && meet(x, dense, cos_sin, 4 * n_pos * rope_dim)));
-        for (const Rows &r : in) over = over || (x && meet(x, dense, r.p, r.bytes()));
-        for (const uint8_t *p : {k_codes, v_codes}) over = over || (x && meet(x, dense, p, plane));
-        for (const uint8_t *p : {k_scales, v_scales}) over = over || (x && meet(x, dense, p, plane / 8));
-        CSA2_REQUIRE(!over, "quantize_fp4_paged: values overlap another argument");
+    const struct {
+        const void *p;
+        int64_t bytes;
+    } outs[6] = {{k_codes, plane}, {v_codes, plane}, {k_scales, plane / 8}, {v_scales, plane / 8}, {k_values, k_values ? dense : 0},
+                 {v_values, v_values ? dense : 0}},
+      ins[5] = {{k, in[0].bytes()}, {v, in[1].bytes()}, {slots, 8 * T}, {pos, pos ? 4 * T : 0},
+                {cos_sin, cos_sin ? 4 * n_pos * rope_dim : 0}};
+    for (int i = 0; i < 6; ++i) {
+        bool over = false;
+        for (const auto &x : ins) over = over || meet(outs[i].p, outs[i].bytes, x.p, x.bytes);
+        for (int j = 0; j < i; ++j) over = over || meet(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes);
+        CSA2_REQUIRE(!over, "quantize_fp4_paged: an output (codes, scales or values) overlaps another argument");
     }
-    CSA2_REQUIRE(!k_values || !v_values || !meet(k_values, dense, v_values, dense), "quantize_fp4_paged: k_values and v_values overlap");
     const bool any = cos_sin && (layout != CSA2_ROPE_HALF || rope_dim != D);
     const Shape4 sh = shape_of(T, Hkv, any ? D / 16 : D / 32);
     Quant4Args a = {};

@@ -231,6 +231,61 @@ def test_cache_beyond_32_bit_offsets(csa2):
         paged_ref.check_attention(out, lse, ref.attention(q, kc[pick], ks[pick], vc[pick], vs[pick], small, [T], [0, new], 0.1))
 
 
+def test_append_and_reading_back_on_another_stream_and_in_graphs(csa2):
+    """A prompt's rows on a stream that is not the current one; then captured and replayed with other rows and slots, and
+    eager calls in between."""
+    T, H, D, S, n = 150, 4, 128, 32, 12
+    gen = torch.Generator().manual_seed(60)
+    planes = [p.zero_() for p in _planes(60, n, H, S, D)]
+    k, v = [torch.zeros(T, H, D, dtype=BF, device=DEV) for _ in range(2)]
+    slots = torch.full((T,), -1, device=DEV)
+    back = [torch.zeros_like(k) for _ in range(2)]
+
+    def fill():
+        for x in (k, v):
+            x.copy_(torch.randn(x.shape, generator=gen).to(BF))
+        slots.copy_(_slots(gen, T, n, S, 0.0))
+
+    def calls(stream=None):
+        csa2.csa2_quantize_kv_fp4_paged(k, v, slots, *planes, stream=stream)
+        csa2.csa2_dequantize_kv_fp4_paged(slots, *planes, *back, stream=stream)
+
+    def right():
+        for x, y in zip((k, v), back):
+            assert np.array_equal(y.double().cpu().numpy(), ref.quantise(x.double().cpu().numpy())[2])
+
+    fill()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    calls(side)
+    side.synchronize()
+    right()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for _ in range(3):
+        fill()
+        g.replay()
+        torch.cuda.synchronize()
+        right()
+        fill()
+        calls()
+        torch.cuda.synchronize()
+        right()
+
+
+@pytest.mark.parametrize("half", [True, False])
+def test_append_of_rows_that_heads_and_tokens_share(csa2, half):
+    """Strides of 0: one row for all heads, one for all tokens."""
+    T, H, D, S = 9, 5, 64, 16
+    gen = torch.Generator().manual_seed(61)
+    k = torch.randn(T, 1, D, generator=gen).to(BF).to(DEV).expand(T, H, D)
+    v = torch.randn(1, H, D, generator=gen).to(BF).to(DEV).expand(T, H, D)
+    table = torch.randn(20, 16, 2, generator=gen).to(DEV)
+    pos = torch.randint(0, 20, (T,), generator=gen).to(I32).to(DEV)
+    _append_both(csa2, k, v, _slots(gen, T, 4, S), _planes(61, 4, H, S, D), rope=(pos, table, 24, half))
+
+
 # ---------------------------------------------------------------- attention
 def _inputs(seed, kv, new, Hq, H, D, S, dtype=BF, q_size=1.0):
     gen = torch.Generator().manual_seed(seed)
@@ -695,3 +750,41 @@ def test_steps_back_to_back_give_the_bits_of_steps_one_by_one(csa2):
     for _ in range(3):
         for a, b in zip(apart, run(False)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_a_request_that_waits_for_blocks_leaves_the_others_alone(csa2, bits):
+    """Rows of a request that found no blocks have no position and are not stored; its tokens come again once another request
+    has ended."""
+    from sparse_attention_fp4_quantize_gb300.paged import PagedCache, PagedShape
+    from sparse_attention_fp4_quantize_gb300.rope import Rope
+    H, Hq, D, S, T = 2, 4, 64, 16, 52
+    cache = PagedCache(PagedShape(requests=2, tokens=T, max_context=64, n_blocks=3, heads=Hq, kv_heads=H, dim=D, block_size=S,
+                                  max_new=32, bits=bits, rope=Rope(D)))
+    gen = torch.Generator().manual_seed(62)
+    for new, flag, there in (([32, 20], csa2.FLAG_NO_BLOCKS, 0), ([-1, 20], 0, 1)):
+        q, k, v = [torch.randn(T, h, D, generator=gen).to(BF).to(DEV) for h in (Hq, H, H)]
+        cache.err.zero_()
+        cache.new_len.copy_(torch.tensor(new, dtype=I32))
+        cache.plan()
+        cache.append(0, k, v)
+        out, lse = cache.attend(0, q)
+        torch.cuda.synchronize()
+        assert int(cache.err) == flag
+        r0, n = int(cache.cu_len[there]), new[there]
+        pos = torch.arange(n)
+        assert cache.positions[r0:r0 + n].tolist() == pos.tolist()
+        assert cache.slots.ge(0).sum() == n and cache.kv_len.tolist()[there] == n and cache.kv_len.tolist()[1 - there] == 0
+        rows = slice(r0, r0 + n)
+        turn = lambda x: ref.rotate(x[rows].cpu(), pos.tolist(), cache.cos_sin, 0, True)  # noqa: E731
+        table, kv, cu = cache.block_table[there:there + 1].cpu(), torch.tensor([n], dtype=I32), [0, n]
+        if bits == 4:
+            t = [x[0].cpu() for x in (cache.k_codes, cache.k_scale, cache.v_codes, cache.v_scale)]
+            want = ref.attention(turn(q), *t, table, kv, cu, cache.sm_scale)
+            held = ref.values(t[0], t[1])[table[0, pos // S].long(), :, pos % S]
+            assert np.array_equal(held, ref.quantise(turn(k).double().numpy())[2])
+        else:
+            t = [x[0].cpu().view(torch.float8_e4m3fn).double() for x in (cache.k_codes, cache.v_codes)]
+            want = paged_ref.attention(turn(q).double(), *t, cache.k_scale[0].double().cpu(), cache.v_scale[0].double().cpu(), table, kv,
+                                       cu, cache.sm_scale)
+        paged_ref.check_attention(out[rows], lse[rows], want)

@@ -211,6 +211,28 @@ def test_rotation_in_a_graph_and_on_another_stream(csa2):
     _same(out, ref.rotate(q2.cpu(), pos.tolist(), table, 0, True).to(DEV))
 
 
+def test_table_in_parts_on_another_stream_and_in_a_graph(csa2):
+    """A table filled in two parts has the bits of one filled at once; captured and replayed with other frequencies."""
+    n, half = 700, 48
+    f = (10000.0 ** (-torch.arange(half, dtype=torch.float64) / half)).to(DEV)
+    whole, parts = [torch.zeros(n, half, 2, device=DEV) for _ in range(2)]
+    csa2.csa2_rope_table(f, whole, start=1 << 30, amplitude=1.5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    csa2.csa2_rope_table(f, parts[:333], start=1 << 30, amplitude=1.5, stream=side)
+    csa2.csa2_rope_table(f, parts[333:], start=(1 << 30) + 333, amplitude=1.5, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(whole, parts)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        csa2.csa2_rope_table(f, parts)
+    f.copy_(f.flip(0).clone())
+    g.replay()
+    csa2.csa2_rope_table(f, whole)
+    torch.cuda.synchronize()
+    assert torch.equal(whole, parts) and (parts[0] == torch.tensor([1.0, 0.0], device=DEV)).all()
+
+
 def test_rows_beyond_32_bit_offsets(csa2):
     """Token strides that put the last row past 2^32 bytes."""
     T, D, step = 3, 64, (1 << 30) + 8

@@ -97,6 +97,9 @@ def _append(lib, dt=0, T=4, H=2, D=64, kt=128, kh=64, n=8, S=16, k=P(0x10000), k
     (dict(pos=FAKE, table=FAKE, n_pos=0), 1, "n_pos=0"), (dict(kval=P(0x500008)), 1, "16-byte"),
     (dict(kval=P(0x10000)), 1, "overlap"), (dict(vval=P(0x30000)), 1, "overlap"), (dict(vval=P(0x300000)), 1, "overlap"),
     (dict(kval=P(0x500000), vval=P(0x500010)), 1, "overlap"),
+    (dict(kc=P(0x200010)), 1, "overlap"), (dict(ks=P(0x400000)), 1, "overlap"), (dict(ks=P(0x101FF0)), 1, "overlap"),
+    (dict(kc=P(0x30000)), 1, "overlap"), (dict(kc=P(0x20000)), 1, "overlap"),
+    (dict(pos=P(0x600000), table=FAKE, ks=P(0x600000)), 1, "overlap"), (dict(pos=FAKE, table=P(0x600000), kc=P(0x600100)), 1, "overlap"),
 ])
 def test_append_rejects_on_host(lib, bad, status, word):
     _refused(_append(lib, **bad), lib, status, word)
