@@ -1,4 +1,4 @@
-// Shared parts of the paged attention (csa2_paged_attn_fp8): arguments, the
+// Shared parts of the paged attention (csa2_paged_attn_fp8, csa2_paged_attn_fp4): arguments, the
 // requests' rows and keys, the line of work that CTAs share out, and the output
 // of a row.
 #pragma once

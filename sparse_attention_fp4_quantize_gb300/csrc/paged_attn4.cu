@@ -9,6 +9,16 @@
 // log2 domain; weights P = 2^(z - M + kUp), rounded to f16's 11 bits for the product,
 // their sum in fp32 before that.  M may lag behind the maximum as long as the weights
 // stay below f16's end.
+//
+// The split kernel (this file) has a warp walk over tiles of 64 keys.  64 requests of up to
+// 16k tokens, 64 heads of 128 over 8 (687 MB): 130 us with the join, 5.3 TB/s, a copy's rate
+// 6.8; with its loads alone 110.  What it lacks are instructions' slots: of the 289 that a warp
+// issues per 16 keys 128 turn codes into f16 and apply the scales, the schedulers issue 0.6 a cycle
+// with 3 warps each, the codes' pipe is busy for 54 % and the tensor cores for 27.  CTAs of an SM end
+// 7 us apart, but shares that make up for it (5 to 15 % more for the first) only slow the last ones'
+// keys down: 131 to 141 us.  48 requests with 5 new tokens in a window of 4096, 15 heads of 64
+// over 5 (61 MB): 34 us, of which 5 go by before the first tile (lengths, table, codes, each after
+// the other) and 3 in the join; the loads alone take 20.  One request of 1000 tokens: 9.4 us in a graph.
 #include "fp4.cuh"
 #include "paged_attn.cuh"
 
@@ -21,7 +31,9 @@ constexpr int kWarps4 = kSplitWarps;
 // fastest with three (8 rows of 128 channels, 64 requests: 130 us, 141 with two, 148 with four;
 // of 64 channels 82, 91 with two).
 constexpr int per_sm4(int D, int NT) { return D == 128 && NT == 2 ? 2 : 3; }
-constexpr int kCost4 = 8;               // tiles that a unit's fixed cost counts as
+// Tiles that a unit's fixed cost counts as (64 requests as above 136 us, 137 with 4, 141 with 16; in a
+// window 38.7, 39.3 and 41.2, as measured then).
+constexpr int kCost4 = 8;
 template <int D>
 struct Stage4 {                         // a tile in shared memory: codes and scales of its keys and of its values
     static constexpr int LOG_KEYS = 6, KEYS = 1 << LOG_KEYS;  // of a warp's tile
@@ -518,6 +530,10 @@ cudaError_t launch_split4(const PagedAttnArgs &a, int ctas, cudaStream_t stream)
     return launch_pdl(paged_attn4_split_kernel<D, NT, HALF>, dim3(ctas), dim3(kWarps4 * 32), split4_smem<D>(), stream, a);
 }
 
+// Requests of more rows per KV head than this are the tile kernel's.  24 requests of up to 16k tokens,
+// 8 KV heads of 128 (of 64) channels, split and tile kernel: 16 rows 78 and 168 us (51, 135), 32 rows
+// 140 and 169 (87, 136), 64 rows 263 and 173 (160, 137); of up to 2000 tokens 27 and 46 (19, 38), 38
+// and 46 (27, 38), 62 and 48 (43, 39).
 constexpr int kSplitRows4 = 32;
 struct Choice4 {
     int NT, split_ctas, tc_ctas, split_rows;
@@ -525,7 +541,7 @@ struct Choice4 {
 inline Choice4 choose4(int B, int G, int D, int max_new) {
     const int64_t rows = (int64_t)G * max_new;
     Choice4 c = {(rows <= kSplitRows4 ? rows : G) <= 8 ? 1 : 2, 0, 0, 0x7FFFFFFF};
-    if (rows > kSplitRows4) {
+    if (rows > kSplitRows4) {               // a batch may hold requests of fewer rows, which the split kernel takes beside the other
         c.tc_ctas = paged_attn_tc_ctas();
         c.split_rows = B == 1 || G > kSplitRows4 ? 0 : (c.NT == 1 ? 8 : kSplitRows4);
     }

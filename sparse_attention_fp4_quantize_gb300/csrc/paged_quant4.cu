@@ -13,12 +13,16 @@
 // is 2^-12 or more (relative) away from every midpoint.  The quotient is formed by a
 // multiplication (relative error below 2^-21) and rounded to 16 bits, which brings exact
 // midpoints back and carries no other value across one.
+//
+// Bound by memory and, in the append, nearly as much by issue (0.56 instructions per cycle).  16384
+// tokens, 8 heads of 128, keys rotated, with the stored values (152 MB): 28.6 us, 5.3 TB/s of a
+// copy's 6.8; a decode step's 64 tokens 2.4 us in a graph.
 #include "fp4.cuh"
 
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 64;
+constexpr int kThreads = 64;         // of a block (16384 tokens as above: 128 0.9 us slower)
 
 struct Rope4 {
     const int32_t *pos;
@@ -171,7 +175,8 @@ __device__ __forceinline__ bool place_of(const Quant4Args &a, int64_t t, bool fi
     return true;
 }
 
-// Any rotation: a thread takes one group of a row and reads its partners beside it.
+// Any rotation: a thread takes one group of a row and reads its partners beside it.  16384 tokens,
+// 8 heads of 128: 36 us, pairs side by side or halves of 64 channels.
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_any_kernel(Quant4Args a) {
     pdl_wait();
@@ -223,7 +228,9 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_any_kernel(Quant4
 }
 
 // No rotation, or one of halves over the whole head: a thread takes a group and the one
-// half a row behind it, which are each other's partners.
+// half a row behind it, which are each other's partners, so nothing is read or turned twice: 29 us
+// where the kernel above takes 37, 27.6 without a rotation.  The next head's loads are on their way
+// meanwhile (34.5 otherwise).
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_kernel(Quant4Args a) {
     pdl_wait();
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(kReadThreads) dequantize_fp4_paged_kernel(Read
 }
 
 // Threads of a block, blocks, and heads per thread: as many heads (loads that share a
-// token's slot, position and table row) as leave every SM its threads.
+// token's slot, position and table row) as leave every SM 8 blocks.
 struct Shape4 {
     dim3 grid, block;
     int per, chunks;
