@@ -39,7 +39,10 @@
 // registers instead of staged (934 against 906 then; over 4 bits the same), the lock given up
 // with half of S to go (750 against 741), before S (772 against 760) or left out (792
 // against 745), strict turns by mbarriers in its place (771 against 745), waits that poll
-// before they sleep (828 against 753 with 16 polls).
+// before they sleep (828 against 753 with 16 polls), S and P in halves of 64 keys that take
+// turns in TMEM (789 against 735: a product of N 64 reads all of Q and takes 59 cycles, not 32), a
+// row's keys shared by two warps that serve the sub-tiles in turn (820 against 734: two
+// warps together need 1080 cycles for what one does in 1340, and 600 to come to the next).
 #include "fp4.cuh"
 #include "paged_attn.cuh"
 #include "tc.cuh"
