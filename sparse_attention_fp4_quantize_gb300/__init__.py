@@ -106,6 +106,18 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
+from . import _csa2_bind  # noqa: E402  (built with the library)
+
+
+def _bind(lib, current_stream=None, current_device=None):
+    """The extension makes the calls of this library."""
+    names = ("csa2_rope_table", "csa2_rope", "csa2_quantize_kv_fp4_paged", "csa2_dequantize_kv_fp4_paged", "csa2_paged_attn_fp4")
+    _csa2_bind.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names],
+                    current_stream or torch._C._cuda_getCurrentRawStream, current_device or torch._C._cuda_getDevice)
+
+
+_bind(_lib)
+
 
 def exported_symbols():
     return ["csa2_quantize_kv_fp4", "csa2_rope_quantize_kv_fp4", "csa2_index_score", "csa2_build_pool", "csa2_build_pool_workspace_bytes",
@@ -633,9 +645,14 @@ def csa2_paged_attn_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, kv_l
 
 
 # ------------------------------------------------------------------ rotary positions
+# These calls and those of the 4-bit cache are made by the extension (csrc/bind.cpp) where their arguments are the
+# usual ones and fit; what it leaves is done, or refused with its reason, here.
 def csa2_rope_table(inv_freq, cos_sin, start=0, amplitude=1.0, stream=None):
     """inv_freq float64 [half], radians per position -> cos_sin fp32 [n_pos,
     half, 2]: amplitude * (cos, sin) of positions start, start + 1, ..."""
+    rc = _csa2_bind.csa2_rope_table(inv_freq, cos_sin, start, amplitude, stream)
+    if rc is not None:
+        return _check(rc)
     dev = _device_of(cos_sin)
     half = inv_freq.numel()
     if cos_sin.dim() != 3:
@@ -657,6 +674,9 @@ def csa2_rope(q, pos, cos_sin, k=None, q_out=None, k_out=None, first=0, layout=R
     cos_sin fp32 [n_pos, rope_dim/2, 2] at pos int32 [T] (-1: the row is left
     out): the rope_dim channels from `first` on, in pairs of `layout`.  Into q_out
     and k_out, or in place where they are None."""
+    rc = _csa2_bind.csa2_rope(q, pos, cos_sin, k, q_out, k_out, first, layout, err_flag, stream)
+    if rc is not None:
+        return _check(rc)
     dev = _device_of(q)
     T, Hq, D = q.shape
     dt = _ROWS.get(q.dtype)
@@ -701,6 +721,10 @@ def csa2_quantize_kv_fp4_paged(k, v, slots, k_codes, v_codes, k_scales, v_scales
     [n_blocks, Hkv, S, D/16], updated in place; with pos and cos_sin the keys
     are rotated first, as csa2_rope does.  k_values, v_values [T, Hkv, D] of
     k's type, or None: what the codes stand for."""
+    rc = _csa2_bind.csa2_quantize_kv_fp4_paged(k, v, slots, k_codes, v_codes, k_scales, v_scales, pos, cos_sin, first, layout, k_values,
+                                               v_values, err_flag, stream)
+    if rc is not None:
+        return _check(rc)
     dev = _device_of(k)
     kc, vc, ks, vs, n, H, S, D = _planes4_args(k_codes, v_codes, k_scales, v_scales, dev)
     (T,) = slots.shape
@@ -724,6 +748,9 @@ def csa2_dequantize_kv_fp4_paged(slots, k_codes, v_codes, k_scales, v_scales, k,
     it was) of planes as csa2_quantize_kv_fp4_paged writes them -> k, v bf16
     (or int16 bits) or fp16 [T, Hkv, D] (any token and head strides that are
     multiples of 8)."""
+    rc = _csa2_bind.csa2_dequantize_kv_fp4_paged(slots, k_codes, v_codes, k_scales, v_scales, k, v, err_flag, stream)
+    if rc is not None:
+        return _check(rc)
     dev = _device_of(k)
     kc, vc, ks, vs, n, H, S, D = _planes4_args(k_codes, v_codes, k_scales, v_scales, dev)
     (T,) = slots.shape
@@ -752,6 +779,10 @@ def csa2_paged_attn_fp4(q, k_codes, v_codes, k_scales, v_scales, block_table, kv
     arguments of csa2_paged_attn_fp8, with planes as
     csa2_quantize_kv_fp4_paged writes them.  workspace: a CUDA byte tensor of at
     least csa2_paged_attn_fp4_workspace_bytes bytes (allocated here when None)."""
+    rc = _csa2_bind.csa2_paged_attn_fp4(q, k_codes, v_codes, k_scales, v_scales, block_table, kv_len, cu_len, out, sm_scale, max_new,
+                                        window, lse, err_flag, workspace, stream)
+    if rc is not None:
+        return _check(rc)
     dev = _device_of(q)
     kc, vc, ks, vs, n, H, S, D = _planes4_args(k_codes, v_codes, k_scales, v_scales, dev)
     T, Hq = q.shape[:2]

@@ -1,12 +1,15 @@
 """Build libcsa2.so in-tree: every .cu in csrc/ compiled for sm_103a (in
-parallel), then linked into one shared library next to this file."""
+parallel), then linked into one shared library next to this file; and beside
+it _csa2_bind.so, the Python extension (csrc/bind.cpp)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -14,6 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcsa2.so")
+BIND = os.path.join(HERE, "_csa2_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -31,14 +35,28 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "csa2.h"), __file__]
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "csa2.h"), __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_bind():
+    """The extension, against the installed torch (found, not imported)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib = os.path.join(torch, "lib")
+    tmp = BIND + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch, "include"), os.path.join(CSRC, "bind.cpp"), "-o", tmp, "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("bind.cpp: %s%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BIND)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -58,7 +76,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        bind = ex.submit(_build_bind)
         objs = list(ex.map(compile_one, sources()))
+        bind.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

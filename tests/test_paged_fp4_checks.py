@@ -3,7 +3,9 @@ own, and the references themselves."""
 from __future__ import annotations
 
 import ctypes
+import inspect
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -14,6 +16,7 @@ import sparse_attention_fp4_quantize_gb300 as csa2
 
 P = ctypes.c_void_p
 FAKE, NULL = P(0x1000), None
+REAL = csa2._lib
 
 
 @pytest.fixture(scope="module")
@@ -204,7 +207,7 @@ PLANES = dict(k_codes=_z(6, 2, 16, 32), v_codes=_z(6, 2, 16, 16, dtype=U8), k_sc
               v_scales=_z(6, 2, 16, 4))
 
 
-@pytest.mark.parametrize("fn,args,bad", [
+BAD = [
     ("csa2_rope_table", _table_args, dict(inv_freq=_z(32), cos_sin=_z(10, 31, 2))),
     ("csa2_rope", _rope_args, dict(q=_z(5, 4, 128), pos=_z(4, dtype=I32), cos_sin=_z(10, 64), k=_z(4, 2, 128, dtype=BF),
                                    q_out=_z(5, 4, 128, dtype=F16), k_out=_z(5, 2, 64, dtype=BF), err_flag=_z(1))),
@@ -215,7 +218,10 @@ PLANES = dict(k_codes=_z(6, 2, 16, 32), v_codes=_z(6, 2, 16, 16, dtype=U8), k_sc
     ("csa2_paged_attn_fp4", _attn_args, dict(q=_z(5, 6, 64), block_table=_z(2, 8, dtype=I32)[:, ::2], kv_len=_z(3, dtype=I32),
                                              cu_len=_z(2, dtype=I32), out=_z(5, 6, 64, dtype=F16), lse=_z(5, 6, dtype=BF),
                                              err_flag=_z(1), workspace=_z(8, 8, dtype=U8).T, **PLANES)),
-])
+]
+
+
+@pytest.mark.parametrize("fn,args,bad", BAD)
 def test_binding_refuses_what_does_not_fit(fake, fn, args, bad):
     getattr(csa2, fn)(**args())
     assert fake.calls == [fn]
@@ -223,6 +229,120 @@ def test_binding_refuses_what_does_not_fit(fake, fn, args, bad):
         with pytest.raises((TypeError, ValueError)):
             getattr(csa2, fn)(**{**args(), name: value})
     assert fake.calls == [fn]
+
+
+class _Recorder:
+    """C functions that keep what they are given."""
+
+    def __init__(self):
+        self.calls = []
+        self.fns = {}
+
+    def __getattr__(self, name):
+        if name not in self.fns:
+            real = getattr(REAL, name)
+            self.fns[name] = ctypes.CFUNCTYPE(real.restype, *real.argtypes)(lambda *a: self.calls.append((name, a)) or 7)
+        return self.fns[name]
+
+
+@pytest.fixture()
+def quick():
+    """The extension, bound to recorders; tensors of the CPU pass for ones of the current device."""
+    r = _Recorder()
+    csa2._bind(r, lambda dev: 0x7700, lambda: -1)
+    yield r
+    csa2._bind(REAL)
+
+
+def _positional(fn, args):
+    """All arguments of the Python function, in its order."""
+    sig = inspect.signature(getattr(csa2, fn))
+    b = sig.bind(**args)
+    b.apply_defaults()
+    assert list(b.arguments) == list(sig.parameters)
+    return list(b.arguments.values())
+
+
+def _as_given(v):
+    return None if v in (None, 0) else (struct.unpack("f", struct.pack("f", v))[0] if isinstance(v, float) else int(v))
+
+
+BINDINGS = [("csa2_rope_table", _table_args), ("csa2_rope", _rope_args), ("csa2_quantize_kv_fp4_paged", _append_args),
+            ("csa2_dequantize_kv_fp4_paged", _read_args), ("csa2_paged_attn_fp4", _attn_args)]
+
+
+def _usual(fn, args):
+    """Calls that fit, of every kind."""
+    a = args()
+    yield a
+    if fn == "csa2_rope_table":
+        yield {**a, "start": 1 << 30, "amplitude": 1.5, "stream": 0x99}
+        yield {**a, "inv_freq": _z(0, dtype=F64), "cos_sin": _z(0, 0, 2)}
+        return
+    yield {**a, "stream": type("S", (), {"cuda_stream": 0x55})()}
+    yield {**a, "err_flag": _z(2, dtype=torch.uint32)}
+    if fn == "csa2_rope":
+        yield {**a, "k": None, "k_out": None}
+        yield {**a, "q_out": None, "k_out": None, "layout": 0, "first": 8}
+        qkv = _z(5, 8, 128, dtype=BF)
+        yield {**a, "q": qkv[:, :4], "k": qkv[:, 4:6]}
+        yield {**a, "q": _z(1, 4, 128, dtype=F16)[:, :1], "k": None, "q_out": _z(1, 1, 200, dtype=F16)[..., :128], "k_out": None, "pos": _z(1, dtype=I32)}
+        return
+    planes = {n: torch.zeros_like(a[n]).view(torch.float8_e4m3fn) for n in ("k_scales", "v_scales")}
+    yield {**a, **planes}
+    if fn == "csa2_quantize_kv_fp4_paged":
+        yield {**a, "pos": None, "cos_sin": None, "k_values": None}
+        yield {**a, "k": _z(2, 5, 64, dtype=BF).transpose(0, 1), "v": _z(5, 1, 64, dtype=BF).expand(5, 2, 64)}
+        yield {**a, "k": _z(5, 2, 64, dtype=torch.int16), "v": _z(5, 2, 64, dtype=torch.int16), "k_values": None, "v_values": None}
+    if fn == "csa2_paged_attn_fp4":
+        yield {**a, "lse": None, "window": 9, "block_table": _z(2, 8, dtype=I32)[:, :3]}
+        yield {**a, "q": _z(5, 20, 64, dtype=BF)[:, 4:10]}
+        yield {**a, "block_table": _z(2, 2, dtype=I32)[:, ::2]}
+
+
+@pytest.mark.parametrize("fn,args", BINDINGS)
+def test_the_extension_hands_over_what_the_binding_does(quick, monkeypatch, fn, args):
+    cases = list(_usual(fn, args))
+    for a in cases:
+        assert getattr(csa2._csa2_bind, fn)(*_positional(fn, a)) == 7
+    given = []
+    monkeypatch.setattr(csa2, "_on_device", lambda t: True)
+    monkeypatch.setattr(csa2, "_stream", lambda s: 0x7700 if s is None else getattr(s, "cuda_stream", s))
+    monkeypatch.setattr(csa2, "_lib", type("L", (), {fn: staticmethod(lambda *a: given.append(a) or 0)}))
+    monkeypatch.setattr(csa2, "_csa2_bind", type("B", (), {fn: staticmethod(lambda *a: None)}))
+    for a in cases:
+        getattr(csa2, fn)(**a)
+    assert len(given) == len(quick.calls) == len(cases)
+    for (name, took), want in zip(quick.calls, given):
+        assert name == fn and [_as_given(v) for v in took] == [_as_given(v) for v in want]
+
+
+@pytest.mark.parametrize("fn,args,bad", BAD)
+def test_the_extension_leaves_what_does_not_fit(quick, fn, args, bad):
+    call = getattr(csa2._csa2_bind, fn)
+    for name, value in bad.items():
+        assert call(*_positional(fn, {**args(), name: value})) is None, name
+    good = _positional(fn, args())
+    names = list(inspect.signature(getattr(csa2, fn)).parameters)
+    for i, v in enumerate(good):                                         # of other kinds altogether
+        for x in ("x", 2 ** 70, _z(3), None):
+            if (x is None and not isinstance(v, (int, float))) or (names[i] == "workspace" and torch.is_tensor(x)):
+                continue
+            assert call(*good[:i], x, *good[i + 1:]) is None, (names[i], x)
+    assert call(*good[:-1]) is None and call(*good, None) is None and call() is None
+    assert quick.calls == []
+
+
+def test_the_extension_leaves_other_devices_and_classes(quick):
+    a = _positional("csa2_rope", _rope_args())
+    sub = a[0].as_subclass(type("T", (torch.Tensor,), {}))
+    meta = torch.empty(a[0].shape, dtype=BF, device="meta")
+    assert csa2._csa2_bind.csa2_rope(sub, *a[1:]) is None and csa2._csa2_bind.csa2_rope(meta, *a[1:]) is None
+    csa2._bind(quick, lambda dev: 0, lambda: 0)                          # the current device is another
+    assert csa2._csa2_bind.csa2_rope(*a) is None
+    b = _positional("csa2_paged_attn_fp4", {**_attn_args(), "workspace": None})
+    csa2._bind(quick, lambda dev: 0, lambda: -1)
+    assert csa2._csa2_bind.csa2_paged_attn_fp4(*b) is None and quick.calls == []
 
 
 def test_binding_refuses_the_rest(fake):
