@@ -13,12 +13,13 @@ namespace {
 // bits, and the Taylor series around 0 end with its 9th and 10th power (the next terms
 // are 2^-28 and 2^-31 of the results).
 //
-// Bound by the stores.  262144 positions of 64 pairs (134 MB): 24.6 us, 5.5 TB/s of the 6.8 that a
-// copy reaches; as fp64 angles through sinpi and cospi 67.  A thread keeps its pair, whose frequency it
-// converts once, and steps over positions: four CTAs to an SM (8: 25.5 us, 16: 27.0).  4096
-// positions of 32 pairs are done within the launch's own 5 us.
-constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;   // 1 / (2 pi) in two parts
-constexpr double kMostFreq = 1048576.0;      // radians per position
+// Bound by the stores.  262144 positions of 64 pairs (134 MB): 21.9 us, 6.1 TB/s of the 6.8 that a
+// copy reaches (24.6 with the frequency converted in fp64; as fp64 angles through sinpi and cospi 67).  A
+// thread keeps its pair, whose frequency it converts once, and steps over positions: four CTAs to an SM
+// (6: 22.3 us, 8: 23.0) and four positions per thread at least: 4096 positions of 32 pairs 1.7 us in a
+// graph (2.4 with one, 1.8 with eight; 5.5 in fp64).
+constexpr uint64_t kTurnHigh = 0x28BE60DB9391054Aull, kTurnLow = 0x7F09D5F47D4D3770ull;      // 2^128 / (2 pi)
+constexpr int kMostExp = 1023 + 20, kLeastExp = 1023 - 30;   // biased exponents: 2^20 radians per position, 2^-30
 
 struct TableArgs {
     const double *freq;
@@ -27,6 +28,18 @@ struct TableArgs {
     int half;
     float amplitude;
 };
+
+// Turns of f radians modulo 1, in 2^-64, nearest, for kLeastExp <= exponent and |f| <= 2^20: its 53 bits
+// times 128 of 1 / (2 pi), in integers (fp64 has a 64th of their rate).
+__device__ __forceinline__ uint64_t turns_of(uint64_t bits) {
+    const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 1ull << 52;
+    const int s = 1139 - (int)(bits >> 52 & 0x7FF);              // 96 .. 146: the product's bits below 2^-64 turns
+    const uint64_t b0 = m * kTurnHigh, p1 = __umul64hi(m, kTurnLow) + b0, p2 = __umul64hi(m, kTurnHigh) + (p1 < b0);
+    const uint64_t at = s < 128 ? p2 << (128 - s) | p1 >> (s - 64) : p2 >> (s - 128);
+    const uint64_t half = s <= 128 ? p1 >> (s - 65) : p2 >> (s - 129);
+    const uint64_t turns = at + (half & 1);
+    return bits >> 63 ? 0 - turns : turns;
+}
 
 // Cosine and sine of phase 2^-64 turns.
 __device__ __forceinline__ float2 cos_sin_of(uint64_t phase) {
@@ -47,20 +60,19 @@ __global__ void __launch_bounds__(512) rope_table_kernel(TableArgs a) {
     pdl_launch_dependents();
     const int i = threadIdx.x;
     const double f = a.freq[i];
-    const bool fine = fabs(f) <= kMostFreq;  // no NaN either
-    const double t = f * kTurn, low = fma(f, kTurn, -t) + f * kTurnLow, r = t - rint(t);
-    const double hi = rint(r * 0x1p32);
-    const uint64_t step = fine ? ((uint64_t)(int64_t)hi << 32) + (uint64_t)llrint((fma(hi, -0x1p-32, r) + low) * 0x1p64) : 0;
+    const uint64_t bits = (uint64_t)__double_as_longlong(f);
+    const bool fine = (bits & 0x7FFFFFFFFFFFFFFFull) <= (uint64_t)kMostExp << 52;     // no NaN either
     const float amp = fine ? a.amplitude : __int_as_float(0x7FC00000);
     const int64_t n0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, ahead = (int64_t)gridDim.x * blockDim.y;
     float2 *out = a.table + n0 * a.half + i;
-    if (fabs(f) < 0x1p-30) {                 // fixed point would cost it leading bits; its angles fit fp64
+    if ((int)(bits >> 52 & 0x7FF) < kLeastExp) {                 // fixed point would cost it leading bits; its angles fit fp64
         for (int64_t n = n0; n < a.n_pos; n += ahead, out += ahead * a.half) {
-            const double x = 2.0 * (t * (double)(a.start + n));
+            const double x = f * 0.3183098861837907 * (double)(a.start + n);
             *out = make_float2(amp * (float)cospi(x), amp * (float)sinpi(x));
         }
         return;
     }
+    const uint64_t step = fine ? turns_of(bits) : 0;
     uint64_t phase = step * (uint64_t)(a.start + n0);
     const uint64_t phases = step * (uint64_t)ahead;
     for (int64_t n = n0; n < a.n_pos; n += ahead, out += ahead * a.half, phase += phases) {
@@ -174,7 +186,7 @@ extern "C" csa2_status csa2_rope_table(const double *inv_freq, int half, int64_t
     const uintptr_t f0 = (uintptr_t)inv_freq, t0 = (uintptr_t)cos_sin;
     CSA2_REQUIRE(f0 + 8 * half <= t0 || t0 + 8 * n_pos * half <= f0, "rope_table: cos_sin overlaps inv_freq");
     const int rows = half >= 256 ? 1 : 256 / half;
-    const int64_t want = (n_pos + rows - 1) / rows, most = (int64_t)num_sms() * 4;
+    const int64_t want = (n_pos + 4 * rows - 1) / (4 * rows), most = (int64_t)num_sms() * 4;     // 4 positions per thread or more
     const TableArgs a = {inv_freq, (float2 *)cos_sin, start, n_pos, half, amplitude};
     CSA2_CUDA_CALL(launch_pdl(rope_table_kernel, dim3((unsigned)(want < most ? want : most)), dim3(half, rows), 0,
                               stream_of(stream), a),
