@@ -300,13 +300,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kSplitPerSm) paged_attn_split
     __shared__ float s_st[kAttnWarps][8][3];
     __shared__ int2 s_seen[kAttnWarps][R];
     __shared__ StageMeta<D> s_meta[kAttnWarps][kStages];
-    __shared__ int64_t s_sum[kAttnWarps], s_found[2];
+    __shared__ int64_t s_sum[kAttnWarps];
+    __shared__ Found s_found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
     pdl_wait();
     pdl_launch_dependents();
     using Work = SplitWork<R, kTileKeys<D>>;
-    const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kAttnWarps, s_sum, s_found);
+    const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kAttnWarps, s_sum, &s_found);
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
     if (tid == 0) a.join[blockIdx.x].last = -1;

@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
     __shared__ float s_st[kWarps4][8][2];
     __shared__ int2 s_seen[kWarps4][R];
     __shared__ uint32_t s_info[kWarps4][N];
-    __shared__ int64_t s_sum[kWarps4], s_found[2];
+    __shared__ int64_t s_sum[kWarps4];
+    __shared__ Found s_found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const float NEG_INF = __int_as_float(0xff800000);
     // A tile's rows of one block are a piece: GR rows, GU pieces to a tile.
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
     pdl_wait();
     pdl_launch_dependents();
     using Work = SplitWork<R, K, kCost4>;
-    const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kWarps4, s_sum, s_found);
+    const Plan plan = plan_of<Work>(a, blockIdx.x, gridDim.x, kWarps4, s_sum, &s_found);
     int64_t at = blockIdx.x * plan.share;
     const int64_t stop = min(plan.total, at + plan.share);
     if (tid == 0) a.join[blockIdx.x].last = -1;
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
     static_assert(RPC % 4 == 0 && RPC <= 16, "the order of a row's chunks goes by its number modulo 4");
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
-        const Request rq = request_of(a, b);
+        const Request rq = b == plan.b ? plan.rq : request_of(a, b);
         const int64_t end = base + Work::tiles(a, rq);
         const int low = Work::low_key(a, rq), key0 = Work::first_key(a, rq), rows = rq.n * a.G;
         while (at < stop && at < end) {

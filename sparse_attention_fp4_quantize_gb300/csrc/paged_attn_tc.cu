@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((128u - (tc::smem_u32(smem_raw) & 127u)) & 127u);
-    __shared__ int64_t s_sum[kTcThreads / 32], s_found[2];
+    __shared__ int64_t s_sum[kTcThreads / 32];
+    __shared__ Found s_found;
     const int tid = threadIdx.x, warp = __shfl_sync(ALL, tid >> 5, 0), lane = tid & 31;
     const uint32_t sb = tc::smem_u32(smem);
     TileMeta *metas = reinterpret_cast<TileMeta *>(smem + L::OFF_META);
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(PagedAttnA
     const uint32_t tmem = __shfl_sync(ALL, *tmem_slot, 0);
     pdl_wait();
     pdl_launch_dependents();
-    const Plan plan = plan_of<TcWork>(a, blockIdx.x, gridDim.x, 1, s_sum, s_found);
+    const Plan plan = plan_of<TcWork>(a, blockIdx.x, gridDim.x, 1, s_sum, &s_found);
     bool run = true;
     uint32_t n_seg = 0;
     // The next segment, of a whole warp.  False: none, or given up.
