@@ -13,11 +13,12 @@ namespace {
 // bits, and the Taylor series around 0 end with its 9th and 10th power (the next terms
 // are 2^-28 and 2^-31 of the results).
 //
-// Bound by the stores.  262144 positions of 64 pairs (134 MB): 21.9 us, 6.1 TB/s of the 6.8 that a
-// copy reaches (24.6 with the frequency converted in fp64; as fp64 angles through sinpi and cospi 67).  A
-// thread keeps its pair, whose frequency it converts once, and steps over positions: four CTAs to an SM
-// (6: 22.3 us, 8: 23.0) and four positions per thread at least: 4096 positions of 32 pairs 1.7 us in a
-// graph (2.4 with one, 1.8 with eight; 5.5 in fp64).
+// Bound by the stores.  262144 positions of 64 pairs (134 MB): 20.0 us, a copy's rate (6.7 TB/s).  It is
+// near what can be issued, too: 24.6 with the frequency converted in fp64, 21.9 with 64-bit arithmetic
+// for the quarter and the rest, 21.4 with two positions in place of four in flight; 67 as fp64 angles
+// through sinpi and cospi.  A thread keeps its pair, whose frequency it converts once, and steps over
+// positions: four CTAs to an SM (8: 20.3 us) and four positions per thread at least: 4096 positions
+// of 32 pairs 1.7 us in a graph (2.4 with one, 1.8 with eight; 5.5 in fp64).
 constexpr uint64_t kTurnHigh = 0x28BE60DB9391054Aull, kTurnLow = 0x7F09D5F47D4D3770ull;      // 2^128 / (2 pi)
 constexpr int kMostExp = 1023 + 20, kLeastExp = 1023 - 30;   // biased exponents: 2^20 radians per position, 2^-30
 
@@ -43,16 +44,17 @@ __device__ __forceinline__ uint64_t turns_of(uint64_t bits) {
 
 // Cosine and sine of phase 2^-64 turns.
 __device__ __forceinline__ float2 cos_sin_of(uint64_t phase) {
-    const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
-    const int64_t rest = (int64_t)(phase << 2) >> 2;             // of the nearest quarter: its two leading bits are the sign's now
+    const uint32_t high = (uint32_t)(phase >> 32) + (1u << 29);  // its two leading bits: the nearest quarter
+    const int32_t hi = (int32_t)((high & 0x3FFFFFFFu) - (1u << 29));                    // of the rest
     constexpr float UNIT = 3.14159265358979f * 0x1p-31f;         // radians of 2^-32 turns
-    const float x = fmaf((float)(int32_t)(rest >> 32), UNIT, (float)(uint32_t)rest * (UNIT * 0x1p-32f)), y = x * x;
+    const float x = fmaf((float)hi, UNIT, (float)(uint32_t)phase * (UNIT * 0x1p-32f)), y = x * x;
     float s = fmaf(y, fmaf(y, fmaf(y, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6);
     float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f);
     s = fmaf(x * y, s, x);
     c = fmaf(y, c, 1.0f);
-    const float u = quarter & 1 ? s : c, v = quarter & 1 ? c : s;
-    return make_float2((quarter + 1) & 2 ? -u : u, quarter & 2 ? -v : v);
+    const bool odd = high & 0x40000000u;
+    const uint32_t u = __float_as_uint(odd ? s : c), v = __float_as_uint(odd ? c : s);
+    return make_float2(__uint_as_float(u ^ ((high + 0x40000000u) & 0x80000000u)), __uint_as_float(v ^ (high & 0x80000000u)));
 }
 
 __global__ void __launch_bounds__(512) rope_table_kernel(TableArgs a) {
@@ -75,7 +77,9 @@ __global__ void __launch_bounds__(512) rope_table_kernel(TableArgs a) {
     const uint64_t step = fine ? turns_of(bits) : 0;
     uint64_t phase = step * (uint64_t)(a.start + n0);
     const uint64_t phases = step * (uint64_t)ahead;
-    for (int64_t n = n0; n < a.n_pos; n += ahead, out += ahead * a.half, phase += phases) {
+    const int64_t out_step = ahead * a.half;
+#pragma unroll 4
+    for (uint32_t n = (uint32_t)n0; n < (uint32_t)a.n_pos; n += (uint32_t)ahead, out += out_step, phase += phases) {      // n_pos <= 2^31
         const float2 v = cos_sin_of(phase);
         *out = make_float2(amp * v.x, amp * v.y);
     }
