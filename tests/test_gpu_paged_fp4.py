@@ -788,3 +788,40 @@ def test_a_request_that_waits_for_blocks_leaves_the_others_alone(csa2, bits):
             want = paged_ref.attention(turn(q).double(), *t, cache.k_scale[0].double().cpu(), cache.v_scale[0].double().cpu(), table, kv,
                                        cu, cache.sm_scale)
         paged_ref.check_attention(out[rows], lse[rows], want)
+
+
+def test_the_extension_makes_the_usual_calls(csa2, monkeypatch):
+    """Every call of the loop without the Python way to the library, in the bits of that way; what does not fit is refused there."""
+    gen = torch.Generator().manual_seed(70)
+    H, Hq, D, S, n, T = 2, 4, 64, 16, 6, 40
+    table = torch.randn(T, D // 2, 2, generator=gen).to(DEV)
+    q, k, v = [torch.randn(T, h, D, generator=gen).to(BF).to(DEV) for h in (Hq, H, H)]
+    pos, slots = torch.arange(T, dtype=I32, device=DEV), torch.randperm(n * S, generator=gen)[:T].to(DEV)
+    bt, kv, cu = torch.arange(n, dtype=I32, device=DEV)[None], torch.tensor([n * S], dtype=I32, device=DEV), torch.tensor([0, T], dtype=I32, device=DEV)
+    ws = csa2.workspace_for_paged_attn_fp4(1, T, Hq, H, D, T)
+    freq = torch.rand(D // 2, generator=gen, dtype=torch.float64).to(DEV)
+
+    def calls():
+        planes = [torch.zeros(n, H, S, w, dtype=U8, device=DEV) for w in (D // 2, D // 2, D // 16, D // 16)]
+        made, qr, kb, vb, out = torch.empty_like(table), torch.empty_like(q), torch.zeros_like(k), torch.zeros_like(k), torch.empty_like(q)
+        csa2.csa2_rope_table(freq, made)
+        csa2.csa2_rope(q, pos, made, q_out=qr)
+        csa2.csa2_quantize_kv_fp4_paged(k, v, slots, *planes, pos=pos, cos_sin=table)
+        csa2.csa2_dequantize_kv_fp4_paged(slots, *planes, kb, vb)
+        csa2.csa2_paged_attn_fp4(qr, *planes, bt, kv, cu, out, 0.1, T, workspace=ws)
+        torch.cuda.synchronize()
+        return [made, qr, *planes, kb, vb, out]
+
+    with monkeypatch.context() as m:
+        m.setattr(csa2, "_lib", None)
+        quick = calls()
+        for bad in (pos[:-1], pos.long(), pos.cpu()):
+            with pytest.raises((TypeError, ValueError, AttributeError)):
+                csa2.csa2_rope(q, bad, table)
+    with monkeypatch.context() as m:
+        m.setattr(csa2, "_csa2_bind", type("Nothing", (), {"__getattr__": lambda self, name: lambda *a: None})())
+        slow = calls()
+    for a, b in zip(quick, slow):
+        assert torch.equal(a, b)
+    with pytest.raises(csa2.Csa2Error):
+        csa2.csa2_rope(q, pos, table, first=8)                           # fits the call, and is refused behind it
