@@ -612,9 +612,13 @@ __device__ __forceinline__ void join_unit(const PagedAttnArgs &a, const JoinUnit
 }
 
 // The first blocks join the split kernel's units of 8 NT rows, 4 rows each; the
-// others the tile kernel's of 256 rows, 16 rows each.
-template <int D, int NT, bool HALF>
-__global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a, int split_ctas, int tc_ctas) {
+// others the tile kernel's of 256 rows, 16 rows each.  Blocks of an SM: what holds all of the split
+// kernel's units at once, whose join is a chain of loads.  The 8-bit cache's two CTAs per SM leave 4, the
+// 4-bit cache's three 6 (64 requests of up to 16k tokens over 4 bits 127.1 us, 128.7 with 4; of
+// 131k over 8 bits 51.4, 51.9 with 6).
+constexpr int kJoinPerSm = 4, kJoinPerSm4 = 6;
+template <int D, int NT, bool HALF, int PER_SM>
+__global__ void __launch_bounds__(128, PER_SM) paged_attn_join_kernel(PagedAttnArgs a, int split_ctas, int tc_ctas) {
     constexpr int JR = 4, JB = 8 * NT / JR;                    // rows per block, blocks per unit
     __shared__ float s_o[4][4][D + 4];
     pdl_wait();
@@ -628,10 +632,10 @@ __global__ void __launch_bounds__(128) paged_attn_join_kernel(PagedAttnArgs a, i
                                              reinterpret_cast<float (*)[4][D + 4]>(s_o));
 }
 
-template <int D, int NT, bool HALF>
+template <int D, int NT, bool HALF, int PER_SM>
 cudaError_t launch_join(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cudaStream_t stream) {
     constexpr int JB = 2 * NT;
-    return launch_pdl(paged_attn_join_kernel<D, NT, HALF>, dim3(JB * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
+    return launch_pdl(paged_attn_join_kernel<D, NT, HALF, PER_SM>, dim3(JB * split_ctas + 16 * tc_ctas), dim3(128), 0, stream, a,
                       split_ctas, tc_ctas);
 }
 
@@ -653,7 +657,7 @@ cudaError_t launch_attn(const PagedAttnArgs &a, int split_ctas, int tc_ctas, cud
         e = launch_paged_attn_tc(a, D, HALF, false, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_join<D, NT, HALF>(a, split_ctas, tc_ctas, stream);
+    return launch_join<D, NT, HALF, kJoinPerSm>(a, split_ctas, tc_ctas, stream);
 }
 
 template <int D, bool HALF>
@@ -689,10 +693,10 @@ inline size_t split_partial_floats(const Choice &c, int D) { return (size_t)2 * 
 }  // namespace
 
 cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, int D, int NT, bool half, int split_ctas, int tc_ctas, cudaStream_t stream) {
-    auto go = D == 64 ? (NT == 1 ? (half ? launch_join<64, 1, true> : launch_join<64, 1, false>)
-                                 : (half ? launch_join<64, 2, true> : launch_join<64, 2, false>))
-                      : (NT == 1 ? (half ? launch_join<128, 1, true> : launch_join<128, 1, false>)
-                                 : (half ? launch_join<128, 2, true> : launch_join<128, 2, false>));
+    auto go = D == 64 ? (NT == 1 ? (half ? launch_join<64, 1, true, kJoinPerSm4> : launch_join<64, 1, false, kJoinPerSm4>)
+                                 : (half ? launch_join<64, 2, true, kJoinPerSm4> : launch_join<64, 2, false, kJoinPerSm4>))
+                      : (NT == 1 ? (half ? launch_join<128, 1, true, kJoinPerSm4> : launch_join<128, 1, false, kJoinPerSm4>)
+                                 : (half ? launch_join<128, 2, true, kJoinPerSm4> : launch_join<128, 2, false, kJoinPerSm4>));
     return go(a, split_ctas, tc_ctas, stream);
 }
 

@@ -316,7 +316,7 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs &a, int64_t o_row,
 csa2_status check_paged_attn(int B, int64_t T, int Hq, int Hkv, int D, csa2_dtype dt, int64_t q_token_stride,
                              int64_t q_head_stride, int64_t n_blocks, int S, int M, int64_t table_stride, int max_new, int window);
 
-// The join kernel (paged_attn.cu): adds up the parts of the units that split_ctas CTAs of a
+// The join kernel (paged_attn.cu) for the 4-bit cache: adds up the parts of the units that split_ctas CTAs of its
 // split kernel with row tiles of 8 NT and tc_ctas of the tile kernel shared.
 cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, int D, int NT, bool half, int split_ctas, int tc_ctas, cudaStream_t stream);
 

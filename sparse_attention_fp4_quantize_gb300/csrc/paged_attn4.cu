@@ -11,14 +11,14 @@
 // stay below f16's end.
 //
 // The split kernel (this file) has a warp walk over tiles of 64 keys.  64 requests of up to
-// 16k tokens, 64 heads of 128 over 8 (687 MB): 128.5 us with the join, 5.3 TB/s, a copy's rate
+// 16k tokens, 64 heads of 128 over 8 (687 MB): 127 us with the join, 5.4 TB/s, a copy's rate
 // 6.8; with its loads alone 110.  What it lacks are instructions' slots: of the 289 that a warp
 // issues per 16 keys 128 turn codes into f16 and apply the scales, the schedulers issue 0.6 a cycle
 // with 3 warps each, the codes' pipe is busy for 54 % and the tensor cores for 27.  CTAs of an SM end
 // 7 us apart, but shares that make up for it (5 to 15 % more for the first) only slow the last ones'
 // keys down: 131 to 141 us.  48 requests with 5 new tokens in a window of 4096, 15 heads of 64
 // over 5 (61 MB): 33 us, of which 5 go by before the first tile (lengths, table, codes, each after
-// the other) and 3 in the join; the loads alone take 20.  One request of 1000 tokens: 9.1 us in a
+// the other) and 3 in the join; the loads alone take 20.  One request of 1000 tokens: 8.8 us in a
 // graph, 1.6 of them a warp's tile.
 #include "fp4.cuh"
 #include "paged_attn.cuh"

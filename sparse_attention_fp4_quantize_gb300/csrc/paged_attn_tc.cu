@@ -35,7 +35,7 @@
 // stay in uniform registers: as one thread's work each product waited for them to be moved
 // there, 94 cycles a product instead of 42 of 64 channels (845 against 783 us over 8 bits, 818
 // against 761 over 4; 730 against 654 of 64 channels).  Tried and slower: P handed over in
-// two halves of 64 keys (1035 against 923 us as first built), E4M3 codes kept in
+// two halves of 64 keys (784 against 734 us), E4M3 codes kept in
 // registers instead of staged (934 against 906 then; over 4 bits the same), the lock given up
 // with half of S to go (750 against 741), before S (772 against 760) or left out (792
 // against 745), strict turns by mbarriers in its place (771 against 745), waits that poll
