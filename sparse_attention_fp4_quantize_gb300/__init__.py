@@ -112,8 +112,10 @@ from . import _csa2_bind  # noqa: E402  (built with the library)
 def _bind(lib, current_stream=None, current_device=None):
     """The extension makes the calls of this library."""
     names = ("csa2_rope_table", "csa2_rope", "csa2_quantize_kv_fp4_paged", "csa2_dequantize_kv_fp4_paged", "csa2_paged_attn_fp4")
+    nothing = lambda *a: None  # noqa: E731  (a torch without CUDA: every call goes the Python way)
     _csa2_bind.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names],
-                    current_stream or torch._C._cuda_getCurrentRawStream, current_device or torch._C._cuda_getDevice)
+                    current_stream or getattr(torch._C, "_cuda_getCurrentRawStream", nothing),
+                    current_device or getattr(torch._C, "_cuda_getDevice", nothing))
 
 
 _bind(_lib)
