@@ -15,8 +15,9 @@
 // midpoints back and carries no other value across one.
 //
 // Bound by memory and, in the append, nearly as much by issue (0.56 instructions per cycle).  16384
-// tokens, 8 heads of 128, keys rotated, with the stored values (152 MB): 28.6 us, 5.3 TB/s of a
-// copy's 6.8; a decode step's 64 tokens 2.4 us in a graph.
+// tokens, 8 heads of 128, keys rotated, with the stored values (152 MB): 27.6 us, 5.5 TB/s of a
+// copy's 6.8 (40000 tokens 59.9, 6.2 TB/s); a decode step's 64 tokens 2.1 us in a graph.  28.5, 61.8 and 2.3 with
+// a row's loads behind those of its place.
 #include "fp4.cuh"
 
 namespace csa2 {
@@ -160,12 +161,12 @@ __device__ __forceinline__ void store_group(const Quant4Args &a, bool is_v, int 
 // Where a token's row goes: false, and a flag if that is an error, if it is not stored.
 __device__ __forceinline__ bool place_of(const Quant4Args &a, int64_t t, bool first_thread, int64_t &row0, int64_t &p) {
     const int64_t slot = a.slots[t];
+    p = a.rope.table ? a.rope.pos[t] : 0;                // on its way beside the slot
     if (slot < 0 || slot >= a.n_slots) {
         if (slot != -1 && first_thread) flag_error(a.err_flag, CSA2_FLAG_BAD_SLOT);
         return false;
     }
     if (a.rope.table) {              // a token without a position is not stored
-        p = a.rope.pos[t];
         if (p < 0 || p >= a.rope.n_pos) {
             if (first_thread) flag_error(a.err_flag, CSA2_FLAG_BAD_INDEX);
             return false;
@@ -228,8 +229,8 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_any_kernel(Quant4
 }
 
 // No rotation, or one of halves over the whole head: a thread takes a group and the one
-// half a row behind it, which are each other's partners, so nothing is read or turned twice: 29 us
-// where the kernel above takes 37, 27.6 without a rotation.  The next head's loads are on their way
+// half a row behind it, which are each other's partners, so nothing is read or turned twice: 27.6 us
+// where the kernel above takes 36.  The next head's loads are on their way
 // meanwhile (34.5 otherwise).
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_kernel(Quant4Args a) {
@@ -240,6 +241,15 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_kernel(Quant4Args
     const int g = threadIdx.x, far = blockDim.x, D = far * 32;
     const bool is_v = blockIdx.y >= a.chunks, turns = a.rope.table && !is_v;
     const int chunk = is_v ? blockIdx.y - a.chunks : blockIdx.y;
+    const int64_t hs = of(a.head_stride, is_v);
+    const uint16_t *x = of(a.x, is_v) + t * of(a.token_stride, is_v) + 16 * g;
+    const int h0 = chunk * a.per, h1 = min(a.H, h0 + a.per);
+    uint4 next[4];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const uint4 *>(x + h * hs + (i >> 1) * (D / 2) + (i & 1) * 8);
+    };
+    load(h0);                        // beside the chain of slot, position and table row
     int64_t row0, p;
     if (!place_of(a, t, g == 0 && blockIdx.y == 0, row0, p)) return;
     float2 cs[16];
@@ -251,15 +261,6 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_kernel(Quant4Args
             cs[2 * k] = make_float2(v.x, v.y), cs[2 * k + 1] = make_float2(v.z, v.w);
         }
     }
-    const int64_t hs = of(a.head_stride, is_v);
-    const uint16_t *x = of(a.x, is_v) + t * of(a.token_stride, is_v) + 16 * g;
-    const int h0 = chunk * a.per, h1 = min(a.H, h0 + a.per);
-    uint4 next[4];
-    auto load = [&](int h) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) next[i] = *reinterpret_cast<const uint4 *>(x + h * hs + (i >> 1) * (D / 2) + (i & 1) * 8);
-    };
-    load(h0);
     for (int h = h0; h < h1; ++h) {
         uint32_t w[2][8] = {{next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w},
                             {next[2].x, next[2].y, next[2].z, next[2].w, next[3].x, next[3].y, next[3].z, next[3].w}};
