@@ -35,9 +35,9 @@ constexpr int per_sm4(int D, int NT) { return D == 128 && NT == 2 ? 2 : 3; }
 // Tiles that a unit's fixed cost counts as (64 requests as above 136 us, 137 with 4, 141 with 16; in a
 // window 38.7, 39.3 and 41.2, as measured then).
 constexpr int kCost4 = 8;
-template <int D>
+template <int D, int LGK>
 struct Stage4 {                         // a tile in shared memory: codes and scales of its keys and of its values
-    static constexpr int LOG_KEYS = 6, KEYS = 1 << LOG_KEYS;  // of a warp's tile
+    static constexpr int KEYS = 1 << LGK;                    // of a warp's tile
     static constexpr int CODES = KEYS * D / 2, SCALES = KEYS * D / 16;
     static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = KS + SCALES, BYTES = VS + SCALES;
     static constexpr int N = 2;                              // of them per warp
@@ -87,12 +87,13 @@ __device__ __forceinline__ uint32_t chunk4_at(int r, int c) { return D == 128 ? 
 //   P^T  C transposed 8 x 8 at a time.
 //   O^T  A: lane g's channels are [g D/8, (g+1) D/8), of which 2 j, 2 j + 1 are rows g and
 //        g + 8 of MMA j; C: those channels of query rows 2 t, 2 t + 1.
-template <int D, int NT>
+template <int D, int NT, int LGK>
 struct Tile4 {
+    using St = Stage4<D, LGK>;
     static constexpr int KS = D / 16, MO = D / 16, ROW = D / 2, SROW = D / 16;
     // Keys whose scores a warp holds together: all of a tile, of 8 rows (64 requests of up to 16k tokens 128.6 us, 134.3 with
-    // 32; one of 1000 9.1 and 8.7); of 16 rows half, as more would spill (48 in a window 33.1 us, 33.5 with 64).
-    static constexpr int AT_ONCE = NT == 2 ? 32 : 64, U = AT_ONCE / 16;
+    // 32); of 16 rows half, as more would spill (48 in a window 33.1 us, 33.5 with 64).
+    static constexpr int AT_ONCE = NT == 2 || LGK == 5 ? 32 : 64, U = AT_ONCE / 16;
     uint32_t q[NT][KS][2];
     float o[NT][MO][4];
     float m[NT][2], l[NT][2];                // rows 2 t, 2 t + 1: reference (log2), sum of P of this lane's keys
@@ -143,7 +144,7 @@ struct Tile4 {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         constexpr uint32_t ALL = 0xFFFFFFFFu;
         const float NEG_INF = __int_as_float(0xff800000);
-        const uint32_t vb = kb + Stage4<D>::V + first * ROW, ksb = kb + Stage4<D>::KS + first * SROW, vsb = kb + Stage4<D>::VS + first * SROW;
+        const uint32_t vb = kb + St::V + first * ROW, ksb = kb + St::KS + first * SROW, vsb = kb + St::VS + first * SROW;
         kb += first * ROW, key0 += first, stored -= first, there >>= first / 16;
         const int kg = key_at(g);
         float s[NT][U][4];
@@ -271,16 +272,16 @@ struct Tile4 {
     }
 };
 
-template <int D>
+template <int D, int LGK>
 constexpr int split4_smem() {
-    constexpr int ring = kWarps4 * Stage4<D>::N * Stage4<D>::BYTES, merge = kWarps4 * 8 * (D + 4) * 4;
+    constexpr int ring = kWarps4 * Stage4<D, LGK>::N * Stage4<D, LGK>::BYTES, merge = kWarps4 * 8 * (D + 4) * 4;
     return ring > merge ? ring : merge;
 }
 
-template <int D, int NT, bool HALF>
+template <int D, int NT, bool HALF, int LGK>
 __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_split_kernel(PagedAttnArgs a) {
-    using St = Stage4<D>;
-    constexpr int R = 8 * NT, K = St::KEYS, ROW = D / 2, SROW = D / 16, N = St::N, LGK = St::LOG_KEYS;
+    using St = Stage4<D, LGK>;
+    constexpr int R = 8 * NT, K = St::KEYS, ROW = D / 2, SROW = D / 16, N = St::N;
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_st[kWarps4][8][2];
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
     const float NEG_INF = __int_as_float(0xff800000);
     // A tile's rows of one block are a piece: GR rows, GU pieces to a tile.
     const int lgGR = 31 - __clz(min(a.S, K)), lgGU = LGK - lgGR, GU = 1 << lgGU, GR = 1 << lgGR;
-    static_assert(K == 1 << LGK && LGK >= 5 && LGK <= 7, "pieces of a tile: blocks are 16, 32, 64 or 128 tokens");
+    static_assert(LGK >= 5 && LGK <= 7, "pieces of a tile: blocks are 16, 32, 64 or 128 tokens");
     pdl_wait();
     pdl_launch_dependents();
     using Work = SplitWork<R, K, kCost4>;
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
 #pragma unroll 1
             for (int i = 0; i < N - 1; ++i) issue(i);
 
-            Tile4<D, NT> tile;
+            Tile4<D, NT, LGK> tile;
             tile.clear();
             float zf[NT][2];
             int all_lo = 0, all_hi = 0x7FFFFFFF;     // keys that every real row of this lane sees
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
                     for (int u = 0; u < GU; ++u)
                         if ((info >> u) & 1) there |= ((1u << (GR / 16)) - 1) << (u * (GR / 16));
 #pragma unroll 1
-                for (int first = 0; first < K; first += Tile4<D, NT>::AT_ONCE)
+                for (int first = 0; first < K; first += Tile4<D, NT, LGK>::AT_ONCE)
                     tile.keys(ring + stage * St::BYTES, first, zf, masked, key, rq.kv - key, there, s_seen[warp]);
                 __syncwarp();
             }
@@ -526,12 +527,22 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
     }
 }
 
-template <int D, int NT, bool HALF>
+template <int D, int NT, bool HALF, int LGK = 6>
 cudaError_t launch_split4(const PagedAttnArgs &a, int ctas, cudaStream_t stream) {
     static bool done[64];
-    cudaError_t e = ensure_smem_limit((const void *)paged_attn4_split_kernel<D, NT, HALF>, split4_smem<D>(), done);
+    cudaError_t e = ensure_smem_limit((const void *)paged_attn4_split_kernel<D, NT, HALF, LGK>, split4_smem<D, LGK>(), done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attn4_split_kernel<D, NT, HALF>, dim3(ctas), dim3(kWarps4 * 32), split4_smem<D>(), stream, a);
+    return launch_pdl(paged_attn4_split_kernel<D, NT, HALF, LGK>, dim3(ctas), dim3(kWarps4 * 32), split4_smem<D, LGK>(), stream, a);
+}
+// Warps' tiles of 32 keys in place of 64, for 8 rows of 128 channels: a tile is done sooner, and where a
+// CTA has few of them that is what counts.  8 KV heads, tiles of 64 and of 32: 1 request of up to 1000 tokens 8.8
+// and 8.2 us, 64 of up to 1000 24.9 and 22.0, of up to 4000 47.3 and 45.6, of up to 8000 72.0 and 75.4,
+// of up to 16k 127.7 and 136.3; 8 of up to 32k 40.3 and 39.8.  The lengths are the GPU's: the rule goes by
+// what the tables (or the windows) could hold, at most so many tiles of 64 keys per CTA.
+constexpr int kShort4 = 96;
+inline bool few_keys4(const PagedAttnArgs &a, int max_new, int ctas) {
+    const int64_t most = (int64_t)a.M * a.S, keys = a.window > 0 && a.window + (int64_t)max_new < most ? a.window + (int64_t)max_new : most;
+    return (int64_t)a.B * a.Hkv * ((keys + 63) / 64) <= (int64_t)kShort4 * ctas;
 }
 
 // Requests of more rows per KV head than this are the tile kernel's.  24 requests of up to 16k tokens,
@@ -600,7 +611,9 @@ extern "C" csa2_status csa2_paged_attn_fp4(int B, int64_t T, int Hq, int Hkv, in
     const bool half = dt == CSA2_FP16;
     auto go = D == 64 ? (c.NT == 1 ? (half ? launch_split4<64, 1, true> : launch_split4<64, 1, false>)
                                    : (half ? launch_split4<64, 2, true> : launch_split4<64, 2, false>))
-                      : (c.NT == 1 ? (half ? launch_split4<128, 1, true> : launch_split4<128, 1, false>)
+                      : (c.NT == 1 ? (few_keys4(a, max_new, c.split_ctas)
+                                          ? (half ? launch_split4<128, 1, true, 5> : launch_split4<128, 1, false, 5>)
+                                          : (half ? launch_split4<128, 1, true> : launch_split4<128, 1, false>))
                                    : (half ? launch_split4<128, 2, true> : launch_split4<128, 2, false>));
     if (c.split_ctas) CSA2_CUDA_CALL(go(a, c.split_ctas, stream_of(stream)), "paged_attn launch");
     if (c.tc_ctas) CSA2_CUDA_CALL(launch_paged_attn_tc(a, D, half, true, stream_of(stream)), "paged_attn tile launch");
