@@ -10,7 +10,7 @@
 // their sum in fp32 before that.  M may lag behind the maximum as long as the weights
 // stay below f16's end.
 //
-// The split kernel (this file) has a warp walk over tiles of 64 keys.  64 requests of up to
+// The split kernel (this file) has a warp walk over tiles of 64 keys (few_keys4: or 32).  64 requests of up to
 // 16k tokens, 64 heads of 128 over 8 (687 MB): 127 us with the join, 5.4 TB/s, a copy's rate
 // 6.8; with its loads alone 110.  What it lacks are instructions' slots: of the 289 that a warp
 // issues per 16 keys 128 turn codes into f16 and apply the scales, the schedulers issue 0.6 a cycle
@@ -18,8 +18,8 @@
 // 7 us apart, but shares that make up for it (5 to 15 % more for the first) only slow the last ones'
 // keys down: 131 to 141 us.  48 requests with 5 new tokens in a window of 4096, 15 heads of 64
 // over 5 (61 MB): 33 us, of which 5 go by before the first tile (lengths, table, codes, each after
-// the other) and 3 in the join; the loads alone take 20.  One request of 1000 tokens: 8.8 us in a
-// graph, 1.6 of them a warp's tile.
+// the other) and 3 in the join; the loads alone take 20.  One request of 1000 tokens: 8.4 us in a
+// graph.
 #include "fp4.cuh"
 #include "paged_attn.cuh"
 
@@ -305,8 +305,11 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
     // this lane's chunk of a copy by the warp, 512 bytes: 8 or 16 rows
     constexpr int CPR = D / 32, RPC = 32 / CPR;
     const uint32_t lane_to = chunk4_at<D>(lane / CPR, lane % CPR);
-    constexpr bool BOTH = St::SCALES == 256;         // one copy takes the keys' and the values' scales
-    static_assert(BOTH || St::SCALES == 512, "a lane's chunk of each plane's scales, or of one's");
+    constexpr int SC = St::SCALES / 16;              // chunks of a plane's scales
+    constexpr bool BOTH = SC <= 16;                  // one copy takes the keys' and the values'
+    static_assert(BOTH || SC == 32, "a lane's chunk of each plane's scales, or of one's");
+    const bool scales = !BOTH || lane < 2 * SC, of_v = BOTH && lane >= SC;
+    const int sc_at = BOTH ? lane & (SC - 1) : lane;
     static_assert(RPC % 4 == 0 && RPC <= 16, "the order of a row's chunks goes by its number modulo 4");
     int64_t base = plan.base;
     for (int b = plan.b; at < stop && b < a.B; ++b) {
@@ -376,8 +379,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
                                 cp_async16(dst + St::K + lane_to + 512 * x, kc + 512 * x, 16);
                                 cp_async16(dst + St::V + lane_to + 512 * x, vc + 512 * x, 16);
                             }
-                            const uint8_t *sc = (BOTH && lane >= 16 ? a.v_scale4 : a.k_scale4) + row * SROW + 16 * (BOTH ? lane & 15 : lane);
-                            cp_async16(dst + St::KS + 16 * lane, sc, 16);
+                            if (scales) cp_async16(dst + St::KS + 16 * lane, (of_v ? a.v_scale4 : a.k_scale4) + row * SROW + 16 * sc_at, 16);
                             if (!BOTH) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + row * SROW + 16 * lane, 16);
                         }
                     } else {
@@ -390,10 +392,10 @@ __global__ void __launch_bounds__(kWarps4 * 32, per_sm4(D, NT)) paged_attn4_spli
                                 cp_async16(dst + St::V + lane_to + 512 * x, a.v_codes + at, 16);
                             }
                         }
-                        const int r = (BOTH ? lane & 15 : lane) * (16 / SROW);          // first row of this lane's scales
+                        const int r = sc_at * (16 / SROW);                   // first row of this lane's scales
                         const int64_t row = __shfl_sync(ALL, off, who + (r >> lgGR)), at = (row + (r & (GR - 1))) * SROW;
-                        if (row >= 0) {
-                            cp_async16(dst + St::KS + 16 * lane, (BOTH && lane >= 16 ? a.v_scale4 : a.k_scale4) + at, 16);
+                        if (row >= 0 && scales) {
+                            cp_async16(dst + St::KS + 16 * lane, (of_v ? a.v_scale4 : a.k_scale4) + at, 16);
                             if (!BOTH) cp_async16(dst + St::VS + 16 * lane, a.v_scale4 + at, 16);
                         }
                     }
@@ -534,15 +536,16 @@ cudaError_t launch_split4(const PagedAttnArgs &a, int ctas, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_attn4_split_kernel<D, NT, HALF, LGK>, dim3(ctas), dim3(kWarps4 * 32), split4_smem<D, LGK>(), stream, a);
 }
-// Warps' tiles of 32 keys in place of 64, for 8 rows of 128 channels: a tile is done sooner, and where a
-// CTA has few of them that is what counts.  8 KV heads, tiles of 64 and of 32: 1 request of up to 1000 tokens 8.8
+// Warps' tiles of 32 keys in place of 64, for 8 rows: a tile is done sooner, and where a CTA has few of
+// them that is what counts.  8 KV heads, tiles of 64 and of 32: 1 request of up to 1000 tokens 8.8
 // and 8.2 us, 64 of up to 1000 24.9 and 22.0, of up to 4000 47.3 and 45.6, of up to 8000 72.0 and 75.4,
-// of up to 16k 127.7 and 136.3; 8 of up to 32k 40.3 and 39.8.  The lengths are the GPU's: the rule goes by
-// what the tables (or the windows) could hold, at most so many tiles of 64 keys per CTA.
-constexpr int kShort4 = 96;
-inline bool few_keys4(const PagedAttnArgs &a, int max_new, int ctas) {
+// of up to 16k 127.7 and 136.3; 8 of up to 32k 40.3 and 39.8.  Of 64 channels 1 of up to 1000 7.4 and 7.0, 64 of up
+// to 1000 16.9 and 15.6, of up to 2000 21.8 and 22.7, 8 of up to 8000 12.9 and 13.2.  The lengths are the
+// GPU's: the rule goes by what the tables (or the windows) could hold, at most so many tiles of 64 keys per CTA.
+constexpr int few4(int D) { return D == 128 ? 96 : 16; }
+inline bool few_keys4(const PagedAttnArgs &a, int D, int max_new, int ctas) {
     const int64_t most = (int64_t)a.M * a.S, keys = a.window > 0 && a.window + (int64_t)max_new < most ? a.window + (int64_t)max_new : most;
-    return (int64_t)a.B * a.Hkv * ((keys + 63) / 64) <= (int64_t)kShort4 * ctas;
+    return (int64_t)a.B * a.Hkv * ((keys + 63) / 64) <= (int64_t)few4(D) * ctas;
 }
 
 // Requests of more rows per KV head than this are the tile kernel's.  24 requests of up to 16k tokens,
@@ -609,9 +612,11 @@ extern "C" csa2_status csa2_paged_attn_fp4(int B, int64_t T, int Hq, int Hkv, in
                              v_scales, block_table, kv_len, cu_len, sm_scale * 1.4426950408889634f, (uint16_t *)out, lse,
                              err_flag, c.split_rows, join, join + c.split_ctas, partial, partial + partial4_floats(c, D)};
     const bool half = dt == CSA2_FP16;
-    auto go = D == 64 ? (c.NT == 1 ? (half ? launch_split4<64, 1, true> : launch_split4<64, 1, false>)
+    auto go = D == 64 ? (c.NT == 1 ? (few_keys4(a, D, max_new, c.split_ctas)
+                                          ? (half ? launch_split4<64, 1, true, 5> : launch_split4<64, 1, false, 5>)
+                                          : (half ? launch_split4<64, 1, true> : launch_split4<64, 1, false>))
                                    : (half ? launch_split4<64, 2, true> : launch_split4<64, 2, false>))
-                      : (c.NT == 1 ? (few_keys4(a, max_new, c.split_ctas)
+                      : (c.NT == 1 ? (few_keys4(a, D, max_new, c.split_ctas)
                                           ? (half ? launch_split4<128, 1, true, 5> : launch_split4<128, 1, false, 5>)
                                           : (half ? launch_split4<128, 1, true> : launch_split4<128, 1, false>))
                                    : (half ? launch_split4<128, 2, true> : launch_split4<128, 2, false>));

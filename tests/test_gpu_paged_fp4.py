@@ -388,6 +388,45 @@ def test_garbage_behind_the_last_token(csa2, new, D, S):
     paged_ref.check_attention(out, lse, want)
 
 
+def _widened(inp, tokens=1 << 22):
+    """The same call with a table that could hold so many tokens of each request."""
+    table, S = inp[5], inp[1].shape[2]
+    wide = torch.full((table.shape[0], tokens // S), -1, dtype=I32)
+    wide[:, :table.shape[1]] = table
+    return [*inp[:5], wide, *inp[6:]]
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("S", [16, 32, 64, 128])
+@pytest.mark.parametrize("D,Hq", [(64, 8), (128, 8), (64, 14), (128, 24)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_tables_that_could_hold_long_contexts(csa2, dtype, S, D, Hq, window):
+    """The longer tiles that few rows get with them, next to those of the same call with tables that just fit; anything may
+    lie behind the last token."""
+    kv, new = [1, 2, 63, 64, 65, 700, 2051, 0, 130], [1, 2, 1, 2, 1, 1, 2, 1, 0]
+    inp = _inputs(80 + S, kv, new, Hq, 2, D, S, dtype)
+    for b, n in enumerate(kv):
+        if n % S:
+            last = int(inp[5][b, n // S])
+            for plane in inp[1:3]:
+                plane[last, :, n % S:] = 255
+            for plane in inp[3:5]:
+                plane[last, :, n % S:] = 127                             # NaN
+    want = _reference(inp, 0.2, window)
+    for x in (_widened(inp), inp):
+        err = torch.zeros(1, dtype=I32, device=DEV)
+        out, lse = _attend(csa2, x, 0.2, 2, window, pad=3, err=err)
+        paged_ref.check_attention(out, lse, want)
+        assert int(err) == 0
+
+
+@pytest.mark.parametrize("kv,new,Hq,H,D,S,window", ATTN_CASES)
+def test_attention_matches_reference_with_wide_tables(csa2, kv, new, Hq, H, D, S, window):
+    inp = _inputs(81, kv, new, Hq, H, D, S)
+    out, lse = _attend(csa2, _widened(inp), 0.3, max(new), window)
+    paged_ref.check_attention(out, lse, _reference(inp, 0.3, window))
+
+
 @pytest.mark.parametrize("new", [1, 90])
 def test_query_rows_do_not_meet(csa2, new):
     """A row of infinities or NaN spoils itself only; magnitudes far from one are exact or nearly."""
