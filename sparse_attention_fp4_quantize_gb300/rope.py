@@ -68,8 +68,13 @@ class Rope:
             if self.factor != 1.0:
                 raise ValueError("a factor stretches theta's frequencies, not those of inv_freq")
         else:
+            if not 0.0 < self.theta < math.inf or not 1.0 <= self.factor < math.inf:
+                raise ValueError("theta=%r must be above 0, factor=%r at least 1" % (self.theta, self.factor))
             f, amplitude = self.theta ** (-torch.arange(0, self.dim, 2, dtype=torch.float64) / self.dim), 1.0
             if self.factor != 1.0:
+                if not (self.theta > 1.0 and self.original > 0 and self.fast > self.slow > 0.0):
+                    raise ValueError("a stretched context wants theta=%r > 1, original=%r > 0 and fast=%r > slow=%r > 0" %
+                                     (self.theta, self.original, self.fast, self.slow))
                 keep = self._keep(f)
                 f, amplitude = f * keep + f / self.factor * (1.0 - keep), 0.1 * math.log(self.factor) + 1.0
         return f, amplitude if self.amplitude is None else float(self.amplitude)

@@ -71,3 +71,14 @@ def test_frequencies_of_the_caller():
     for bad in (dict(inv_freq=own[:7]), dict(inv_freq=[own]), dict(inv_freq=own, factor=2.0), dict(ramp="linear", factor=2.0)):
         with pytest.raises(ValueError):
             Rope(16, **bad).frequencies()
+
+
+@pytest.mark.parametrize("bad", [dict(theta=-10000.0), dict(theta=0.0), dict(theta=math.nan), dict(theta=math.inf), dict(factor=0.5), dict(factor=0.0),
+                                 dict(factor=-2.0), dict(factor=math.nan), dict(factor=math.inf), dict(factor=2.0, theta=1.0),
+                                 dict(factor=2.0, original=0), dict(factor=2.0, original=-4096), dict(factor=2.0, fast=1.0),
+                                 dict(factor=2.0, fast=0.5), dict(factor=2.0, slow=0.0), dict(factor=2.0, slow=-1.0),
+                                 dict(factor=2.0, fast=math.nan)])
+@pytest.mark.parametrize("ramp", ["index", "turns"])
+def test_frequencies_without_a_meaning_are_refused(ramp, bad):
+    with pytest.raises(ValueError, match="theta|factor|original|fast"):
+        Rope(64, ramp=ramp, **bad).frequencies()
