@@ -72,7 +72,7 @@ class Rope:
                 raise ValueError("theta=%r must be above 0, factor=%r at least 1" % (self.theta, self.factor))
             f, amplitude = self.theta ** (-torch.arange(0, self.dim, 2, dtype=torch.float64) / self.dim), 1.0
             if self.factor != 1.0:
-                if not (self.theta > 1.0 and self.original > 0 and self.fast > self.slow > 0.0):
+                if not (self.theta > 1.0 and self.original > 0 and self.fast > self.slow >= 0.0 and (self.slow > 0.0 or self.ramp == "turns")):
                     raise ValueError("a stretched context wants theta=%r > 1, original=%r > 0 and fast=%r > slow=%r > 0" %
                                      (self.theta, self.original, self.fast, self.slow))
                 keep = self._keep(f)

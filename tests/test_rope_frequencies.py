@@ -76,9 +76,17 @@ def test_frequencies_of_the_caller():
 @pytest.mark.parametrize("bad", [dict(theta=-10000.0), dict(theta=0.0), dict(theta=math.nan), dict(theta=math.inf), dict(factor=0.5), dict(factor=0.0),
                                  dict(factor=-2.0), dict(factor=math.nan), dict(factor=math.inf), dict(factor=2.0, theta=1.0),
                                  dict(factor=2.0, original=0), dict(factor=2.0, original=-4096), dict(factor=2.0, fast=1.0),
-                                 dict(factor=2.0, fast=0.5), dict(factor=2.0, slow=0.0), dict(factor=2.0, slow=-1.0),
+                                 dict(factor=2.0, fast=0.5), dict(factor=2.0, slow=-1.0),
                                  dict(factor=2.0, fast=math.nan)])
 @pytest.mark.parametrize("ramp", ["index", "turns"])
 def test_frequencies_without_a_meaning_are_refused(ramp, bad):
     with pytest.raises(ValueError, match="theta|factor|original|fast"):
         Rope(64, ramp=ramp, **bad).frequencies()
+
+
+def test_a_ramp_in_turns_may_end_at_none():
+    f, _ = Rope(64, factor=2.0, slow=0.0, ramp="turns").frequencies()
+    want = [p * (0.5 + 0.5 * min(4096 * p / (2 * math.pi) / 32, 1.0)) for p in _plain(64, 10000.0).tolist()]
+    assert torch.allclose(f, torch.tensor(want, dtype=F64), rtol=1e-13, atol=0.0)
+    with pytest.raises(ValueError, match="slow"):
+        Rope(64, factor=2.0, slow=0.0).frequencies()                     # no pair makes no turns
