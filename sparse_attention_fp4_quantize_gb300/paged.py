@@ -99,7 +99,7 @@ class PagedCache:
                   err_flag=self.err, stream=stream)
         return out
 
-    def append(self, layer: int, k, v, k_values=None, v_values=None, stream=None):
+    def append(self, layer: int, k, v, stream=None, *, k_values=None, v_values=None):
         """Store the layer's new rows k, v [tokens, kv_heads, dim].  k_values, v_values (4 bits): buffers of their shape that
         get what is stored."""
         planes = self.k_codes[layer], self.v_codes[layer], self.k_scale[layer], self.v_scale[layer]
