@@ -54,6 +54,6 @@ def test_append_gives_the_stored_values_by_name(calls):
     kv, values = torch.zeros(4, 2, 64, dtype=BF), [torch.zeros(4, 2, 64, dtype=BF) for _ in range(2)]
     _cache(4).append(0, kv, kv, 77, k_values=values[0], v_values=values[1])
     (name, args), = calls.calls
-    assert [p.value for p in args[-4:-2]] == [t.data_ptr() for t in values] and args[-1] == 77
+    assert list(args[-4:-2]) == [t.data_ptr() for t in values] and args[-1] == 77
     with pytest.raises(TypeError):
         _cache(4).append(0, kv, kv, 77, *values)
