@@ -26,7 +26,9 @@ same cache in 4 bits (``csa2_quantize_kv_fp4_paged``,
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
+import warnings
 
 import torch
 
@@ -106,7 +108,20 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
-from . import _csa2_bind  # noqa: E402  (built with the library)
+
+class _NoBinding:
+    """In place of the extension: what it would make, the Python functions do."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+try:
+    _csa2_bind = importlib.import_module("._csa2_bind", __name__)        # built with the library
+except ImportError as e:
+    warnings.warn("the quick binding cannot be used (%s): rotary and 4-bit cache calls take some microseconds longer; "
+                  "build.py makes it" % e, RuntimeWarning)
+    _csa2_bind = _NoBinding()
 
 
 def _bind(lib, current_stream=None, current_device=None):

@@ -1,0 +1,67 @@
+"""The package without its quick binding: everything works the Python way, and a binding that cannot be used is as one that
+is not there (CPU)."""
+from __future__ import annotations
+
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NAME = "sparse_attention_fp4_quantize_gb300"
+PACKAGE = os.path.join(ROOT, NAME)
+
+# Calls of every function that the binding has, on tensors of the CPU with a stand-in for the library.
+CALLS = """
+import warnings
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    import %s as csa2
+print([str(w.message) for w in seen if "quick binding" in str(w.message)])
+import sys, torch
+sys.path.insert(0, %r)
+import test_paged_fp4_checks as t
+csa2._lib, csa2._on_device, csa2._stream = t._FakeLib(), lambda x: True, lambda s: None
+for fn, args in t.BINDINGS:
+    getattr(csa2, fn)(**args())
+print(csa2._lib.calls == [fn for fn, _ in t.BINDINGS])
+csa2._bind(t.REAL)
+print(t.REAL.csa2_version())
+""" % (NAME, os.path.join(ROOT, "tests"))
+
+
+@pytest.fixture(scope="module")
+def built():
+    import __graft_entry__
+    __graft_entry__._build_module().build()
+
+
+def _package(tmp_path, binding):
+    """A copy of the package (by links) with this binding, or none."""
+    at = tmp_path / NAME
+    at.mkdir()
+    for f in os.listdir(PACKAGE):
+        if f.endswith(".py") or f == "libcsa2.so":
+            os.symlink(os.path.join(PACKAGE, f), at / f)
+    if binding is not None:
+        (at / "_csa2_bind.so").write_bytes(binding)
+    r = subprocess.run([sys.executable, "-c", CALLS], cwd=tmp_path, capture_output=True, text=True,
+                       env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert r.returncode == 0, r.stderr
+    return r.stdout.splitlines()
+
+
+def _binding():
+    with open(os.path.join(PACKAGE, "_csa2_bind.so"), "rb") as f:
+        return f.read()
+
+
+def test_the_package_works_with_its_binding(built, tmp_path):
+    assert _package(tmp_path, _binding()) == ["[]", "True", "100"]
+
+
+@pytest.mark.parametrize("binding", [None, b"", b"no library"])
+def test_the_package_works_without_its_binding(built, tmp_path, binding):
+    said, called, version = _package(tmp_path, binding)
+    assert "quick binding" in said and called == "True" and version == "100"
