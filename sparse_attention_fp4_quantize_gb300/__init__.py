@@ -28,6 +28,7 @@ from __future__ import annotations
 import ctypes
 import importlib
 import os
+import sysconfig
 import warnings
 
 import torch
@@ -118,6 +119,10 @@ class _NoBinding:
 
 try:
     _csa2_bind = importlib.import_module("._csa2_bind", __name__)        # built with the library
+    _here = "torch %s, %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+    _its = getattr(_csa2_bind, "built_for", "an unknown one")
+    if _its != _here:
+        raise ImportError("it is for %s, this is %s" % (_its, _here))
 except ImportError as e:
     warnings.warn("the quick binding cannot be used (%s): rotary and 4-bit cache calls take some microseconds longer; "
                   "build.py makes it" % e, RuntimeWarning)

@@ -7,6 +7,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -38,19 +39,33 @@ def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "csa2.h"), __file__]
 
 
+def _torch() -> str:
+    """The installed torch's folder (found, not imported)."""
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def built_for() -> str:
+    """What the extension is built against and holds as a text, so that another torch's or Python's is told apart."""
+    version = runpy.run_path(os.path.join(_torch(), "version.py"))["__version__"]
+    return "torch %s, %s" % (version, sysconfig.get_config_var("SOABI"))
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    with open(BIND, "rb") as f:
+        if built_for().encode() not in f.read():
+            return False
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
 def _build_bind():
-    """The extension, against the installed torch (found, not imported)."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """The extension, against the installed torch."""
+    torch = _torch()
     lib = os.path.join(torch, "lib")
     tmp = BIND + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", '-DCSA2_BUILT_FOR="%s"' % built_for(), "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(torch, "include"), os.path.join(CSRC, "bind.cpp"), "-o", tmp, "-L", lib, "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -319,4 +319,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_csa2_bind", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__csa2_bind() { return PyModule_Create(&module); }
+// built_for: the torch and Python whose objects the functions read; the package uses them with no other.
+PyMODINIT_FUNC PyInit__csa2_bind() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", CSA2_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}

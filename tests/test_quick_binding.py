@@ -65,3 +65,31 @@ def test_the_package_works_with_its_binding(built, tmp_path):
 def test_the_package_works_without_its_binding(built, tmp_path, binding):
     said, called, version = _package(tmp_path, binding)
     assert "quick binding" in said and called == "True" and version == "100"
+
+
+def test_the_package_leaves_a_binding_for_another_torch_alone(built, tmp_path):
+    """at::Tensor's layout is another's there: the binding says what it was built for."""
+    import torch
+    mine = ("torch %s," % torch.__version__).encode()
+    other = mine[:-2] + (b"9" if mine[-2:-1] != b"9" else b"8") + b","
+    assert _binding().count(mine) == 1
+    said, called, version = _package(tmp_path, _binding().replace(mine, other))
+    assert "quick binding" in said and other.decode() in said and called == "True" and version == "100"
+
+
+def test_the_package_leaves_a_binding_that_says_nothing_alone(built, tmp_path):
+    said, called, version = _package(tmp_path, _binding().replace(b"built_for\0", b"built_xyz\0"))
+    assert "quick binding" in said and called == "True" and version == "100"
+
+
+def test_a_binding_for_another_torch_is_built_anew(built, tmp_path, monkeypatch):
+    import __graft_entry__
+    m = __graft_entry__._build_module()
+    assert m.up_to_date()
+    monkeypatch.setattr(m, "built_for", lambda: "torch 0.0, another Python")
+    assert not m.up_to_date()
+    monkeypatch.setattr(m, "BIND", str(tmp_path / "_csa2_bind.so"))
+    m._build_bind()
+    assert m.up_to_date()
+    monkeypatch.undo()
+    assert m.up_to_date()
