@@ -35,10 +35,6 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "csa2.h"), __file__]
-
-
 def _torch() -> str:
     """The installed torch's folder (found, not imported)."""
     return importlib.util.find_spec("torch").submodule_search_locations[0]
@@ -50,14 +46,23 @@ def built_for() -> str:
     return "torch %s, %s" % (version, sysconfig.get_config_var("SOABI"))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+def _newer(target, sources) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in sources)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "csa2.h"), __file__])
+
+
+def _bind_up_to_date() -> bool:
+    if not _newer(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "csa2.h"), __file__]):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     with open(BIND, "rb") as f:
-        if built_for().encode() not in f.read():
-            return False
-    return all(os.path.getmtime(p) <= t for p in _deps())
+        return built_for().encode() in f.read()
+
+
+def up_to_date() -> bool:
+    return _lib_up_to_date() and _bind_up_to_date()
 
 
 def _build_bind():
@@ -65,8 +70,8 @@ def _build_bind():
     torch = _torch()
     lib = os.path.join(torch, "lib")
     tmp = BIND + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", '-DCSA2_BUILT_FOR="%s"' % built_for(), "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-           "-I", os.path.join(torch, "include"), os.path.join(CSRC, "bind.cpp"), "-o", tmp, "-L", lib, "-ltorch_python",
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", '-DCSA2_BUILT_FOR="%s"' % built_for(),
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include"), os.path.join(CSRC, "bind.cpp"), "-o", tmp, "-L", lib, "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -74,8 +79,20 @@ def _build_bind():
     os.replace(tmp, BIND)
 
 
+def _bring_bind(force):
+    """The package works without the extension: what keeps it from being built is said, and a stale one goes."""
+    try:
+        if force or not _bind_up_to_date():
+            _build_bind()
+    except Exception as e:
+        if os.path.exists(BIND):
+            os.remove(BIND)
+        sys.stderr.write("%s is not built, calls will take some microseconds longer: %s\n" % (os.path.basename(BIND), e))
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+    if not force and _lib_up_to_date():
+        _bring_bind(False)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -91,7 +108,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        bind = ex.submit(_build_bind)
+        bind = ex.submit(_bring_bind, force)
         objs = list(ex.map(compile_one, sources()))
         bind.result()
     tmp = LIB + ".tmp%d" % os.getpid()

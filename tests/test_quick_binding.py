@@ -93,3 +93,22 @@ def test_a_binding_for_another_torch_is_built_anew(built, tmp_path, monkeypatch)
     assert m.up_to_date()
     monkeypatch.undo()
     assert m.up_to_date()
+
+
+def test_the_library_is_built_without_a_compiler_for_the_binding(built, tmp_path, monkeypatch, capsys):
+    """No torch headers, no host compiler: the library is there all the same, and no binding of before is left."""
+    import __graft_entry__
+    m = __graft_entry__._build_module()
+    old = tmp_path / "_csa2_bind.so"
+    old.write_bytes(b"of before")
+    monkeypatch.setattr(m, "BIND", str(old))
+    monkeypatch.setenv("CXX", "false")
+    before = os.path.getmtime(m.LIB)
+    assert m.build() == m.LIB and os.path.exists(m.LIB)
+    assert os.path.getmtime(m.LIB) == before                             # nor is the library compiled again for it
+    assert not old.exists() and "_csa2_bind.so" in capsys.readouterr().err
+    monkeypatch.delenv("CXX")
+    m.build()
+    assert old.exists() and m.up_to_date() and os.path.getmtime(m.LIB) == before
+    monkeypatch.setattr(m, "_torch", lambda: str(tmp_path))             # no torch
+    assert m.build() == m.LIB and not old.exists()
