@@ -235,7 +235,7 @@ extern "C" csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_t
         CSA2_REQUIRE(out[i].apart(), "rope: rows of an output share elements");
         const bool same = a.in[i] == a.out[i] && (T == 1 || a.in_token[i] == a.out_token[i]) &&
                           (a.heads[i] == 1 || a.in_head[i] == a.out_head[i]);
-        CSA2_REQUIRE(same || !meet(in[i].p, in[i].bytes(), out[i].p, out[i].bytes()), "rope: an output overlaps its input");
+        CSA2_REQUIRE(same || !share(out[i], in[i]), "rope: an output overlaps its input");
         CSA2_REQUIRE(!meet(out[i].p, out[i].bytes(), pos, 4 * T) && !meet(out[i].p, out[i].bytes(), cos_sin, 4 * n_pos * rope_dim) &&
                          !meet(out[i].p, out[i].bytes(), err_flag, err_flag ? 4 : 0),
                      "rope: an output overlaps pos, cos_sin or the flag");
