@@ -80,14 +80,30 @@ struct Rows {
 static inline bool meet(const void *p, int64_t n, const void *q, int64_t m) {
     return n > 0 && m > 0 && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
 }
-// Whether two tensors' rows may share elements: not if one lies behind the other, nor if
-// they are different parts of the same tokens (slices of one projection's output).
+// Whether two tensors' rows may share elements.  They do not if one lies behind the other, nor if they are different
+// parts of the same tokens (slices of one projection's output), of the same heads (the same with heads first) or of the
+// same rows (projections side by side in each head): modulo strides that both have, their elements are in intervals
+// that do not meet.
 static inline bool share(const Rows &x, const Rows &y) {
     if (!meet(x.p, x.bytes(), y.p, y.bytes())) return false;
-    const int64_t step = ((int64_t)(uintptr_t)y.p - (int64_t)(uintptr_t)x.p) / 2, s = x.token;
-    if (x.T <= 1 || s != y.token || s <= 0 || ((uintptr_t)y.p - (uintptr_t)x.p) % 2) return true;
-    const int64_t d = (step % s + s) % s;
-    return (x.H - 1) * x.head + x.D > d || d + (y.H - 1) * y.head + y.D > s;
+    const int64_t gap = (int64_t)(uintptr_t)y.p - (int64_t)(uintptr_t)x.p;
+    if (gap % 2) return true;
+    auto common = [](int64_t a, int64_t b) {
+        while (b) {
+            const int64_t r = a % b;
+            a = b, b = r;
+        }
+        return a;
+    };
+    auto apart = [&](int64_t m, int64_t nx, int64_t ny) {            // x in [0, nx), y in [d, d + ny) modulo m
+        if (m <= 0) return false;
+        const int64_t d = ((gap / 2) % m + m) % m;
+        return nx <= d && d + ny <= m;
+    };
+    auto across = [](int64_t n, int64_t stride) { return n > 1 ? stride : 0; };      // a stride of an extent of one says nothing
+    const int64_t token = common(across(x.T, x.token), across(y.T, y.token)), head = common(across(x.H, x.head), across(y.H, y.head));
+    return !apart(token, (x.H - 1) * x.head + x.D, (y.H - 1) * y.head + y.D) &&
+           !apart(head, (x.T - 1) * x.token + x.D, (y.T - 1) * y.token + y.D) && !apart(common(token, head), x.D, y.D);
 }
 
 }  // namespace csa2

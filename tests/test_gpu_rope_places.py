@@ -40,3 +40,29 @@ def test_rotation_into_other_columns_of_the_same_buffer(csa2, half, T, H, D, dim
         csa2.csa2_rope(at(got, src), pos, table, q_out=at(got, dst), first=first, layout=layout)
         torch.cuda.synchronize()
         _same(got, want)
+
+
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("T,H,D", [(1, 5, 64), (37, 3, 128), (2000, 4, 64)])
+def test_projections_side_by_side_in_every_head(csa2, T, H, D, heads_first):
+    """q, k and v of a head beside one another: rotated in place, and written there by the reading back."""
+    gen = torch.Generator().manual_seed(T + D)
+    buf = torch.randn(T, H, 3 * D, generator=gen).to(F16).to(DEV)
+    if heads_first:
+        buf = buf.transpose(0, 1).contiguous().transpose(0, 1)
+    pos, table = torch.randint(0, 40, (T,), generator=gen).int().to(DEV), _table(gen, 40, D // 2)
+    q, k, v = buf[..., :D], buf[..., D:2 * D], buf[..., 2 * D:]
+    want = [ref.rotate(x.cpu(), pos.tolist(), table, 0, True).to(DEV) for x in (q, k)] + [v.clone()]
+    csa2.csa2_rope(q, pos, table, k=k)
+    torch.cuda.synchronize()
+    for got, w in zip((q, k, v), want):
+        _same(got, w)
+    n, S = T // 16 + 2, 16
+    planes = [t.to(DEV) for _ in range(2) for t in ref.random_planes(gen, n, H, S, D)]
+    kc, ks, vc, vs = planes
+    at = torch.randperm(n * S, generator=gen)[:T].to(DEV)
+    csa2.csa2_dequantize_kv_fp4_paged(at, kc, vc, ks, vs, k, v)
+    torch.cuda.synchronize()
+    held = [torch.from_numpy(ref.values(c[at // S, :, at % S], s[at // S, :, at % S])).to(F16).to(DEV) for c, s in ((kc, ks), (vc, vs))]
+    for got, w in zip((q, k, v), [want[0]] + held):
+        _same(got, w)
