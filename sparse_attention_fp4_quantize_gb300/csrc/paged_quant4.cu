@@ -406,8 +406,8 @@ extern "C" csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, 
         int64_t bytes;
     } outs[6] = {{k_codes, plane}, {v_codes, plane}, {k_scales, plane / 8}, {v_scales, plane / 8}, {k_values, k_values ? dense : 0},
                  {v_values, v_values ? dense : 0}},
-      ins[5] = {{k, in[0].bytes()}, {v, in[1].bytes()}, {slots, 8 * T}, {pos, pos ? 4 * T : 0},
-                {cos_sin, cos_sin ? 4 * n_pos * rope_dim : 0}};
+      ins[6] = {{k, in[0].bytes()}, {v, in[1].bytes()}, {slots, 8 * T}, {pos, pos ? 4 * T : 0},
+                {cos_sin, cos_sin ? 4 * n_pos * rope_dim : 0}, {err_flag, err_flag ? 4 : 0}};
     for (int i = 0; i < 6; ++i) {
         bool over = false;
         for (const auto &x : ins) over = over || meet(outs[i].p, outs[i].bytes, x.p, x.bytes);
@@ -449,7 +449,7 @@ extern "C" csa2_status csa2_dequantize_kv_fp4_paged(const int64_t *slots, int64_
     const int64_t plane = n_blocks * Hkv * S * (D / 2);
     for (const Rows &r : out) {
         CSA2_REQUIRE(r.apart(), "dequantize_fp4_paged: rows of an output share elements");
-        bool over = meet(r.p, r.bytes(), slots, 8 * T);
+        bool over = meet(r.p, r.bytes(), slots, 8 * T) || meet(r.p, r.bytes(), err_flag, err_flag ? 4 : 0);
         for (const uint8_t *p : {k_codes, v_codes}) over = over || meet(r.p, r.bytes(), p, plane);
         for (const uint8_t *p : {k_scales, v_scales}) over = over || meet(r.p, r.bytes(), p, plane / 8);
         CSA2_REQUIRE(!over, "dequantize_fp4_paged: an output overlaps another argument");
