@@ -606,7 +606,7 @@ csa2_status csa2_dequantize_kv_fp4_paged(const int64_t *slots, int64_t T, int64_
  * Keys and values enter the tensor cores as exact f16, q as f16 scaled per row by a
  * power of two (bf16 values within 2^-31 of the row's largest are exact); sums and
  * softmax statistics are fp32, the weights P_j are rounded to f16's 11 bits, those
- * below 2^-22 of the row's largest to a step of 2^-32 of it.
+ * below 2^-22 of their sum to a step of 2^-32 of it.
  * Stored scales must be no NaN (csa2_quantize_kv_fp4_paged writes none); rows at or
  * beyond kv_len may hold anything.
  * workspace csa2_paged_attn_fp4_workspace_bytes() bytes, 16-byte aligned (at most 64 MiB).
