@@ -539,7 +539,8 @@ csa2_status csa2_rope_table(const double *inv_freq, int half, int64_t start, int
  *           of 8, 0..D - rope_dim.
  * pos       int32 [T], -1: a row without a token, whose output is left as it was;
  *           so is that of a position outside [0, n_pos) (CSA2_FLAG_BAD_INDEX).
- * cos_sin   float [n_pos, rope_dim/2, 2], 16-byte aligned.
+ * cos_sin   float [n_pos, rope_dim/2, 2], 16-byte aligned, n_pos 1..2^31.  Outputs overlap
+ *           neither pos, cos_sin nor the flag.  T <= 2^30, Hq <= 32768, Hk <= 32767.
  */
 csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_token_stride, int64_t q_head_stride,
                       int64_t qo_token_stride, int64_t qo_head_stride, const void *k, void *k_out, int Hk,
@@ -556,7 +557,10 @@ csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_token_stride
  *   k_scales, v_scales  uint8 [n_blocks, Hkv, S, D/16], E4M3; a value is code * scale
  * all 16-byte aligned; S in {16, 32, 64, 128}, D in {64, 128}.  Block tables, slots
  * and lengths are those of csa2_build_slots.  A row needs 9/16 of the 8-bit cache's bytes
- * and is stored for good: later rows do not move its scales.
+ * and is stored for good: later rows do not move its scales.  With no second scale, 16
+ * channels have the format's 4 + 2 bits while their amax is from 0.094 (6 * 2^-6) to 2688: below, the
+ * scale is a subnormal E4M3 number with up to 3 bits fewer, up to 6 * 2^-10 it is 0 and so are
+ * they; above, values end at 2688.
  */
 
 /*
@@ -576,7 +580,7 @@ csa2_status csa2_rope(const void *q, void *q_out, int Hq, int64_t q_token_stride
  *         codes stand for (exact), so that a prompt may attend to the values that later
  *         steps will see.  Rows that are not stored are left as they were.
  * Infinities are stored as +-6 scale and NaN as 0, neither counts toward amax
- * (CSA2_FLAG_NONFINITE).  Codes, scales and values overlap nothing else.
+ * (CSA2_FLAG_NONFINITE).  Codes, scales and values overlap nothing else, nor the flag.
  */
 csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, csa2_dtype dt, int64_t T, int Hkv, int D,
                                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
@@ -591,7 +595,8 @@ csa2_status csa2_quantize_kv_fp4_paged(const void *k, const void *v, csa2_dtype 
  * slots[t], exact in bf16 and fp16.  A slot may be given any number of times; -1 leaves its
  * row as it was, as does a slot outside [-1, n_blocks * S) (CSA2_FLAG_BAD_SLOT).
  * k, v bf16 or fp16 [T, Hkv, D], 16-byte aligned, D contiguous, token and head
- * strides in elements (multiples of 8 below 2^31); no two rows share elements.
+ * strides in elements (multiples of 8 below 2^31); no two rows share elements, nor does one
+ * with another argument.  T <= 2^30, Hkv <= 32767.
  */
 csa2_status csa2_dequantize_kv_fp4_paged(const int64_t *slots, int64_t T, int64_t n_blocks, int Hkv, int S, int D,
                                          const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_scales,

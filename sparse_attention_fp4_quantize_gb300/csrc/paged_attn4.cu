@@ -18,7 +18,7 @@
 // 7 us apart, but shares that make up for it (5 to 15 % more for the first) only slow the last ones'
 // keys down: 131 to 141 us.  48 requests with 5 new tokens in a window of 4096, 15 heads of 64
 // over 5 (61 MB): 33 us, of which 5 go by before the first tile (lengths, table, codes, each after
-// the other) and 3 in the join; the loads alone take 20.  One request of 1000 tokens: 8.4 us in a
+// the other) and 3 in the join; the loads alone take 20.  One request of 1000 tokens: 8.2 us in a
 // graph.
 #include "fp4.cuh"
 #include "paged_attn.cuh"
@@ -542,6 +542,9 @@ cudaError_t launch_split4(const PagedAttnArgs &a, int ctas, cudaStream_t stream)
 // of up to 16k 127.7 and 136.3; 8 of up to 32k 40.3 and 39.8.  Of 64 channels 1 of up to 1000 7.4 and 7.0, 64 of up
 // to 1000 16.9 and 15.6, of up to 2000 21.8 and 22.7, 8 of up to 8000 12.9 and 13.2.  The lengths are the
 // GPU's: the rule goes by what the tables (or the windows) could hold, at most so many tiles of 64 keys per CTA.
+// It is wrong where that says little: short contexts behind tables that could hold long ones get the long tiles (64 of up to
+// 1000 tokens with room for 131072: 24.9 in place of 22.0), and of 64 channels the two sides are not parted by it, 64 of up
+// to 1000 (18 tiles per CTA) want the short tiles and get the long ones, 1.3 us, as 8 of up to 8000 (17.5) want them.
 constexpr int few4(int D) { return D == 128 ? 96 : 16; }
 inline bool few_keys4(const PagedAttnArgs &a, int D, int max_new, int ctas) {
     const int64_t most = (int64_t)a.M * a.S, keys = a.window > 0 && a.window + (int64_t)max_new < most ? a.window + (int64_t)max_new : most;

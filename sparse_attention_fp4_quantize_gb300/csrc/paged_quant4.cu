@@ -177,7 +177,8 @@ __device__ __forceinline__ bool place_of(const Quant4Args &a, int64_t t, bool fi
 }
 
 // Any rotation: a thread takes one group of a row and reads its partners beside it.  16384 tokens,
-// 8 heads of 128: 36 us, pairs side by side or halves of 64 channels.
+// 8 heads of 128: 33.7 us with pairs side by side, 34.1 with halves of 64 channels (4.5 TB/s; issue 0.49 a cycle,
+// and loads that it waits for: none are under way while a row is stored, and partners are asked for twice).
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_any_kernel(Quant4Args a) {
     pdl_wait();
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_any_kernel(Quant4
 
 // No rotation, or one of halves over the whole head: a thread takes a group and the one
 // half a row behind it, which are each other's partners, so nothing is read or turned twice: 27.6 us
-// where the kernel above takes 36.  The next head's loads are on their way
+// where the kernel above takes 34.  The next head's loads are on their way
 // meanwhile (34.5 otherwise).
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads) quantize_fp4_paged_kernel(Quant4Args a) {
